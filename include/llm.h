@@ -474,6 +474,120 @@ int32_t llm_op_attn_decode_noalloc(const float *q, const void *k_cache, const vo
                                    int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq,
                                    int32_t n_split, void *stream);
 
+/* --------------------------------------------------------------------------
+ * 4-bit operators: Q4_0 weights, a Q4_0 cache, and the per-head query/key norm
+ * that feeds it.  None of these calls allocates or waits: each enqueues its
+ * kernels on `stream` and returns, so all but the prefill attention can be
+ * captured into a CUDA graph.  Pointers belong to the current device.
+ *
+ * Q4_0 blocks ("LLama.cpp — how it works" names four-bit types in "The GGUF
+ * format (reference)" and a quantised cache in "KV-cache" without a layout;
+ * the one taken): a row is cut into blocks of 32 consecutive elements.  With m
+ * the block's element of largest magnitude (the first of equals) and the
+ * unrounded scale m / -8, a block keeps d = f16(m / -8) and codes c = the
+ * nearest integer to w / (m / -8) (ties to even) + 8, clamped to 0..15, and
+ * stands for d * (c - 8).  Codes lie eight to a 32-bit word: in a group of nb
+ * blocks word t * nb + b (t = 0..3) holds elements 32 b + 8 t + {0..7} of the
+ * group, element 8 t + 2 i in bits 4 i.., element 8 t + 2 i + 1 in bits
+ * 16 + 4 i...
+ *   Weight rows (K a multiple of 256): chunks of 256 elements, 144 bytes each:
+ *   two groups of 128 elements (nb = 4, 64 bytes), then the 8 fp16 scales.
+ *   Caches of one layer: the codes [n_seq][Hkv][n_ctx][head_dim / 2 bytes]
+ *   (nb = head_dim / 32), then the fp16 scales [n_seq][Hkv][n_ctx][head_dim / 32];
+ *   llm_op_kv_q4_0_bytes bytes for K and the same for V, 16-byte aligned.
+ * ------------------------------------------------------------------------*/
+
+/* Q4_0 encoding of the fp16 matrix W [N][K] into out (N rows of 9 K / 16
+ * bytes), both 16-byte aligned; W is only read.  LLM_ERR_INVALID for a null
+ * or misaligned pointer, N < 1 or a K that is not a positive multiple of 256. */
+int32_t llm_op_quantize_q4_0(const void *W, int32_t N, int32_t K, void *out, void *stream);
+
+/* y[t][n] = sum over blocks b of d[n][b] * sum over k in b of
+ * (c[n][k] - 8) * x[t][k], t < T <= 8, fp32 sums: the decode GEMV over Q4_0
+ * rows (as written by llm_op_quantize_q4_0).  x fp16 [T][ldx] (16-byte
+ * aligned, ldx >= K a multiple of 8), y fp32 [T][ldy] (ldy >= N; the entries
+ * between N and ldy are left as they are).  Any N >= 1, any K that is a
+ * positive multiple of 256, else LLM_ERR_INVALID. */
+int32_t llm_op_gemv_q4_0(const void *Wq, const void *x, float *y, int32_t N, int32_t K, int32_t T, int32_t ldx,
+                         int32_t ldy, void *stream);
+
+/* Bytes of one layer's Q4_0 cache of K (V takes the same); LLM_ERR_INVALID for
+ * a head_dim other than 32, 64, 128 or a non-positive size. */
+int64_t llm_op_kv_q4_0_bytes(int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq);
+
+/* Queries and keys normed per head and rotated, keys and values appended to
+ * the cache, in one pass over the QKV projection's output: for row t < T and
+ * each query or key head x of it, u = x * gain / sqrt(mean(x^2) + eps) (the
+ * head itself where its gain pointer is NULL), then the rotation of pairs
+ * (u[2i], u[2i+1]) by rope[pos[t]][i] = (cos, sin).  Values are appended as
+ * they are.
+ *   qkv     fp32 [T][ld]: H query heads, Hkv key heads, Hkv value heads of hd
+ *           elements; ld a multiple of 4, at least (H + 2 Hkv) * hd
+ *   q_gain, k_gain  fp32 [hd] or NULL
+ *   rope    fp32 [n_ctx][hd / 2][2]: cos and sin of a position's angles
+ *   pos, seq  int32 [T]: the cell each row's K and V go to
+ *   q       [T][H * hd], fp32 (q_type LLM_Q_F32) or fp16 (LLM_Q_F16)
+ *   k_cache, v_cache  one layer [n_seq][Hkv][n_ctx][hd] of fp16 (kv_type
+ *           LLM_KV_F16), FP8 E4M3 bytes (LLM_KV_E4M3, nearest, saturating) or
+ *           Q4_0 (LLM_KV_Q4_0: the codes of the exact values, also where
+ *           fp32 arithmetic would leave them next to a border)
+ *   err     DEVICE word or NULL: ORed with 2 when a row's pos lies outside
+ *           [0, n_ctx) or its seq outside [0, n_seq) (its queries are then
+ *           zero and nothing is appended), with 8 when a value narrowed to
+ *           fp16 or Q4_0 is not finite or beyond +-65504
+ * Rows of one call have distinct (seq, pos): of two with the same cell, which
+ * one's values the cell ends with is undefined.  Pointers 16-byte aligned;
+ * head_dim 32, 64 or 128; H a multiple of Hkv, at most 4096; else
+ * LLM_ERR_INVALID before anything is enqueued (reason in llm_last_error(NULL)). */
+#define LLM_Q_F32 0
+#define LLM_Q_F16 1
+#define LLM_KV_F16 0
+#define LLM_KV_E4M3 1
+#define LLM_KV_Q4_0 2
+int32_t llm_op_qk_norm_rope(const float *qkv, int32_t ld, const float *q_gain, const float *k_gain, float eps,
+                            const float *rope, const int32_t *pos, const int32_t *seq, void *q, int32_t q_type,
+                            void *k_cache, void *v_cache, int32_t kv_type, int32_t T, int32_t H, int32_t Hkv,
+                            int32_t hd, int32_t n_ctx, int32_t n_seq, uint32_t *err, void *stream);
+
+/* The values that rows of a Q4_0 cache (K's or V's) stand for: out fp16
+ * [T][Hkv][hd], row t the cell pos[t] of sequence seq[t] (int32 [T], DEVICE).
+ * A row outside the cache is zero and ORs 2 into *err (DEVICE word or NULL). */
+int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, const int32_t *seq, void *out, int32_t T,
+                            int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq, uint32_t *err, void *stream);
+
+/* Decode attention over a Q4_0 cache: for each row t < T <= 4096 and query
+ * head h, o[t][h] = softmax_c(q[t][h] . K[c] / sqrt(hd)) V[c] over the cache
+ * positions c of sequence seq[t] with c <= pos[t] and, when window > 0,
+ * c > pos[t] - window.  q fp32 [T][H*hd]; pos, seq int32 [T] (DEVICE); o fp16
+ * [T][H*hd]; any H that is a multiple of Hkv, up to 4096.  Cells outside a
+ * row's visible positions may hold anything.  scratch: scratch_bytes bytes,
+ * zeroed once before its first use; each call leaves it ready for the next of
+ * the same shape, and calls that may overlap need one each.  A row whose pos
+ * lies outside [0, n_ctx) or whose seq lies outside [0, n_seq) gives zeros and
+ * ORs 2 into *err (DEVICE word or NULL). */
+int64_t llm_op_attn_decode_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
+                                              int32_t n_seq);
+int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void *v_cache, const int32_t *pos,
+                                const int32_t *seq, void *o, int32_t T, int32_t H, int32_t Hkv, int32_t hd,
+                                int32_t n_ctx, int32_t n_seq, int32_t window, void *scratch, int64_t scratch_bytes,
+                                uint32_t *err, void *stream);
+
+/* Prefill attention over a Q4_0 cache: rows r < T of q fp16 [T][H*hd] belong to
+ * sequence seq[r] at position pos[r] and see the positions a decode row would.
+ * pos, seq are HOST arrays, read before the call returns: the rows of a
+ * sequence are consecutive with consecutive positions, else LLM_ERR_INVALID
+ * before anything is enqueued.  o fp16 [T][H*hd].  scratch (contents need not
+ * be initialised) takes the visible cells widened to fp16; calls that may
+ * overlap need one each.  err: DEVICE word or NULL, ORed with 4 when a bounded
+ * wait of the kernel timed out.  Not for stream capture: the row list is
+ * copied from host memory. */
+int64_t llm_op_attn_prefill_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
+                                               int32_t n_seq);
+int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void *v_cache, const int32_t *pos,
+                                 const int32_t *seq, void *o, int32_t T, int32_t H, int32_t Hkv, int32_t hd,
+                                 int32_t n_ctx, int32_t n_seq, int32_t window, void *scratch, int64_t scratch_bytes,
+                                 uint32_t *err, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(HERE, "libllm.so")
 LLM_OK, LLM_NO_KV_ROOM, LLM_ERR_INVALID, LLM_ERR_ALLOC, LLM_ERR_COMPUTE = 0, 1, -1, -2, -3
 LLM_BATCH_TOKENS_ON_DEVICE = 1
 LLM_WTYPE_Q8_0 = 1
+LLM_Q_F32, LLM_Q_F16 = 0, 1
+LLM_KV_F16, LLM_KV_E4M3, LLM_KV_Q4_0 = 0, 1, 2
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with llama_decoder_forward_02_gb300.build.build()")
@@ -101,6 +103,21 @@ llm_op_attn_decode_noalloc = _proto("llm_op_attn_decode_noalloc", c_i32, c_vp, c
                                     c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp)
 llm_op_attn_prefill = _proto("llm_op_attn_prefill", c_i32, c_vp, c_vp, c_vp, c_i32p, c_i32p, c_vp, c_i32, c_i32,
                              c_i32, c_i32, c_i32, c_i32, c_vp)
+
+llm_op_quantize_q4_0 = _proto("llm_op_quantize_q4_0", c_i32, c_vp, c_i32, c_i32, c_vp, c_vp)
+llm_op_gemv_q4_0 = _proto("llm_op_gemv_q4_0", c_i32, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp)
+llm_op_kv_q4_0_bytes = _proto("llm_op_kv_q4_0_bytes", c_i64, c_i32, c_i32, c_i32, c_i32)
+llm_op_qk_norm_rope = _proto("llm_op_qk_norm_rope", c_i32, c_vp, c_i32, c_vp, c_vp, c_f32, c_vp, c_vp, c_vp, c_vp,
+                             c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp)
+llm_op_kv_rows_q4_0 = _proto("llm_op_kv_rows_q4_0", c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32,
+                             c_vp, c_vp)
+llm_op_attn_decode_q4_0_scratch_bytes = _proto("llm_op_attn_decode_q4_0_scratch_bytes", c_i64, c_i32, c_i32, c_i32,
+                                               c_i32, c_i32, c_i32)
+llm_op_attn_prefill_q4_0_scratch_bytes = _proto("llm_op_attn_prefill_q4_0_scratch_bytes", c_i64, c_i32, c_i32, c_i32,
+                                                c_i32, c_i32, c_i32)
+_attn_q4_args = [c_vp] * 6 + [c_i32] * 7 + [c_vp, c_i64, c_vp, c_vp]
+llm_op_attn_decode_q4_0 = _proto("llm_op_attn_decode_q4_0", c_i32, *_attn_q4_args)
+llm_op_attn_prefill_q4_0 = _proto("llm_op_attn_prefill_q4_0", c_i32, *_attn_q4_args)
 
 EXPORTED = [n for n in dir() if n.startswith("llm_") and callable(globals()[n]) and
             not isinstance(globals()[n], type)]

@@ -35,6 +35,11 @@ struct KvView {
     // FP8 E4M3 cache (one byte an element, same element offsets) when not null;
     // k and v are then unused
     uint8_t *k8 = nullptr, *v8 = nullptr;
+    // Q4_0 cache when not null (q4.cuh has the layout): the codes of the row
+    // that starts at element e lie at byte e / 2 of k4 / v4, its block scales
+    // at entry e / 32 of kd / vd; k, v, k8 and v8 are then unused
+    uint8_t *k4 = nullptr, *v4 = nullptr;
+    f16 *kd = nullptr, *vd = nullptr;
 };
 
 // ------------------------------------------------------------------ decode GEMV
@@ -288,5 +293,56 @@ size_t q8_0_row_bytes(int K);
 // `polls` times; a wait that never completes raises ERRF_WAIT_TIMEOUT in *err.
 cudaError_t launch_wait_check(int arrive, uint32_t polls, uint32_t *err, cudaStream_t st);
 cudaError_t launch_quantize_q8_0(f16 *w, int N, int K, uint8_t *q8, bool write_back, cudaStream_t st);
+
+// ------------------------------------------------------------------ Q4_0
+// Q4_0 encoding of the fp16 matrix w [N][K] (K % 32 == 0): into q4 (rows of
+// q4_0_row_bytes(K) bytes, K % 256 == 0) when not null, and with write_back w
+// itself replaced by the weights the blocks stand for, f16(d * (c - 8)).
+size_t q4_0_row_bytes(int K);
+cudaError_t launch_quantize_q4_0(f16 *w, int N, int K, uint8_t *q4, bool write_back, cudaStream_t st);
+
+// y[t][n] = sum_k W[n][k] x[t][k] with Q4_0 rows W, t < T <= 8.
+struct GemvQ4Args {
+    const uint8_t *W;         // [N] rows of q4_0_row_bytes(K)
+    int N, K, T;
+    const f16 *x; int ldx;
+    float *out; int ldo;
+    uint32_t *err;
+};
+cudaError_t launch_gemv_q4(const GemvQ4Args &a, int num_sms, const Launch &l);
+
+// Per-head RMSNorm (gains may be null: no norm) and rotation of the query and
+// key heads of qkv rows [T][ld] (H query, Hkv key, Hkv value heads), q to q32
+// or q16 [T][H * hd], keys and values appended to the cache kv.
+struct QkNormArgs {
+    const float *qkv; int ld;
+    const float *q_gain, *k_gain; float eps;
+    const float2 *rope;        // [n_ctx][hd / 2]
+    const int *pos, *seq;
+    float *q32; f16 *q16;
+    KvView kv;
+    int T, H;
+    uint32_t *err;
+};
+cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l);
+
+// Decode attention over a Q4_0 cache (AttnDecodeArgs with kv.k4 set; any T,
+// any H / Hkv).  part: attn_q4_part_floats; counters: T * Hkv * head chunks,
+// zero before the first launch and left zero.
+int attn_q4_pick_split(int T, int H, int Hkv, int n_ctx);
+int attn_q4_chunks(int H, int Hkv);
+size_t attn_q4_part_floats(int T, int H, int hd, int n_split);
+cudaError_t launch_attn_decode_q4(const AttnDecodeArgs &a, const Launch &l);
+
+// Key ranges [lo, hi) of sequences to widen from a Q4_0 cache to fp16.
+struct KvSpan { int seq, lo, hi; };
+// Widen the spans' rows of both caches into k16, v16, laid out
+// [n_seq][Hkv][n_pad][hd] (n_pad a multiple of 128): rows [lo, hi) as the
+// values they stand for, the other rows of the 128-row tiles they touch zero.
+cudaError_t launch_kv_widen_q4(const KvView &kv, const KvSpan *spans, int n_spans, int max_rows, f16 *k16, f16 *v16,
+                               int n_pad, const Launch &l);
+// out[t][j][:] = the values of row pos[t], kv head j of sequence seq[t].
+cudaError_t launch_kv_rows_q4(const uint8_t *codes, const f16 *scales, const KvView &kv, const int *pos,
+                              const int *seq, f16 *out, int T, uint32_t *err, const Launch &l);
 
 }  // namespace llm

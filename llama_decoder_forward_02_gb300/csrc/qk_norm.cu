@@ -1,0 +1,180 @@
+// Queries and keys normed per head, rotated by their position, and the keys
+// and values appended to the cache, in one pass over the QKV projection's
+// output ("Inside the inference engine: model architectures and forward
+// pass", section "Detailed explanation: Llama's forward pass in Go": RoPE on Q
+// and K, then the cache's Put; the per-head norm is RMSNorm over head_dim with
+// a gain shared by the heads, as model families with normed queries and keys
+// apply it between the projection and the rotation):
+//   u = x * gain / sqrt(mean(x^2) + eps),  (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
+// on adjacent pairs.  A model without such gains skips the norm; it comes here
+// when its cache is Q4_0, whose blocks need 32 neighbouring elements at once,
+// which no projection epilogue holds.
+//
+// head_dim / 4 lanes take one head of one row, four elements (two rotation
+// pairs) a lane, so the norm's sum and a block's largest magnitude are a few
+// shuffles and every access is a 16-byte vector.  Bound by memory: 4 bytes
+// read and about 2 written an element.
+//
+// Q4_0 codes are those of the exact values.  A float32 value carries a few
+// ulp of error from the norm and the rotation, which matters only next to a
+// border between two codes; a row with an element within NEAR of one (about
+// one row in 200) is encoded again from float64 arithmetic.
+#include "common.cuh"
+#include "launch.cuh"
+#include "q4.cuh"
+
+namespace llm {
+
+namespace {
+
+constexpr int THREADS = 256;
+// Distance from a code border, in codes, under which float32 does not settle
+// the code: |v / d| <= 8 with a relative error below 16 * 2^-24 gives 8e-6.
+constexpr float NEAR = 1.5e-5f;
+
+template <int W, class R>
+__device__ __forceinline__ R group_sum(R v) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The head's values after norm and rotation, in R.
+template <int HD, class R>
+__device__ __forceinline__ void transform(const float (&x)[4], const float (&gain)[4], const float4 cs, bool norm,
+                                          bool turn, float eps, R (&u)[4]) {
+    // the shuffles run for every lane: heads without a norm share the warp
+    R ss = R(0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ss += R(x[e]) * R(x[e]);
+    ss = group_sum<HD / 4>(ss);
+    const R r = R(1) / sqrt(ss / R(HD) + R(eps));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = norm ? R(x[e]) * r * R(gain[e]) : R(x[e]);
+    if (turn) {
+        const R a0 = u[0] * R(cs.x) - u[1] * R(cs.y), b0 = u[0] * R(cs.y) + u[1] * R(cs.x);
+        const R a1 = u[2] * R(cs.z) - u[3] * R(cs.w), b1 = u[2] * R(cs.w) + u[3] * R(cs.z);
+        u[0] = a0; u[1] = b0; u[2] = a1; u[3] = b1;
+    }
+}
+
+// The codes of a lane's four elements and the scale of its block (8 lanes).
+// Returns whether a value lies so near a border that R does not settle it.
+template <class R>
+__device__ __forceinline__ bool encode(const R (&u)[4], int lane, R &d, int (&c)[4]) {
+    R m = u[0];
+#pragma unroll
+    for (int e = 1; e < 4; ++e)
+        if (fabs(u[e]) > fabs(m)) m = u[e];
+    R top = fabs(m);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+        const R other = __shfl_xor_sync(0xffffffffu, top, o);
+        top = other > top ? other : top;
+    }
+    // the first element of that magnitude gives the sign
+    const unsigned has = __ballot_sync(0xffffffffu, fabs(m) == top) >> (lane & ~7) & 0xffu;
+    m = __shfl_sync(0xffffffffu, m, (lane & ~7) + (has ? __ffs(has) - 1 : 0));
+    d = m * R(-0.125);
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        c[e] = q4::code_of(u[e], d);
+        if (d != R(0)) {
+            const R q = u[e] / d;                     // in [-8, 8]: the top itself is at -8
+            near |= fabs(fabs(q - rint(q)) - R(0.5)) < R(NEAR) || q > R(8) - R(NEAR);
+        }
+    }
+    return near;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkNormArgs a) {
+    constexpr int L = HD / 4;                         // lanes of a head
+    const int lane = threadIdx.x & 31, sub = lane % L, e0 = 4 * sub;
+    const int Hkv = a.kv.n_kv_head, heads = a.H + 2 * Hkv;
+    const long long unit = ((long long)blockIdx.x * THREADS + threadIdx.x) / L;
+    pdl_wait();
+    pdl_trigger();
+    // every lane stays for the shuffles; the ones past the end store nothing
+    const bool in = unit < (long long)a.T * heads;
+    const int t = in ? (int)(unit / heads) : 0, h = in ? (int)(unit - (long long)t * heads) : 0;
+    const bool is_q = h < a.H, is_k = !is_q && h < a.H + Hkv;
+    const int pos = a.pos[t], seq = a.seq[t];
+    const bool ok = pos >= 0 && pos < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
+    if (in && !ok && h == 0 && sub == 0) raise_error(a.err, ERRF_BAD_INDEX);
+
+    const float4 xv = *reinterpret_cast<const float4 *>(a.qkv + (size_t)t * a.ld + (size_t)h * HD + e0);
+    const float x[4] = {xv.x, xv.y, xv.z, xv.w};
+    const float *gp = is_q ? a.q_gain : is_k ? a.k_gain : nullptr;
+    const float4 gv = gp ? *reinterpret_cast<const float4 *>(gp + e0) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float gain[4] = {gv.x, gv.y, gv.z, gv.w};
+    float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (ok && (is_q || is_k))
+        cs = *reinterpret_cast<const float4 *>(a.rope + (size_t)pos * (HD / 2) + 2 * sub);
+    float u[4];
+    transform<HD, float>(x, gain, cs, gp != nullptr, is_q || is_k, a.eps, u);
+
+    const bool bad = f16_bad(u[0]) | f16_bad(u[1]) | f16_bad(u[2]) | f16_bad(u[3]);
+    if (is_q) {
+        if (in) {
+            const size_t off = (size_t)t * a.H * HD + (size_t)h * HD + e0;
+            const bool z = !ok;                       // a row outside the cache has zero queries
+            if (a.q32) *reinterpret_cast<float4 *>(a.q32 + off) =
+                z ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(u[0], u[1], u[2], u[3]);
+            else {
+                if (bad && ok) raise_error(a.err, ERRF_F16_RANGE);
+                *reinterpret_cast<uint2 *>(a.q16 + off) =
+                    z ? make_uint2(0u, 0u) : make_uint2(pack_h2(u[0], u[1]), pack_h2(u[2], u[3]));
+            }
+        }
+    }
+    const int j = h - a.H - (is_k ? 0 : Hkv);
+    const bool put = in && ok && !is_q;
+    const size_t base = put ? (size_t)seq * a.kv.seq_stride + ((size_t)j * a.kv.n_ctx + pos) * HD : 0;
+    if (a.kv.k4) {
+        float d;
+        int c[4];
+        const bool near = encode<float>(u, lane, d, c);
+        if (__any_sync(0xffffffffu, near && put)) {
+            double u64[4], d64;
+            transform<HD, double>(x, gain, cs, gp != nullptr, is_q || is_k, a.eps, u64);
+            encode<double>(u64, lane, d64, c);
+            d = (float)d64;
+        }
+        // elements 4 sub .. of the head: half of a word (8 elements)
+        uint32_t w = (uint32_t)c[0] | (uint32_t)c[1] << 16 | (uint32_t)c[2] << 4 | (uint32_t)c[3] << 20;
+        w |= __shfl_xor_sync(0xffffffffu, w << 8, 1);
+        if (put) {
+            if (bad) raise_error(a.err, ERRF_F16_RANGE);
+            const int blk = sub >> 3, tt = (sub & 7) >> 1;
+            if (!(sub & 1))
+                reinterpret_cast<uint32_t *>((is_k ? a.kv.k4 : a.kv.v4) + base / 2)[tt * (HD / 32) + blk] = w;
+            if ((sub & 7) == 0) (is_k ? a.kv.kd : a.kv.vd)[base / 32 + blk] = f2h(d);
+        }
+    } else if (put) {
+        if (a.kv.k8) {
+            *reinterpret_cast<uint32_t *>((is_k ? a.kv.k8 : a.kv.v8) + base + e0) =
+                (uint32_t)pack_e4m3x2(u[0], u[1]) | (uint32_t)pack_e4m3x2(u[2], u[3]) << 16;
+        } else {
+            if (bad) raise_error(a.err, ERRF_F16_RANGE);
+            *reinterpret_cast<uint2 *>((is_k ? a.kv.k : a.kv.v) + base + e0) =
+                make_uint2(pack_h2(u[0], u[1]), pack_h2(u[2], u[3]));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l) {
+    const int hd = a.kv.head_dim;
+    const long long units = (long long)a.T * (a.H + 2 * a.kv.n_kv_head);
+    if (a.T < 1 || units * hd / 4 > (1ll << 31) * THREADS / 2 || (!a.q32 && !a.q16)) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)((units * (hd / 4) + THREADS - 1) / THREADS)), block(THREADS);
+    if (hd == 32) return launch_kernel(qk_norm_rope_kernel<32>, grid, block, 0, l, a);
+    if (hd == 64) return launch_kernel(qk_norm_rope_kernel<64>, grid, block, 0, l, a);
+    if (hd == 128) return launch_kernel(qk_norm_rope_kernel<128>, grid, block, 0, l, a);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace llm

@@ -79,7 +79,8 @@ def round_to_e4m3(x: np.ndarray) -> np.ndarray:
 def round_to(x: np.ndarray, store) -> np.ndarray:
     """Storage rounding of cached K/V: None keeps the values, "bf16" / "fp16"
     round to that type (nearest, ties to even), "e4m3" to FP8 E4M3
-    (round_to_e4m3)."""
+    (round_to_e4m3), "q4_0" to the values Q4_0 blocks of 32 along head_dim
+    stand for (quantize_q4_0)."""
     if store is None:
         return x
     if store == "bf16":
@@ -88,6 +89,8 @@ def round_to(x: np.ndarray, store) -> np.ndarray:
         return np.asarray(x).astype(np.float16).astype(np.asarray(x).dtype)
     if store == "e4m3":
         return round_to_e4m3(x)
+    if store == "q4_0":
+        return dequantize_q4_0(*quantize_q4_0(x)).astype(np.asarray(x).dtype)
     raise ValueError(store)
 
 
@@ -133,6 +136,40 @@ def dequantize_q8_0(q: np.ndarray, d: np.ndarray, dtype=np.float64) -> np.ndarra
     k = q.shape[1]
     scale = np.repeat(np.asarray(d).astype(dtype), Q8_0_BLOCK, axis=1)[:, :k]
     return q.astype(dtype) * scale
+
+
+# --------------------------------------------------------------------------
+# Q4_0 blocks (weights and cache)
+# --------------------------------------------------------------------------
+
+Q4_0_BLOCK = 32
+
+
+def quantize_q4_0(w: np.ndarray):
+    """Q4_0 encoding along the last axis (a multiple of 32).  [LC] names
+    four-bit types ("The GGUF format (reference)") and a quantised cache
+    ("KV-cache") without a layout; the reading taken: blocks of 32 consecutive
+    elements; with m the element of largest magnitude (the first of equals)
+    and the unrounded scale m / -8, a block stores d = fp16(m / -8) and codes
+
+        c = clamp(nearest integer to w / (m / -8), ties to even, + 8, 0, 15)
+
+    in float64 here.  A block of zeros has d = 0 and codes 8.  Returns
+    (c uint8 with w's shape, d float16 [..., K / 32])."""
+    w = np.asarray(w, dtype=np.float64)
+    blocks = w.reshape(w.shape[:-1] + (-1, Q4_0_BLOCK))
+    at = np.abs(blocks).argmax(axis=-1)            # the first of equals
+    d = np.take_along_axis(blocks, at[..., None], -1)[..., 0] / -8
+    safe = np.where(d != 0, d, 1.0)
+    c = np.clip(np.rint(blocks / safe[..., None]) + 8, 0, 15)
+    c = np.where(d[..., None] != 0, c, 8).astype(np.uint8)
+    return c.reshape(w.shape), d.astype(np.float16)
+
+
+def dequantize_q4_0(c: np.ndarray, d: np.ndarray, dtype=np.float64) -> np.ndarray:
+    """The values Q4_0 blocks stand for: d * (c - 8), exact in float64."""
+    scale = np.repeat(np.asarray(d).astype(dtype), Q4_0_BLOCK, axis=-1)
+    return (np.asarray(c).astype(dtype) - 8) * scale
 
 
 def bf16_to_float(bits: np.ndarray, dtype=np.float64) -> np.ndarray:
