@@ -4,10 +4,34 @@
 // sqrt(hd)) V over the visible positions of sequence seq[t], K and V standing
 // for d * (c - 8) (q4.cuh).
 //
-// Decode: one CTA per (split, kv head and chunk of 8 of its query heads, row)
-// walks its span of keys, a warp 32 keys at a time with its own online
-// softmax; the splits' (max, sum, numerators) are merged in split order by the
-// CTA that arrives last.
+// Decode.  Bound by HBM reads of K and V: 9/8 bytes a (key, element), which
+// leaves an SM about 100 clocks for 16 keys of 128 elements at the copy
+// bandwidth.  Widening every code on the CUDA cores costs more than that, so
+// the codes go to mma.sync as they are, the fp16 subnormals that masking a
+// word leaves (q4.cuh):
+//   * S^T = K q^T with 16 keys as the M side.  A block of 32 dimensions is one
+//     fp32 sum of two mma (the second's q divided by 16 for the nibbles that
+//     stand four bits higher), scaled by the key's d in fp32.  The offset 8 is
+//     the sums' start value, -8 sum(q) of the block, made once.
+//   * The N side has 8 columns and a kv head rarely 8 query heads, so each
+//     head takes two: q as the sum of two fp16 numbers (22 bits), and so its
+//     weights.  Four heads fill a column tile, larger groups take NT = 2.
+//   * O^T += V^T w with 16 dimensions as the M side and w = p * d[key][block],
+//     again as two fp16 numbers; neighbouring keys' halves of a word are put
+//     together by one byte permute.  S^T comes out with keys along the lanes'
+//     rows and w is wanted with heads there: a register transpose of the warp
+//     (movmatrix) for each block.  The offset is taken off at the end,
+//     8 * sum(w).
+// So neither q, K, V nor the weights are rounded to fewer than 22 bits on the
+// way to the fp32 sums; only o is.
+//
+// A warp walks every NW-th group of 16 keys of its CTA's span through a ring
+// of its own, filled by cp.async (16-byte chunks swizzled so that both K's and
+// V's fragment reads are free of bank conflicts); warps meet only at the end.
+// The running maximum of a head is raised by a warp-uniform branch when a key
+// passes it.  Splits over the keys write (max, sum, numerators) and the CTA
+// that arrives last merges them in split order: results do not depend on
+// timing and nothing spins.
 //
 // Prefill: the visible rows of the ubatch's sequences are widened once to fp16
 // and the fp16 prefill attention runs on them.
@@ -21,8 +45,10 @@ namespace {
 
 constexpr int THREADS = 128, NW = THREADS / 32;
 constexpr int GC = 8;                    // query heads of a chunk
+constexpr int KG = 16;                   // keys of a group
+constexpr int NST = 4;                   // ring stages of a warp
 constexpr int MAX_SPLIT = ATTN_DECODE_MAX_SPLIT;
-constexpr int MIN_KEYS = 64;             // keys of a split
+constexpr int MIN_KEYS = NW * KG;        // keys of a split
 constexpr int SMS = 152;                 // of the one GPU this library is compiled for: scratch sizes follow from it
 
 __device__ __forceinline__ int split_chunk(int S, int n_split) {
@@ -32,13 +58,84 @@ __device__ __forceinline__ int split_chunk(int S, int n_split) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(THREADS) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
-    constexpr int REC = HD + 2, DPL = HD / 32;
-    __shared__ float qs[GC][HD];
-    __shared__ float wst[NW][GC][REC];
+struct Ring {
+    static constexpr int NB = HD / 32;               // blocks of a row
+    static constexpr int ROW = HD / 2;               // bytes of a row's codes
+    static constexpr int CODES = KG * ROW;           // ... of a group's
+    static constexpr int SCALES = HD == 32 ? 0 : KG * NB * 2;   // ... and of its scales (HD 32: read from global)
+    static constexpr int STAGE = 2 * CODES + 2 * SCALES;
+    static constexpr size_t BYTES = (size_t)NW * NST * STAGE;
+    static constexpr size_t MERGE = (size_t)NW * GC * (HD + 2) * sizeof(float);
+    static constexpr size_t SMEM = (BYTES > MERGE ? BYTES : MERGE) + (size_t)GC * MAX_SPLIT * sizeof(float);
+    // byte offset of word block `part` (4 NB bytes, lane t4 of a K row) of row r
+    __device__ static __forceinline__ int at(int r, int part) {
+        if (HD == 128) return r * ROW + ((part ^ ((r >> 1) & 3)) << 4);
+        if (HD == 64) return r * ROW + (((part >> 1) ^ ((r >> 2) & 1)) << 4) + (part & 1) * 8;
+        return r * ROW + part * 4;
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool pred) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" :: "r"(dst), "l"(src), "n"(N), "r"(pred ? N : 0));
+}
+
+__device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// v as the sum of two fp16 numbers, the larger in the low half: the low 13
+// mantissa bits are split off exactly, so the pair keeps 22 bits where the
+// first part is normal and 2^-25 absolute below.
+__device__ __forceinline__ uint32_t two_halves(float v) {
+    const float hi = __uint_as_float(__float_as_uint(v) & 0xFFFFE000u);
+    return pack_h2(hi, v - hi);
+}
+
+// NB words of a row part
+template <int NB>
+__device__ __forceinline__ void load_words(uint32_t (&w)[NB], const uint8_t *p) {
+    if constexpr (NB == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (NB == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// NB fp16 scales as float
+template <int NB>
+__device__ __forceinline__ void load_scales(float (&d)[NB], const void *p) {
+    if constexpr (NB == 1) {
+        d[0] = hf(*reinterpret_cast<const f16 *>(p));
+    } else {
+        uint32_t w[NB / 2];
+        load_words<NB / 2>(w, reinterpret_cast<const uint8_t *>(p));
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) { d[2 * i] = h2lo(w[i]); d[2 * i + 1] = h2hi(w[i]); }
+    }
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
+    using R = Ring<HD>;
+    constexpr int NB = R::NB, REC = HD + 2;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ int s_last;
     const int sp = blockIdx.x, j = blockIdx.y / chunks, ck = blockIdx.y - j * chunks, t = blockIdx.z;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int Hkv = a.kv.n_kv_head, G = a.H / Hkv, h0 = j * G + ck * GC, gn = min(GC, G - ck * GC);
     pdl_wait();
     pdl_trigger();
@@ -51,93 +148,240 @@ __global__ void __launch_bounds__(THREADS) attn_decode_q4_kernel(const AttnDecod
     const int n_eff = S > 0 ? (S + chunk - 1) / chunk : 1;
     if (sp >= n_eff) return;
     const int kb = lo + sp * chunk, ke = min(lo + S, kb + chunk);
-    const size_t base = ok ? (size_t)seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * HD : 0;
-    const float scale = 1.4426950408889634f / sqrtf((float)HD);
-    for (int i = tid; i < GC * HD; i += THREADS) {
-        const int g = i / HD, d = i - g * HD;
-        qs[g][d] = g < gn ? a.q[((size_t)t * a.H + h0 + g) * HD + d] * scale : 0.f;
-    }
-    __syncthreads();
+    const size_t row0 = ok ? ((size_t)seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * HD) / HD : 0;   // rows before the head's
 
-    float o[GC][DPL], m[GC], l[GC];
+    // ---- this warp's groups: keys kb + KG (warp + NW i)
+    uint8_t *ring = smem_raw + (size_t)warp * NST * R::STAGE;
+    const int n_grp = ke > kb + KG * warp ? (ke - kb - KG * warp + NW * KG - 1) / (NW * KG) : 0;
+    auto request = [&](int i) {
+        if (i < n_grp) {
+            const int k0 = kb + KG * (warp + NW * i);
+            const uint32_t st = smem_u32(ring + (size_t)(i % NST) * R::STAGE);
+            constexpr int CH = R::ROW / 16, PER = KG * CH;        // 16-byte chunks of a row, of a group
 #pragma unroll
-    for (int g = 0; g < GC; ++g) {
-        m[g] = -INFINITY; l[g] = 0.f;
+            for (int q = 0; q < (PER + 31) / 32; ++q) {
+                const int c = lane + 32 * q, r = c / CH, ch = c - r * CH;
+                if (PER % 32 == 0 || c < PER) {
+                    const bool in = k0 + r < ke;
+                    const size_t off = (row0 + (in ? k0 + r : k0)) * R::ROW + ch * 16;
+                    const uint32_t dst = st + R::at(r, HD == 128 ? ch : HD == 64 ? 2 * ch : 0);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(a.kv.k4 + off), "r"(in ? 16 : 0));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst + R::CODES), "l"(a.kv.v4 + off), "r"(in ? 16 : 0));
+                }
+            }
+            if constexpr (HD != 32) {
+                const int r = lane & 15;
+                const bool in = k0 + r < ke;
+                const f16 *src = (lane < 16 ? a.kv.kd : a.kv.vd) + (row0 + (in ? k0 + r : k0)) * NB;
+                cp_async_small<NB * 2>(st + 2 * R::CODES + (lane < 16 ? 0 : R::SCALES) + r * NB * 2, src, in);
+            }
+        }
+        cp_async_commit();
+    };
 #pragma unroll
-        for (int e = 0; e < DPL; ++e) o[g][e] = 0.f;
+    for (int i = 0; i < NST - 1; ++i) request(i);
+
+    // ---- q as the N side: column g of tile n is half g % 2 of head 4 n + g / 2
+    const float scale = 1.4426950408889634f / sqrtf((float)HD);
+    uint32_t qb[NT][NB][4];
+    float off[NT][NB][2], undo[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int hq = 4 * n + (g >> 1);
+        float v[NB][8], top = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+            if (hq < gn) {
+                const float4 *qp = reinterpret_cast<const float4 *>(a.q + ((size_t)t * a.H + h0 + hq) * HD + 32 * b + 8 * t4);
+                x0 = __ldcg(qp);                  // through L2: q is rewritten between uses
+                x1 = __ldcg(qp + 1);
+            }
+            v[b][0] = x0.x; v[b][1] = x0.y; v[b][2] = x0.z; v[b][3] = x0.w;
+            v[b][4] = x1.x; v[b][5] = x1.y; v[b][6] = x1.z; v[b][7] = x1.w;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) { v[b][e] *= scale; top = fmaxf(top, fabsf(v[b][e])); }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // a power of two brings the head's largest element to 2^8 .. 2^9, so
+        // that the halves of elements 2^-18 times as large are normal
+        int ex = 8 - ((int)(__float_as_uint(top) >> 23) - 127);
+        ex = top > 0.f ? max(-100, min(120, ex)) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+        // the inverse, times 2^24 of the codes, for the head of this lane's sums (column 2 t4)
+        undo[n] = __shfl_sync(0xffffffffu, 16777216.f / up, 8 * t4);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = v[b][e] * up * ((e & 2) ? 0.0625f : 1.f);      // elements 2, 3, 6, 7: nibbles four bits up
+                const uint32_t two = two_halves(x);
+                h[e] = g & 1 ? two >> 16 : two & 0xFFFFu;
+            }
+            qb[n][b][0] = h[0] | h[1] << 16;
+            qb[n][b][1] = h[4] | h[5] << 16;
+            qb[n][b][2] = h[2] | h[3] << 16;
+            qb[n][b][3] = h[6] | h[7] << 16;
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_acc(c, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, qb[n][b][0], qb[n][b][1]);
+            mma_acc(c, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, qb[n][b][2], qb[n][b][3]);
+            off[n][b][0] = c[0]; off[n][b][1] = c[1];
+        }
     }
-    for (int k0 = kb + warp * 32; k0 < ke; k0 += THREADS) {
-        const int key = k0 + lane;
-        float s[GC];
+
+    // sums of the lane's head(s) 4 n + t4: O^T tiles of 16 dimensions (two a block), weights, offsets
+    float o[NT][NB][2][4], m[NT], l[NT], sw[NT][NB];
 #pragma unroll
-        for (int g = 0; g < GC; ++g) s[g] = -INFINITY;
-        if (key < ke) {
-            const size_t row = base + (size_t)key * HD;
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(a.kv.k4 + row / 2);
-            const f16 *sc = a.kv.kd + row / 32;
+    for (int n = 0; n < NT; ++n) {
+        m[n] = -INFINITY; l[n] = 0.f;
 #pragma unroll
-            for (int g = 0; g < GC; ++g) s[g] = 0.f;
-            for (int i = 0; i < HD / 8; ++i) {
-                const uint32_t word = w[i];
-                const int b = i % (HD / 32), tt = i / (HD / 32);
-                const float d = hf(sc[b]);
+        for (int b = 0; b < NB; ++b) {
+            sw[n][b] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = (float)((int)((word >> q4::shift_of(e)) & 15u) - 8) * d;
+            for (int e = 0; e < 4; ++e) o[n][b][0][e] = o[n][b][1][e] = 0.f;
+        }
+    }
+    const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;       // V: lane g takes half g % 2 of words of part g / 2
+
+    for (int i = 0; i < n_grp; ++i) {
+        cp_async_wait<NST - 2>();
+        __syncwarp();
+        request(i + NST - 1);                             // into the stage read in step i - 1
+        const uint8_t *st = ring + (size_t)(i % NST) * R::STAGE;
+        const int k0 = kb + KG * (warp + NW * i);
+        const bool in0 = k0 + g < ke, in1 = k0 + g + 8 < ke;
+        uint32_t kw[2][NB];
+        load_words<NB>(kw[0], st + R::at(g, t4));
+        load_words<NB>(kw[1], st + R::at(g + 8, t4));
+        float dk[2][NB], dv[2][NB];
+        if constexpr (HD == 32) {
+            const size_t r = row0 + k0 + g;
+            dk[0][0] = in0 ? hf(a.kv.kd[r]) : 0.f; dk[1][0] = in1 ? hf(a.kv.kd[r + 8]) : 0.f;
+            dv[0][0] = in0 ? hf(a.kv.vd[r]) : 0.f; dv[1][0] = in1 ? hf(a.kv.vd[r + 8]) : 0.f;
+        } else {
+            const uint8_t *sc = st + 2 * R::CODES + g * NB * 2;
+            load_scales<NB>(dk[0], sc);
+            load_scales<NB>(dk[1], sc + 8 * NB * 2);
+            load_scales<NB>(dv[0], sc + R::SCALES);
+            load_scales<NB>(dv[1], sc + R::SCALES + 8 * NB * 2);
+        }
+        float s[NT][2];
 #pragma unroll
-                    for (int g = 0; g < GC; ++g) s[g] += qs[g][32 * b + 8 * tt + e] * v;
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t u = kw[0][b], v = kw[1][b], u8 = u >> 8, v8 = v >> 8;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float c[4] = {off[n][b][0], off[n][b][1], off[n][b][0], off[n][b][1]};
+                mma_acc(c, u & 0x000F000Fu, v & 0x000F000Fu, u8 & 0x000F000Fu, v8 & 0x000F000Fu, qb[n][b][0], qb[n][b][1]);
+                mma_acc(c, u & 0x00F000F0u, v & 0x00F000F0u, u8 & 0x00F000F0u, v8 & 0x00F000F0u, qb[n][b][2], qb[n][b][3]);
+                s[n][0] = fmaf(dk[0][b], c[0] + c[1], s[n][0]);
+                s[n][1] = fmaf(dk[1][b], c[2] + c[3], s[n][1]);
+            }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            s[n][0] = in0 ? s[n][0] * undo[n] : -INFINITY;
+            s[n][1] = in1 ? s[n][1] * undo[n] : -INFINITY;
+            raise |= fmaxf(s[n][0], s[n][1]) > m[n];
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float mx = fmaxf(s[n][0], s[n][1]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                mx = fmaxf(mx, m[n]);
+                const float f = mx == -INFINITY ? 1.f : exp2f(m[n] - mx);
+                m[n] = mx;
+                l[n] *= f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    sw[n][b] *= f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { o[n][b][0][e] *= f; o[n][b][1][e] *= f; }
                 }
             }
         }
+        // weights, 8 times as large: w <= 8 * 8188 (the largest scale) still is an fp16 number
+        float p[NT][2];
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
-            const float mn = fmaxf(m[g], warp_max(s[g]));
-            const float f = m[g] == -INFINITY ? 0.f : exp2f(m[g] - mn);
-            s[g] = exp2f(s[g] - mn);
-            l[g] = l[g] * f + warp_sum(s[g]);
-            m[g] = mn;
-#pragma unroll
-            for (int e = 0; e < DPL; ++e) o[g][e] *= f;
+        for (int n = 0; n < NT; ++n) {
+            const float base = m[n] == -INFINITY ? 0.f : 3.f - m[n];
+            p[n][0] = exp2f(s[n][0] + base);
+            p[n][1] = exp2f(s[n][1] + base);
+            l[n] += p[n][0] + p[n][1];
         }
-        for (int k = 0; k < 32 && k0 + k < ke; ++k) {
-            const size_t row = base + (size_t)(k0 + k) * HD;
-            float v[DPL];
+        uint32_t vw[4][NB];
 #pragma unroll
-            for (int e = 0; e < DPL; ++e) {
-                const int d = lane * DPL + e, b = d >> 5, r = d & 31;
-                const uint32_t word = reinterpret_cast<const uint32_t *>(a.kv.v4 + row / 2)[(r >> 3) * (HD / 32) + b];
-                v[e] = (float)((int)((word >> (4 * ((r & 7) >> 1) + 16 * (r & 1))) & 15u) - 8) * hf(a.kv.vd[row / 32 + b]);
-            }
+        for (int q = 0; q < 4; ++q) load_words<NB>(vw[q], st + R::CODES + R::at(2 * t4 + (q & 1) + 8 * (q >> 1), g >> 1));
 #pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                const float p = __shfl_sync(0xffffffffu, s[g], k);
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t u = __byte_perm(vw[0][b], vw[1][b], sel), v = __byte_perm(vw[2][b], vw[3][b], sel);
+            const uint32_t u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
-                for (int e = 0; e < DPL; ++e) o[g][e] += p * v[e];
+            for (int n = 0; n < NT; ++n) {
+                const float w0 = p[n][0] * dv[0][b], w1 = p[n][1] * dv[1][b];
+                sw[n][b] += w0 + w1;
+                const uint32_t b0 = transpose8x8(two_halves(w0)), b1 = transpose8x8(two_halves(w1));
+                mma_acc(o[n][b][0], u & 0x000F000Fu, u8 & 0x000F000Fu, v & 0x000F000Fu, v8 & 0x000F000Fu, b0, b1);
+                mma_acc(o[n][b][1], u & 0x00F000F0u, u8 & 0x00F000F0u, v & 0x00F000F0u, v8 & 0x00F000F0u, b0, b1);
             }
         }
     }
+    cp_async_wait<0>();
+    __syncthreads();                                      // the rings become the warps' results
+
+    float *wst = reinterpret_cast<float *>(smem_raw);     // [NW][GC][REC]: max, sum, numerators
+    float *wgt = reinterpret_cast<float *>(smem_raw + (R::BYTES > R::MERGE ? R::BYTES : R::MERGE));   // [GC][MAX_SPLIT]
 #pragma unroll
-    for (int g = 0; g < GC; ++g) {
-        if (lane == 0) { wst[warp][g][0] = m[g]; wst[warp][g][1] = l[g]; }
+    for (int n = 0; n < NT; ++n) {
+        float *ws = wst + ((size_t)warp * GC + 4 * n + t4) * REC;
 #pragma unroll
-        for (int e = 0; e < DPL; ++e) wst[warp][g][2 + lane * DPL + e] = o[g][e];
+        for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
+        if (g == 0) { ws[0] = m[n]; ws[1] = l[n]; }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) sw[n][b] += __shfl_xor_sync(0xffffffffu, sw[n][b], x);
+            float *d = ws + 2 + 32 * b + 8 * (g >> 1) + (g & 1);
+            const float o8 = 8.f * sw[n][b];
+            d[0] = fmaf(o[n][b][0][0] + o[n][b][0][1], 16777216.f, -o8);
+            d[4] = fmaf(o[n][b][0][2] + o[n][b][0][3], 16777216.f, -o8);
+            d[2] = fmaf(o[n][b][1][0] + o[n][b][1][1], 1048576.f, -o8);
+            d[6] = fmaf(o[n][b][1][2] + o[n][b][1][3], 1048576.f, -o8);
+        }
     }
     __syncthreads();
+    const bool one = n_eff == 1;
     float *part = a.part + ((size_t)(t * a.H + h0) * a.n_split + sp) * REC;
     for (int i = tid; i < gn * HD; i += THREADS) {
-        const int g = i / HD, d = i - g * HD;
+        const int h = i / HD, d = i - h * HD;
         float M = -INFINITY, num = 0.f, den = 0.f;
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, wst[w][g][0]);
-        if (M != -INFINITY)
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, wst[((size_t)w * GC + h) * REC]);
+        if (M != -INFINITY) {
+#pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float f = exp2f(wst[w][g][0] - M);
-                num += f * wst[w][g][2 + d];
-                den += f * wst[w][g][1];
+                const float *ws = wst + ((size_t)w * GC + h) * REC;
+                const float f = exp2f(ws[0] - M);
+                num += f * ws[2 + d];
+                den += f * ws[1];
             }
-        float *rp = part + (size_t)g * a.n_split * REC;
-        rp[2 + d] = num;
-        if (d == 0) { rp[0] = M; rp[1] = den; }
+        }
+        if (one) {
+            a.o[((size_t)t * a.H + h0 + h) * HD + d] = f2h(den > 0.f ? num / den : 0.f);
+        } else {
+            float *rp = part + (size_t)h * a.n_split * REC;
+            rp[2 + d] = num;
+            if (d == 0) { rp[0] = M; rp[1] = den; }
+        }
     }
+    if (one) return;
     __threadfence();
     __syncthreads();
     unsigned *cnt = a.counters + (size_t)t * gridDim.y + blockIdx.y;
@@ -145,19 +389,46 @@ __global__ void __launch_bounds__(THREADS) attn_decode_q4_kernel(const AttnDecod
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    for (int i = tid; i < gn * HD; i += THREADS) {
-        const int g = i / HD, d = i - g * HD;
-        const float *rp = a.part + ((size_t)(t * a.H + h0 + g) * a.n_split) * REC;
-        float M = -INFINITY, num = 0.f, den = 0.f;
-        for (int p = 0; p < n_eff; ++p) {
-            const float pm = __ldcg(rp + (size_t)p * REC);
-            if (pm == -INFINITY) continue;
-            const float mn = fmaxf(M, pm), fo = M == -INFINITY ? 0.f : exp2f(M - mn), fn = exp2f(pm - mn);
-            num = num * fo + __ldcg(rp + (size_t)p * REC + 2 + d) * fn;
-            den = den * fo + __ldcg(rp + (size_t)p * REC + 1) * fn;
-            M = mn;
+
+    // ---- last CTA of this (row, kv head, chunk): a warp finds its heads' split
+    // weights, then every thread sums its dimensions over the splits, in order
+    const float *all = a.part + (size_t)(t * a.H + h0) * a.n_split * REC;
+    for (int h = warp; h < gn; h += NW) {
+        const float *rp = all + (size_t)h * a.n_split * REC;
+        float mx = -INFINITY;
+        float2 ml[MAX_SPLIT / 32];
+#pragma unroll
+        for (int q = 0; q < MAX_SPLIT / 32; ++q) {
+            const int p = lane + 32 * q;
+            ml[q] = p < n_eff ? __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC)) : make_float2(-INFINITY, 0.f);
+            mx = fmaxf(mx, ml[q].x);
         }
-        a.o[((size_t)t * a.H + h0 + g) * HD + d] = f2h(den > 0.f ? num / den : 0.f);
+        mx = warp_max(mx);
+        float den = 0.f;
+#pragma unroll
+        for (int q = 0; q < MAX_SPLIT / 32; ++q) {
+            ml[q].x = mx == -INFINITY ? 0.f : exp2f(ml[q].x - mx);
+            den += ml[q].x * ml[q].y;
+        }
+        den = warp_sum(den);
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+        for (int q = 0; q < MAX_SPLIT / 32; ++q)
+            if (lane + 32 * q < n_eff) wgt[h * MAX_SPLIT + lane + 32 * q] = ml[q].x * inv;
+    }
+    __syncthreads();
+    for (int i = tid; i < gn * HD / 2; i += THREADS) {
+        const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
+        const float *rp = all + (size_t)h * a.n_split * REC + 2 + d;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 8
+        for (int p = 0; p < n_eff; ++p) {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC));
+            const float f = wgt[h * MAX_SPLIT + p];
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+        }
+        *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(acc.x, acc.y);
     }
     if (tid == 0) *cnt = 0u;
 }
@@ -234,10 +505,28 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeArgs &a, const Launch &l) {
     const int chunks = attn_q4_chunks(a.H, Hkv);
     if ((long long)Hkv * chunks > 65535) return cudaErrorInvalidValue;
     const dim3 grid(a.n_split, Hkv * chunks, a.T), block(THREADS);
-    if (a.kv.head_dim == 32) return launch_kernel(attn_decode_q4_kernel<32>, grid, block, 0, l, a, chunks);
-    if (a.kv.head_dim == 64) return launch_kernel(attn_decode_q4_kernel<64>, grid, block, 0, l, a, chunks);
-    if (a.kv.head_dim == 128) return launch_kernel(attn_decode_q4_kernel<128>, grid, block, 0, l, a, chunks);
+    // four heads fill the 8 columns of a tile; larger groups take two tiles
+#define Q4_DEC_CASE(HDV)                                                                                       \
+    if (a.kv.head_dim == HDV)                                                                                  \
+        return a.H / Hkv <= 4                                                                                  \
+                   ? launch_kernel(attn_decode_q4_kernel<HDV, 1>, grid, block, Ring<HDV>::SMEM, l, a, chunks)  \
+                   : launch_kernel(attn_decode_q4_kernel<HDV, 2>, grid, block, Ring<HDV>::SMEM, l, a, chunks);
+    Q4_DEC_CASE(32) Q4_DEC_CASE(64) Q4_DEC_CASE(128)
+#undef Q4_DEC_CASE
     return cudaErrorInvalidValue;
+}
+
+cudaError_t init_attn_q4_attributes() {
+    cudaError_t e = cudaSuccess;
+#define Q4_DEC_ATTR1(HDV, NT)                                                              \
+    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT>, Ring<HDV>::SMEM);               \
+    if (!e) e = cudaFuncSetAttribute(attn_decode_q4_kernel<HDV, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, \
+                                     cudaSharedmemCarveoutMaxShared);
+#define Q4_DEC_ATTR(HDV) Q4_DEC_ATTR1(HDV, 1) Q4_DEC_ATTR1(HDV, 2)
+    Q4_DEC_ATTR(32) Q4_DEC_ATTR(64) Q4_DEC_ATTR(128)
+#undef Q4_DEC_ATTR
+#undef Q4_DEC_ATTR1
+    return e;
 }
 
 cudaError_t launch_kv_widen_q4(const KvView &kv, const KvSpan *spans, int n_spans, int max_rows, f16 *k16, f16 *v16,

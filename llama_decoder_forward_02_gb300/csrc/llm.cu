@@ -31,6 +31,8 @@ cudaError_t init_attn_decode_attributes();
 cudaError_t init_attn_prefill_tc_attributes();
 cudaError_t init_sample_attributes();
 cudaError_t init_gemv_stream_attributes();
+cudaError_t init_gemv_q4_attributes();
+cudaError_t init_attn_q4_attributes();
 
 // Kernel attributes (dynamic shared-memory limits, carveouts) take effect on
 // the device that is current when they are set, so they are set once per
@@ -53,6 +55,8 @@ cudaError_t init_kernel_attributes() {
         if (!e) e = init_attn_prefill_tc_attributes();
         if (!e) e = init_sample_attributes();
         if (!e) e = init_gemv_stream_attributes();
+        if (!e) e = init_gemv_q4_attributes();
+        if (!e) e = init_attn_q4_attributes();
         status[dev] = e;
         done[dev] = true;
     }
