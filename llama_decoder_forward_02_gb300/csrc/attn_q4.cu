@@ -11,8 +11,8 @@
 // word leaves (q4.cuh):
 //   * S^T = K q^T with 16 keys as the M side.  A block of 32 dimensions is one
 //     fp32 sum of two mma (the second's q divided by 16 for the nibbles that
-//     stand four bits higher), scaled by the key's d in fp32.  The offset 8 is
-//     the sums' start value, -8 sum(q) of the block, made once.
+//     stand four bits higher), less 8 sum(q) of the block, made once, for the
+//     offset, and scaled by the key's d in fp32.
 //   * The N side has 8 columns and a kv head rarely 8 query heads, so each
 //     head takes two: q as the sum of two fp16 numbers (22 bits), and so its
 //     weights.  Four heads fill a column tile, larger groups take NT = 2.
@@ -43,7 +43,7 @@ namespace llm {
 
 namespace {
 
-constexpr int THREADS = 128, NW = THREADS / 32;
+constexpr int NW = 8, THREADS = NW * 32;
 constexpr int GC = 8;                    // query heads of a chunk
 constexpr int KG = 16;                   // keys of a group
 constexpr int NST = 4;                   // ring stages of a warp
@@ -66,7 +66,10 @@ struct Ring {
     static constexpr int STAGE = 2 * CODES + 2 * SCALES;
     static constexpr size_t BYTES = (size_t)NW * NST * STAGE;
     static constexpr size_t MERGE = (size_t)NW * GC * (HD + 2) * sizeof(float);
-    static constexpr size_t SMEM = (BYTES > MERGE ? BYTES : MERGE) + (size_t)GC * MAX_SPLIT * sizeof(float);
+    static constexpr size_t QFRAG = (size_t)2 * NB * (32 * 16 + 16);      // q's fragments, two tiles at most
+    static constexpr size_t WGT = BYTES > MERGE ? BYTES : MERGE;          // split weights, after the rings or the results
+    static constexpr size_t SMEM = BYTES + QFRAG > WGT + (size_t)GC * MAX_SPLIT * sizeof(float)
+                                       ? BYTES + QFRAG : WGT + (size_t)GC * MAX_SPLIT * sizeof(float);
     // byte offset of word block `part` (4 NB bytes, lane t4 of a K row) of row r
     __device__ static __forceinline__ int at(int r, int part) {
         if (HD == 128) return r * ROW + ((part ^ ((r >> 1) & 3)) << 4);
@@ -85,6 +88,13 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1,
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^x with a relative error of 2^-22, 0 below 2^-126
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -129,7 +139,7 @@ __device__ __forceinline__ void load_scales(float (&d)[NB], const void *p) {
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
     using R = Ring<HD>;
     constexpr int NB = R::NB, REC = HD + 2;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -153,83 +163,89 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
     // ---- this warp's groups: keys kb + KG (warp + NW i)
     uint8_t *ring = smem_raw + (size_t)warp * NST * R::STAGE;
     const int n_grp = ke > kb + KG * warp ? (ke - kb - KG * warp + NW * KG - 1) / (NW * KG) : 0;
-    auto request = [&](int i) {
-        if (i < n_grp) {
-            const int k0 = kb + KG * (warp + NW * i);
-            const uint32_t st = smem_u32(ring + (size_t)(i % NST) * R::STAGE);
-            constexpr int CH = R::ROW / 16, PER = KG * CH;        // 16-byte chunks of a row, of a group
+    // this lane's rows and chunks of a group; sources of the next group to request
+    constexpr int CH = R::ROW / 16, PER = KG * CH, NCP = (PER + 31) / 32;   // 16-byte chunks of a row, of a group
+    constexpr int RSTEP = 32 / CH;                                          // rows between a lane's chunks
+    const int cr = lane / CH, cc = lane - cr * CH, left0 = ke - kb - KG * warp;
+    const uint8_t *ksrc = a.kv.k4 + (row0 + kb + KG * warp + cr) * R::ROW + cc * 16;
+    const uint8_t *vsrc = a.kv.v4 + (row0 + kb + KG * warp + cr) * R::ROW + cc * 16;
+    const f16 *ssrc = (lane < 16 ? a.kv.kd : a.kv.vd) + (row0 + kb + KG * warp + (lane & 15)) * NB;
+    const uint32_t ring0 = smem_u32(ring);
+    int left = left0, want = 0;                       // keys from the next requested group on; its ring slot
+    auto request = [&]() {
+        if (left > 0) {
+            const uint32_t st = ring0 + (uint32_t)want * R::STAGE;
 #pragma unroll
-            for (int q = 0; q < (PER + 31) / 32; ++q) {
-                const int c = lane + 32 * q, r = c / CH, ch = c - r * CH;
-                if (PER % 32 == 0 || c < PER) {
-                    const bool in = k0 + r < ke;
-                    const size_t off = (row0 + (in ? k0 + r : k0)) * R::ROW + ch * 16;
-                    const uint32_t dst = st + R::at(r, HD == 128 ? ch : HD == 64 ? 2 * ch : 0);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(a.kv.k4 + off), "r"(in ? 16 : 0));
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst + R::CODES), "l"(a.kv.v4 + off), "r"(in ? 16 : 0));
+            for (int q = 0; q < NCP; ++q) {
+                const int r = cr + q * RSTEP;
+                if (PER % 32 == 0 || lane < PER) {
+                    const bool in = r < left;         // rows past the span are zeros, their address the span's first
+                    const uint32_t dst = st + R::at(r, HD == 128 ? cc : HD == 64 ? 2 * cc : 0);
+                    const int o = in ? q * RSTEP * R::ROW : -cr * R::ROW;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(ksrc + o), "r"(in ? 16 : 0));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst + R::CODES), "l"(vsrc + o), "r"(in ? 16 : 0));
                 }
             }
             if constexpr (HD != 32) {
                 const int r = lane & 15;
-                const bool in = k0 + r < ke;
-                const f16 *src = (lane < 16 ? a.kv.kd : a.kv.vd) + (row0 + (in ? k0 + r : k0)) * NB;
-                cp_async_small<NB * 2>(st + 2 * R::CODES + (lane < 16 ? 0 : R::SCALES) + r * NB * 2, src, in);
+                const bool in = r < left;
+                cp_async_small<NB * 2>(st + 2 * R::CODES + (lane < 16 ? 0 : R::SCALES) + r * NB * 2, in ? ssrc : ssrc - r * NB, in);
             }
+            left -= NW * KG;
+            ksrc += NW * KG * R::ROW;
+            vsrc += NW * KG * R::ROW;
+            ssrc += NW * KG * NB;
+            want = want + 1 == NST ? 0 : want + 1;
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < NST - 1; ++i) request(i);
+    for (int i = 0; i < NST - 1; ++i) request();
 
-    // ---- q as the N side: column g of tile n is half g % 2 of head 4 n + g / 2
-    const float scale = 1.4426950408889634f / sqrtf((float)HD);
-    uint32_t qb[NT][NB][4];
-    float off[NT][NB][2], undo[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int hq = 4 * n + (g >> 1);
-        float v[NB][8], top = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-            if (hq < gn) {
-                const float4 *qp = reinterpret_cast<const float4 *>(a.q + ((size_t)t * a.H + h0 + hq) * HD + 32 * b + 8 * t4);
-                x0 = __ldcg(qp);                  // through L2: q is rewritten between uses
-                x1 = __ldcg(qp + 1);
-            }
-            v[b][0] = x0.x; v[b][1] = x0.y; v[b][2] = x0.z; v[b][3] = x0.w;
-            v[b][4] = x1.x; v[b][5] = x1.y; v[b][6] = x1.z; v[b][7] = x1.w;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) { v[b][e] *= scale; top = fmaxf(top, fabsf(v[b][e])); }
+    // ---- q as the N side: column g of tile n is half g % 2 of head 4 n + g / 2.
+    // The fragments are the same for every warp: each makes some blocks' and
+    // leaves them in shared memory.  q * log2(e) / sqrt(hd), times 16 for the
+    // nibbles at bits 0 and 8 and as it is for those four bits higher; values
+    // beyond fp16's range count as its end.
+    uint4 *qf = reinterpret_cast<uint4 *>(smem_raw + R::BYTES);            // [NT * NB][32]
+    float *q8 = reinterpret_cast<float *>(qf + NT * NB * 32);              // [NT * NB][4]: 8 sum(q) * 2^-20 of the columns' head
+    const float scale = 16.f * 1.4426950408889634f / sqrtf((float)HD);
+    for (int u = warp; u < NT * NB; u += NW) {
+        const int n = u / NB, b = u - n * NB, hq = 4 * n + (g >> 1);
+        float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+        if (hq < gn) {
+            const float4 *qp = reinterpret_cast<const float4 *>(a.q + ((size_t)t * a.H + h0 + hq) * HD + 32 * b + 8 * t4);
+            x0 = __ldcg(qp);                          // through L2: q is rewritten between uses
+            x1 = __ldcg(qp + 1);
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // a power of two brings the head's largest element to 2^8 .. 2^9, so
-        // that the halves of elements 2^-18 times as large are normal
-        int ex = 8 - ((int)(__float_as_uint(top) >> 23) - 127);
-        ex = top > 0.f ? max(-100, min(120, ex)) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
-        // the inverse, times 2^24 of the codes, for the head of this lane's sums (column 2 t4)
-        undo[n] = __shfl_sync(0xffffffffu, 16777216.f / up, 8 * t4);
+        const float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        uint32_t h[8];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = v[b][e] * up * ((e & 2) ? 0.0625f : 1.f);      // elements 2, 3, 6, 7: nibbles four bits up
-                const uint32_t two = two_halves(x);
-                h[e] = g & 1 ? two >> 16 : two & 0xFFFFu;
-            }
-            qb[n][b][0] = h[0] | h[1] << 16;
-            qb[n][b][1] = h[4] | h[5] << 16;
-            qb[n][b][2] = h[2] | h[3] << 16;
-            qb[n][b][3] = h[6] | h[7] << 16;
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_acc(c, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, qb[n][b][0], qb[n][b][1]);
-            mma_acc(c, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, qb[n][b][2], qb[n][b][3]);
-            off[n][b][0] = c[0]; off[n][b][1] = c[1];
+        for (int e = 0; e < 8; ++e) {
+            float x = v[e] * scale;
+            x = x > 65504.f ? 65504.f : x < -65504.f ? -65504.f : x;          // a NaN stays one
+            const uint32_t two = two_halves((e & 2) ? x * 0.0625f : x);   // elements 2, 3, 6, 7: nibbles four bits up
+            h[e] = g & 1 ? two >> 16 : two & 0xFFFFu;
         }
+        const uint4 f = make_uint4(h[0] | h[1] << 16, h[4] | h[5] << 16, h[2] | h[3] << 16, h[6] | h[7] << 16);
+        qf[u * 32 + lane] = f;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_acc(c, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, f.x, f.y);
+        mma_acc(c, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, f.z, f.w);
+        if (g == 0) q8[u * 4 + t4] = c[0] + c[1];
     }
+    __syncthreads();
+    uint32_t qb[NT][NB][4];
+    float off[NT][NB];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint4 f = qf[(n * NB + b) * 32 + lane];
+            qb[n][b][0] = f.x; qb[n][b][1] = f.y; qb[n][b][2] = f.z; qb[n][b][3] = f.w;
+            off[n][b] = q8[(n * NB + b) * 4 + t4];
+        }
+    constexpr float UNDO = 1048576.f;                 // 2^24 of the codes over the 16 of q
 
     // sums of the lane's head(s) 4 n + t4: O^T tiles of 16 dimensions (two a block), weights, offsets
     float o[NT][NB][2][4], m[NT], l[NT], sw[NT][NB];
@@ -245,19 +261,19 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
     }
     const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;       // V: lane g takes half g % 2 of words of part g / 2
 
+    int slot = 0, valid = left0;                      // keys from this group on
     for (int i = 0; i < n_grp; ++i) {
         cp_async_wait<NST - 2>();
         __syncwarp();
-        request(i + NST - 1);                             // into the stage read in step i - 1
-        const uint8_t *st = ring + (size_t)(i % NST) * R::STAGE;
-        const int k0 = kb + KG * (warp + NW * i);
-        const bool in0 = k0 + g < ke, in1 = k0 + g + 8 < ke;
+        request();                                        // into the slot read in step i - 1
+        const uint8_t *st = ring + (size_t)slot * R::STAGE;
+        const bool in0 = g < valid, in1 = g + 8 < valid;
         uint32_t kw[2][NB];
         load_words<NB>(kw[0], st + R::at(g, t4));
         load_words<NB>(kw[1], st + R::at(g + 8, t4));
         float dk[2][NB], dv[2][NB];
         if constexpr (HD == 32) {
-            const size_t r = row0 + k0 + g;
+            const size_t r = row0 + kb + KG * (warp + NW * i) + g;
             dk[0][0] = in0 ? hf(a.kv.kd[r]) : 0.f; dk[1][0] = in1 ? hf(a.kv.kd[r + 8]) : 0.f;
             dv[0][0] = in0 ? hf(a.kv.vd[r]) : 0.f; dv[1][0] = in1 ? hf(a.kv.vd[r + 8]) : 0.f;
         } else {
@@ -275,18 +291,19 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
             const uint32_t u = kw[0][b], v = kw[1][b], u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float c[4] = {off[n][b][0], off[n][b][1], off[n][b][0], off[n][b][1]};
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
                 mma_acc(c, u & 0x000F000Fu, v & 0x000F000Fu, u8 & 0x000F000Fu, v8 & 0x000F000Fu, qb[n][b][0], qb[n][b][1]);
                 mma_acc(c, u & 0x00F000F0u, v & 0x00F000F0u, u8 & 0x00F000F0u, v8 & 0x00F000F0u, qb[n][b][2], qb[n][b][3]);
-                s[n][0] = fmaf(dk[0][b], c[0] + c[1], s[n][0]);
-                s[n][1] = fmaf(dk[1][b], c[2] + c[3], s[n][1]);
+                s[n][0] = fmaf(dk[0][b], (c[0] + c[1]) + off[n][b], s[n][0]);
+                s[n][1] = fmaf(dk[1][b], (c[2] + c[3]) + off[n][b], s[n][1]);
             }
         }
+        // m and s in units of 2^-20 (the codes' 2^-24 and the 16 of q)
         bool raise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            s[n][0] = in0 ? s[n][0] * undo[n] : -INFINITY;
-            s[n][1] = in1 ? s[n][1] * undo[n] : -INFINITY;
+            s[n][0] = in0 ? s[n][0] : -INFINITY;
+            s[n][1] = in1 ? s[n][1] : -INFINITY;
             raise |= fmaxf(s[n][0], s[n][1]) > m[n];
         }
         if (__any_sync(0xffffffffu, raise)) {
@@ -296,7 +313,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
                 mx = fmaxf(mx, m[n]);
-                const float f = mx == -INFINITY ? 1.f : exp2f(m[n] - mx);
+                const float f = mx == -INFINITY ? 1.f : exp2f((m[n] - mx) * UNDO);
                 m[n] = mx;
                 l[n] *= f;
 #pragma unroll
@@ -311,9 +328,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
         float p[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float base = m[n] == -INFINITY ? 0.f : 3.f - m[n];
-            p[n][0] = exp2f(s[n][0] + base);
-            p[n][1] = exp2f(s[n][1] + base);
+            const float base = m[n] == -INFINITY ? 0.f : fmaf(m[n], -UNDO, 3.f);
+            p[n][0] = exp2_fast(fmaf(s[n][0], UNDO, base));
+            p[n][1] = exp2_fast(fmaf(s[n][1], UNDO, base));
             l[n] += p[n][0] + p[n][1];
         }
         uint32_t vw[4][NB];
@@ -332,18 +349,20 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
                 mma_acc(o[n][b][1], u & 0x00F000F0u, u8 & 0x00F000F0u, v & 0x00F000F0u, v8 & 0x00F000F0u, b0, b1);
             }
         }
+        valid -= NW * KG;
+        slot = slot + 1 == NST ? 0 : slot + 1;
     }
     cp_async_wait<0>();
     __syncthreads();                                      // the rings become the warps' results
 
     float *wst = reinterpret_cast<float *>(smem_raw);     // [NW][GC][REC]: max, sum, numerators
-    float *wgt = reinterpret_cast<float *>(smem_raw + (R::BYTES > R::MERGE ? R::BYTES : R::MERGE));   // [GC][MAX_SPLIT]
+    float *wgt = reinterpret_cast<float *>(smem_raw + R::WGT);   // [GC][MAX_SPLIT]
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float *ws = wst + ((size_t)warp * GC + 4 * n + t4) * REC;
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
-        if (g == 0) { ws[0] = m[n]; ws[1] = l[n]; }
+        if (g == 0) { ws[0] = m[n] * UNDO; ws[1] = l[n]; }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -421,7 +440,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 4 : 2) attn_decode_q4_kerne
         const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
         const float *rp = all + (size_t)h * a.n_split * REC + 2 + d;
         float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
         for (int p = 0; p < n_eff; ++p) {
             const float2 v = __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC));
             const float f = wgt[h * MAX_SPLIT + p];
@@ -490,7 +509,7 @@ int attn_q4_chunks(int H, int Hkv) { return (H / Hkv + GC - 1) / GC; }
 
 int attn_q4_pick_split(int T, int H, int Hkv, int n_ctx) {
     const int mx = (n_ctx + MIN_KEYS - 1) / MIN_KEYS;
-    long long s = 4LL * SMS / ((long long)T * Hkv * attn_q4_chunks(H, Hkv));
+    long long s = 2LL * SMS / ((long long)T * Hkv * attn_q4_chunks(H, Hkv));
     if (s > MAX_SPLIT) s = MAX_SPLIT;
     if (s > mx) s = mx;
     return s < 1 ? 1 : (int)s;
