@@ -309,7 +309,8 @@ struct GemvQ4Args {
     float *out; int ldo;
     uint32_t *err;
 };
-cudaError_t launch_gemv_q4(const GemvQ4Args &a, int num_sms, const Launch &l);
+// early: weights may be read before the kernel that precedes the launch is done
+cudaError_t launch_gemv_q4(const GemvQ4Args &a, int num_sms, const Launch &l, bool early);
 
 // Per-head RMSNorm (gains may be null: no norm) and rotation of the query and
 // key heads of qkv rows [T][ld] (H query, Hkv key, Hkv value heads), q to q32

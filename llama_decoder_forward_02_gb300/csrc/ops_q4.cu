@@ -32,6 +32,12 @@ int32_t launched(const char *who, cudaError_t e) {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// The kernels of these calls wait for the previous one before they touch
+// memory, so their launches may overlap its end (programmatic dependent
+// launch): calls in a row then follow each other without the gap of a launch,
+// 2 to 4 us.
+Launch overlapped(void *stream) { return Launch{(cudaStream_t)stream, true, nullptr}; }
+
 int current_sms() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -97,7 +103,7 @@ extern "C" int32_t llm_op_gemv_q4_0(const void *Wq, const void *x, float *y, int
     GemvQ4Args a;
     a.W = (const uint8_t *)Wq; a.N = N; a.K = K; a.T = T;
     a.x = (const f16 *)x; a.ldx = ldx; a.out = y; a.ldo = ldy; a.err = nullptr;
-    return launched(who, launch_gemv_q4(a, current_sms(), Launch{(cudaStream_t)stream, false, nullptr}));
+    return launched(who, launch_gemv_q4(a, current_sms(), overlapped(stream), false));
 }
 
 extern "C" int64_t llm_op_kv_q4_0_bytes(int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq) {
@@ -130,7 +136,7 @@ extern "C" int32_t llm_op_qk_norm_rope(const float *qkv, int32_t ld, const float
     if (kv_type == LLM_KV_F16) { a.kv.k = (f16 *)k_cache; a.kv.v = (f16 *)v_cache; }
     if (kv_type == LLM_KV_E4M3) { a.kv.k8 = (uint8_t *)k_cache; a.kv.v8 = (uint8_t *)v_cache; }
     a.T = T; a.H = H; a.err = err;
-    return launched(who, launch_qk_norm_rope(a, Launch{(cudaStream_t)stream, false, nullptr}));
+    return launched(who, launch_qk_norm_rope(a, overlapped(stream)));
 }
 
 extern "C" int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, const int32_t *seq, void *out, int32_t T,
@@ -175,7 +181,7 @@ extern "C" int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, 
     at.part = (float *)scratch;
     at.counters = (unsigned *)(at.part + attn_q4_part_floats(T, H, hd, at.n_split));
     at.err = err; at.window = window;
-    return launched(who, launch_attn_decode_q4(at, Launch{(cudaStream_t)stream, false, nullptr}));
+    return launched(who, launch_attn_decode_q4(at, overlapped(stream)));
 }
 
 // scratch: K, then V widened [n_seq][Hkv][padded n_ctx][hd], tiles, spans
