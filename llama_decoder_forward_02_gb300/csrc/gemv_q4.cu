@@ -3,20 +3,21 @@
 // layers of a decode step whose weights are held in four bits.
 //
 // Bound by HBM: 9/16 byte a weight, each read once, leaves 10 weights a clock
-// to an SM sub-partition at the copy bandwidth.  Widening codes on the CUDA
-// cores costs more than two instructions a weight, over that; so the codes go
-// to the tensor cores as they are.  On this GPU mma.sync m16n8k16 (f16, f32
-// sums) takes 8 clocks of a sub-partition, logic and shift instructions 2,
-// FFMA 1.  The M side is 16 weight rows, the N side the rows of x (the other
-// columns are zero).  A word of eight codes becomes four fragment registers by
-// four ANDs and one shift: the masked halves are fp16 subnormals, c * 2^-24
-// (bits 0, 16) and 16 c * 2^-24 (bits 4, 20), which the tensor cores multiply
-// exactly; x is divided by 16 for the latter (where x is not in shared memory
-// their sums are kept apart and divided instead).  The offset 8 is taken off by starting a sum at -8 sum(x) of its block: from a
-// table in shared memory where x is there too, else from the product of x with
-// a constant fragment, shared by every row of a warp's tile.  Each block of
-// 32 k is one sum of at most 32 exact products in fp32, scaled by d in fp32
-// and added in fp32: x and the codes are never rounded.
+// to an SM sub-partition at the copy bandwidth, for which scalar products on
+// the CUDA cores are too many instructions.  So they run on mma.sync m16n8k16
+// (f16, f32 sums; 8 clocks of a sub-partition on this GPU, where logic, shift
+// and fp16-pair instructions take 2 and FFMA 1): 16 weight rows are the M side,
+// the rows of x the N side (its other columns are not used).  A word of eight
+// codes becomes four fragment registers by one shift and, for each, one logic
+// instruction and one exact fp16 subtraction: (w & 0x000F000F) | 0x64006400
+// reads 1024 + c in both halves, (w & 0x00F000F0) | 0x54005400 reads 64 + c,
+// and less 1032 and 72 that is c - 8.  Each block of 32 k is one sum of 32
+// exact products in fp32, scaled by d in fp32 and added in fp32: x and the
+// codes are never rounded.  (Codes as fp16 subnormals c * 2^-24, with
+// 8 sum(x) taken off a block's sum, save the subtractions, but the tensor
+// cores truncate their addends to the largest one's exponent: y was 9e-7 off
+// instead of 4e-7, and x needed scaling and a table of sums before the first
+// product.)
 //
 // One CTA an SM owns a contiguous run of rows.  Its 16 warps are 16 / units
 // row groups of `units` warps: a group takes every (16 / units)-th tile of 32
@@ -65,13 +66,11 @@ bool make_plan(int N, int K, int T, int ctas, Plan *p) {
         const long long mine = (tiles + CW / u - 1) / (CW / u), cost = mine * (2LL * ((groups + u - 1) / u) + 1);
         if (u == CW || cost < best) { best = cost; p->units = u; }
     }
-    // x and the table of its block sums (16 bytes a block and column pair)
     p->red_warp = (T + 1) / 2 * 2 * RED_COL;
     const size_t red = (size_t)2 * CW * p->red_warp * sizeof(float);
-    const size_t x = (size_t)T * (K + X_PAD) * sizeof(f16) + (size_t)K * 2;
-    // beside four ring stages, or three (74 KB in flight on an SM, still above
-    // what the copy bandwidth needs at 1 us), where it fits, and a row tile
-    // reads x from shared memory; else each warp reads its fragments from L2 a
+    const size_t x = (size_t)T * (K + X_PAD) * sizeof(f16);
+    // x beside four ring stages, or three (74 KB in flight on an SM, still above
+    // what the copy bandwidth needs at 1 us), where it fits; else each warp reads its fragments from L2 a
     // step ahead: with so long a K a CTA has few row tiles to read x again for
     const size_t ring = (size_t)CW * STAGE;
     p->x_smem = x + red + 3 * ring <= SMEM_CAP;
@@ -81,25 +80,36 @@ bool make_plan(int N, int K, int T, int ctas, Plan *p) {
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1, const float (&c)[4]) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The power of two that brings an fp16 number of these bits (no sign) to
-// 2^14 .. 2^15, 0 for zero; subnormals count by their leading bit.
-__device__ __forceinline__ int row_shift(uint32_t bits) {
-    return bits == 0u ? 0 : bits < 0x400u ? 14 + 24 - (31 - __clz(bits)) : bits >= 0x7C00u ? 0 : 14 - ((int)(bits >> 10) - 15);
-}
+// c - 8 of the codes at bits 0 and 16 / at bits 4 and 20, as an fp16 pair.  One
+// LOP3 takes at most one constant as an immediate, so the masks and biases are
+// kept in registers the compiler cannot see through (with immediates it emits
+// two: 63 us instead of MEASURE for 128256 x 4096).
+struct Widen {
+    uint32_t m0, e0, m1, e1;
+    __device__ __forceinline__ Widen() {
+        asm volatile("mov.b32 %0, 0x000F000F;\n\tmov.b32 %1, 0x64006400;\n\tmov.b32 %2, 0x00F000F0;\n\tmov.b32 %3, 0x54005400;"
+                     : "=r"(m0), "=r"(e0), "=r"(m1), "=r"(e1));
+    }
+    __device__ __forceinline__ static uint32_t pick(uint32_t w, uint32_t m, uint32_t e, uint32_t bias) {
+        uint32_t v;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(m), "r"(e));       // (w & m) | e
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&bias));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    __device__ __forceinline__ uint32_t low(uint32_t w) const { return pick(w, m0, e0, 0x64086408u); }
+    __device__ __forceinline__ uint32_t high(uint32_t w) const { return pick(w, m1, e1, 0x54805480u); }
+};
 
 // XS: x in shared memory; NST: ring stages of a warp
 template <bool XS, int NST>
 __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a, const Plan p, const int early) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ uint32_t s_top[8];                    // the rows' largest |x|, as fp16 bits
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int r0 = (int)((long long)blockIdx.x * a.N / gridDim.x);
     const int nrows = (int)((long long)(blockIdx.x + 1) * a.N / gridDim.x) - r0;
@@ -165,62 +175,33 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     pdl_trigger();
 
     // ---- x: column g of the N side is row g of x (columns from T on repeat row 0, their sums are not stored)
-    float4 *tab = reinterpret_cast<float4 *>(xs + (size_t)a.T * (a.K + X_PAD));     // [K / 32][4]: {u, v, u, v}
     const f16 *xp = a.x;
     int ldx = a.ldx;
     if (XS) {
-        // Into shared memory, as the fragments want it: pieces of 8 elements,
-        // (0,1) (4,5) | (2,3) (6,7), the second half divided by 16 for the
-        // nibbles that stand four bits higher.  So that the division rounds
-        // nothing that counts, a row is first multiplied by the power of two
-        // that brings its largest element to 2^14 .. 2^15, which is exact;
-        // what is then rounded off is 2^-35 of that element at most.
-        ldx = a.K + X_PAD;
-        xp = xs;
-        const int per = a.K / 8, n = a.T * per;      // pieces, a multiple of 32 a row
-        if (tid < 8) s_top[tid] = 0u;
-        __syncthreads();
-        constexpr int HOLD = 4;                      // pieces a thread keeps between the two passes
+        const int per = a.K / 8, n = a.T * per;      // 16-byte pieces of x
+        constexpr int HOLD = 4;                      // pieces a thread asks for before the ring's first steps
         uint4 held[HOLD];
         auto piece = [&](int i) { return *reinterpret_cast<const uint4 *>(a.x + (size_t)(i / per) * a.ldx + (i % per) * 8); };
+        auto put = [&](int i, const uint4 &u) {
+            *reinterpret_cast<uint4 *>(xs + (size_t)(i / per) * (a.K + X_PAD) + (i % per) * 8) = u;
+        };
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (tid + j * THREADS < n) held[j] = piece(tid + j * THREADS);
-        auto top = [&](int i, const uint4 &u) {      // of a warp's pieces, all of one row
-            const uint32_t m = 0x7FFF7FFFu;
-            const uint32_t v = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
-            const uint32_t w = __reduce_max_sync(0xffffffffu, max(v & 0xFFFFu, v >> 16));
-            if (lane == 0) atomicMax(&s_top[i / per], w);
-        };
-#pragma unroll
-        for (int j = 0; j < HOLD; ++j)
-            if (tid + j * THREADS < n) top(tid + j * THREADS, held[j]);      // whole warps: n % 32 == 0
-        for (int i = tid + HOLD * THREADS; i < n; i += THREADS) top(i, piece(i));
-        __syncthreads();
-        auto put = [&](int i, const uint4 &u) {
-            const int t = i / per, c = i - t * per;
-            const float up = __uint_as_float((uint32_t)(127 + row_shift(s_top[t])) << 23);
-            const float e[8] = {h2lo(u.x) * up, h2hi(u.x) * up, h2lo(u.y) * up, h2hi(u.y) * up,
-                                h2lo(u.z) * up, h2hi(u.z) * up, h2lo(u.w) * up, h2hi(u.w) * up};
-            *reinterpret_cast<uint4 *>(xs + (size_t)t * ldx + c * 8) =
-                make_uint4(pack_h2(e[0], e[1]), pack_h2(e[4], e[5]), pack_h2(e[2] * 0.0625f, e[3] * 0.0625f),
-                           pack_h2(e[6] * 0.0625f, e[7] * 0.0625f));
-            // -8 * 2^-24 * sum(x) of the block, where the lanes that sum x's column pair t / 2 look for it
-            float v = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            if ((lane & 3) < 2) reinterpret_cast<float *>(tab + 4 * (c >> 2) + (t >> 1))[(t & 1) + 2 * (lane & 3)] = v * (-8.f / 16777216.f);
-        };
+        if (!early)                                  // behind x in the queue, before x is waited for
+            for (int j = 0; j < NST - 1; ++j) request();
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (tid + j * THREADS < n) put(tid + j * THREADS, held[j]);
+#pragma unroll 4
         for (int i = tid + HOLD * THREADS; i < n; i += THREADS) put(i, piece(i));
-    }
-    if (!early)                                      // x was asked for first: it is not behind the weights' burst
+        ldx = a.K + X_PAD;
+        xp = xs;
+        __syncthreads();
+    } else if (!early) {
         for (int j = 0; j < NST - 1; ++j) request();
-    if (XS) __syncthreads();
+    }
     xp += (size_t)(g < a.T ? g : 0) * ldx + cu * 128 + 8 * t4;
-    const float4 *tp = tab + (size_t)cu * 16 + t4;
     uint4 bx[4];                                     // !XS: the next step's x
     auto load_x = [&](int kc) {
 #pragma unroll
@@ -228,6 +209,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     };
     if (!XS && nsteps > 0) load_x(0);
 
+    const Widen q;
     uint32_t slot = 0;
     const uint8_t *wr = ring + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4), *dr = ring + CODES + g * 8;
     for (int tile = 0; tile < ntiles; ++tile) {
@@ -256,14 +238,6 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const uint4 x = xv[b];
-                float off1[4], off16[4] = {0.f, 0.f, 0.f, 0.f};
-                if (XS) {
-                    const float4 f = tp[kc * units * 16 + 4 * b];
-                    off1[0] = f.x; off1[1] = f.y; off1[2] = f.z; off1[3] = f.w;
-                } else {
-                    mma(off1, 0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u, x.x, x.z, off16);
-                    mma(off16, 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, x.y, x.w, off16);
-                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t wg = b == 0 ? w[i][0].x : b == 1 ? w[i][0].y : b == 2 ? w[i][0].z : w[i][0].w;
@@ -271,19 +245,13 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
                     const uint32_t sg = wg >> 8, sh = wh >> 8;
                     const uint32_t pg = b < 2 ? dd[i][0].x : dd[i][0].y, ph = b < 2 ? dd[i][1].x : dd[i][1].y;
                     const float dg = b & 1 ? h2hi(pg) : h2lo(pg), dh = b & 1 ? h2hi(ph) : h2lo(ph);
-                    float s1[4], s16[4];
-                    mma(s1, wg & 0x000F000Fu, wh & 0x000F000Fu, sg & 0x000F000Fu, sh & 0x000F000Fu, x.x, XS ? x.y : x.z, off1);
-                    if (XS) {
-                        mma(s16, wg & 0x00F000F0u, wh & 0x00F000F0u, sg & 0x00F000F0u, sh & 0x00F000F0u, x.z, x.w, s1);
-                    } else {
-                        mma(s16, wg & 0x00F000F0u, wh & 0x00F000F0u, sg & 0x00F000F0u, sh & 0x00F000F0u, x.y, x.w, off16);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s16[e] = fmaf(s16[e], 0.0625f, s1[e]);
-                    }
-                    y[i][0] = fmaf(dg, s16[0], y[i][0]);
-                    y[i][1] = fmaf(dg, s16[1], y[i][1]);
-                    y[i][2] = fmaf(dh, s16[2], y[i][2]);
-                    y[i][3] = fmaf(dh, s16[3], y[i][3]);
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma(s, q.low(wg), q.low(wh), q.low(sg), q.low(sh), x.x, x.z);
+                    mma(s, q.high(wg), q.high(wh), q.high(sg), q.high(sh), x.y, x.w);
+                    y[i][0] = fmaf(dg, s[0], y[i][0]);
+                    y[i][1] = fmaf(dg, s[1], y[i][1]);
+                    y[i][2] = fmaf(dh, s[2], y[i][2]);
+                    y[i][3] = fmaf(dh, s[3], y[i][3]);
                 }
             }
         }
@@ -303,8 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         for (int t = cu; t < a.T; t += units) {
             float v = 0.f;
             for (int c = 0; c < units; ++c) v += sums[c * p.red_warp + t * RED_COL + lane];
-            const int sh = XS ? row_shift(s_top[t]) : 0;
-            if (row < nrows) a.out[(size_t)t * a.ldo + r0 + row] = v * __uint_as_float((uint32_t)(127 + 24 - sh) << 23);
+            if (row < nrows) a.out[(size_t)t * a.ldo + r0 + row] = v;
         }
     }
     cp_async_wait<0>();
