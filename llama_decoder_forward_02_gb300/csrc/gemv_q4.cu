@@ -21,14 +21,15 @@
 //
 // One CTA an SM owns a contiguous run of rows.  Its 16 warps are 16 / units
 // row groups of `units` warps: a group takes every (16 / units)-th tile of 32
-// rows (two m16 tiles), warp cu of it the 128-element groups cu, cu + units, ..
-// of K.  A warp brings its codes and scales itself, with cp.async, through a
-// ring of its own (2304 bytes a step; the first steps before the dependency
-// wait where the launch overlaps the previous kernel: weights never depend on
-// it).  The warps of a row group join their sums in shared memory, in a fixed
-// order, so results do not depend on timing.  More units spread few rows over all
-// warps, fewer meet less often: the launcher takes the split with the fewest
-// steps a warp, counting a meeting as half a step (with 16 units throughout,
+// rows (two m16 tiles), warp cu of it the 256-element chunks cu, cu + units, ..
+// of K, each in two steps of 128.  A warp brings its codes and scales itself,
+// with cp.async, through a ring of its own (2 KB of codes a step, the scales of
+// a chunk with its first; the first steps before the dependency wait where the
+// launch overlaps the previous kernel: weights never depend on it).  The warps
+// of a row group join their sums in shared memory, in a fixed order, so results
+// do not depend on timing.  More units spread few rows over all warps, fewer
+// meet less often: the launcher takes the split with the fewest chunks a warp,
+// counting a meeting as a quarter of one (with 16 units throughout,
 // 128256 x 4096 took 83 us, a quarter of it in meetings).
 // (Bulk copies by a producer warp, one a row and step, took 26.7 us for
 // 28672 x 4096: about 130 clocks a copy of 1152 bytes.)
@@ -44,7 +45,9 @@ constexpr int CW = 16;                       // warps
 constexpr int THREADS = CW * 32;
 constexpr int RG = 32;                       // rows of a warp's tile (two m16 tiles)
 constexpr int CODES = RG * 64;               // bytes of a step's codes in a warp's ring
-constexpr int STAGE = CODES + RG * 8;        // ... and its scales
+constexpr int SCALES = RG * 16;              // bytes of a chunk's scales
+constexpr int SC_SLOTS = 3;                  // chunks whose scales are held: NST - 1 <= 4 steps ahead touch three
+constexpr size_t ring_bytes(int nst) { return (size_t)CW * (nst * CODES + SC_SLOTS * SCALES); }
 constexpr int RED_COL = 36;                  // floats between columns of a warp's sums (bank-conflict free)
 constexpr size_t SMEM_CAP = 224 * 1024;
 constexpr int X_PAD = 32;                    // elements between rows of x in shared memory beyond K
@@ -60,10 +63,10 @@ struct Plan {
 // false: K is not a positive multiple of 256
 bool make_plan(int N, int K, int T, int ctas, Plan *p) {
     if (K < q4::CHUNK || K % q4::CHUNK) return false;
-    const int groups = K / 128, rows = (N + ctas - 1) / ctas, tiles = (rows + RG - 1) / RG;
+    const int chunks = K / q4::CHUNK, rows = (N + ctas - 1) / ctas, tiles = (rows + RG - 1) / RG;
     long long best = 0;
-    for (int u = CW; u >= 2; u /= 2) {
-        const long long mine = (tiles + CW / u - 1) / (CW / u), cost = mine * (2LL * ((groups + u - 1) / u) + 1);
+    for (int u = CW; u >= 1; u /= 2) {
+        const long long mine = (tiles + CW / u - 1) / (CW / u), cost = mine * (4LL * ((chunks + u - 1) / u) + 1);
         if (u == CW || cost < best) { best = cost; p->units = u; }
     }
     p->red_warp = (T + 1) / 2 * 2 * RED_COL;
@@ -72,10 +75,9 @@ bool make_plan(int N, int K, int T, int ctas, Plan *p) {
     // x beside four ring stages, or three (74 KB in flight on an SM, still above
     // what the copy bandwidth needs at 1 us), where it fits; else each warp reads its fragments from L2 a
     // step ahead: with so long a K a CTA has few row tiles to read x again for
-    const size_t ring = (size_t)CW * STAGE;
-    p->x_smem = x + red + 3 * ring <= SMEM_CAP;
-    p->nst = !p->x_smem || x + red + 4 * ring <= SMEM_CAP ? 4 : 3;
-    p->smem = p->nst * ring + red + (p->x_smem ? x : 0);
+    p->x_smem = x + red + ring_bytes(3) <= SMEM_CAP;
+    p->nst = !p->x_smem || x + red + ring_bytes(4) <= SMEM_CAP ? 4 : 3;
+    p->smem = ring_bytes(p->nst) + red + (p->x_smem ? x : 0);
     return true;
 }
 
@@ -86,10 +88,17 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // c - 8 of the codes at bits 0 and 16 / at bits 4 and 20, as an fp16 pair.  One
 // LOP3 takes at most one constant as an immediate, so the masks and biases are
 // kept in registers the compiler cannot see through (with immediates it emits
-// two: 63 us instead of MEASURE for 128256 x 4096).
+// two: 20% more instructions in all).
 struct Widen {
     uint32_t m0, e0, m1, e1;
     __device__ __forceinline__ Widen() {
@@ -113,59 +122,64 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int r0 = (int)((long long)blockIdx.x * a.N / gridDim.x);
     const int nrows = (int)((long long)(blockIdx.x + 1) * a.N / gridDim.x) - r0;
-    const int groups = a.K / 128;
+    const int chunks = a.K / q4::CHUNK;
     const int units = p.units, cu = warp % units, rg = warp / units, TR = RG * CW / units;
-    float *red = reinterpret_cast<float *>(smem_raw + (size_t)NST * CW * STAGE);
+    float *red = reinterpret_cast<float *>(smem_raw + ring_bytes(NST));
     f16 *xs = reinterpret_cast<f16 *>(red + 2 * CW * p.red_warp);
 
-    // ---- this warp's ring: rows r0 + (tile * ngroups + rg) * 32 .., group kc * units + cu
-    const int my_kc = cu < groups ? (groups - cu + units - 1) / units : 0;          // this warp's steps of a row tile
+    // ---- this warp's ring: rows r0 + (tile * ngroups + rg) * 32 .., chunk kc * units + cu
+    const int my_kc = cu < chunks ? (chunks - cu + units - 1) / units : 0;          // this warp's chunks of a row tile
     const int ntiles = nrows > rg * RG ? (nrows - rg * RG + TR - 1) / TR : 0;       // its row group's tiles
-    const int nsteps = my_kc * ntiles;
-    uint8_t *ring = smem_raw + (size_t)warp * NST * STAGE;
-    const uint32_t row_bytes = (uint32_t)groups / 2 * q4::CHUNK_BYTES;
-    // sources of this lane's chunk of row g and of the scales of row `lane`, in the next step to request
-    const uint8_t *csrc = a.W + (size_t)(r0 + rg * RG) * row_bytes + (size_t)(cu >> 1) * q4::CHUNK_BYTES;
-    const uint8_t *ssrc = csrc + 128 + 8 * (cu & 1) + (size_t)lane * row_bytes;
-    csrc += 64 * (cu & 1) + 16 * t4 + (size_t)g * row_bytes;
+    uint8_t *ring = smem_raw + (size_t)warp * (NST * CODES + SC_SLOTS * SCALES);
+    const uint32_t row_bytes = (uint32_t)chunks * q4::CHUNK_BYTES;
+    // sources of this lane's piece of row g (codes) and of row `lane` (scales), in the next chunk to request
+    const uint8_t *csrc = a.W + (size_t)(r0 + rg * RG) * row_bytes + (size_t)cu * q4::CHUNK_BYTES;
+    const uint8_t *ssrc = csrc + 128 + (size_t)lane * row_bytes;
+    csrc += 16 * t4 + (size_t)g * row_bytes;
     const uint32_t cdst = smem_u32(ring) + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4);   // rows 8 apart have the same swizzle
-    const uint32_t sdst = smem_u32(ring) + CODES + lane * 8;
+    const uint32_t sdst = smem_u32(ring) + NST * CODES + lane * 16;
     const size_t row8 = 8 * (size_t)row_bytes;
-    const int kc_step = units / 2 * q4::CHUNK_BYTES;
+    const int kc_step = units * q4::CHUNK_BYTES;
     const long long tile_step = (long long)TR * row_bytes - (long long)(my_kc - 1) * kc_step;
-    int want = nsteps, want_kc = my_kc, want_left = nrows - rg * RG;   // steps, steps of the tile and rows not requested
-    uint32_t want_off = 0;                           // ring offset of the next step's slot
+    int want = my_kc * ntiles, want_kc = my_kc, want_left = nrows - rg * RG;   // chunks, chunks of the tile and rows not requested
+    uint32_t want_c = 0, want_s = 0;                 // ring offsets of the next step's codes and the next chunk's scales
+    bool second = false;                             // the next step is a chunk's second
     auto request = [&]() {
         if (want > 0) {
-            const uint32_t d = cdst + want_off;
+            const uint32_t d = cdst + want_c;
+            const uint8_t *q = csrc + (second ? 64 : 0);
             if (want_left >= RG) {
-                const uint8_t *q = csrc;
 #pragma unroll
                 for (int i = 0; i < RG / 8; ++i) {
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(d + i * 512), "l"(q));
                     q += row8;
                 }
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(sdst + want_off), "l"(ssrc));
+                if (!second) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(sdst + want_s), "l"(ssrc));
             } else {
                 // rows past the CTA's repeat its last: their sums are not stored
                 const int last = want_left - 1;
 #pragma unroll
                 for (int i = 0; i < RG / 8; ++i)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 :: "r"(d + i * 512), "l"(csrc + (long long)(min(g + 8 * i, last) - g) * row_bytes));
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
-                             :: "r"(sdst + want_off), "l"(ssrc + (long long)(min(lane, last) - lane) * row_bytes));
+                                 :: "r"(d + i * 512), "l"(q + (long long)(min(g + 8 * i, last) - g) * row_bytes));
+                if (!second)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 :: "r"(sdst + want_s), "l"(ssrc + (long long)(min(lane, last) - lane) * row_bytes));
             }
-            --want;
-            want_off = want_off == (NST - 1) * STAGE ? 0 : want_off + STAGE;
-            long long step = kc_step;
-            if (--want_kc == 0) {
-                want_kc = my_kc;
-                want_left -= TR;
-                step = tile_step;
+            want_c = want_c == (NST - 1) * CODES ? 0 : want_c + CODES;
+            if (second) {
+                --want;
+                want_s = want_s == (SC_SLOTS - 1) * SCALES ? 0 : want_s + SCALES;
+                long long step = kc_step;
+                if (--want_kc == 0) {
+                    want_kc = my_kc;
+                    want_left -= TR;
+                    step = tile_step;
+                }
+                csrc += step;
+                ssrc += step;
             }
-            csrc += step;
-            ssrc += step;
+            second = !second;
         }
         cp_async_commit();
     };
@@ -201,59 +215,64 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     } else if (!early) {
         for (int j = 0; j < NST - 1; ++j) request();
     }
-    xp += (size_t)(g < a.T ? g : 0) * ldx + cu * 128 + 8 * t4;
+    xp += (size_t)(g < a.T ? g : 0) * ldx + cu * q4::CHUNK + 8 * t4;
     uint4 bx[4];                                     // !XS: the next step's x
-    auto load_x = [&](int kc) {
+    auto load_x = [&](int k) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) bx[b] = *reinterpret_cast<const uint4 *>(xp + (size_t)kc * units * 128 + 32 * b);
+        for (int b = 0; b < 4; ++b) bx[b] = *reinterpret_cast<const uint4 *>(xp + (size_t)k + 32 * b);
     };
-    if (!XS && nsteps > 0) load_x(0);
+    if (!XS && my_kc * ntiles > 0) load_x(0);
 
     const Widen q;
-    uint32_t slot = 0;
-    const uint8_t *wr = ring + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4), *dr = ring + CODES + g * 8;
+    uint32_t cslot = 0, sslot = 0;
+    const uint8_t *wr = ring + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4), *dr = ring + NST * CODES + g * 16;
     for (int tile = 0; tile < ntiles; ++tile) {
         float y[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
         for (int kc = 0; kc < my_kc; ++kc) {
-            cp_async_wait<NST - 2>();
-            __syncwarp();
-            request();                           // into the slot read in the step before
-            uint4 xv[4];
+            const int k0 = kc * units * q4::CHUNK;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                xv[b] = XS ? *reinterpret_cast<const uint4 *>(xp + kc * units * 128 + 32 * b) : bx[b];
-            if (!XS) load_x(kc + 1 < my_kc ? kc + 1 : 0);
-            uint4 w[2][2];                       // words of rows g and g + 8 of each m16 tile
-            uint2 dd[2][2];                      // and their scales
+            for (int half = 0; half < 2; ++half) {
+                cp_async_wait<NST - 2>();
+                __syncwarp();
+                request();                           // into the slot read in the step before
+                uint4 xv[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int b = 0; b < 4; ++b)
+                    xv[b] = XS ? *reinterpret_cast<const uint4 *>(xp + k0 + 128 * half + 32 * b) : bx[b];
+                if (!XS) load_x(half == 0 ? k0 + 128 : kc + 1 < my_kc ? k0 + units * q4::CHUNK : 0);
+                uint4 w[2][2];                       // words of rows g and g + 8 of each m16 tile
+                uint2 dd[2][2];                      // and their scales
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    w[i][h] = *reinterpret_cast<const uint4 *>(wr + slot + (16 * i + 8 * h) * 64);
-                    dd[i][h] = *reinterpret_cast<const uint2 *>(dr + slot + (16 * i + 8 * h) * 8);
-                }
-            slot = slot + STAGE == NST * STAGE ? 0 : slot + STAGE;
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint4 x = xv[b];
+                    for (int h = 0; h < 2; ++h) {
+                        w[i][h] = *reinterpret_cast<const uint4 *>(wr + cslot + (16 * i + 8 * h) * 64);
+                        dd[i][h] = *reinterpret_cast<const uint2 *>(dr + sslot + (16 * i + 8 * h) * 16 + 8 * half);
+                    }
+                cslot = cslot == (NST - 1) * CODES ? 0 : cslot + CODES;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t wg = b == 0 ? w[i][0].x : b == 1 ? w[i][0].y : b == 2 ? w[i][0].z : w[i][0].w;
-                    const uint32_t wh = b == 0 ? w[i][1].x : b == 1 ? w[i][1].y : b == 2 ? w[i][1].z : w[i][1].w;
-                    const uint32_t sg = wg >> 8, sh = wh >> 8;
-                    const uint32_t pg = b < 2 ? dd[i][0].x : dd[i][0].y, ph = b < 2 ? dd[i][1].x : dd[i][1].y;
-                    const float dg = b & 1 ? h2hi(pg) : h2lo(pg), dh = b & 1 ? h2hi(ph) : h2lo(ph);
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma(s, q.low(wg), q.low(wh), q.low(sg), q.low(sh), x.x, x.z);
-                    mma(s, q.high(wg), q.high(wh), q.high(sg), q.high(sh), x.y, x.w);
-                    y[i][0] = fmaf(dg, s[0], y[i][0]);
-                    y[i][1] = fmaf(dg, s[1], y[i][1]);
-                    y[i][2] = fmaf(dh, s[2], y[i][2]);
-                    y[i][3] = fmaf(dh, s[3], y[i][3]);
+                for (int b = 0; b < 4; ++b) {
+                    const uint4 x = xv[b];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t wg = b == 0 ? w[i][0].x : b == 1 ? w[i][0].y : b == 2 ? w[i][0].z : w[i][0].w;
+                        const uint32_t wh = b == 0 ? w[i][1].x : b == 1 ? w[i][1].y : b == 2 ? w[i][1].z : w[i][1].w;
+                        const uint32_t sg = wg >> 8, sh = wh >> 8;
+                        const uint32_t pg = b < 2 ? dd[i][0].x : dd[i][0].y, ph = b < 2 ? dd[i][1].x : dd[i][1].y;
+                        const float dg = b & 1 ? h2hi(pg) : h2lo(pg), dh = b & 1 ? h2hi(ph) : h2lo(ph);
+                        float s[4];
+                        mma0(s, q.low(wg), q.low(wh), q.low(sg), q.low(sh), x.x, x.z);
+                        mma(s, q.high(wg), q.high(wh), q.high(sg), q.high(sh), x.y, x.w);
+                        y[i][0] = fmaf(dg, s[0], y[i][0]);
+                        y[i][1] = fmaf(dg, s[1], y[i][1]);
+                        y[i][2] = fmaf(dh, s[2], y[i][2]);
+                        y[i][3] = fmaf(dh, s[3], y[i][3]);
+                    }
                 }
             }
+            sslot = sslot == (SC_SLOTS - 1) * SCALES ? 0 : sslot + SCALES;
         }
         // ---- the row tile is done: join the group's sums, in a fixed order
         float *sums = red + ((tile & 1) * CW + rg * units) * p.red_warp;
@@ -266,7 +285,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             }
         }
         // once a tile: the readers of these sums are done before the next but one overwrites them
-        asm volatile("bar.sync %0, %1;" :: "r"(rg + 1), "r"(units * 32) : "memory");
+        if (units > 1) asm volatile("bar.sync %0, %1;" :: "r"(rg + 1), "r"(units * 32) : "memory");
+        else __syncwarp();
         const int row = (tile * (CW / units) + rg) * RG + lane;
         for (int t = cu; t < a.T; t += units) {
             float v = 0.f;
