@@ -119,7 +119,8 @@ struct Widen {
 template <bool XS, int NST>
 __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a, const Plan p, const int early) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    // the warp's number from a shuffle: what follows from it is then known to be the same for its lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int r0 = (int)((long long)blockIdx.x * a.N / gridDim.x);
     const int nrows = (int)((long long)(blockIdx.x + 1) * a.N / gridDim.x) - r0;
     const int chunks = a.K / q4::CHUNK;
@@ -132,59 +133,55 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     const int ntiles = nrows > rg * RG ? (nrows - rg * RG + TR - 1) / TR : 0;       // its row group's tiles
     uint8_t *ring = smem_raw + (size_t)warp * (NST * CODES + SC_SLOTS * SCALES);
     const uint32_t row_bytes = (uint32_t)chunks * q4::CHUNK_BYTES;
-    // sources of this lane's piece of row g (codes) and of row `lane` (scales), in the next chunk to request
-    const uint8_t *csrc = a.W + (size_t)(r0 + rg * RG) * row_bytes + (size_t)cu * q4::CHUNK_BYTES;
-    const uint8_t *ssrc = csrc + 128 + (size_t)lane * row_bytes;
-    csrc += 16 * t4 + (size_t)g * row_bytes;
+    // source of the next chunk to request (the warp's) and this lane's offsets from it: rows g, g + 8, .. of the codes
+    // and row `lane` of the scales
+    const uint8_t *src = a.W + (size_t)(r0 + rg * RG) * row_bytes + (size_t)cu * q4::CHUNK_BYTES;
+    uint32_t coff[RG / 8];
+#pragma unroll
+    for (int i = 0; i < RG / 8; ++i) coff[i] = (uint32_t)(g + 8 * i) * row_bytes + 16 * t4;
+    const uint32_t soff = (uint32_t)lane * row_bytes + 128;
     const uint32_t cdst = smem_u32(ring) + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4);   // rows 8 apart have the same swizzle
     const uint32_t sdst = smem_u32(ring) + NST * CODES + lane * 16;
-    const size_t row8 = 8 * (size_t)row_bytes;
     const int kc_step = units * q4::CHUNK_BYTES;
     const long long tile_step = (long long)TR * row_bytes - (long long)(my_kc - 1) * kc_step;
     int want = my_kc * ntiles, want_kc = my_kc, want_left = nrows - rg * RG;   // chunks, chunks of the tile and rows not requested
     uint32_t want_c = 0, want_s = 0;                 // ring offsets of the next step's codes and the next chunk's scales
-    bool second = false;                             // the next step is a chunk's second
-    auto request = [&]() {
+    auto request = [&](int half) {
         if (want > 0) {
-            const uint32_t d = cdst + want_c;
-            const uint8_t *q = csrc + (second ? 64 : 0);
             if (want_left >= RG) {
-#pragma unroll
-                for (int i = 0; i < RG / 8; ++i) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(d + i * 512), "l"(q));
-                    q += row8;
-                }
-                if (!second) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(sdst + want_s), "l"(ssrc));
-            } else {
-                // rows past the CTA's repeat its last: their sums are not stored
-                const int last = want_left - 1;
 #pragma unroll
                 for (int i = 0; i < RG / 8; ++i)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 :: "r"(d + i * 512), "l"(q + (long long)(min(g + 8 * i, last) - g) * row_bytes));
-                if (!second)
+                                 :: "r"(cdst + want_c + i * 512), "l"(src + 64 * half + coff[i]));
+                if (half == 0) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(sdst + want_s), "l"(src + soff));
+            } else {
+                // rows past the CTA's repeat its last: their sums are not stored
+                const uint32_t last = (uint32_t)(want_left - 1) * row_bytes;
+#pragma unroll
+                for (int i = 0; i < RG / 8; ++i)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                                 :: "r"(sdst + want_s), "l"(ssrc + (long long)(min(lane, last) - lane) * row_bytes));
+                                 :: "r"(cdst + want_c + i * 512), "l"(src + 64 * half + min(coff[i], last + 16 * t4)));
+                if (half == 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(sdst + want_s), "l"(src + min(soff, last + 128)));
             }
             want_c = want_c == (NST - 1) * CODES ? 0 : want_c + CODES;
-            if (second) {
+            if (half == 1) {
                 --want;
                 want_s = want_s == (SC_SLOTS - 1) * SCALES ? 0 : want_s + SCALES;
-                long long step = kc_step;
                 if (--want_kc == 0) {
                     want_kc = my_kc;
                     want_left -= TR;
-                    step = tile_step;
+                    src += tile_step;
+                } else {
+                    src += kc_step;
                 }
-                csrc += step;
-                ssrc += step;
             }
-            second = !second;
         }
         cp_async_commit();
     };
     if (early)                                       // beside the previous kernel: weights never depend on it
-        for (int j = 0; j < NST - 1; ++j) request();
+#pragma unroll
+        for (int j = 0; j < NST - 1; ++j) request(j & 1);
     pdl_wait();
     pdl_trigger();
 
@@ -203,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         for (int j = 0; j < HOLD; ++j)
             if (tid + j * THREADS < n) held[j] = piece(tid + j * THREADS);
         if (!early)                                  // behind x in the queue, before x is waited for
-            for (int j = 0; j < NST - 1; ++j) request();
+            for (int j = 0; j < NST - 1; ++j) request(j & 1);
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
             if (tid + j * THREADS < n) put(tid + j * THREADS, held[j]);
@@ -213,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         xp = xs;
         __syncthreads();
     } else if (!early) {
-        for (int j = 0; j < NST - 1; ++j) request();
+        for (int j = 0; j < NST - 1; ++j) request(j & 1);
     }
     xp += (size_t)(g < a.T ? g : 0) * ldx + cu * q4::CHUNK + 8 * t4;
     uint4 bx[4];                                     // !XS: the next step's x
@@ -236,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             for (int half = 0; half < 2; ++half) {
                 cp_async_wait<NST - 2>();
                 __syncwarp();
-                request();                           // into the slot read in the step before
+                request((half + NST - 1) & 1);       // NST - 1 steps on, into the slot read in the step before
                 uint4 xv[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
