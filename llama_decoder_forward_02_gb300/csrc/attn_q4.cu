@@ -49,6 +49,7 @@ constexpr int KG = 16;                   // keys of a group
 constexpr int NST = 4;                   // ring stages of a warp
 constexpr int MAX_SPLIT = ATTN_DECODE_MAX_SPLIT;
 constexpr int MIN_KEYS = NW * KG;        // keys of a split
+constexpr int MERGE_AHEAD = 32;          // splits whose partials a merging thread asks for at once
 constexpr int SMS = 152;                 // of the one GPU this library is compiled for: scratch sizes follow from it
 
 __device__ __forceinline__ int split_chunk(int S, int n_split) {
@@ -199,9 +200,6 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
         }
         cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i) request();
-
     // ---- q as the N side: column g of tile n is half g % 2 of head 4 n + g / 2.
     // The fragments are the same for every warp: each makes some blocks' and
     // leaves them in shared memory.  q * log2(e) / sqrt(hd), times 16 for the
@@ -210,14 +208,18 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     uint4 *qf = reinterpret_cast<uint4 *>(smem_raw + R::BYTES);            // [NT * NB][32]
     float *q8 = reinterpret_cast<float *>(qf + NT * NB * 32);              // [NT * NB][4]: 8 sum(q) * 2^-20 of the columns' head
     const float scale = 16.f * 1.4426950408889634f / sqrtf((float)HD);
-    for (int u = warp; u < NT * NB; u += NW) {
-        const int n = u / NB, b = u - n * NB, hq = 4 * n + (g >> 1);
-        float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-        if (hq < gn) {
-            const float4 *qp = reinterpret_cast<const float4 *>(a.q + ((size_t)t * a.H + h0 + hq) * HD + 32 * b + 8 * t4);
-            x0 = __ldcg(qp);                          // through L2: q is rewritten between uses
-            x1 = __ldcg(qp + 1);
-        }
+    static_assert(NT * NB <= NW, "a warp makes one block's fragments");
+    float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+    if (warp < NT * NB && 4 * (warp / NB) + (g >> 1) < gn) {
+        const float4 *qp = reinterpret_cast<const float4 *>(a.q + ((size_t)t * a.H + h0 + 4 * (warp / NB) + (g >> 1)) * HD +
+                                                            32 * (warp % NB) + 8 * t4);
+        x0 = __ldcg(qp);                              // through L2: q is rewritten between uses; ahead of the
+        x1 = __ldcg(qp + 1);                          // ring's burst, behind which it would wait 2 us
+    }
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) request();
+    if (warp < NT * NB) {
+        const int u = warp;
         const float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         uint32_t h[8];
 #pragma unroll
@@ -355,49 +357,66 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     cp_async_wait<0>();
     __syncthreads();                                      // the rings become the warps' results
 
-    float *wst = reinterpret_cast<float *>(smem_raw);     // [NW][GC][REC]: max, sum, numerators
+    // the warps' largest maximum of each head, then their results in its units
+    float *wst = reinterpret_cast<float *>(smem_raw);     // [NW][GC][REC]: numerators, sum
     float *wgt = reinterpret_cast<float *>(smem_raw + R::WGT);   // [GC][MAX_SPLIT]
+    __shared__ float s_max[NW][GC];
+    if (g == 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s_max[warp][4 * n + t4] = m[n] * UNDO;
+    }
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_max[w][4 * n + t4]);
+        const float f = m[n] == -INFINITY ? 0.f : exp2_fast(m[n] * UNDO - M);
         float *ws = wst + ((size_t)warp * GC + 4 * n + t4) * REC;
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
-        if (g == 0) { ws[0] = m[n] * UNDO; ws[1] = l[n]; }
+        if (g == 0) ws[HD] = l[n] * f;
+        const float f1 = 16777216.f * f, f16 = 1048576.f * f, f8 = -8.f * f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) sw[n][b] += __shfl_xor_sync(0xffffffffu, sw[n][b], x);
-            float *d = ws + 2 + 32 * b + 8 * (g >> 1) + (g & 1);
-            const float o8 = 8.f * sw[n][b];
-            d[0] = fmaf(o[n][b][0][0] + o[n][b][0][1], 16777216.f, -o8);
-            d[4] = fmaf(o[n][b][0][2] + o[n][b][0][3], 16777216.f, -o8);
-            d[2] = fmaf(o[n][b][1][0] + o[n][b][1][1], 1048576.f, -o8);
-            d[6] = fmaf(o[n][b][1][2] + o[n][b][1][3], 1048576.f, -o8);
+            float *d = ws + 32 * b + 8 * (g >> 1) + (g & 1);
+            const float o8 = f8 * sw[n][b];
+            d[0] = fmaf(o[n][b][0][0] + o[n][b][0][1], f1, o8);
+            d[4] = fmaf(o[n][b][0][2] + o[n][b][0][3], f1, o8);
+            d[2] = fmaf(o[n][b][1][0] + o[n][b][1][1], f16, o8);
+            d[6] = fmaf(o[n][b][1][2] + o[n][b][1][3], f16, o8);
         }
     }
     __syncthreads();
+    // records of a split: numerators, sum, maximum
     const bool one = n_eff == 1;
     float *part = a.part + ((size_t)(t * a.H + h0) * a.n_split + sp) * REC;
-    for (int i = tid; i < gn * HD; i += THREADS) {
-        const int h = i / HD, d = i - h * HD;
-        float M = -INFINITY, num = 0.f, den = 0.f;
+    for (int i = tid; i < gn * (HD / 2); i += THREADS) {
+        const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
+        float2 num = make_float2(0.f, 0.f);
+        float den = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, wst[((size_t)w * GC + h) * REC]);
-        if (M != -INFINITY) {
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float *ws = wst + ((size_t)w * GC + h) * REC;
-                const float f = exp2f(ws[0] - M);
-                num += f * ws[2 + d];
-                den += f * ws[1];
-            }
+        for (int w = 0; w < NW; ++w) {
+            const float *ws = wst + ((size_t)w * GC + h) * REC;
+            const float2 v = *reinterpret_cast<const float2 *>(ws + d);
+            num.x += v.x;
+            num.y += v.y;
+            den += ws[HD];
         }
         if (one) {
-            a.o[((size_t)t * a.H + h0 + h) * HD + d] = f2h(den > 0.f ? num / den : 0.f);
+            const float inv = den > 0.f ? 1.f / den : 0.f;
+            *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(num.x * inv, num.y * inv);
         } else {
             float *rp = part + (size_t)h * a.n_split * REC;
-            rp[2 + d] = num;
-            if (d == 0) { rp[0] = M; rp[1] = den; }
+            *reinterpret_cast<float2 *>(rp + d) = num;
+            if (d == 0) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) M = fmaxf(M, s_max[w][h]);
+                *reinterpret_cast<float2 *>(rp + HD) = make_float2(den, M);
+            }
         }
     }
     if (one) return;
@@ -409,43 +428,63 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     if (!s_last) return;
     __threadfence();
 
-    // ---- last CTA of this (row, kv head, chunk): a warp finds its heads' split
-    // weights, then every thread sums its dimensions over the splits, in order
+    // ---- last CTA of this (row, kv head, chunk): each thread asks for its two
+    // dimensions of the first MERGE_AHEAD splits while the warps find the splits'
+    // weights, then sums them in split order
     const float *all = a.part + (size_t)(t * a.H + h0) * a.n_split * REC;
+    float2 v[MERGE_AHEAD];
+    const int mh = tid / (HD / 2), md = 2 * (tid - mh * (HD / 2));
+    if (mh < gn) {
+        const float *rp = all + (size_t)mh * a.n_split * REC + md;
+#pragma unroll
+        for (int p = 0; p < MERGE_AHEAD; ++p)
+            if (p < n_eff) v[p] = __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC));
+    }
     for (int h = warp; h < gn; h += NW) {
-        const float *rp = all + (size_t)h * a.n_split * REC;
+        const float *rp = all + (size_t)h * a.n_split * REC + HD;
         float mx = -INFINITY;
-        float2 ml[MAX_SPLIT / 32];
+        float2 lm[MAX_SPLIT / 32];
 #pragma unroll
         for (int q = 0; q < MAX_SPLIT / 32; ++q) {
             const int p = lane + 32 * q;
-            ml[q] = p < n_eff ? __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC)) : make_float2(-INFINITY, 0.f);
-            mx = fmaxf(mx, ml[q].x);
+            lm[q] = p < n_eff ? __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC)) : make_float2(0.f, -INFINITY);
+            mx = fmaxf(mx, lm[q].y);
         }
         mx = warp_max(mx);
         float den = 0.f;
 #pragma unroll
         for (int q = 0; q < MAX_SPLIT / 32; ++q) {
-            ml[q].x = mx == -INFINITY ? 0.f : exp2f(ml[q].x - mx);
-            den += ml[q].x * ml[q].y;
+            lm[q].y = mx == -INFINITY ? 0.f : exp2_fast(lm[q].y - mx);
+            den += lm[q].y * lm[q].x;
         }
         den = warp_sum(den);
         const float inv = den > 0.f ? 1.f / den : 0.f;
 #pragma unroll
         for (int q = 0; q < MAX_SPLIT / 32; ++q)
-            if (lane + 32 * q < n_eff) wgt[h * MAX_SPLIT + lane + 32 * q] = ml[q].x * inv;
+            if (lane + 32 * q < n_eff) wgt[h * MAX_SPLIT + lane + 32 * q] = lm[q].y * inv;
     }
     __syncthreads();
-    for (int i = tid; i < gn * HD / 2; i += THREADS) {
+    for (int i = tid; i < gn * (HD / 2); i += THREADS) {
         const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
-        const float *rp = all + (size_t)h * a.n_split * REC + 2 + d;
+        const float *rp = all + (size_t)h * a.n_split * REC + d;
         float2 acc = make_float2(0.f, 0.f);
+        int p = 0;
+        if (i == tid) {
+#pragma unroll
+            for (int q = 0; q < MERGE_AHEAD; ++q)
+                if (q < n_eff) {
+                    const float f = wgt[h * MAX_SPLIT + q];
+                    acc.x = fmaf(f, v[q].x, acc.x);
+                    acc.y = fmaf(f, v[q].y, acc.y);
+                }
+            p = MERGE_AHEAD;
+        }
 #pragma unroll 16
-        for (int p = 0; p < n_eff; ++p) {
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC));
+        for (; p < n_eff; ++p) {
+            const float2 w = __ldcg(reinterpret_cast<const float2 *>(rp + (size_t)p * REC));
             const float f = wgt[h * MAX_SPLIT + p];
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
+            acc.x = fmaf(f, w.x, acc.x);
+            acc.y = fmaf(f, w.y, acc.y);
         }
         *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(acc.x, acc.y);
     }
@@ -509,7 +548,12 @@ int attn_q4_chunks(int H, int Hkv) { return (H / Hkv + GC - 1) / GC; }
 
 int attn_q4_pick_split(int T, int H, int Hkv, int n_ctx) {
     const int mx = (n_ctx + MIN_KEYS - 1) / MIN_KEYS;
-    long long s = 2LL * SMS / ((long long)T * Hkv * attn_q4_chunks(H, Hkv));
+    const long long units = (long long)T * Hkv * attn_q4_chunks(H, Hkv);
+    long long s = 2LL * SMS / units;
+    // the merge asks for 32 splits at once: beyond, it pays another round trip
+    // (32000 keys, 8 kv heads: 38 splits 15.7 us, 32 splits 15.2), so more only
+    // where fewer leave SMs without work
+    if (s > MERGE_AHEAD && units * MERGE_AHEAD >= SMS) s = MERGE_AHEAD;
     if (s > MAX_SPLIT) s = MAX_SPLIT;
     if (s > mx) s = mx;
     return s < 1 ? 1 : (int)s;
