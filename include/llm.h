@@ -93,8 +93,12 @@ void llm_model_free(llm_model *m);
 
 /* Weight types of llm_model_quantize. */
 #define LLM_WTYPE_Q8_0 1
+#define LLM_WTYPE_Q4_0 2
 
-/* Re-encode the model's matrices as Q8_0 blocks.  "LLama.cpp — how it
+/* Re-encode the model's matrices as Q8_0 or Q4_0 blocks.  Q4_0: the blocks and
+ * the row layout stand with the 4-bit operators below; otherwise as Q8_0, but
+ * that its rows (9 K / 16 bytes) are read by every step of 1..8 rows whose rows
+ * are all outputs, 9/32 of the fp16 bytes.  Q8_0:  "LLama.cpp — how it
  * works", section "The GGUF format (reference)", names Q8_0 among the
  * quantised tensor element types without giving its layout; the one taken:
  * each row of Wq, Wk, Wv, Wo, gate, up, down and the output projection is cut
@@ -115,6 +119,17 @@ void llm_model_free(llm_model *m);
  * LLM_ERR_COMPUTE if a launch fails, after which the model's weights are
  * undefined and it should be freed.  Runs on `stream` and synchronizes it. */
 int32_t llm_model_quantize(llm_model *m, int32_t wtype, void *stream);
+
+/* Give the model per-head norms of its queries and keys, as model families
+ * with normed attention have them: between the QKV projection and the
+ * rotation each query head becomes x * q_norm[layer] / sqrt(mean(x^2) +
+ * rms_eps) over its head_dim elements, each key head the same with k_norm.
+ * q_norm, k_norm: HOST arrays of n_layer DEVICE pointers to bf16 [head_dim]
+ * (read only during the call), or NULL for queries or keys without a norm (not
+ * both).  A second call replaces the gains.  LLM_ERR_INVALID (nothing changed)
+ * for a NULL model or pointer or a model with live contexts; LLM_ERR_ALLOC,
+ * LLM_ERR_COMPUTE as llm_model_create.  Runs on `stream` and synchronizes it. */
+int32_t llm_model_set_qk_norm(llm_model *m, const void *const *q_norm, const void *const *k_norm, void *stream);
 
 /* Create a context ("llama_new_context"): an fp16 KV cache of n_ctx positions
  * for each of n_seq_max sequences and every layer, laid out
@@ -328,6 +343,13 @@ int32_t llm_debug_fail_alloc(int32_t n);
  *                  at +-448, no scale; half the bytes of the fp16 cache), 0 =
  *                  fp16 (default); allowed only while every sequence is empty
  *                  (the cache is reallocated);
+ *   "kv_q4"        1 = the KV cache holds Q4_0 blocks (the 4-bit operators below
+ *                  have the layout; 9/32 of the fp16 cache's bytes, plus one
+ *                  layer's rows in fp16 that prefill widens into), 0 = fp16
+ *                  (default); allowed only while every sequence is empty, and not
+ *                  together with kv_fp8; a failed call changes nothing;
+ *   "gemv_q4"      1 = steps of 1..8 rows of a Q4_0 model read its Q4_0 rows
+ *                  (default); 0 = its fp16 copies;
  *   "swa_window"   sliding-window attention ("KV Cache" of the pages): a query at
  *                  position p sees only keys at p - W < position <= p of its
  *                  sequence (0 = every earlier position, the default);
@@ -351,7 +373,7 @@ int64_t llm_kernel_launches(const llm_ctx *c);
  * LLM_KERNEL_CLASSES-1), the summed duration in milliseconds, the launch count
  * and a static name ("gemv_gateup_swiglu", "attn_decode", ...); it returns
  * LLM_ERR_INVALID past the last class. */
-#define LLM_KERNEL_CLASSES 16
+#define LLM_KERNEL_CLASSES 18
 int32_t llm_kernel_timing(llm_ctx *c, int32_t enable);
 int32_t llm_kernel_time(llm_ctx *c, int32_t kernel, double *total_ms, int64_t *count, const char **name);
 
@@ -507,7 +529,7 @@ int32_t llm_op_quantize_q4_0(const void *W, int32_t N, int32_t K, void *out, voi
  * rows (as written by llm_op_quantize_q4_0).  x fp16 [T][ldx] (16-byte
  * aligned, ldx >= K a multiple of 8), y fp32 [T][ldy] (ldy >= N; the entries
  * between N and ldy are left as they are).  Any N >= 1, any K that is a
- * positive multiple of 256, else LLM_ERR_INVALID. */
+ * positive multiple of 256 up to 2^24, else LLM_ERR_INVALID. */
 int32_t llm_op_gemv_q4_0(const void *Wq, const void *x, float *y, int32_t N, int32_t K, int32_t T, int32_t ldx,
                          int32_t ldy, void *stream);
 

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(HERE, "libllm.so")
 
 LLM_OK, LLM_NO_KV_ROOM, LLM_ERR_INVALID, LLM_ERR_ALLOC, LLM_ERR_COMPUTE = 0, 1, -1, -2, -3
 LLM_BATCH_TOKENS_ON_DEVICE = 1
-LLM_WTYPE_Q8_0 = 1
+LLM_WTYPE_Q8_0, LLM_WTYPE_Q4_0 = 1, 2
 LLM_Q_F32, LLM_Q_F16 = 0, 1
 LLM_KV_F16, LLM_KV_E4M3, LLM_KV_Q4_0 = 0, 1, 2
 
@@ -66,6 +66,7 @@ llm_model_create = _proto("llm_model_create", c_i32, ctypes.POINTER(llm_hparams)
                           c_vp, ctypes.POINTER(c_vp))
 llm_model_free = _proto("llm_model_free", None, c_vp)
 llm_model_quantize = _proto("llm_model_quantize", c_i32, c_vp, c_i32, c_vp)
+llm_model_set_qk_norm = _proto("llm_model_set_qk_norm", c_i32, c_vp, ctypes.POINTER(c_vp), ctypes.POINTER(c_vp), c_vp)
 llm_kv_alloc = _proto("llm_kv_alloc", c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, ctypes.POINTER(c_vp))
 llm_kv_free = _proto("llm_kv_free", None, c_vp)
 llm_decode = _proto("llm_decode", c_i32, c_vp, ctypes.POINTER(llm_batch))
@@ -223,6 +224,15 @@ class Model:
     def quantize(self, wtype=None, stream=0):
         """llm_model_quantize (default LLM_WTYPE_Q8_0)."""
         check(llm_model_quantize(self.handle, LLM_WTYPE_Q8_0 if wtype is None else wtype, c_vp(stream)))
+
+    def set_qk_norm(self, q_norm=None, k_norm=None, stream=0):
+        """llm_model_set_qk_norm from lists of n_layer bf16 device tensors [head_dim] (or None)."""
+        def ptrs(ts):
+            return None if ts is None else (c_vp * len(ts))(*[t.data_ptr() for t in ts])
+        for ts in (q_norm, k_norm):
+            if ts is not None and len(ts) != self.shape.n_layer:
+                raise ValueError("one gain tensor a layer")
+        check(llm_model_set_qk_norm(self.handle, ptrs(q_norm), ptrs(k_norm), c_vp(stream)))
 
     def free(self):
         if self.handle:

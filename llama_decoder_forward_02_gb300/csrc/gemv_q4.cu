@@ -115,14 +115,19 @@ struct Widen {
     __device__ __forceinline__ uint32_t high(uint32_t w) const { return pick(w, m1, e1, 0x54805480u); }
 };
 
+constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : 1; }
+
 // XS: x in shared memory; NST: ring stages of a warp
-template <bool XS, int NST>
+template <int EPI, bool XS, int NST>
 __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a, const Plan p, const int early) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     // the warp's number from a shuffle: what follows from it is then known to be the same for its lanes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    const int r0 = (int)((long long)blockIdx.x * a.N / gridDim.x);
-    const int nrows = (int)((long long)(blockIdx.x + 1) * a.N / gridDim.x) - r0;
+    constexpr int UNIT = row_unit(EPI);              // rows kept together
+    const int r0 = (int)((long long)blockIdx.x * (a.N / UNIT) / gridDim.x) * UNIT;
+    const int nrows = (int)((long long)(blockIdx.x + 1) * (a.N / UNIT) / gridDim.x) * UNIT - r0;
+    __shared__ float s_r[8];                         // the rows' RMSNorm factors
+    __shared__ float s_sq[EPI == EPI_RESID ? CW : 1][8];   // sums of h^2 by row group
     const int chunks = a.K / q4::CHUNK;
     const int units = p.units, cu = warp % units, rg = warp / units, TR = RG * CW / units;
     float *red = reinterpret_cast<float *>(smem_raw + ring_bytes(NST));
@@ -188,6 +193,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     // ---- x: column g of the N side is row g of x (columns from T on repeat row 0, their sums are not stored)
     const f16 *xp = a.x;
     int ldx = a.ldx;
+    if (warp < a.T) {
+        float r = 1.f;
+        if (a.ss_in) {
+            float ss = 0.f;
+            for (int i = lane; i < a.n_ss_in; i += 32) ss += a.ss_in[(size_t)warp * a.n_ss_in + i];
+            r = 1.f / sqrtf(warp_sum(ss) / (float)a.K + a.eps);
+        }
+        if (lane == 0) s_r[warp] = r;
+    }
     if (XS) {
         const int per = a.K / 8, n = a.T * per;      // 16-byte pieces of x
         constexpr int HOLD = 4;                      // pieces a thread asks for before the ring's first steps
@@ -209,8 +223,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         ldx = a.K + X_PAD;
         xp = xs;
         __syncthreads();
-    } else if (!early) {
-        for (int j = 0; j < NST - 1; ++j) request(j & 1);
+    } else {
+        if (!early)
+            for (int j = 0; j < NST - 1; ++j) request(j & 1);
+        __syncthreads();
     }
     xp += (size_t)(g < a.T ? g : 0) * ldx + cu * q4::CHUNK + 8 * t4;
     uint4 bx[4];                                     // !XS: the next step's x
@@ -220,7 +236,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     };
     if (!XS && my_kc * ntiles > 0) load_x(0);
 
-    const Widen q;
+    const Widen wd;
+    float ssq[EPI == EPI_RESID ? 8 : 1];             // RESID: this warp's sums of h^2, by its rows of x in turn
+#pragma unroll
+    for (float &v : ssq) v = 0.f;
     uint32_t cslot = 0, sslot = 0;
     const uint8_t *wr = ring + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4), *dr = ring + NST * CODES + g * 16;
     for (int tile = 0; tile < ntiles; ++tile) {
@@ -260,8 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
                         const uint32_t pg = b < 2 ? dd[i][0].x : dd[i][0].y, ph = b < 2 ? dd[i][1].x : dd[i][1].y;
                         const float dg = b & 1 ? h2hi(pg) : h2lo(pg), dh = b & 1 ? h2hi(ph) : h2lo(ph);
                         float s[4];
-                        mma0(s, q.low(wg), q.low(wh), q.low(sg), q.low(sh), x.x, x.z);
-                        mma(s, q.high(wg), q.high(wh), q.high(sg), q.high(sh), x.y, x.w);
+                        mma0(s, wd.low(wg), wd.low(wh), wd.low(sg), wd.low(sh), x.x, x.z);
+                        mma(s, wd.high(wg), wd.high(wh), wd.high(sg), wd.high(sh), x.y, x.w);
                         y[i][0] = fmaf(dg, s[0], y[i][0]);
                         y[i][1] = fmaf(dg, s[1], y[i][1]);
                         y[i][2] = fmaf(dh, s[2], y[i][2]);
@@ -284,11 +303,56 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         // once a tile: the readers of these sums are done before the next but one overwrites them
         if (units > 1) asm volatile("bar.sync %0, %1;" :: "r"(rg + 1), "r"(units * 32) : "memory");
         else __syncwarp();
-        const int row = (tile * (CW / units) + rg) * RG + lane;
-        for (int t = cu; t < a.T; t += units) {
+        const int row = (tile * (CW / units) + rg) * RG + lane, n = r0 + row;
+        const bool in = row < nrows;
+        int q = 0;
+        for (int t = cu; t < a.T; t += units, ++q) {
             float v = 0.f;
             for (int c = 0; c < units; ++c) v += sums[c * p.red_warp + t * RED_COL + lane];
-            if (row < nrows) a.out[(size_t)t * a.ldo + r0 + row] = v;
+            v *= s_r[t];
+            if (EPI == EPI_STORE) {
+                if (in) a.out[(size_t)t * a.ldo + n] = v;
+            } else if (EPI == EPI_RESID) {
+                float h = 0.f;
+                if (in) {
+                    h = a.hres[(size_t)t * a.ldh + n] + v;
+                    a.hres[(size_t)t * a.ldh + n] = h;
+                    if (a.xg_out) {
+                        const float xg = h * a.gain_next[n];
+                        if (f16_bad(xg)) raise_error(a.err, ERRF_F16_RANGE);
+                        a.xg_out[(size_t)t * a.ldxg + n] = f2h(xg);
+                    }
+                }
+                const float sq = warp_sum(h * h);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k == q) ssq[k] += sq;
+            } else {
+                // a gate row's lane takes its up row from the lane GU_GROUP on
+                const float up = __shfl_down_sync(0xffffffffu, v, GU_GROUP);
+                if (in && !(lane & GU_GROUP)) {
+                    const float u = silu(v) * up;
+                    if (f16_bad(u)) raise_error(a.err, ERRF_F16_RANGE);
+                    a.u_out[(size_t)t * a.ldu + n / (2 * GU_GROUP) * GU_GROUP + (lane & (GU_GROUP - 1))] = f2h(u);
+                }
+            }
+        }
+    }
+    if (EPI == EPI_RESID && a.xg_out) {
+        // this CTA's sums of squares of the new h, in a fixed order
+        int q = 0;
+        for (int t = cu; t < a.T; t += units, ++q) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k == q) v = ssq[k];
+            if (lane == 0) s_sq[rg][t] = v;
+        }
+        __syncthreads();
+        if (tid < a.T) {
+            float v = 0.f;
+            for (int k = 0; k < CW / units; ++k) v += s_sq[k][tid];
+            a.ss_out[(size_t)tid * gridDim.x + blockIdx.x] = v;
         }
     }
     cp_async_wait<0>();
@@ -296,21 +360,36 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
 
 }  // namespace
 
+int gemv_q4_ctas(int epi, int N, int num_sms) {
+    const int units = N / row_unit(epi);
+    return units < num_sms ? units : num_sms;
+}
+
 // early: with l.pdl, weights may be read before the previous kernel is done
-cudaError_t launch_gemv_q4(const GemvQ4Args &a, int num_sms, const Launch &l, bool early) {
+cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Launch &l, bool early) {
     Plan p;
-    const int ctas = a.N < num_sms ? a.N : num_sms;
-    if (a.T < 1 || a.T > 8 || ctas < 1 || !make_plan(a.N, a.K, a.T, ctas, &p)) return cudaErrorInvalidValue;
+    const int ctas = gemv_q4_ctas(epi, a.N, num_sms);
+    if (a.T < 1 || a.T > 8 || ctas < 1 || a.N % row_unit(epi) || !make_plan(a.N, a.K, a.T, ctas, &p))
+        return cudaErrorInvalidValue;
     const dim3 grid(ctas), block(THREADS);
-    return !p.x_smem      ? launch_kernel(gemv_q4_kernel<false, 4>, grid, block, p.smem, l, a, p, (int)early)
-           : p.nst == 4   ? launch_kernel(gemv_q4_kernel<true, 4>, grid, block, p.smem, l, a, p, (int)early)
-                          : launch_kernel(gemv_q4_kernel<true, 3>, grid, block, p.smem, l, a, p, (int)early);
+#define Q4_GEMV(E)                                                                                             \
+    if (epi == E)                                                                                              \
+        return !p.x_smem    ? launch_kernel(gemv_q4_kernel<E, false, 4>, grid, block, p.smem, l, a, p, (int)early) \
+               : p.nst == 4 ? launch_kernel(gemv_q4_kernel<E, true, 4>, grid, block, p.smem, l, a, p, (int)early)  \
+                            : launch_kernel(gemv_q4_kernel<E, true, 3>, grid, block, p.smem, l, a, p, (int)early);
+    Q4_GEMV(EPI_STORE) Q4_GEMV(EPI_RESID) Q4_GEMV(EPI_SWIGLU)
+#undef Q4_GEMV
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t init_gemv_q4_attributes() {
-    cudaError_t e = allow_smem(gemv_q4_kernel<true, 4>, SMEM_CAP);
-    if (!e) e = allow_smem(gemv_q4_kernel<true, 3>, SMEM_CAP);
-    if (!e) e = allow_smem(gemv_q4_kernel<false, 4>, SMEM_CAP);
+    cudaError_t e = cudaSuccess;
+#define Q4_GEMV_ATTR(E)                                                       \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, true, 4>, SMEM_CAP);             \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, true, 3>, SMEM_CAP);             \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, false, 4>, SMEM_CAP);
+    Q4_GEMV_ATTR(EPI_STORE) Q4_GEMV_ATTR(EPI_RESID) Q4_GEMV_ATTR(EPI_SWIGLU)
+#undef Q4_GEMV_ATTR
     return e;
 }
 

@@ -301,16 +301,26 @@ cudaError_t launch_quantize_q8_0(f16 *w, int N, int K, uint8_t *q8, bool write_b
 size_t q4_0_row_bytes(int K);
 cudaError_t launch_quantize_q4_0(f16 *w, int N, int K, uint8_t *q4, bool write_back, cudaStream_t st);
 
-// y[t][n] = sum_k W[n][k] x[t][k] with Q4_0 rows W, t < T <= 8.
+// y[t][n] = r[t] * sum_k W[n][k] x[t][k] with Q4_0 rows W, t < T <= 8, and
+// what becomes of y (EPI_STORE, EPI_RESID or EPI_SWIGLU).
 struct GemvQ4Args {
     const uint8_t *W;         // [N] rows of q4_0_row_bytes(K)
     int N, K, T;
     const f16 *x; int ldx;
-    float *out; int ldo;
+    // r[t] = 1 / sqrt(sum_i ss_in[t * n_ss_in + i] / K + eps), the RMSNorm of
+    // rows whose gain x carries already; 1 where ss_in is null
+    const float *ss_in; int n_ss_in; float eps;
+    float *out; int ldo;      // EPI_STORE
+    // EPI_RESID: hres += y; with xg_out also the next norm's input
+    // xg_out[t * ldxg + n] = f16(h * gain_next[n]) and each CTA's sum of h^2
+    // over its rows to ss_out[t * (CTAs of the launch, gemv_q4_ctas) + cta]
+    float *hres; int ldh; const float *gain_next; f16 *xg_out; int ldxg; float *ss_out;
+    f16 *u_out; int ldu;      // EPI_SWIGLU: rows as GU_GROUP interleaves gate and up
     uint32_t *err;
 };
+int gemv_q4_ctas(int epi, int N, int num_sms);
 // early: weights may be read before the kernel that precedes the launch is done
-cudaError_t launch_gemv_q4(const GemvQ4Args &a, int num_sms, const Launch &l, bool early);
+cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Launch &l, bool early);
 
 // Per-head RMSNorm (gains may be null: no norm) and rotation of the query and
 // key heads of qkv rows [T][ld] (H query, Hkv key, Hkv value heads), q to q32
@@ -326,6 +336,10 @@ struct QkNormArgs {
     uint32_t *err;
 };
 cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l);
+// launch_kv_shift of a Q4_0 cache: keys are rotated as the values they stand
+// for and encoded again.
+cudaError_t launch_kv_shift_q4(const KvView &kv0, int n_layer, int seq, int p0, int n, int end, const float2 *rope,
+                               const Launch &l);
 
 // Decode attention over a Q4_0 cache (AttnDecodeArgs with kv.k4 set; any T,
 // any H / Hkv).  part: attn_q4_part_floats; counters: T * Hkv * head chunks,

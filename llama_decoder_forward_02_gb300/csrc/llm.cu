@@ -81,7 +81,8 @@ struct LayerW {
     f16 *wqkv, *wo, *wgu, *wdown;
     float *attn_norm, *ffn_norm;
     WMap mqkv, mo, mgu, mdown;
-    // Q8_0 rows of the same matrices (llm_model_quantize), or null
+    float *q_norm = nullptr, *k_norm = nullptr;   // per-head gains [hd] (llm_model_set_qk_norm), or null
+    // Q8_0 or Q4_0 rows of the same matrices (llm_model_quantize), or null
     const uint8_t *q_qkv = nullptr, *q_o = nullptr, *q_gu = nullptr, *q_down = nullptr;
 };
 
@@ -95,8 +96,9 @@ struct llm_model {
     WMap mout;
     std::vector<LayerW> layers;
     int wtype = 0;                     // LLM_WTYPE_* of llm_model_quantize (0: as created)
-    uint8_t *qbuf = nullptr;           // Q8_0 rows of every decode matrix
-    const uint8_t *q_out = nullptr;    // Q8_0 rows of the output projection
+    uint8_t *qbuf = nullptr;           // Q8_0 or Q4_0 rows of every decode matrix
+    const uint8_t *q_out = nullptr;    // ... of the output projection
+    float *nbuf = nullptr;             // query and key gains of every layer (llm_model_set_qk_norm)
     int num_sms = 0;
     int device = 0;
     int n_contexts = 0;
@@ -106,12 +108,12 @@ struct llm_model {
 enum KId {
     K_EMBED, K_GATHER, K_GEMV_QKV, K_ATTN_DECODE, K_GEMV_O, K_GEMV_GATEUP, K_GEMV_DOWN,
     K_GEMV_LMHEAD, K_GEMM_QKV, K_ATTN_PREFILL, K_GEMM_O, K_GEMM_GATEUP, K_GEMM_DOWN, K_GEMM_LMHEAD,
-    K_ARGMAX, K_COPY, K_COUNT
+    K_ARGMAX, K_COPY, K_QK_NORM, K_KV_WIDEN, K_COUNT
 };
 static const char *const KNAME[K_COUNT] = {
     "embed", "gather_rows", "gemv_qkv_rope_kv", "attn_decode", "gemv_o_resid", "gemv_gateup_swiglu",
     "gemv_down_resid", "gemv_lm_head", "gemm_qkv_rope_kv", "attn_prefill", "gemm_o_resid", "gemm_gateup_swiglu",
-    "gemm_down_resid", "gemm_lm_head", "argmax", "copy"};
+    "gemm_down_resid", "gemm_lm_head", "argmax", "copy", "qk_norm_rope_kv", "kv_widen"};
 
 struct KtRec { int id; cudaEvent_t a, b; };
 
@@ -124,6 +126,16 @@ struct llm_ctx {
     f16 *kc = nullptr, *vc = nullptr;
     size_t kv_elems = 0;                      // elements of each of kc, vc
     bool kv_fp8 = false;                      // kc, vc hold FP8 E4M3 (one byte an element)
+    // Q4_0 cache (option "kv_q4"): kc, vc hold a plane of codes, then one of
+    // scales (9/16 byte an element); decode attention's split scratch; prefill
+    // widens a layer's visible rows into k16, v16 [seq][kv_head][n_pad][hd]
+    bool kv_q4 = false;
+    float *q4_part = nullptr; unsigned *q4_cnt = nullptr;
+    f16 *k16 = nullptr, *v16 = nullptr;
+    int n_pad = 0;
+    TmaMap ak16, av16;
+    float *qkv = nullptr;          // QKV projection rows [n_ubatch][n_qkv], where a kernel of its own norms, rotates and appends
+    float *ss_q4 = nullptr;        // Q4_0 steps: per-CTA sums of h^2 [8][num_sms]
     float2 *rope = nullptr;
     float2 *rope_t = nullptr;      // the same table position-minor [hd / 2][n_ctx] (prefill QKV epilogue)
     // workspaces
@@ -183,6 +195,7 @@ struct llm_ctx {
     float *dbg = nullptr; int dbg_rows = 0, dbg_ub = 0;
     bool stream_ok = false, use_stream = true;    // one-row GEMVs streamed through shared memory
     bool stream_q8 = false, use_q8 = true;        // ... reading the model's Q8_0 rows (when it has them)
+    bool q4_ok = false, use_q4 = true;            // steps of 1-8 rows read the model's Q4_0 rows (when it has them)
     int stream_pf_kb = 128;                       // L2 prefetch of the next streamed GEMV (KB per CTA)
     int stream_pf2_kb = 256;                      // ... of the gate/up GEMV by the QKV GEMV (KB per CTA)
     int stream_attn_kb = 136;                     // smem cap of the GEMVs beside decode attention (0 = none)
@@ -352,20 +365,61 @@ extern "C" int32_t llm_model_create(const llm_hparams *hp, const llm_weights *w,
 extern "C" void llm_model_free(llm_model *m) {
     if (!m) return;
     cudaFree(m->qbuf);
+    cudaFree(m->nbuf);
     cudaFree(m->wbuf);
     cudaFree(m->fbuf);
     delete m;
 }
 
-// Q8_0 weights: every matrix a projection multiplies by is encoded in place
-// (its fp16 copy, which the prefill GEMMs and the 2-8-row GEMVs read, becomes
-// f16(q * d)), and, where its rows suit the streamed GEMV (K % 256 == 0 for
-// every decode matrix), its Q8_0 rows are kept beside it for the one-row
-// decode GEMVs, which then stream about half the bytes.
+// Gains of the per-head query and key norms, widened to fp32.
+extern "C" int32_t llm_model_set_qk_norm(llm_model *m, const void *const *q_norm, const void *const *k_norm,
+                                         void *stream) {
+    llm_ctx *c = nullptr;
+    if (!m) return fail(c, LLM_ERR_INVALID, "model is NULL");
+    if (!q_norm && !k_norm) return fail(c, LLM_ERR_INVALID, "q_norm and k_norm are both NULL");
+    if (m->n_contexts) return fail(c, LLM_ERR_INVALID, "the model has live contexts");
+    for (int l = 0; l < m->L; ++l)
+        if ((q_norm && !q_norm[l]) || (k_norm && !k_norm[l]))
+            return fail(c, LLM_ERR_INVALID, "missing per-layer gain pointer");
+    float *buf = nullptr;
+    const int hd = m->hd;
+    if (cudaMalloc(&buf, (size_t)2 * m->L * hd * sizeof(float)) != cudaSuccess) {
+        cudaGetLastError();
+        return fail(c, LLM_ERR_ALLOC, "query and key gain allocation failed");
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
+    for (int l = 0; l < m->L && !e; ++l) {
+        float *g = buf + (size_t)2 * l * hd;
+        if (q_norm) e = launch_widen_bf16((const bf16 *)q_norm[l], g, hd, st);
+        if (!e && k_norm) e = launch_widen_bf16((const bf16 *)k_norm[l], g + hd, hd, st);
+    }
+    if (!e) e = cudaStreamSynchronize(st);
+    if (e) {
+        cudaFree(buf);
+        return fail(c, LLM_ERR_COMPUTE, "query and key gain copy", e);
+    }
+    cudaFree(m->nbuf);
+    m->nbuf = buf;
+    for (int l = 0; l < m->L; ++l) {
+        m->layers[l].q_norm = q_norm ? buf + (size_t)2 * l * hd : nullptr;
+        m->layers[l].k_norm = k_norm ? buf + (size_t)2 * l * hd + hd : nullptr;
+    }
+    return LLM_OK;
+}
+
+// Q8_0 or Q4_0 weights: every matrix a projection multiplies by is encoded in
+// place (its fp16 copy, which the prefill GEMMs read, becomes the values the
+// blocks stand for, rounded to fp16), and, where its rows suit the decode GEMV
+// (K % 256 == 0 for every decode matrix), its encoded rows are kept beside it:
+// Q8_0 rows for the one-row steps, Q4_0 rows for steps of 1-8 rows, which then
+// read 17/32 or 9/32 of the bytes.
 extern "C" int32_t llm_model_quantize(llm_model *m, int32_t wtype, void *stream) {
     llm_ctx *c = nullptr;
     if (!m) return fail(c, LLM_ERR_INVALID, "model is NULL");
-    if (wtype != LLM_WTYPE_Q8_0) return fail(c, LLM_ERR_INVALID, "unknown weight type");
+    if (wtype != LLM_WTYPE_Q8_0 && wtype != LLM_WTYPE_Q4_0) return fail(c, LLM_ERR_INVALID, "unknown weight type");
+    const bool q4 = wtype == LLM_WTYPE_Q4_0;
+    auto row_bytes = [&](int K) { return q4 ? q4_0_row_bytes(K) : q8_0_row_bytes(K); };
     if (m->wtype) return fail(c, LLM_ERR_INVALID, "the model is already quantised");
     if (m->n_contexts) return fail(c, LLM_ERR_INVALID, "the model has live contexts");
     const int d = m->d;
@@ -381,19 +435,19 @@ extern "C" int32_t llm_model_quantize(llm_model *m, int32_t wtype, void *stream)
     const bool rows = d % 256 == 0 && m->n_q % 256 == 0 && m->F_pad % 256 == 0;
     size_t total = 0;
     if (rows)
-        for (const Mat &mt : mats) total += align_up((size_t)mt.N * q8_0_row_bytes(mt.K), 256);
+        for (const Mat &mt : mats) total += align_up((size_t)mt.N * row_bytes(mt.K), 256);
     uint8_t *qb = nullptr;
     if (total && cudaMalloc(&qb, total) != cudaSuccess) {
         cudaGetLastError();
-        return fail(c, LLM_ERR_ALLOC, "Q8_0 allocation failed");
+        return fail(c, LLM_ERR_ALLOC, "allocation of the encoded rows failed");
     }
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
     size_t off = 0;
     for (const Mat &mt : mats) {
         uint8_t *q = qb ? qb + off : nullptr;
-        if (qb) off += align_up((size_t)mt.N * q8_0_row_bytes(mt.K), 256);
-        if (!e) e = launch_quantize_q8_0(mt.w, mt.N, mt.K, q, true, st);
+        if (qb) off += align_up((size_t)mt.N * row_bytes(mt.K), 256);
+        if (!e) e = q4 ? launch_quantize_q4_0(mt.w, mt.N, mt.K, q, true, st) : launch_quantize_q8_0(mt.w, mt.N, mt.K, q, true, st);
         *mt.q = q;
     }
     if (!e) e = cudaStreamSynchronize(st);
@@ -401,7 +455,7 @@ extern "C" int32_t llm_model_quantize(llm_model *m, int32_t wtype, void *stream)
         for (const Mat &mt : mats) *mt.q = nullptr;
         cudaFree(qb);
         m->wtype = -1;     // the fp16 copies may be partly rewritten
-        return fail(c, LLM_ERR_COMPUTE, "Q8_0 encoding failed; the model's weights are undefined", e);
+        return fail(c, LLM_ERR_COMPUTE, "weight encoding failed; the model's weights are undefined", e);
     }
     m->qbuf = qb;
     m->wtype = wtype;
@@ -412,7 +466,7 @@ extern "C" int32_t llm_model_quantize(llm_model *m, int32_t wtype, void *stream)
 static bool q8_plans_ok(const llm_ctx *c) {
     const llm_model *m = c->m;
     const int d = m->d, n = m->num_sms;
-    return m->qbuf && gemv_stream_ok(EPI_QKV, m->n_qkv, d, n, c->stream_attn_kb, true) &&
+    return m->qbuf && m->wtype == LLM_WTYPE_Q8_0 && gemv_stream_ok(EPI_QKV, m->n_qkv, d, n, c->stream_attn_kb, true) &&
            gemv_stream_ok(EPI_RESID, d, m->n_q, n, c->stream_attn_kb, true) &&
            gemv_stream_ok(EPI_SWIGLU, 2 * m->F_pad, d, n, 0, true) && gemv_stream_ok(EPI_RESID, d, m->F_pad, n, 0, true) &&
            gemv_stream_ok(EPI_STORE, m->V, d, n, 0, true);
@@ -427,7 +481,8 @@ static void ctx_release(llm_ctx *c) {
     void *dev[] = {c->kc, c->vc, c->rope, c->rope_t, c->h, c->h2, c->ss, c->ss2, c->qf, c->x, c->qb, c->o, c->u,
                    c->gemv_part, c->gemv_cnt, c->sk_ws, c->sk_flags, c->attn_part, c->attn_cnt, c->meta_dev, c->dec_dev,
                    c->logits, c->argmax_dev, c->gen_tokens, c->err_dev,
-                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b};
+                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->q4_part, c->q4_cnt,
+                   c->k16, c->v16};
     for (void *p : dev) if (p) cudaFree(p);
     for (int i = 0; i < 2; ++i) {
         if (c->meta_host[i]) cudaFreeHost(c->meta_host[i]);
@@ -453,6 +508,16 @@ static void make_attn_maps(llm_ctx *c) {
     const llm_model *m = c->m;
     const long long rows = (long long)c->n_seq_max * m->L * m->Hkv * c->n_ctx;
     const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
+    if (c->kv_q4) {
+        // the widened rows of one layer
+        const long long rows16 = (long long)c->n_seq_max * m->Hkv * c->n_pad;
+        c->attn_pair_ok = false;
+        c->attn_tc_ok = attn_prefill_tc_ok(m->hd, false) && rows16 < (1ll << 31) &&
+                        make_operand_map(&c->aq, c->qb, nub, m->n_q, 128) &&
+                        make_operand_map(&c->ak16, c->k16, (int)rows16, m->hd, 128) &&
+                        make_operand_map(&c->av16, c->v16, (int)rows16, m->hd, 128);
+        return;
+    }
     c->attn_tc_ok = !c->kv_fp8 && attn_prefill_tc_ok(m->hd, false) && rows < (1ll << 31) &&
                     make_operand_map(&c->aq, c->qb, nub, m->n_q, 128) &&
                     make_operand_map(&c->akc, c->kc, (int)rows, m->hd, 128) &&
@@ -572,6 +637,10 @@ extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, 
     c->attn_part_floats = ap;
     dmal((void **)&c->attn_part, ap * sizeof(float));
     dmal((void **)&c->attn_cnt, (size_t)8 * m->Hkv * sizeof(unsigned));
+    // Q4_0 steps and models with normed queries and keys store the QKV projection plainly
+    c->q4_ok = m->qbuf && m->wtype == LLM_WTYPE_Q4_0;
+    if (m->nbuf || c->q4_ok) dmal((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float));
+    if (c->q4_ok) dmal((void **)&c->ss_q4, (size_t)8 * m->num_sms * sizeof(float));
     dmal((void **)&c->dec_dev, DEC_INTS * sizeof(int));
     dmal((void **)&c->err_dev, sizeof(uint32_t));
     if (ok) {
@@ -642,6 +711,8 @@ struct UbDev {
     int n_tiles;
     const AttnTile *tiles128; // up to 128 rows each (tcgen05 prefill attention)
     int n_tiles128;
+    const KvSpan *spans;      // Q4_0 cache: the sequences' visible rows (prefill widens them)
+    int n_spans, max_span;
     int T, n_out;
     int out_base;             // first logits row of this ubatch
     int ub_index;
@@ -680,7 +751,14 @@ KvView kv_view(llm_ctx *c, int layer) {
     const llm_model *m = c->m;
     const size_t per_layer = (size_t)m->Hkv * c->n_ctx * m->hd;
     KvView v;
-    if (c->kv_fp8) {
+    if (c->kv_q4) {
+        v.k = v.v = nullptr;
+        uint8_t *k = reinterpret_cast<uint8_t *>(c->kc), *vv = reinterpret_cast<uint8_t *>(c->vc);
+        v.k4 = k + layer * per_layer / 2;
+        v.v4 = vv + layer * per_layer / 2;
+        v.kd = reinterpret_cast<f16 *>(k + c->kv_elems / 2) + layer * per_layer / 32;
+        v.vd = reinterpret_cast<f16 *>(vv + c->kv_elems / 2) + layer * per_layer / 32;
+    } else if (c->kv_fp8) {
         v.k = v.v = nullptr;
         v.k8 = reinterpret_cast<uint8_t *>(c->kc) + layer * per_layer;
         v.v8 = reinterpret_cast<uint8_t *>(c->vc) + layer * per_layer;
@@ -718,8 +796,87 @@ cudaError_t debug_copy(llm_ctx *c, const UbDev &u, int layer, const float *h, in
     return timed(c, K_COPY, [&] { return launch_copy_f32(h, dst, (size_t)n * d, lnch(c)); });
 }
 
+// Whether the QKV projection's rows are stored plainly for a kernel of its own
+// that norms, rotates and appends: normed queries and keys, and a Q4_0 cache,
+// need a whole head at once.
+bool plain_qkv(const llm_ctx *c) { return c->m->nbuf || c->kv_q4; }
+
+cudaError_t qk_norm(llm_ctx *c, const UbDev &u, int layer, bool prefill, const Launch &L) {
+    const llm_model *m = c->m;
+    QkNormArgs n;
+    n.qkv = c->qkv; n.ld = m->n_qkv;
+    n.q_gain = m->layers[layer].q_norm; n.k_gain = m->layers[layer].k_norm; n.eps = m->hp.rms_eps;
+    n.rope = c->rope; n.pos = u.pos; n.seq = u.seq;
+    n.q32 = prefill ? nullptr : c->qf; n.q16 = prefill ? c->qb : nullptr;
+    n.kv = kv_view(c, layer); n.T = u.T; n.H = m->H; n.err = c->err_dev;
+    return timed(c, K_QK_NORM, [&] { return launch_qk_norm_rope(n, L); });
+}
+
+cudaError_t attn_decode(llm_ctx *c, const UbDev &u, int layer) {
+    const llm_model *m = c->m;
+    AttnDecodeArgs at;
+    at.q = c->qf; at.kv = kv_view(c, layer); at.pos = u.pos; at.seq = u.seq; at.o = c->o; at.T = u.T; at.H = m->H;
+    at.err = c->err_dev; at.window = c->swa_window;
+    if (c->kv_q4) {
+        at.n_split = attn_q4_pick_split(u.T, m->H, m->Hkv, c->n_ctx);
+        at.part = c->q4_part; at.counters = c->q4_cnt;
+        return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode_q4(at, lnch_attn(c)); });
+    }
+    at.n_split = c->attn_split[u.T]; at.part = c->attn_part; at.counters = c->attn_cnt;
+    return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode(at, lnch_attn(c)); });
+}
+
+// Steps of 1-8 output rows of a Q4_0 model, out of its Q4_0 rows.  As in the
+// prefill, the kernel that last updates h also writes f16(h * gain) of the next
+// norm and sums of h^2; the GEMV that reads them scales its products.
+cudaError_t run_small_q4(llm_ctx *c, const UbDev &u) {
+    const llm_model *m = c->m;
+    const int d = m->d, T = u.T;
+    const Launch L = lnch_stream(c);
+    cudaError_t e = timed(c, K_EMBED, [&] {
+        return launch_embed(m->token_embd, u.tok, T, d, m->V, c->h, nullptr, c->err_dev, lnch(c), m->layers[0].attn_norm,
+                            c->x, c->ss32);
+    });
+    if (e) return e;
+    const float *ss = c->ss32;
+    int n_ss = d / 32;
+    auto gemv = [&](int kid, int epi, const uint8_t *W, int N, int K, const f16 *x, bool norm, auto &&set) {
+        GemvQ4Args a = {};
+        a.W = W; a.N = N; a.K = K; a.T = T; a.x = x; a.ldx = K; a.err = c->err_dev; a.eps = m->hp.rms_eps;
+        if (norm) { a.ss_in = ss; a.n_ss_in = n_ss; }
+        set(a);
+        return timed(c, kid, [&] { return launch_gemv_q4(epi, a, m->num_sms, L, L.pdl); });
+    };
+    auto resid = [&](GemvQ4Args &a, const float *gain_next) {
+        a.hres = c->h; a.ldh = d; a.gain_next = gain_next; a.xg_out = c->x; a.ldxg = d; a.ss_out = c->ss_q4;
+    };
+    for (int l = 0; l < m->L; ++l) {
+        const LayerW &w = m->layers[l];
+        if ((e = gemv(K_GEMV_QKV, EPI_STORE, w.q_qkv, m->n_qkv, d, c->x, true,
+                      [&](GemvQ4Args &a) { a.out = c->qkv; a.ldo = m->n_qkv; })))
+            return e;
+        if ((e = qk_norm(c, u, l, false, lnch_attn(c)))) return e;
+        if ((e = attn_decode(c, u, l))) return e;
+        if ((e = gemv(K_GEMV_O, EPI_RESID, w.q_o, d, m->n_q, c->o, false, [&](GemvQ4Args &a) { resid(a, w.ffn_norm); })))
+            return e;
+        ss = c->ss_q4; n_ss = gemv_q4_ctas(EPI_RESID, d, m->num_sms);
+        if ((e = gemv(K_GEMV_GATEUP, EPI_SWIGLU, w.q_gu, 2 * m->F_pad, d, c->x, true,
+                      [&](GemvQ4Args &a) { a.u_out = c->u; a.ldu = m->F_pad; })))
+            return e;
+        const float *next = l + 1 < m->L ? m->layers[l + 1].attn_norm : m->output_norm;
+        if ((e = gemv(K_GEMV_DOWN, EPI_RESID, w.q_down, d, m->F_pad, c->u, false, [&](GemvQ4Args &a) { resid(a, next); })))
+            return e;
+        if ((e = debug_copy(c, u, l, c->h, T))) return e;
+    }
+    return gemv(K_GEMV_LMHEAD, EPI_STORE, m->q_out, m->V, d, c->x, true, [&](GemvQ4Args &a) {
+        a.out = c->logits + (size_t)u.out_base * m->V;
+        a.ldo = m->V;
+    });
+}
+
 // Decode-sized ubatch (1..8 rows): GEMV kernels and split attention.
 cudaError_t run_small(llm_ctx *c, const UbDev &u) {
+    if (c->q4_ok && c->use_q4 && !u.out_rows && u.n_out == u.T) return run_small_q4(c, u);
     const llm_model *m = c->m;
     const int d = m->d, T = u.T;
     const Launch L = lnch(c);
@@ -758,7 +915,6 @@ cudaError_t run_small(llm_ctx *c, const UbDev &u) {
     int Tc = T;
     for (int l = 0; l < m->L; ++l) {
         const LayerW &w = m->layers[l];
-        const KvView kv = kv_view(c, l);
         GemvArgs a = gemv_base(c, w.wqkv, m->n_qkv, d, T, GV_QKV);
         wq(a, w.q_qkv);
         a.h = c->h; a.ldh = d; a.ss_part = c->ss; a.gain = w.attn_norm;
@@ -772,14 +928,16 @@ cudaError_t run_small(llm_ctx *c, const UbDev &u) {
             }
         }
         if (stream && l > 0) take_x(a);                                // h * attn_norm from the down GEMV
-        a.n_q = m->n_q; a.n_kv = m->n_kv; a.rope = c->rope; a.q_out = c->qf; a.kv = kv;
-        a.pos = u.pos; a.seq = u.seq;
-        if ((e = timed(c, K_GEMV_QKV, [&] { return gv(PRO_NORM, EPI_QKV, a, akb); }))) return e;
-        AttnDecodeArgs at;
-        at.q = c->qf; at.kv = kv; at.pos = u.pos; at.seq = u.seq; at.o = c->o; at.T = T; at.H = m->H;
-        at.n_split = c->attn_split[T]; at.part = c->attn_part; at.counters = c->attn_cnt; at.err = c->err_dev;
-        at.window = c->swa_window;
-        if ((e = timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode(at, lnch_attn(c)); }))) return e;
+        if (plain_qkv(c)) {
+            a.out = c->qkv; a.ldo = m->n_qkv;
+            if ((e = timed(c, K_GEMV_QKV, [&] { return gv(PRO_NORM, EPI_STORE, a, akb); }))) return e;
+            if ((e = qk_norm(c, u, l, false, lnch_attn(c)))) return e;
+        } else {
+            a.n_q = m->n_q; a.n_kv = m->n_kv; a.rope = c->rope; a.q_out = c->qf; a.kv = kv_view(c, l);
+            a.pos = u.pos; a.seq = u.seq;
+            if ((e = timed(c, K_GEMV_QKV, [&] { return gv(PRO_NORM, EPI_QKV, a, akb); }))) return e;
+        }
+        if ((e = attn_decode(c, u, l))) return e;
         a = gemv_base(c, w.wo, d, m->n_q, T, GV_O);
         wq(a, w.q_o);
         a.x = c->o; a.ldx = m->n_q; a.hres = c->h; a.ldh_res = d; a.ss_out = c->ss;
@@ -868,6 +1026,32 @@ GemmArgs gemm_base(llm_ctx *c, const f16 *A, const f16 *W, int M, int N, int K) 
     return g;
 }
 
+// Prefill attention of a Q4_0 cache: the layer's visible rows widened to fp16,
+// then the fp16 attention on them.  It starts after the widening has ended, not
+// beside it: every key it reads comes from there.
+cudaError_t attn_prefill_q4(llm_ctx *c, const UbDev &u, const KvView &kv) {
+    const llm_model *m = c->m;
+    const Launch L{c->stream, false, &c->launches};
+    cudaError_t e = timed(c, K_KV_WIDEN, [&] {
+        return launch_kv_widen_q4(kv, u.spans, u.n_spans, u.max_span, c->k16, c->v16, c->n_pad, lnch_prefill(c));
+    });
+    if (e) return e;
+    if (c->attn_tc_ok && c->attn_mode > 0) {
+        AttnPrefillTcArgs at;
+        at.tiles = u.tiles128; at.n_tiles = u.n_tiles128; at.H = m->H; at.Hkv = m->Hkv; at.head_dim = m->hd;
+        at.n_layer = 1; at.layer = 0; at.n_ctx = c->n_pad; at.n_seq = c->n_seq_max;
+        at.o = c->o; at.ldo = m->n_q; at.err = c->err_dev; at.window = c->swa_window;
+        return timed(c, K_ATTN_PREFILL, [&] { return launch_attn_prefill_tc(at, c->aq, c->ak16, c->av16, L); });
+    }
+    AttnPrefillArgs at;
+    at.q = c->qb;
+    at.kv.k = c->k16; at.kv.v = c->v16;
+    at.kv.seq_stride = (long long)m->Hkv * c->n_pad * m->hd;
+    at.kv.n_ctx = c->n_pad; at.kv.n_seq = c->n_seq_max; at.kv.head_dim = m->hd; at.kv.n_kv_head = m->Hkv;
+    at.tiles = u.tiles; at.n_tiles = u.n_tiles; at.o = c->o; at.H = m->H; at.err = c->err_dev; at.window = c->swa_window;
+    return timed(c, K_ATTN_PREFILL, [&] { return launch_attn_prefill(at, L); });
+}
+
 // Prefill-sized ubatch: tensor-core GEMMs and tiled causal attention.  Each
 // RMSNorm is fused across two GEMMs: the kernel that last updates h (the
 // embedding, or a residual GEMM's epilogue) also writes f16(h * gain) as the
@@ -895,10 +1079,18 @@ cudaError_t run_large(llm_ctx *c, const UbDev &u) {
         const KvView kv = kv_view(c, l);
         GemmArgs g = gemm_base(c, c->x, w.wqkv, T, m->n_qkv, d);
         norm_in(g);
-        g.n_q = m->n_q; g.n_kv = m->n_kv; g.rope = c->rope; g.q_out = c->qb; g.kv = kv; g.pos = u.pos; g.seq = u.seq;
-        g.rope_t = c->rope_t; g.rope_n = c->n_ctx;
-        if ((e = timed(c, K_GEMM_QKV, [&] { return gemm(c, EPI_QKV, g, c->ax, w.mqkv); }))) return e;
-        if (c->attn_tc_ok && c->attn_mode > 0) {
+        if (plain_qkv(c)) {
+            g.C = c->qkv; g.ldc = m->n_qkv;
+            if ((e = timed(c, K_GEMM_QKV, [&] { return gemm(c, EPI_STORE, g, c->ax, w.mqkv); }))) return e;
+            if ((e = qk_norm(c, u, l, true, L))) return e;
+        } else {
+            g.n_q = m->n_q; g.n_kv = m->n_kv; g.rope = c->rope; g.q_out = c->qb; g.kv = kv; g.pos = u.pos; g.seq = u.seq;
+            g.rope_t = c->rope_t; g.rope_n = c->n_ctx;
+            if ((e = timed(c, K_GEMM_QKV, [&] { return gemm(c, EPI_QKV, g, c->ax, w.mqkv); }))) return e;
+        }
+        if (c->kv_q4) {
+            if ((e = attn_prefill_q4(c, u, kv))) return e;
+        } else if (c->attn_tc_ok && c->attn_mode > 0) {
             AttnPrefillTcArgs at;
             at.tiles = u.tiles128; at.n_tiles = u.n_tiles128; at.H = m->H; at.Hkv = m->Hkv; at.head_dim = m->hd;
             at.n_layer = m->L; at.layer = l; at.n_ctx = c->n_ctx; at.n_seq = c->n_seq_max;
@@ -1029,6 +1221,22 @@ cudaError_t launch_decode_graph(llm_ctx *c, int T) {
     return cudaGraphLaunch(c->graph[T], c->stream);
 }
 
+// The sequences of ubatch rows [s0, s1) with the cells their rows see: from the
+// first row's window on, up to the last row.
+int build_spans(const std::vector<int32_t> &seq, const std::vector<int32_t> &pos, int s0, int s1, int window,
+                std::vector<KvSpan> &out) {
+    out.clear();
+    for (int i = s0; i < s1; ++i) {
+        size_t k = 0;
+        while (k < out.size() && out[k].seq != seq[i]) ++k;
+        const int lo = window > 0 && pos[i] + 1 > window ? pos[i] + 1 - window : 0;
+        if (k == out.size()) out.push_back(KvSpan{seq[i], lo, pos[i] + 1});
+        out[k].lo = std::min(out[k].lo, lo);
+        out[k].hi = std::max(out[k].hi, pos[i] + 1);
+    }
+    return (int)out.size();
+}
+
 // The attention tiles of ubatch rows [s0, s1): runs of at most max_rows rows
 // of one sequence (consecutive positions); kv_ready is the sequence's first
 // position in the ubatch, below which its keys were cached before it.
@@ -1081,6 +1289,9 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
         const int nub = (int)p.ub_start.size() - 1;
         std::vector<size_t> off_tok(nub), off_rows(nub), off_tiles(nub), off_tiles128(nub);
         std::vector<int> n_tiles(nub), n_tiles128(nub), n_out(nub);
+        // Q4_0 cache: the visible cells of each ubatch's sequences
+        std::vector<std::vector<KvSpan>> spans(c->kv_q4 ? nub : 0);
+        std::vector<size_t> off_spans(nub);
         constexpr size_t TILE_INTS = sizeof(AttnTile) / sizeof(int);
         size_t ints = 3 * (size_t)p.n;
         for (int k = 0; k < nub; ++k) {
@@ -1094,6 +1305,10 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             ints = align_up(ints, 4);
             off_tiles[k] = ints; ints += (size_t)n_tiles[k] * TILE_INTS;
             off_tiles128[k] = ints; ints += (size_t)n_tiles128[k] * TILE_INTS;
+            if (c->kv_q4) {
+                off_spans[k] = ints;
+                ints += build_spans(p.seq, p.pos, s0, s1, c->swa_window, spans[k]) * (sizeof(KvSpan) / sizeof(int));
+            }
         }
         if (c->meta_cap < ints) {
             CK(cudaStreamSynchronize(c->stream));
@@ -1123,6 +1338,7 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             for (int i = s0; i < s1; ++i) if (p.out[i]) rows[r++] = i - s0;
             build_tiles(p.seq, p.pos, s0, s1, 64, reinterpret_cast<AttnTile *>(hs + off_tiles[k]));
             build_tiles(p.seq, p.pos, s0, s1, 128, reinterpret_cast<AttnTile *>(hs + off_tiles128[k]));
+            if (c->kv_q4) memcpy(hs + off_spans[k], spans[k].data(), spans[k].size() * sizeof(KvSpan));
         }
         CK(cudaMemcpyAsync(c->meta_dev, hs, ints * sizeof(int), cudaMemcpyHostToDevice, c->stream));
         CK(cudaEventRecord(c->meta_ev[slot], c->stream));
@@ -1140,6 +1356,12 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             u.n_tiles = n_tiles[k];
             u.tiles128 = reinterpret_cast<const AttnTile *>(c->meta_dev + off_tiles128[k]);
             u.n_tiles128 = n_tiles128[k];
+            u.spans = nullptr; u.n_spans = u.max_span = 0;
+            if (c->kv_q4) {
+                u.spans = reinterpret_cast<const KvSpan *>(c->meta_dev + off_spans[k]);
+                u.n_spans = (int)spans[k].size();
+                for (const KvSpan &sp : spans[k]) u.max_span = std::max(u.max_span, sp.hi - sp.lo);
+            }
             u.out_base = out_base;
             u.ub_index = k;
             out_base += n_out[k];
@@ -1323,7 +1545,9 @@ extern "C" int32_t llm_seq_shift(llm_ctx *c, int32_t seq_id, int32_t p0, int32_t
     if (p0 < 0 || n_discard < 1 || p0 + n_discard > end)
         return fail(c, LLM_ERR_INVALID, "shift range outside the sequence's positions");
     const llm_model *m = c->m;
-    CK(launch_kv_shift(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, c->rope, Launch{c->stream, false, &c->launches}));
+    const Launch L{c->stream, false, &c->launches};
+    CK(c->kv_q4 ? launch_kv_shift_q4(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, c->rope, L)
+                : launch_kv_shift(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, c->rope, L));
     c->seq_next[seq_id] = end - n_discard;
     return LLM_OK;
 }
@@ -1355,6 +1579,46 @@ extern "C" int32_t llm_debug_hidden(llm_ctx *c, float *dst, int32_t max_rows, in
     if (!c) return LLM_ERR_INVALID;
     if (dst && (max_rows < 1 || max_ubatches < 1)) return fail(c, LLM_ERR_INVALID, "invalid debug buffer");
     c->dbg = dst; c->dbg_rows = max_rows; c->dbg_ub = max_ubatches;
+    return LLM_OK;
+}
+
+// Swap the (empty) cache for one of the other element type.  Everything the new
+// one needs is allocated first: a failure changes nothing.
+static int32_t set_kv_q4(llm_ctx *c, bool want) {
+    const llm_model *m = c->m;
+    const size_t bytes = want ? c->kv_elems / 2 + c->kv_elems / 16 : c->kv_elems * sizeof(f16);
+    const int n_pad = (c->n_ctx + 127) / 128 * 128, nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
+    const size_t plane = (size_t)c->n_seq_max * m->Hkv * n_pad * m->hd * sizeof(f16);
+    size_t part = 0, cnt = 0;
+    for (int T = 1; T <= 8; ++T) {
+        part = std::max(part, attn_q4_part_floats(T, m->H, m->hd, attn_q4_pick_split(T, m->H, m->Hkv, c->n_ctx)));
+        cnt = std::max(cnt, (size_t)T * m->Hkv * attn_q4_chunks(m->H, m->Hkv));
+    }
+    void *p[7] = {nullptr};
+    const size_t need[7] = {bytes, bytes, plane, plane, part * sizeof(float), cnt * sizeof(unsigned),
+                            c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
+    const int n = want ? 7 : 2;
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) ok = !need[i] || cudaMalloc(&p[i], need[i]) == cudaSuccess;
+    if (ok) {
+        cudaStreamSynchronize(c->stream);
+        ok = cudaMemsetAsync(p[0], 0, bytes, c->stream) == cudaSuccess && cudaMemsetAsync(p[1], 0, bytes, c->stream) == cudaSuccess &&
+             (!want || cudaMemsetAsync(p[5], 0, need[5], c->stream) == cudaSuccess);
+    }
+    if (!ok) {
+        cudaGetLastError();
+        for (void *q : p) cudaFree(q);
+        return fail(c, LLM_ERR_ALLOC, "KV cache reallocation failed");
+    }
+    cudaFree(c->kc); cudaFree(c->vc);
+    cudaFree(c->k16); cudaFree(c->v16); cudaFree(c->q4_part); cudaFree(c->q4_cnt);
+    c->kc = (f16 *)p[0]; c->vc = (f16 *)p[1];
+    c->k16 = (f16 *)p[2]; c->v16 = (f16 *)p[3]; c->n_pad = want ? n_pad : 0;
+    c->q4_part = (float *)p[4]; c->q4_cnt = (unsigned *)p[5];
+    if (p[6]) c->qkv = (float *)p[6];
+    c->kv_q4 = want;
+    make_attn_maps(c);
+    drop_graphs(c);
     return LLM_OK;
 }
 
@@ -1399,6 +1663,7 @@ extern "C" int32_t llm_set_option(llm_ctx *c, const char *key, int32_t value) {
             if (c->seq_next[s] != 0) return fail(c, LLM_ERR_INVALID, "kv_fp8 needs an empty cache (llm_seq_clear)");
         const bool want = value != 0;
         if (want == c->kv_fp8) return LLM_OK;
+        if (c->kv_q4) return fail(c, LLM_ERR_INVALID, "the cache is Q4_0 (kv_q4)");
         const size_t bytes = c->kv_elems * (want ? 1 : sizeof(f16));
         cudaStreamSynchronize(c->stream);
         cudaFree(c->kc); cudaFree(c->vc);
@@ -1411,6 +1676,19 @@ extern "C" int32_t llm_set_option(llm_ctx *c, const char *key, int32_t value) {
         }
         c->kv_fp8 = want;
         make_attn_maps(c);
+        drop_graphs(c);
+        return LLM_OK;
+    }
+    if (!strcmp(key, "kv_q4")) {
+        if (value < 0 || value > 1) return fail(c, LLM_ERR_INVALID, "kv_q4 must be 0 or 1");
+        for (int s = 0; s < c->n_seq_max; ++s)
+            if (c->seq_next[s] != 0) return fail(c, LLM_ERR_INVALID, "kv_q4 needs an empty cache (llm_seq_clear)");
+        if ((value != 0) == c->kv_q4) return LLM_OK;
+        if (c->kv_fp8) return fail(c, LLM_ERR_INVALID, "the cache is FP8 (kv_fp8)");
+        return set_kv_q4(c, value != 0);
+    }
+    if (!strcmp(key, "gemv_q4")) {
+        c->use_q4 = value != 0;
         drop_graphs(c);
         return LLM_OK;
     }

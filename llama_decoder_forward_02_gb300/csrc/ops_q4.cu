@@ -95,15 +95,16 @@ extern "C" int32_t llm_op_gemv_q4_0(const void *Wq, const void *x, float *y, int
     const char *who = "llm_op_gemv_q4_0";
     if (!Wq || !x || !y) return refuse(who, "a pointer is NULL");
     if (T < 1 || T > 8) return refuse(who, "T must be 1..8");
-    if (N < 1 || K < 256 || K % 256) return refuse(who, "N must be positive and K a positive multiple of 256");
+    if (N < 1 || K < 256 || K % 256 || K > (1 << 24))
+        return refuse(who, "N must be positive and K a positive multiple of 256, at most 2^24");
     if (ldx < K || ldx % 8 || ldy < N) return refuse(who, "ldx must be a multiple of 8 and at least K, ldy at least N");
     if (!aligned(Wq, 16) || !aligned(x, 16) || !aligned(y, 4))
         return refuse(who, "Wq and x must be 16-byte aligned, y 4-byte");
     if (cudaError_t e = init_kernel_attributes()) return launched(who, e);
-    GemvQ4Args a;
+    GemvQ4Args a = {};
     a.W = (const uint8_t *)Wq; a.N = N; a.K = K; a.T = T;
-    a.x = (const f16 *)x; a.ldx = ldx; a.out = y; a.ldo = ldy; a.err = nullptr;
-    return launched(who, launch_gemv_q4(a, current_sms(), overlapped(stream), false));
+    a.x = (const f16 *)x; a.ldx = ldx; a.out = y; a.ldo = ldy;
+    return launched(who, launch_gemv_q4(EPI_STORE, a, current_sms(), overlapped(stream), false));
 }
 
 extern "C" int64_t llm_op_kv_q4_0_bytes(int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq) {

@@ -181,7 +181,77 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const QkNormArgs 
     if (out_of_range) raise_error(a.err, ERRF_F16_RANGE);
 }
 
+// Context shift of a sequence's Q4_0 cache (kv_shift_kernel's of the other
+// caches, with its order of reads and writes): rows [p0 + n, end) move down by
+// n, a key's values rotated by -n and encoded again, a value row copied.  One
+// CTA per (layer, kv head) walks the rows upward, all its lanes' rows read
+// before any is written.
+constexpr int SHIFT_THREADS = 512;
+
+template <int HD>
+__global__ void __launch_bounds__(SHIFT_THREADS) kv_shift_q4_kernel(KvView kv, int p0, int n, int end, const float2 *rope) {
+    constexpr int L = HD / 4, ROWS = SHIFT_THREADS / L, NB = HD / 32;
+    const size_t base = (size_t)blockIdx.x * kv.n_ctx * HD;      // (layer, head) block of this sequence, in elements
+    const int lane = threadIdx.x & 31, sub = threadIdx.x % L, r = threadIdx.x / L;
+    const int blk = sub >> 3, word = ((sub & 7) >> 1) * NB + blk, half = 8 * (sub & 1);
+    uint32_t *kw = reinterpret_cast<uint32_t *>(kv.k4 + base / 2), *vw = reinterpret_cast<uint32_t *>(kv.v4 + base / 2);
+    f16 *kd = kv.kd + base / 32, *vd = kv.vd + base / 32;
+    const float4 c = *reinterpret_cast<const float4 *>(rope + (size_t)n * (HD / 2) + 2 * sub);
+    const float4 back = make_float4(c.x, -c.y, c.z, -c.w);
+    const float gain[4] = {1.f, 1.f, 1.f, 1.f};
+    for (int r0 = p0 + n; r0 < end; r0 += ROWS) {
+        const bool in = r0 + r < end;
+        const size_t src = in ? r0 + r : r0, dst = src - n;
+        const uint32_t w = kw[src * (HD / 8) + word] >> half, wv = vw[src * (HD / 8) + word];
+        const float d = hf(kd[src * NB + blk]);
+        const f16 dv = vd[src * NB + blk];
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = (float)((int)((w >> q4::shift_of(e)) & 15u) - 8) * d;     // exact
+        float u[4], nd;
+        int code[4];
+        transform<HD, float>(x, gain, back, false, true, 0.f, u);
+        const bool near = encode<float>(u, lane, nd, code);
+        if (__any_sync(0xffffffffu, near)) {
+            double u64[4], d64;
+            transform<HD, double>(x, gain, back, false, true, 0.f, u64);
+            encode<double>(u64, lane, d64, code);
+            nd = (float)d64;
+        }
+        uint32_t out = (uint32_t)code[0] | (uint32_t)code[1] << 16 | (uint32_t)code[2] << 4 | (uint32_t)code[3] << 20;
+        out |= __shfl_xor_sync(0xffffffffu, out << 8, 1);
+        __syncthreads();
+        if (in) {
+            if (half == 0) {
+                kw[dst * (HD / 8) + word] = out;
+                vw[dst * (HD / 8) + word] = wv;
+            }
+            if ((sub & 7) == 0) {
+                kd[dst * NB + blk] = f2h(nd);
+                vd[dst * NB + blk] = dv;
+            }
+        }
+        __syncthreads();
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_kv_shift_q4(const KvView &kv0, int n_layer, int seq, int p0, int n, int end, const float2 *rope,
+                               const Launch &l) {
+    const int hd = kv0.head_dim;
+    if (n < 1 || p0 < 0 || p0 + n > end || end > kv0.n_ctx || seq < 0 || seq >= kv0.n_seq || !kv0.k4)
+        return cudaErrorInvalidValue;
+    if (p0 + n == end) return cudaSuccess;                  // nothing after the dropped rows
+    KvView kv = kv0;
+    const size_t so = (size_t)seq * kv0.seq_stride;
+    kv.k4 += so / 2; kv.v4 += so / 2; kv.kd += so / 32; kv.vd += so / 32;
+    const dim3 grid(n_layer * kv0.n_kv_head), block(SHIFT_THREADS);
+    if (hd == 32) return launch_kernel(kv_shift_q4_kernel<32>, grid, block, 0, l, kv, p0, n, end, rope);
+    if (hd == 64) return launch_kernel(kv_shift_q4_kernel<64>, grid, block, 0, l, kv, p0, n, end, rope);
+    if (hd == 128) return launch_kernel(kv_shift_q4_kernel<128>, grid, block, 0, l, kv, p0, n, end, rope);
+    return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l) {
     const int hd = a.kv.head_dim, heads = a.H + 2 * a.kv.n_kv_head;

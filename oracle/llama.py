@@ -261,9 +261,9 @@ def silu(x):
     return x / (1.0 + np.exp(-x))
 
 
-def swiglu_mlp(x, w_gate, w_up, w_down):
+def swiglu_mlp(x, w_gate, w_up, w_down, operands=None):
     """[EN] MLP: Down(SiLU(Gate x) * Up x), weights [out][in]."""
-    return (silu(x @ w_gate.T) * (x @ w_up.T)) @ w_down.T
+    return round_to(silu(x @ w_gate.T) * (x @ w_up.T), operands) @ w_down.T
 
 
 # --------------------------------------------------------------------------
@@ -285,9 +285,12 @@ class Model:
         return bf16_to_float(self.w[name], self.dtype)
 
     def layer(self, i):
-        return {t: self.get(f"blk.{i}.{t}") for t in (
+        lw = {t: self.get(f"blk.{i}.{t}") for t in (
             "attn_norm", "attn_q", "attn_k", "attn_v", "attn_output",
             "ffn_norm", "ffn_gate", "ffn_up", "ffn_down")}
+        # per-head query and key gains, where the model has them
+        lw.update({t: self.get(f"blk.{i}.{t}") for t in ("attn_q_norm", "attn_k_norm") if f"blk.{i}.{t}" in self.w})
+        return lw
 
     def embed_rows(self, tokens):
         """[LC] Step 11: row ``token[i]`` of the embedding table becomes input
@@ -305,16 +308,25 @@ class Model:
         embedding table is a lookup, kept as it is, unless it is also the
         output projection (tied), when the lookup reads the quantised table
         too.  Norm gains stay as they are."""
+        return self._quantized(lambda v: dequantize_q8_0(*quantize_q8_0(v), np.float64))
+
+    def quantized_q4_0(self) -> "Model":
+        """The same model with the same matrices stored as Q4_0 (quantize_q4_0)
+        and used as the weights they stand for.  A row's last, shorter block is
+        filled up with zeros, which do not change its largest element."""
+        def values(v):
+            k = v.shape[1]
+            v = np.pad(v, ((0, 0), (0, -k % Q4_0_BLOCK)))
+            return dequantize_q4_0(*quantize_q4_0(v))[:, :k]
+
+        return self._quantized(values)
+
+    def _quantized(self, values):
         w = dict(self.w)
-
-        def q8(name):
-            q, d = quantize_q8_0(bf16_to_float(self.w[name], np.float32))
-            w[name] = dequantize_q8_0(q, d, np.float64)
-
-        for i in range(self.hp.n_layer):
-            for t in self.MATRICES:
-                q8(f"blk.{i}.{t}")
-        q8("token_embd" if self.hp.tied_output or "output" not in self.w else "output")
+        names = [f"blk.{i}.{t}" for i in range(self.hp.n_layer) for t in self.MATRICES]
+        names.append("token_embd" if self.hp.tied_output or "output" not in self.w else "output")
+        for name in names:
+            w[name] = values(bf16_to_float(self.w[name], np.float32))
         return Model(self.hp, w, self.dtype)
 
 
@@ -322,10 +334,13 @@ class KVCache:
     """Per-sequence, per-layer cache of K and V by position ([EN] ``Causal``:
     per-layer keys/values plus position and sequence metadata per cell; [LC]
     "KV-cache and the Prefill / Decode stages").  Entries stay in ``dtype``
-    unless ``store`` asks to round them as a lower-precision cache would."""
+    unless ``store`` asks to round them as a lower-precision cache would.
+    ``operands`` "fp16" also rounds what the projections read (norm_operand,
+    attention outputs, gated products) to fp16: a cache whose store picks codes
+    decides them on those values."""
 
-    def __init__(self, hp: Hparams, n_ctx: int, n_seq_max: int, dtype, store=None, window=0):
-        self.hp, self.n_ctx, self.n_seq_max, self.store = hp, n_ctx, n_seq_max, store
+    def __init__(self, hp: Hparams, n_ctx: int, n_seq_max: int, dtype, store=None, window=0, operands=None):
+        self.hp, self.n_ctx, self.n_seq_max, self.store, self.operands = hp, n_ctx, n_seq_max, store, operands
         self.window = window          # sliding-window size, 0 = full causal
         shape = (n_seq_max, hp.n_layer, n_ctx, hp.n_head_kv, hp.head_dim)
         self.k = np.zeros(shape, dtype)
@@ -360,6 +375,27 @@ class KVCache:
         self.filled[s, end - n:end] = False
 
 
+def norm_operand(h, g, eps, operands):
+    """RMSNorm rows as a projection's operand.  With operands "fp16" the product
+    h * g is stored as fp16 and the row factor applied to it afterwards, as an
+    implementation with 16-bit operands and 32-bit sums does."""
+    if operands is None:
+        return rms_norm(h, g, eps)
+    return round_to(h * g, operands) / np.sqrt(np.mean(h * h, axis=-1, keepdims=True) + eps)
+
+
+def head_norms(hp, lw, q, k):
+    """Query and key heads [rows][heads][head_dim] normed per head (RMSNorm over
+    head_dim, the gain shared by the heads) where the layer has gains for them,
+    as model families with normed attention apply it between the projection
+    and the rotation."""
+    if "attn_q_norm" in lw:
+        q = rms_norm(q, lw["attn_q_norm"], hp.rms_eps)
+    if "attn_k_norm" in lw:
+        k = rms_norm(k, lw["attn_k_norm"], hp.rms_eps)
+    return q, k
+
+
 def layer_forward(hp, lw, h, pos, seq, cache, layer, out_rows=None):
     """One decoder layer on the rows of a ubatch ([EN] sequence diagram of
     ``layer.Forward``): RMSNorm -> Q,K,V -> RoPE(Q,K) -> store K,V for the new
@@ -371,10 +407,11 @@ def layer_forward(hp, lw, h, pos, seq, cache, layer, out_rows=None):
     K,V for new positions" precedes "Build attention mask")."""
     t_rows = h.shape[0]
     H, Hkv, hd = hp.n_head, hp.n_head_kv, hp.head_dim
-    x = rms_norm(h, lw["attn_norm"], hp.rms_eps)
+    x = norm_operand(h, lw["attn_norm"], hp.rms_eps, cache.operands)
     q = (x @ lw["attn_q"].T).reshape(t_rows, H, hd)
     k = (x @ lw["attn_k"].T).reshape(t_rows, Hkv, hd)
     v = (x @ lw["attn_v"].T).reshape(t_rows, Hkv, hd)
+    q, k = head_norms(hp, lw, q, k)
     q = rope(q, pos, hp.rope_theta)
     k = rope(k, pos, hp.rope_theta)
     for r in range(t_rows):
@@ -387,13 +424,13 @@ def layer_forward(hp, lw, h, pos, seq, cache, layer, out_rows=None):
         cells = np.nonzero(cache.filled[s])[0]
         o[rows] = attention_one_seq(q[rows], cache.k[s, layer, cells], cache.v[s, layer, cells],
                                     pos[rows], cells, Hkv, window=cache.window)
-    h = h + o.reshape(t_rows, H * hd) @ lw["attn_output"].T
+    h = h + round_to(o, cache.operands).reshape(t_rows, H * hd) @ lw["attn_output"].T
     if out_rows is not None:
         # [EN] Model.Forward: in the last layer the hidden state keeps only the
         # rows batch.Outputs selects, before the MLP.
         h = h[out_rows]
-    x = rms_norm(h, lw["ffn_norm"], hp.rms_eps)
-    return h + swiglu_mlp(x, lw["ffn_gate"], lw["ffn_up"], lw["ffn_down"])
+    x = norm_operand(h, lw["ffn_norm"], hp.rms_eps, cache.operands)
+    return h + swiglu_mlp(x, lw["ffn_gate"], lw["ffn_up"], lw["ffn_down"], cache.operands)
 
 
 def layer_rows(hp, lw, h, pos, rows):
@@ -409,9 +446,10 @@ def layer_rows(hp, lw, h, pos, rows):
     rows = np.asarray(rows, dtype=np.int64)
     pos = np.asarray(pos, dtype=np.int64)
     x = rms_norm(h, lw["attn_norm"], hp.rms_eps)
-    k = rope((x @ lw["attn_k"].T).reshape(-1, Hkv, hd), pos, hp.rope_theta)
+    q, k = head_norms(hp, lw, (x[rows] @ lw["attn_q"].T).reshape(-1, H, hd), (x @ lw["attn_k"].T).reshape(-1, Hkv, hd))
+    k = rope(k, pos, hp.rope_theta)
     v = (x @ lw["attn_v"].T).reshape(-1, Hkv, hd)
-    q = rope((x[rows] @ lw["attn_q"].T).reshape(-1, H, hd), pos[rows], hp.rope_theta)
+    q = rope(q, pos[rows], hp.rope_theta)
     o = np.empty_like(q)
     for i, r in enumerate(rows):
         n = int(np.count_nonzero(pos <= pos[r]))      # keys with position <= the row's (cache order)

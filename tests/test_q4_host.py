@@ -138,3 +138,30 @@ def test_prefill_rows_refused():
         assert lib.llm_op_attn_prefill_q4_0(P, P, P, ph, sh, P, len(pos), 8, 2, 64, 64, 2, 0, P, 1 << 40, None,
                                             None) == BAD
         assert reason in why(), (pos, seq, why())
+
+
+def test_oracle_head_norms_and_q4_model():
+    """Normed heads have unit RMS before the gain, and the Q4_0 model's weights lie on their own grid."""
+    rng = np.random.default_rng(2)
+    hp = O.Hparams(64, 64, 1, 4, 2, 32, 40, 0.0, 1e4, False)
+    q, k = rng.standard_normal((3, 4, 32)) * 5, rng.standard_normal((3, 2, 32))
+    nq, nk = O.head_norms(hp, {"attn_q_norm": np.full(32, 2.0)}, q, k)
+    assert np.allclose((nq * nq).mean(-1), 4.0) and np.array_equal(nk, k)
+    w = {n: rng.standard_normal(s) for n, s in (
+        ("token_embd", (64, 64)), ("output_norm", 64), ("output", (64, 64)), ("blk.0.attn_norm", 64), ("blk.0.attn_q", (128, 64)),
+        ("blk.0.attn_k", (64, 64)), ("blk.0.attn_v", (64, 64)), ("blk.0.attn_output", (64, 128)), ("blk.0.ffn_norm", 64),
+        ("blk.0.ffn_gate", (40, 64)), ("blk.0.ffn_up", (40, 64)), ("blk.0.ffn_down", (64, 40)))}
+    m = O.Model(hp, w)
+    for name in ("blk.0.attn_q", "blk.0.ffn_down", "output"):
+        v = m.quantized_q4_0().w[name]
+        full = np.pad(v, ((0, 0), (0, -v.shape[1] % 32)))
+        assert v.shape == w[name].shape and not np.array_equal(v, w[name])
+        # at most 16 levels a block, evenly spaced
+        for block in full.reshape(-1, 32):
+            levels = np.unique(block[block != 0])
+            assert levels.size <= 15
+    assert np.array_equal(m.quantized_q4_0().w["token_embd"], w["token_embd"])
+    # rounding of the operands changes what a projection reads by half an fp16 step
+    h = rng.standard_normal((2, 64))
+    a, b = (O.norm_operand(h, w["blk.0.attn_norm"], 1e-5, o) for o in (None, "fp16"))
+    assert 0 < np.abs(a - b).max() <= np.abs(a).max() * 2.0 ** -11
