@@ -83,16 +83,27 @@ def layer_matrix_params(s):
     return (q + 2 * kv) * s.n_embd + s.n_embd * q + 3 * s.n_ff * s.n_embd
 
 
-# bytes a matrix element takes in the decode GEMVs: fp16, or Q8_0 (32 one-byte
-# codes and one fp16 scale a block)
-WEIGHT_BYTES = {"f16": 2.0, "q8_0": 34 / 32}
+# bytes a matrix element takes in the decode GEMVs: fp16, Q8_0 (32 one-byte
+# codes and one fp16 scale a block) or Q4_0 (32 four-bit codes and the scale)
+WEIGHT_BYTES = {"f16": 2.0, "q8_0": 34 / 32, "q4_0": 18 / 32}
+WEIGHT_NOTES = {"f16": "N(0,0.02) rounded to bf16, fp16 inside",
+                "q8_0": "N(0,0.02) rounded to bf16, re-encoded as Q8_0 blocks (32 one-byte codes, fp16 scale); "
+                        "one-row GEMVs stream the Q8_0 rows, prefill reads f16(q*d)",
+                "q4_0": "N(0,0.02) rounded to bf16, re-encoded as Q4_0 blocks (32 four-bit codes, fp16 scale); "
+                        "decode GEMVs read the Q4_0 rows, prefill reads f16(d*(c-8))"}
+# bytes an element of the KV cache takes, by context option
+KV_BYTES = {"kv_fp8": 1.0, "kv_q4": 18 / 32}
 
 
-def decode_bytes(s, positions, wb=2.0):
+def kv_bytes(options):
+    return next((KV_BYTES[o.partition("=")[0]] for o in options if o in ("kv_fp8=1", "kv_q4=1")), 2.0)
+
+
+def decode_bytes(s, positions, wb=2.0, kvb=2.0):
     """HBM bytes one decode token must move: every weight matrix once (wb B per
     element), one embedding row (fp16), the norm gains, K and V of positions
-    0..p (read) and p (write), the logits row (fp32)."""
-    kvrow = s.n_layer * s.n_head_kv * s.head_dim * 2 * 2
+    0..p (read) and p (write), kvb B per element, the logits row (fp32)."""
+    kvrow = s.n_layer * s.n_head_kv * s.head_dim * 2 * kvb
     fixed = round((s.n_layer * layer_matrix_params(s) + s.n_vocab * s.n_embd) * wb) + s.n_embd * 2
     fixed += (2 * s.n_layer + 1) * s.n_embd * 2 + s.n_vocab * 4
     return sum(fixed + kvrow * (p + 1) + kvrow for p in positions)
@@ -263,8 +274,8 @@ def run_ours(args, rank, world, local_rank):
         tensors = synth.make_weights(s, wl["seed"], dev)
     stream.synchronize()
     model = L.Model(s, tensors, stream=st)
-    if args.wtype == "q8_0":
-        model.quantize(stream=st)
+    if args.wtype != "f16":
+        model.quantize({"q8_0": L.LLM_WTYPE_Q8_0, "q4_0": L.LLM_WTYPE_Q4_0}[args.wtype], stream=st)
     wb = WEIGHT_BYTES[args.wtype]
     del tensors
     torch.cuda.empty_cache()
@@ -322,7 +333,7 @@ def run_ours(args, rank, world, local_rank):
     hbm, tf_burst, tf_sust, peak_kind = peaks()
     dec_tps = job_rate(world, n_dec * args.steps, total_dec)
     pre_tps = job_rate(world, wl["prompt"] * args.steps, total_pre)
-    dec_bytes = decode_bytes(s, range(wl["prompt"], wl["prompt"] + n_dec), wb)
+    dec_bytes = decode_bytes(s, range(wl["prompt"], wl["prompt"] + n_dec), wb, kv_bytes(args.option))
     dec_gbs = dec_bytes * args.steps / (total_dec / 1e3) / 1e9
     pf = prefill_flops(s, wl["prompt"])
     pre_tfs = pf * args.steps / (total_pre / 1e3) / 1e12
@@ -337,9 +348,7 @@ def run_ours(args, rank, world, local_rank):
                                f"last position, then {n_dec} greedy decode steps at batch 1",
                    "global_batch": world, "seq_len": wl["prompt"] + n_dec, "n_ctx": wl["n_ctx"],
                    "parallelism": f"replicas{world}",
-                   "weights": "N(0,0.02) rounded to bf16, fp16 inside" if args.wtype == "f16" else
-                              "N(0,0.02) rounded to bf16, re-encoded as Q8_0 blocks (32 one-byte codes, fp16 scale); "
-                              "one-row GEMVs stream the Q8_0 rows, prefill reads f16(q*d)",
+                   "weights": WEIGHT_NOTES[args.wtype],
                    "l2": f"inputs larger than L2 ({dec_bytes / n_dec / 1e9:.1f} GB read per decode token)",
                    **({"options": list(args.option)} if args.option else {})},
         "decode": {"tok_per_s": round(dec_tps, 3), "ms_per_token": round(total_dec / args.steps / n_dec, 4),
@@ -685,7 +694,7 @@ def main():
     ap.add_argument("--impl", choices=("ours", "reference"), default="ours")
     ap.add_argument("--workload", choices=sorted(WORKLOADS), default="llama8b")
     ap.add_argument("--wtype", choices=sorted(WEIGHT_BYTES), default="f16",
-                    help="q8_0: re-encode the model as Q8_0 blocks before the run (the JSON says so)")
+                    help="q8_0, q4_0: re-encode the model as such blocks before the run (the JSON says so)")
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-kernel-timing", action="store_true")
