@@ -499,8 +499,8 @@ int32_t llm_op_attn_decode_noalloc(const float *q, const void *k_cache, const vo
 /* --------------------------------------------------------------------------
  * 4-bit operators: Q4_0 weights, a Q4_0 cache, and the per-head query/key norm
  * that feeds it.  None of these calls allocates or waits: each enqueues its
- * kernels on `stream` and returns, so all but the prefill attention can be
- * captured into a CUDA graph.  Pointers belong to the current device.
+ * kernels on `stream` and returns, so they can be captured into a CUDA graph
+ * (the prefill attention as it says).  Pointers belong to the current device.
  *
  * Q4_0 blocks ("LLama.cpp — how it works" names four-bit types in "The GGUF
  * format (reference)" and a quantised cache in "KV-cache" without a layout;
@@ -601,8 +601,8 @@ int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void 
  * before anything is enqueued.  o fp16 [T][H*hd].  scratch (contents need not
  * be initialised) takes the visible cells widened to fp16; calls that may
  * overlap need one each.  err: DEVICE word or NULL, ORed with 4 when a bounded
- * wait of the kernel timed out.  Not for stream capture: the row list is
- * copied from host memory. */
+ * wait of the kernel timed out.  For stream capture only with rows of at most
+ * 64 sequences (a longer list is copied from host memory). */
 int64_t llm_op_attn_prefill_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
                                                int32_t n_seq);
 int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void *v_cache, const int32_t *pos,

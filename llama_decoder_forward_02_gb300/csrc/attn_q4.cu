@@ -502,12 +502,9 @@ __device__ __forceinline__ uint4 widen_word(uint32_t word, float d) {
 
 constexpr int WT = 256;
 
-// blockIdx (row block, kv head, span); a thread widens one word of K and of V.
-__global__ void __launch_bounds__(WT) kv_widen_q4_kernel(const KvView kv, const KvSpan *spans, f16 *k16, f16 *v16,
-                                                         int n_pad) {
-    pdl_wait();
-    pdl_trigger();
-    const KvSpan sp = spans[blockIdx.z];
+// A thread's part of widening span sp: row block blockIdx.x, kv head blockIdx.y,
+// one word of K and of V.
+__device__ __forceinline__ void widen_span(const KvView &kv, const KvSpan &sp, f16 *k16, f16 *v16, int n_pad) {
     const int hd = kv.head_dim, wpr = hd / 8, nb = hd / 32;      // words of a row, blocks of a row
     const int r0 = sp.lo / 128 * 128, r1 = (sp.hi + 127) / 128 * 128;
     const int row = r0 + (int)(blockIdx.x * (WT / wpr) + threadIdx.x / wpr), w = threadIdx.x % wpr;
@@ -521,6 +518,28 @@ __global__ void __launch_bounds__(WT) kv_widen_q4_kernel(const KvView kv, const 
     }
     *reinterpret_cast<uint4 *>(k16 + dst) = k;
     *reinterpret_cast<uint4 *>(v16 + dst) = v;
+}
+
+__global__ void __launch_bounds__(WT) kv_widen_q4_kernel(const KvView kv, const KvSpan *spans, f16 *k16, f16 *v16,
+                                                         int n_pad) {
+    pdl_wait();
+    pdl_trigger();
+    widen_span(kv, spans[blockIdx.z], k16, v16, n_pad);
+}
+
+// The same for runs of rows passed by value, which also leaves their tiles of
+// at most tile_rows rows in device memory: no copy from the host is needed.
+__global__ void __launch_bounds__(WT) kv_widen_q4_runs_kernel(const KvView kv, const KvRuns runs, int window, int tile_rows,
+                                                              AttnTile *tiles, f16 *k16, f16 *v16, int n_pad) {
+    pdl_wait();
+    pdl_trigger();
+    const KvRuns::Run r = runs.run[blockIdx.z];
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i * tile_rows < r.n_rows; i += WT)
+            tiles[r.tile0 + i] = AttnTile{r.row0 + i * tile_rows, min(tile_rows, r.n_rows - i * tile_rows), r.seq,
+                                          r.pos0 + i * tile_rows, 0};
+    const int lo = window > 0 && r.pos0 + 1 > window ? r.pos0 + 1 - window : 0;
+    widen_span(kv, KvSpan{r.seq, lo, r.pos0 + r.n_rows}, k16, v16, n_pad);
 }
 
 __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, const f16 *scales, const KvView kv,
@@ -600,6 +619,15 @@ cudaError_t launch_kv_widen_q4(const KvView &kv, const KvSpan *spans, int n_span
     const int rows = (max_rows / 128 + 2) * 128, per = WT / (kv.head_dim / 8);
     return launch_kernel(kv_widen_q4_kernel, dim3((rows + per - 1) / per, kv.n_kv_head, n_spans), dim3(WT), 0, l, kv,
                          spans, k16, v16, n_pad);
+}
+
+cudaError_t launch_kv_widen_q4_runs(const KvView &kv, const KvRuns &runs, int n_runs, int max_rows, int window,
+                                    int tile_rows, AttnTile *tiles, f16 *k16, f16 *v16, int n_pad, const Launch &l) {
+    if (n_runs < 1 || n_runs > KvRuns::MAX || kv.n_kv_head > 65535 || n_pad % 128 || n_pad < kv.n_ctx || !kv.k4)
+        return cudaErrorInvalidValue;
+    const int rows = (max_rows / 128 + 2) * 128, per = WT / (kv.head_dim / 8);
+    return launch_kernel(kv_widen_q4_runs_kernel, dim3((rows + per - 1) / per, kv.n_kv_head, n_runs), dim3(WT), 0, l, kv,
+                         runs, window, tile_rows, tiles, k16, v16, n_pad);
 }
 
 cudaError_t launch_kv_rows_q4(const uint8_t *codes, const f16 *scales, const KvView &kv, const int *pos,

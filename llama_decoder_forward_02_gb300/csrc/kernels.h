@@ -356,6 +356,15 @@ struct KvSpan { int seq, lo, hi; };
 // values they stand for, the other rows of the 128-row tiles they touch zero.
 cudaError_t launch_kv_widen_q4(const KvView &kv, const KvSpan *spans, int n_spans, int max_rows, f16 *k16, f16 *v16,
                                int n_pad, const Launch &l);
+// The same for runs of rows of one sequence each (n_rows rows from pos0 on,
+// rows row0.. of the batch), passed by value; it also writes their attention
+// tiles (of at most tile_rows rows, a run's from tiles[tile0] on).
+struct KvRuns {
+    static constexpr int MAX = 64;
+    struct Run { int row0, n_rows, seq, pos0, tile0; } run[MAX];
+};
+cudaError_t launch_kv_widen_q4_runs(const KvView &kv, const KvRuns &runs, int n_runs, int max_rows, int window,
+                                    int tile_rows, AttnTile *tiles, f16 *k16, f16 *v16, int n_pad, const Launch &l);
 // out[t][j][:] = the values of row pos[t], kv head j of sequence seq[t].
 cudaError_t launch_kv_rows_q4(const uint8_t *codes, const f16 *scales, const KvView &kv, const int *pos,
                               const int *seq, f16 *out, int T, uint32_t *err, const Launch &l);

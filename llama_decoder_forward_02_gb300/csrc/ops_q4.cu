@@ -210,6 +210,7 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
     const int rows_max = tc ? 128 : 64;
     std::vector<AttnTile> tiles;
     std::vector<KvSpan> spans;
+    KvRuns runs;
     std::vector<int> span_of((size_t)n_seq, -1);
     int longest = 0;
     for (int i = 0; i < T;) {
@@ -226,6 +227,7 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
         const int lo = window > 0 && pos[i] + 1 > window ? pos[i] + 1 - window : 0, hi = pos[j - 1] + 1;
         spans.push_back(KvSpan{seq[i], lo, hi});
         longest = std::max(longest, hi - lo);
+        if (spans.size() <= KvRuns::MAX) runs.run[spans.size() - 1] = KvRuns::Run{i, j - i, seq[i], pos[i], (int)tiles.size()};
         for (int r = i; r < j; r += rows_max)
             tiles.push_back(AttnTile{r, std::min(rows_max, j - r), seq[i], pos[r], 0});
         i = j;
@@ -237,11 +239,17 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
     f16 *k16 = (f16 *)base, *v16 = (f16 *)(base + plane);
     AttnTile *dtiles = (AttnTile *)(base + 2 * plane);
     KvSpan *dspans = (KvSpan *)(base + 2 * plane + align256((size_t)T * sizeof(AttnTile)));
-    // copies from pageable memory: staged before the call returns
-    cudaError_t e = cudaMemcpyAsync(dtiles, tiles.data(), tiles.size() * sizeof(AttnTile), cudaMemcpyHostToDevice, L.stream);
-    if (!e) e = cudaMemcpyAsync(dspans, spans.data(), spans.size() * sizeof(KvSpan), cudaMemcpyHostToDevice, L.stream);
-    if (!e) e = launch_kv_widen_q4(q4_view(k_cache, v_cache, Hkv, hd, n_ctx, n_seq), dspans, (int)spans.size(), longest,
-                                   k16, v16, n_pad, L);
+    const KvView kv = q4_view(k_cache, v_cache, Hkv, hd, n_ctx, n_seq);
+    cudaError_t e = cudaSuccess;
+    if (spans.size() <= KvRuns::MAX) {
+        e = launch_kv_widen_q4_runs(kv, runs, (int)spans.size(), longest, window, rows_max, dtiles, k16, v16, n_pad,
+                                    overlapped(stream));
+    } else {
+        // copies from pageable memory: staged before the call returns
+        e = cudaMemcpyAsync(dtiles, tiles.data(), tiles.size() * sizeof(AttnTile), cudaMemcpyHostToDevice, L.stream);
+        if (!e) e = cudaMemcpyAsync(dspans, spans.data(), spans.size() * sizeof(KvSpan), cudaMemcpyHostToDevice, L.stream);
+        if (!e) e = launch_kv_widen_q4(kv, dspans, (int)spans.size(), longest, k16, v16, n_pad, L);
+    }
     if (!e && tc) {
         TmaMap mq, mk, mv;
         const int rows = n_seq * Hkv * n_pad;

@@ -519,3 +519,48 @@ def test_decode_step_block(lib, hd, H, Hkv, d, T):
         mag = np.abs(got) @ np.repeat(np.abs(do.astype(np.float64)), 32, 1).T * 23
         assert np.all(np.abs(y.cpu().double().numpy() - ref_y) <= mag * U32 * (8 + H * hd // 32))
     assert int(err) == 0
+
+
+def test_attn_prefill_many_sequences_and_capture(lib):
+    """Rows of more sequences than a launch carries by value, and a captured call replayed after q and the cache moved."""
+    hd, H, Hkv, n_ctx, n_seq = 64, 4, 2, 70, 80
+    rng = np.random.default_rng(17)
+
+    def case(runs):
+        pos = np.concatenate([np.arange(a, a + n) for _, a, n in runs]).astype(np.int32)
+        seq = np.concatenate([np.full(n, s) for s, _, n in runs]).astype(np.int32)
+        vis = visible_cells(pos, seq, n_seq, n_ctx, 0)
+        (kc, kd), (vc, vd) = (make_cache(rng, n_seq, Hkv, n_ctx, hd, vis) for _ in range(2))
+        q = (rng.standard_normal((len(pos), H * hd)) * 1.5).astype(np.float16)
+        ref = reference(q.astype(np.float64).reshape(-1, H, hd), O.dequantize_q4_0(kc, kd), O.dequantize_q4_0(vc, vd), pos, seq,
+                        Hkv, 0).reshape(len(pos), -1)
+        return pos, seq, dev(q), dev(pack_cache(kc, kd)), dev(pack_cache(vc, vd)), ref
+
+    def call(pos, seq, q, kc, vc, o, scratch):
+        assert lib.llm_op_attn_prefill_q4_0(q.data_ptr(), kc.data_ptr(), vc.data_ptr(), pos.ctypes.data, seq.ctypes.data,
+                                            o.data_ptr(), len(pos), H, Hkv, hd, n_ctx, n_seq, 0, scratch.data_ptr(),
+                                            scratch.numel(), 0, stream()) == 0, lib.llm_last_error(None)
+
+    def buffers(T):
+        n = lib.llm_op_attn_prefill_q4_0_scratch_bytes(T, H, Hkv, hd, n_ctx, n_seq)
+        return torch.zeros((T, H * hd), dtype=torch.float16, device="cuda"), torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    many = [(s, s % 60, 1 + s % 3) for s in range(n_seq)]
+    pos, seq, q, kc, vc, ref = case(many)
+    o, scratch = buffers(len(pos))
+    call(pos, seq, q, kc, vc, o, scratch)
+    assert np.abs(o.cpu().double().numpy() - ref).max() <= 1e-2
+    few = [(3, 10, 40), (79, 0, 17)]
+    pos, seq, q, kc, vc, ref = case(few)
+    o, scratch = buffers(len(pos))
+    call(pos, seq, q, kc, vc, o, scratch)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(pos, seq, q, kc, vc, o, scratch)
+    _, _, q2, kc2, vc2, ref = case(few)
+    for a, b in ((q, q2), (kc, kc2), (vc, vc2)):
+        a.copy_(b)
+    g.replay()
+    torch.cuda.synchronize()
+    assert np.abs(o.cpu().double().numpy() - ref).max() <= 1e-2
