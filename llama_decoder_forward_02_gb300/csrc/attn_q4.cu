@@ -29,12 +29,13 @@
 // of its own, filled by cp.async (16-byte chunks swizzled so that both K's and
 // V's fragment reads are free of bank conflicts); warps meet only at the end.
 // The running maximum of a head is raised by a warp-uniform branch when a key
-// passes it.  Splits over the keys write (max, sum, numerators) and the CTA
-// that arrives last merges them in split order: results do not depend on
-// timing and nothing spins.
+// passes it.  Splits over the keys leave (numerators, sum, max) and are merged
+// in split order, up to eight of them by the cluster they form, more by the CTA
+// that arrives last: results do not depend on timing and nothing spins.
 //
 // Prefill: the visible rows of the ubatch's sequences are widened once to fp16
 // and the fp16 prefill attention runs on them.
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"
@@ -50,6 +51,8 @@ constexpr int NST = 4;                   // ring stages of a warp
 constexpr int MAX_SPLIT = ATTN_DECODE_MAX_SPLIT;
 constexpr int MIN_KEYS = NW * KG;        // keys of a split
 constexpr int MERGE_AHEAD = 32;          // splits whose partials a merging thread asks for at once
+constexpr int MAX_CLUSTER = 8;           // splits merged in a cluster
+constexpr int CLUSTER_CTX = 8192;        // longest cache whose splits always are one cluster
 constexpr int SMS = 152;                 // of the one GPU this library is compiled for: scratch sizes follow from it
 
 __device__ __forceinline__ int split_chunk(int S, int n_split) {
@@ -69,8 +72,8 @@ struct Ring {
     static constexpr size_t MERGE = (size_t)NW * GC * (HD + 2) * sizeof(float);
     static constexpr size_t QFRAG = (size_t)2 * NB * (32 * 16 + 16);      // q's fragments, two tiles at most
     static constexpr size_t WGT = BYTES > MERGE ? BYTES : MERGE;          // split weights, after the rings or the results
-    static constexpr size_t SMEM = BYTES + QFRAG > WGT + (size_t)GC * MAX_SPLIT * sizeof(float)
-                                       ? BYTES + QFRAG : WGT + (size_t)GC * MAX_SPLIT * sizeof(float);
+    static constexpr size_t TAIL = (size_t)GC * (MAX_SPLIT > HD + 2 ? MAX_SPLIT : HD + 2) * sizeof(float);   // or a cluster's records
+    static constexpr size_t SMEM = BYTES + QFRAG > WGT + TAIL ? BYTES + QFRAG : WGT + TAIL;
     // byte offset of word block `part` (4 NB bytes, lane t4 of a K row) of row r
     __device__ static __forceinline__ int at(int r, int part) {
         if (HD == 128) return r * ROW + ((part ^ ((r >> 1) & 3)) << 4);
@@ -139,7 +142,10 @@ __device__ __forceinline__ void load_scales(float (&d)[NB], const void *p) {
     }
 }
 
-template <int HD, int NT>
+// CL: the splits of a (row, kv head, chunk) are the CTAs of one cluster and are
+// merged through distributed shared memory; else through a.part by the CTA that
+// arrives last.
+template <int HD, int NT, bool CL>
 __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
     using R = Ring<HD>;
     constexpr int NB = R::NB, REC = HD + 2;
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     const int S = ok ? pos + 1 - lo : 0;
     const int chunk = split_chunk(S, a.n_split);
     const int n_eff = S > 0 ? (S + chunk - 1) / chunk : 1;
-    if (sp >= n_eff) return;
+    if (!CL && sp >= n_eff) return;                   // a cluster's CTAs stay for its barriers
     const int kb = lo + sp * chunk, ke = min(lo + S, kb + chunk);
     const size_t row0 = ok ? ((size_t)seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * HD) / HD : 0;   // rows before the head's
 
@@ -391,8 +397,10 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     }
     __syncthreads();
     // records of a split: numerators, sum, maximum
-    const bool one = n_eff == 1;
-    float *part = a.part + ((size_t)(t * a.H + h0) * a.n_split + sp) * REC;
+    const bool one = !CL && n_eff == 1;
+    float *rec = reinterpret_cast<float *>(smem_raw + R::WGT);             // CL: this CTA's records, [GC][REC]
+    float *part = CL ? rec : a.part + ((size_t)(t * a.H + h0) * a.n_split + sp) * REC;
+    const size_t part_head = CL ? REC : (size_t)a.n_split * REC;
     for (int i = tid; i < gn * (HD / 2); i += THREADS) {
         const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
         float2 num = make_float2(0.f, 0.f);
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
             const float inv = den > 0.f ? 1.f / den : 0.f;
             *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(num.x * inv, num.y * inv);
         } else {
-            float *rp = part + (size_t)h * a.n_split * REC;
+            float *rp = part + h * part_head;
             *reinterpret_cast<float2 *>(rp + d) = num;
             if (d == 0) {
                 float M = -INFINITY;
@@ -420,13 +428,51 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
         }
     }
     if (one) return;
-    __threadfence();
+    if constexpr (CL) {
+        // rank r merges its share of the (head, dimension pair)s from every rank's records, in split order
+        const int ranks = (int)gridDim.x, n = gn * (HD / 2);
+        cluster_sync();
+        for (int i = sp * n / ranks + tid; i < (sp + 1) * n / ranks; i += THREADS) {
+            const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
+            float2 num[MAX_CLUSTER], lm[MAX_CLUSTER];
+#pragma unroll
+            for (int p = 0; p < MAX_CLUSTER; ++p) {
+                num[p] = make_float2(0.f, 0.f);
+                lm[p] = make_float2(0.f, -INFINITY);
+                if (p < ranks) {
+                    const uint32_t at = dsmem(rec + h * REC, (uint32_t)p);
+                    num[p] = dsmem_ld_f32x2(at + 4u * d);
+                    lm[p] = dsmem_ld_f32x2(at + 4u * HD);
+                }
+            }
+            float M = -INFINITY, den = 0.f;
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < MAX_CLUSTER; ++p) M = fmaxf(M, lm[p].y);
+#pragma unroll
+            for (int p = 0; p < MAX_CLUSTER; ++p) {
+                const float f = lm[p].y == -INFINITY ? 0.f : exp2_fast(lm[p].y - M);
+                acc.x = fmaf(f, num[p].x, acc.x);
+                acc.y = fmaf(f, num[p].y, acc.y);
+                den = fmaf(f, lm[p].x, den);
+            }
+            const float inv = den > 0.f ? 1.f / den : 0.f;
+            *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(acc.x * inv, acc.y * inv);
+        }
+        cluster_sync();                               // no CTA leaves while another reads its records
+        return;
+    }
     __syncthreads();
     unsigned *cnt = a.counters + (size_t)t * gridDim.y + blockIdx.y;
-    if (tid == 0) s_last = atomicAdd(cnt, 1u) == (unsigned)(n_eff - 1);
+    // one thread's release covers the CTA's writes before the barrier, its
+    // acquire the reads of every thread after the next
+    if (tid == 0) {
+        unsigned before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(cnt) : "memory");
+        s_last = before == (unsigned)(n_eff - 1);
+    }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
 
     // ---- last CTA of this (row, kv head, chunk): each thread asks for its two
     // dimensions of the first MERGE_AHEAD splits while the warps find the splits'
@@ -565,17 +611,28 @@ __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, co
 
 int attn_q4_chunks(int H, int Hkv) { return (H / Hkv + GC - 1) / GC; }
 
+// Splits of a (row, kv head, chunk): about two CTAs an SM in all.  Up to
+// MAX_CLUSTER splits (a power of two) are one cluster, whose merge costs about
+// a microsecond less than the one through memory (eight rows of 748 to 3415
+// keys, 8 kv heads: 10.4 us, 11.6 merged through memory), and a cache of at
+// most CLUSTER_CTX positions always takes that (one row: 2100 keys 5.9 us in a
+// cluster of 8, 6.9 in 32 splits; 8000 keys 8.2 and 8.4; two rows of 8000 and
+// 5000 keys 10.1 and 9.4 in 19).  Beyond, the merge through memory asks for 32
+// splits at once and would pay another round trip for more (32000 keys: 38
+// splits 15.7 us, 32 splits 14.7), so more only where fewer leave SMs without
+// work.
 int attn_q4_pick_split(int T, int H, int Hkv, int n_ctx) {
     const int mx = (n_ctx + MIN_KEYS - 1) / MIN_KEYS;
     const long long units = (long long)T * Hkv * attn_q4_chunks(H, Hkv);
     long long s = 2LL * SMS / units;
-    // the merge asks for 32 splits at once: beyond, it pays another round trip
-    // (32000 keys, 8 kv heads: 38 splits 15.7 us, 32 splits 15.2), so more only
-    // where fewer leave SMs without work
     if (s > MERGE_AHEAD && units * MERGE_AHEAD >= SMS) s = MERGE_AHEAD;
+    if (s > MAX_CLUSTER && n_ctx <= CLUSTER_CTX) s = MAX_CLUSTER;
     if (s > MAX_SPLIT) s = MAX_SPLIT;
     if (s > mx) s = mx;
-    return s < 1 ? 1 : (int)s;
+    if (s < 1) s = 1;
+    if (s <= MAX_CLUSTER)
+        while (s & (s - 1)) ++s;
+    return (int)s;
 }
 
 size_t attn_q4_part_floats(int T, int H, int hd, int n_split) { return (size_t)T * H * n_split * (hd + 2); }
@@ -588,11 +645,16 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeArgs &a, const Launch &l) {
     if ((long long)Hkv * chunks > 65535) return cudaErrorInvalidValue;
     const dim3 grid(a.n_split, Hkv * chunks, a.T), block(THREADS);
     // four heads fill the 8 columns of a tile; larger groups take two tiles
-#define Q4_DEC_CASE(HDV)                                                                                       \
-    if (a.kv.head_dim == HDV)                                                                                  \
-        return a.H / Hkv <= 4                                                                                  \
-                   ? launch_kernel(attn_decode_q4_kernel<HDV, 1>, grid, block, Ring<HDV>::SMEM, l, a, chunks)  \
-                   : launch_kernel(attn_decode_q4_kernel<HDV, 2>, grid, block, Ring<HDV>::SMEM, l, a, chunks);
+#define Q4_DEC_CASE(HDV)                                                                                             \
+    if (a.kv.head_dim == HDV) {                                                                                      \
+        const size_t smem = Ring<HDV>::SMEM;                                                                         \
+        const bool small = a.H / Hkv <= 4;                                                                           \
+        if (a.n_split <= MAX_CLUSTER)                                                                                \
+            return launch_cluster_kernel(small ? attn_decode_q4_kernel<HDV, 1, true> : attn_decode_q4_kernel<HDV, 2, true>, \
+                                         grid, block, a.n_split, smem, l, a, chunks);                                \
+        return launch_kernel(small ? attn_decode_q4_kernel<HDV, 1, false> : attn_decode_q4_kernel<HDV, 2, false>,    \
+                             grid, block, smem, l, a, chunks);                                                       \
+    }
     Q4_DEC_CASE(32) Q4_DEC_CASE(64) Q4_DEC_CASE(128)
 #undef Q4_DEC_CASE
     return cudaErrorInvalidValue;
@@ -600,11 +662,12 @@ cudaError_t launch_attn_decode_q4(const AttnDecodeArgs &a, const Launch &l) {
 
 cudaError_t init_attn_q4_attributes() {
     cudaError_t e = cudaSuccess;
-#define Q4_DEC_ATTR1(HDV, NT)                                                              \
-    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT>, Ring<HDV>::SMEM);               \
-    if (!e) e = cudaFuncSetAttribute(attn_decode_q4_kernel<HDV, NT>, cudaFuncAttributePreferredSharedMemoryCarveout, \
+#define Q4_DEC_ATTR1(HDV, NT, CL)                                                              \
+    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT, CL>, Ring<HDV>::SMEM);               \
+    if (!e) e = cudaFuncSetAttribute(attn_decode_q4_kernel<HDV, NT, CL>, cudaFuncAttributePreferredSharedMemoryCarveout, \
                                      cudaSharedmemCarveoutMaxShared);
-#define Q4_DEC_ATTR(HDV) Q4_DEC_ATTR1(HDV, 1) Q4_DEC_ATTR1(HDV, 2)
+#define Q4_DEC_ATTR(HDV) \
+    Q4_DEC_ATTR1(HDV, 1, false) Q4_DEC_ATTR1(HDV, 2, false) Q4_DEC_ATTR1(HDV, 1, true) Q4_DEC_ATTR1(HDV, 2, true)
     Q4_DEC_ATTR(32) Q4_DEC_ATTR(64) Q4_DEC_ATTR(128)
 #undef Q4_DEC_ATTR
 #undef Q4_DEC_ATTR1

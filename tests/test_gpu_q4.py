@@ -327,6 +327,9 @@ class Decode:
     (128, 16, 4, 700, [699, 50], [0, 1], 33), (64, 8, 2, 700, [699, 350], [0, 1], 1), (32, 4, 1, 500, [499], [0], 128),
     (128, 4, 2, 5000, [4999], [0], 0),
     (64, 4, 2, 90, list(range(70, 90)), [i % 3 for i in range(20)], 0),   # more than eight rows
+    # splits merged through memory: 32 of them, more, and fewer than were launched
+    (64, 32, 8, 10000, [9999], [0], 0), (128, 8, 2, 9000, [8999], [0], 0), (128, 5, 1, 9000, [8000, 130], [0, 0], 0),
+    (32, 8, 2, 8300, [8299, 20, 4000], [0, 0, 0], 5000),
 ])
 def test_attn_decode(lib, hd, H, Hkv, n_ctx, pos, seq, window):
     c = Decode(lib, hd, H, Hkv, n_ctx, max(seq) + 1, pos, seq, window)
