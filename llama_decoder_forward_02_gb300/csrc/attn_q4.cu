@@ -590,6 +590,8 @@ __global__ void __launch_bounds__(WT) kv_widen_q4_runs_kernel(const KvView kv, c
 
 __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, const f16 *scales, const KvView kv,
                                                         const int *pos, const int *seq, f16 *out, int T, uint32_t *err) {
+    pdl_wait();
+    pdl_trigger();
     const int hd = kv.head_dim, wpr = hd / 8, nb = hd / 32;
     const long long i = (long long)blockIdx.x * WT + threadIdx.x;
     const long long row = i / wpr;

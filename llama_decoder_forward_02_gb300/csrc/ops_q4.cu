@@ -148,8 +148,7 @@ extern "C" int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, co
     if (const char *why = shape_error(T, Hkv, Hkv, hd, n_ctx, n_seq)) return refuse(who, why);
     if (!aligned(cache, 16) || !aligned(out, 16)) return refuse(who, "cache and out must be 16-byte aligned");
     const KvView kv = q4_view(cache, cache, Hkv, hd, n_ctx, n_seq);
-    return launched(who, launch_kv_rows_q4(kv.k4, kv.kd, kv, pos, seq, (f16 *)out, T, err,
-                                           Launch{(cudaStream_t)stream, false, nullptr}));
+    return launched(who, launch_kv_rows_q4(kv.k4, kv.kd, kv, pos, seq, (f16 *)out, T, err, overlapped(stream)));
 }
 
 extern "C" int64_t llm_op_attn_decode_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,

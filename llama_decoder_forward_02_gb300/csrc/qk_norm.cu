@@ -50,7 +50,7 @@ constexpr int E = 8;                      // elements of a lane
 // The head's values after norm and rotation, in R.
 template <int HD, class R>
 __device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
-                                          float eps, R (&u)[E]) {
+                                          bool turn, float eps, R (&u)[E]) {
     // the shuffles run for every lane: heads without a norm share the warp
     R ss = R(0);
 #pragma unroll
@@ -60,9 +60,9 @@ __device__ __forceinline__ void transform(const float (&x)[E], const float (&gai
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
         const R a = norm ? R(x[e]) * r * R(gain[e]) : R(x[e]), b = norm ? R(x[e + 1]) * r * R(gain[e + 1]) : R(x[e + 1]);
-        const float2 c = cs[e / 2];       // (1, 0) for a head that is not rotated
-        u[e] = a * R(c.x) - b * R(c.y);
-        u[e + 1] = a * R(c.y) + b * R(c.x);
+        const float2 c = cs[e / 2];
+        u[e] = turn ? a * R(c.x) - b * R(c.y) : a;
+        u[e + 1] = turn ? a * R(c.y) + b * R(c.x) : b;
     }
 }
 
@@ -106,11 +106,11 @@ __device__ __forceinline__ bool encode(const R (&u)[E], int lane, R &d, uint32_t
 // The word and scale of the exact values.
 template <int HD>
 __device__ __forceinline__ void encode_exact(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
-                                             float eps, const float (&u)[E], bool used, int lane, float &d, uint32_t &word) {
+                                             bool turn, float eps, const float (&u)[E], bool used, int lane, float &d, uint32_t &word) {
     const bool near = encode<float>(u, lane, d, word);
     if (__any_sync(0xffffffffu, near && used)) {
         double u64[E], d64;
-        transform<HD, double>(x, gain, cs, norm, eps, u64);
+        transform<HD, double>(x, gain, cs, norm, turn, eps, u64);
         encode<double>(u64, lane, d64, word);
         d = (float)d64;
     }
@@ -124,9 +124,9 @@ __device__ __forceinline__ void load8(float (&v)[E], const float *p) {
 
 // grid (row, part): part p of gridDim.y takes the warps' heads p, p + parts, ..
 // Q4: the cache is Q4_0 (its float64 path would take registers from the others).
-// Four CTAs an SM keep enough loads in flight.
+// Four or five CTAs an SM keep the loads in flight.
 template <int HD, bool Q4>
-__global__ void __launch_bounds__(THREADS, 4) qk_norm_rope_kernel(const QkNormArgs a) {
+__global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const QkNormArgs a) {
     constexpr int L = HD / E, PER = 32 / L;           // lanes of a head, heads of a warp at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, e0 = E * sub;
     const int Hkv = a.kv.n_kv_head, heads = a.H + 2 * Hkv;
@@ -166,11 +166,8 @@ __global__ void __launch_bounds__(THREADS, 4) qk_norm_rope_kernel(const QkNormAr
 #pragma unroll
             for (int e = 0; e < E; ++e) gain[e] = 1.f;
         }
-        float2 cs[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) cs[e] = is_q || is_k ? turn[e] : make_float2(1.f, 0.f);
         float u[E];
-        transform<HD, float>(x, gain, cs, gp != nullptr, a.eps, u);
+        transform<HD, float>(x, gain, turn, gp != nullptr, is_q || is_k, a.eps, u);
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) bad |= f16_bad(u[e]);
@@ -193,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 4) qk_norm_rope_kernel(const QkNormAr
         if (Q4) {
             float d;
             uint32_t word;
-            encode_exact<HD>(x, gain, cs, gp != nullptr, a.eps, u, put, lane, d, word);
+            encode_exact<HD>(x, gain, turn, gp != nullptr, is_k, a.eps, u, put, lane, d, word);
             if (put) {
                 out_of_range |= bad;
                 const int blk = sub >> 2, tt = sub & 3;
@@ -246,8 +243,8 @@ __global__ void __launch_bounds__(SHIFT_THREADS) kv_shift_q4_kernel(KvView kv, i
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = (float)((int)((w >> q4::shift_of(e)) & 15u) - 8) * d;     // exact
         uint32_t out;
-        transform<HD, float>(x, gain, back, false, 0.f, u);
-        encode_exact<HD>(x, gain, back, false, 0.f, u, true, lane, nd, out);
+        transform<HD, float>(x, gain, back, false, true, 0.f, u);
+        encode_exact<HD>(x, gain, back, false, true, 0.f, u, true, lane, nd, out);
         __syncthreads();
         if (in) {
             kw[dst * (HD / 8) + at] = out;
