@@ -1027,13 +1027,12 @@ GemmArgs gemm_base(llm_ctx *c, const f16 *A, const f16 *W, int M, int N, int K) 
 }
 
 // Prefill attention of a Q4_0 cache: the layer's visible rows widened to fp16,
-// then the fp16 attention on them.  It starts after the widening has ended, not
-// beside it: every key it reads comes from there.
+// then the fp16 attention on them (its tiles say that no key is ready before).
 cudaError_t attn_prefill_q4(llm_ctx *c, const UbDev &u, const KvView &kv) {
     const llm_model *m = c->m;
-    const Launch L{c->stream, false, &c->launches};
+    const Launch L = lnch_prefill(c);
     cudaError_t e = timed(c, K_KV_WIDEN, [&] {
-        return launch_kv_widen_q4(kv, u.spans, u.n_spans, u.max_span, c->k16, c->v16, c->n_pad, lnch_prefill(c));
+        return launch_kv_widen_q4(kv, u.spans, u.n_spans, u.max_span, c->k16, c->v16, c->n_pad, L);
     });
     if (e) return e;
     if (c->attn_tc_ok && c->attn_mode > 0) {
@@ -1338,7 +1337,12 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             for (int i = s0; i < s1; ++i) if (p.out[i]) rows[r++] = i - s0;
             build_tiles(p.seq, p.pos, s0, s1, 64, reinterpret_cast<AttnTile *>(hs + off_tiles[k]));
             build_tiles(p.seq, p.pos, s0, s1, 128, reinterpret_cast<AttnTile *>(hs + off_tiles128[k]));
-            if (c->kv_q4) memcpy(hs + off_spans[k], spans[k].data(), spans[k].size() * sizeof(KvSpan));
+            if (c->kv_q4) {
+                memcpy(hs + off_spans[k], spans[k].data(), spans[k].size() * sizeof(KvSpan));
+                // every key the attention reads comes from the widening just before it
+                for (int i = 0; i < n_tiles[k]; ++i) reinterpret_cast<AttnTile *>(hs + off_tiles[k])[i].kv_ready = 0;
+                for (int i = 0; i < n_tiles128[k]; ++i) reinterpret_cast<AttnTile *>(hs + off_tiles128[k])[i].kv_ready = 0;
+            }
         }
         CK(cudaMemcpyAsync(c->meta_dev, hs, ints * sizeof(int), cudaMemcpyHostToDevice, c->stream));
         CK(cudaEventRecord(c->meta_ev[slot], c->stream));
