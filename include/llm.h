@@ -583,8 +583,8 @@ int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, const int32_t
  * c > pos[t] - window.  q fp32 [T][H*hd]; pos, seq int32 [T] (DEVICE); o fp16
  * [T][H*hd]; any H that is a multiple of Hkv, up to 4096.  Cells outside a
  * row's visible positions may hold anything.  scratch: scratch_bytes bytes,
- * zeroed once before its first use; each call leaves it ready for the next of
- * the same shape, and calls that may overlap need one each.  A row whose pos
+ * zeroed once before its first use; each call leaves it ready for the next, of
+ * any shape it is large enough for, and calls that may overlap need one each.  A row whose pos
  * lies outside [0, n_ctx) or whose seq lies outside [0, n_seq) gives zeros and
  * ORs 2 into *err (DEVICE word or NULL). */
 int64_t llm_op_attn_decode_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,

@@ -30,11 +30,13 @@
 // V's fragment reads are free of bank conflicts); warps meet only at the end.
 // The running maximum of a head is raised by a warp-uniform branch when a key
 // passes it.  Splits over the keys leave (numerators, sum, max) and are merged
-// in split order, up to eight of them by the cluster they form, more by the CTA
-// that arrives last: results do not depend on timing and nothing spins.
+// in split order, by the cluster they form or, over long caches, by the CTA that
+// arrives last: results do not depend on timing and nothing spins.
 //
 // Prefill: the visible rows of the ubatch's sequences are widened once to fp16
 // and the fp16 prefill attention runs on them.
+#include <algorithm>
+
 #include "cluster.cuh"
 #include "common.cuh"
 #include "launch.cuh"
@@ -44,24 +46,19 @@ namespace llm {
 
 namespace {
 
-constexpr int NW = 8, THREADS = NW * 32;
 constexpr int GC = 8;                    // query heads of a chunk
 constexpr int KG = 16;                   // keys of a group
 constexpr int NST = 4;                   // ring stages of a warp
 constexpr int MAX_SPLIT = ATTN_DECODE_MAX_SPLIT;
-constexpr int MIN_KEYS = NW * KG;        // keys of a split
-constexpr int MERGE_AHEAD = 32;          // splits whose partials a merging thread asks for at once
+constexpr int MIN_GRP = 8;               // groups of a split, at least
+constexpr int MERGE_AHEAD = 40;          // splits whose partials a merging thread asks for at once
 constexpr int MAX_CLUSTER = 8;           // splits merged in a cluster
-constexpr int CLUSTER_CTX = 8192;        // longest cache whose splits always are one cluster
+constexpr int CLUSTER_CTX = 4096;        // longest cache whose splits always are one cluster
+constexpr int BALANCE_T = 128;           // most rows that share the splits of a launch ...
+constexpr int BALANCE_UNITS = 2048;      // ... and most (row, kv head, chunk)s, each of which has a counter
 constexpr int SMS = 152;                 // of the one GPU this library is compiled for: scratch sizes follow from it
 
-__device__ __forceinline__ int split_chunk(int S, int n_split) {
-    int chunk = (S + n_split - 1) / n_split;
-    chunk = (chunk + MIN_KEYS - 1) / MIN_KEYS * MIN_KEYS;
-    return chunk < MIN_KEYS ? MIN_KEYS : chunk;
-}
-
-template <int HD>
+template <int HD, int NW>
 struct Ring {
     static constexpr int NB = HD / 32;               // blocks of a row
     static constexpr int ROW = HD / 2;               // bytes of a row's codes
@@ -142,30 +139,120 @@ __device__ __forceinline__ void load_scales(float (&d)[NB], const void *p) {
     }
 }
 
+// The keys a row sees: S of them from lo on, none if its position or sequence
+// lies outside the cache.
+struct Row {
+    int lo, S;
+    bool ok;
+    __device__ __forceinline__ int groups() const { return (S + KG - 1) / KG; }
+};
+__device__ __forceinline__ Row row_keys(const AttnDecodeArgs &a, int pos, int seq) {
+    Row r;
+    r.ok = pos >= 0 && pos < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
+    r.lo = r.ok && a.window > 0 && pos + 1 > a.window ? pos + 1 - a.window : 0;
+    r.S = r.ok ? pos + 1 - r.lo : 0;
+    return r;
+}
+
+// Which row and split of it CTA x of a.n_split works on, by its warp: the rows
+// share the splits by their lengths, each row's being of len groups (the last
+// shorter) and at least one.  With X splits, T rows and N groups in all, len =
+// ceil(N / (X - T + 1)) needs no more than X, as a row with keys rounds up by
+// less than one; half that allowance is tried first.  Returns the split, or -1
+// where none is left for x.
+__device__ __forceinline__ int find_split(const AttnDecodeArgs &a, int x, int lane, int &t, Row &rw, int &pos, int &seq,
+                                          int &len, int &n_eff) {
+    const int X = a.n_split, T = a.T;
+    auto load = [&](int r) {
+        pos = r < T ? a.pos[r] : -1;
+        seq = r < T ? a.seq[r] : -1;
+        rw = row_keys(a, pos, seq);
+        return rw.groups();
+    };
+    if (T == 1) {
+        pos = a.pos[0];
+        seq = a.seq[0];
+        rw = row_keys(a, pos, seq);
+        t = 0;
+        len = max(MIN_GRP, (rw.groups() + X - 1) / X);
+        n_eff = max(1, (rw.groups() + len - 1) / len);
+        return x < n_eff ? x : -1;
+    }
+    unsigned sum = 0, most = 0;
+    int mine = 0;
+    for (int r = lane; r < (T + 31) / 32 * 32; r += 32) {
+        mine = load(r);
+        sum += mine;
+        most = max(most, (unsigned)mine);
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const unsigned least = max((unsigned)MIN_GRP, (most + MAX_SPLIT - 1) / MAX_SPLIT);
+    auto splits = [&](int r, int groups) { return r < T ? max(1, (groups + len - 1) / len) : 0; };
+    for (int take = T / 2;; take = T - 1) {
+        const unsigned n = (unsigned)(X - take);
+        len = (int)max(least, (sum + n - 1) / n);
+        if (take == T - 1) break;
+        unsigned used = 0;
+        for (int r = lane; r < (T + 31) / 32 * 32; r += 32) used += splits(r, T <= 32 ? mine : load(r));
+        if (__reduce_add_sync(0xffffffffu, used) <= (unsigned)X) break;
+    }
+    int base = 0;
+    for (int r0 = 0; r0 < T; r0 += 32) {
+        const int n = splits(r0 + lane, T <= 32 ? mine : load(r0 + lane));
+        int end = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + end > x);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            t = r0 + l;
+            n_eff = __shfl_sync(0xffffffffu, n, l);
+            const int first = base + __shfl_sync(0xffffffffu, end, l) - n_eff;
+            pos = __shfl_sync(0xffffffffu, pos, l);
+            seq = __shfl_sync(0xffffffffu, seq, l);
+            rw = row_keys(a, pos, seq);
+            return x - first;
+        }
+        base += __shfl_sync(0xffffffffu, end, 31);
+    }
+    return -1;
+}
+
 // CL: the splits of a (row, kv head, chunk) are the CTAs of one cluster and are
 // merged through distributed shared memory; else through a.part by the CTA that
 // arrives last.
-template <int HD, int NT, bool CL>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
-    using R = Ring<HD>;
-    constexpr int NB = R::NB, REC = HD + 2;
+template <int HD, int NT, int NW, bool CL>
+__global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_decode_q4_kernel(const AttnDecodeArgs a, int chunks) {
+    using R = Ring<HD, NW>;
+    constexpr int NB = R::NB, REC = HD + 2, THREADS = NW * 32;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ int s_last;
-    const int sp = blockIdx.x, j = blockIdx.y / chunks, ck = blockIdx.y - j * chunks, t = blockIdx.z;
+    const int j = blockIdx.y / chunks, ck = blockIdx.y - j * chunks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int Hkv = a.kv.n_kv_head, G = a.H / Hkv, h0 = j * G + ck * GC, gn = min(GC, G - ck * GC);
     pdl_wait();
     pdl_trigger();
-    const int pos = a.pos[t], seq = a.seq[t];
-    const bool ok = pos >= 0 && pos < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
-    if (!ok && tid == 0 && sp == 0 && blockIdx.y == 0) raise_error(a.err, ERRF_BAD_INDEX);
-    const int lo = (ok && a.window > 0 && pos + 1 > a.window) ? pos + 1 - a.window : 0;
-    const int S = ok ? pos + 1 - lo : 0;
-    const int chunk = split_chunk(S, a.n_split);
-    const int n_eff = S > 0 ? (S + chunk - 1) / chunk : 1;
-    if (!CL && sp >= n_eff) return;                   // a cluster's CTAs stay for its barriers
-    const int kb = lo + sp * chunk, ke = min(lo + S, kb + chunk);
-    const size_t row0 = ok ? ((size_t)seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * HD) / HD : 0;   // rows before the head's
+    int sp = blockIdx.x, t = blockIdx.z, pos, seq, n_eff;
+    Row rw;
+    int len;                                          // groups of a split
+    if constexpr (CL) {
+        pos = a.pos[t];
+        seq = a.seq[t];
+        rw = row_keys(a, pos, seq);
+        len = max(MIN_GRP, (rw.groups() + a.n_split - 1) / a.n_split);
+        n_eff = a.n_split;                            // all stay for the cluster's barriers
+    } else {
+        sp = find_split(a, blockIdx.x, lane, t, rw, pos, seq, len, n_eff);
+        if (sp < 0) return;
+    }
+    if (!rw.ok && tid == 0 && sp == 0 && blockIdx.y == 0) raise_error(a.err, ERRF_BAD_INDEX);
+    const long long at = (long long)sp * len * KG;    // first key of the split
+    const int kb = rw.lo + (int)min((long long)rw.S, at), ke = rw.lo + (int)min((long long)rw.S, at + (long long)len * KG);
+    const size_t row0 = rw.ok ? ((size_t)seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * HD) / HD : 0;   // rows before the head's
 
     // ---- this warp's groups: keys kb + KG (warp + NW i)
     uint8_t *ring = smem_raw + (size_t)warp * NST * R::STAGE;
@@ -399,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     // records of a split: numerators, sum, maximum
     const bool one = !CL && n_eff == 1;
     float *rec = reinterpret_cast<float *>(smem_raw + R::WGT);             // CL: this CTA's records, [GC][REC]
-    float *part = CL ? rec : a.part + ((size_t)(t * a.H + h0) * a.n_split + sp) * REC;
+    float *part = CL ? rec : a.part + ((size_t)h0 * a.n_split + blockIdx.x) * REC;
     const size_t part_head = CL ? REC : (size_t)a.n_split * REC;
     for (int i = tid; i < gn * (HD / 2); i += THREADS) {
         const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
@@ -477,7 +564,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 2 : 1) attn_decode_q4_kerne
     // ---- last CTA of this (row, kv head, chunk): each thread asks for its two
     // dimensions of the first MERGE_AHEAD splits while the warps find the splits'
     // weights, then sums them in split order
-    const float *all = a.part + (size_t)(t * a.H + h0) * a.n_split * REC;
+    const float *all = a.part + ((size_t)h0 * a.n_split + (blockIdx.x - sp)) * REC;
     float2 v[MERGE_AHEAD];
     const int mh = tid / (HD / 2), md = 2 * (tid - mh * (HD / 2));
     if (mh < gn) {
@@ -611,65 +698,91 @@ __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, co
 
 }  // namespace
 
-int attn_q4_chunks(int H, int Hkv) { return (H / Hkv + GC - 1) / GC; }
+// How the keys are split.
+//
+// Short caches and many rows: every (row, kv head, chunk) has the same number
+// of splits, a power of two up to MAX_CLUSTER, and they are one cluster; about
+// two CTAs of 8 warps an SM in all.  The merge inside a cluster costs about a
+// microsecond less than the one through memory (one row of 2100 keys, 8 kv
+// heads of 128: 5.7 us, 6.3 in 16 splits through memory; eight rows of 4000
+// keys 12.9 and 14.7).
+//
+// Long caches: the rows share the splits by their lengths (find_split), merged
+// through memory.  One or two rows of 8 kv heads get one CTA of 16 warps an SM,
+// more rows two of 8.  One row of 8000 keys 7.6 us (a cluster of eight 8.2), of
+// 32000 keys 12.8 (two CTAs of 8 warps, 32 splits: 14.8, as 104 SMs had two of
+// them and 48 one; 38 splits 15.9 for their merge); two rows of 8000 and 5000
+// keys 9.1 (clusters 10.0); eight rows of 1000 to 30000 keys 32 us (clusters of
+// four, whose CTAs wait for the longest row's, 56).  Eight rows of 4000 keys in
+// a cache of 8192 still are faster as clusters, so more than two rows share
+// from 2 CLUSTER_CTX positions on.
+namespace {
 
-// Splits of a (row, kv head, chunk): about two CTAs an SM in all.  Up to
-// MAX_CLUSTER splits (a power of two) are one cluster, whose merge costs about
-// a microsecond less than the one through memory (eight rows of 748 to 3415
-// keys, 8 kv heads: 10.4 us, 11.6 merged through memory), and a cache of at
-// most CLUSTER_CTX positions always takes that (one row: 2100 keys 5.9 us in a
-// cluster of 8, 6.9 in 32 splits; 8000 keys 8.2 and 8.4; two rows of 8000 and
-// 5000 keys 10.1 and 9.4 in 19).  Beyond, the merge through memory asks for 32
-// splits at once and would pay another round trip for more (32000 keys: 38
-// splits 15.7 us, 32 splits 14.7), so more only where fewer leave SMs without
-// work.
-int attn_q4_pick_split(int T, int H, int Hkv, int n_ctx) {
-    const int mx = (n_ctx + MIN_KEYS - 1) / MIN_KEYS;
-    const long long units = (long long)T * Hkv * attn_q4_chunks(H, Hkv);
-    long long s = 2LL * SMS / units;
-    if (s > MERGE_AHEAD && units * MERGE_AHEAD >= SMS) s = MERGE_AHEAD;
-    if (s > MAX_CLUSTER && n_ctx <= CLUSTER_CTX) s = MAX_CLUSTER;
-    if (s > MAX_SPLIT) s = MAX_SPLIT;
-    if (s > mx) s = mx;
-    if (s < 1) s = 1;
-    if (s <= MAX_CLUSTER)
+int chunks_of(int H, int Hkv) { return (H / Hkv + GC - 1) / GC; }
+
+struct Plan { int n_split, warps; bool cluster; };
+
+Plan plan_of(int T, int H, int Hkv, int n_ctx) {
+    const long long heads = (long long)Hkv * chunks_of(H, Hkv), units = T * heads;
+    const long long most = std::max(1, n_ctx / (MIN_GRP * KG) + (n_ctx % (MIN_GRP * KG) > 0));   // splits of a row
+    const bool wide = H / Hkv > 4;
+    Plan p;
+    p.cluster = n_ctx <= (8 * units <= SMS ? 1 : 2) * CLUSTER_CTX || T > BALANCE_T || units > BALANCE_UNITS || (long long)T * n_ctx > 1ll << 34;
+    if (p.cluster) {
+        long long s = std::min((wide ? 1ll : 2ll) * SMS / units, most);
+        s = std::min(std::max(s, 1ll), (long long)MAX_CLUSTER);
         while (s & (s - 1)) ++s;
-    return (int)s;
+        p.n_split = (int)s;
+        p.warps = 8;
+    } else {
+        p.warps = !wide && 8 * units <= SMS ? 16 : 8;
+        const long long s = (wide || p.warps == 16 ? 1 : 2) * SMS / heads;
+        p.n_split = (int)std::min(std::max(s, 2ll * T), T * std::min(most, (long long)MAX_SPLIT));
+    }
+    return p;
 }
 
-size_t attn_q4_part_floats(int T, int H, int hd, int n_split) { return (size_t)T * H * n_split * (hd + 2); }
+}  // namespace
 
-cudaError_t launch_attn_decode_q4(const AttnDecodeArgs &a, const Launch &l) {
+size_t attn_q4_scratch_bytes(int T, int H, int Hkv, int hd, int n_ctx) {
+    const Plan p = plan_of(T, H, Hkv, n_ctx);
+    return BALANCE_UNITS * sizeof(unsigned) + (p.cluster ? 0 : (size_t)p.n_split * H * (hd + 2) * sizeof(float));
+}
+
+cudaError_t launch_attn_decode_q4(AttnDecodeArgs a, void *scratch, const Launch &l) {
     const int Hkv = a.kv.n_kv_head;
-    if (a.T < 1 || a.T > 65535 || a.n_split < 1 || a.n_split > MAX_SPLIT || Hkv < 1 || a.H % Hkv || !a.kv.k4)
-        return cudaErrorInvalidValue;
-    const int chunks = attn_q4_chunks(a.H, Hkv);
+    if (a.T < 1 || a.T > 65535 || Hkv < 1 || a.H % Hkv || !a.kv.k4) return cudaErrorInvalidValue;
+    const int chunks = chunks_of(a.H, Hkv);
     if ((long long)Hkv * chunks > 65535) return cudaErrorInvalidValue;
-    const dim3 grid(a.n_split, Hkv * chunks, a.T), block(THREADS);
-    // four heads fill the 8 columns of a tile; larger groups take two tiles
-#define Q4_DEC_CASE(HDV)                                                                                             \
-    if (a.kv.head_dim == HDV) {                                                                                      \
-        const size_t smem = Ring<HDV>::SMEM;                                                                         \
-        const bool small = a.H / Hkv <= 4;                                                                           \
-        if (a.n_split <= MAX_CLUSTER)                                                                                \
-            return launch_cluster_kernel(small ? attn_decode_q4_kernel<HDV, 1, true> : attn_decode_q4_kernel<HDV, 2, true>, \
-                                         grid, block, a.n_split, smem, l, a, chunks);                                \
-        return launch_kernel(small ? attn_decode_q4_kernel<HDV, 1, false> : attn_decode_q4_kernel<HDV, 2, false>,    \
-                             grid, block, smem, l, a, chunks);                                                       \
-    }
+    const Plan p = plan_of(a.T, a.H, Hkv, a.kv.n_ctx);
+    a.n_split = p.n_split;
+    a.counters = (unsigned *)scratch;
+    a.part = (float *)(a.counters + BALANCE_UNITS);
+    const bool wide = a.H / Hkv > 4;                  // four heads fill the 8 columns of a tile; larger groups take two tiles
+    const dim3 grid(p.n_split, Hkv * chunks, p.cluster ? a.T : 1), block(p.warps * 32);
+#define Q4_DEC_CASE1(HDV, NT, NW)                                                                                     \
+    if (a.kv.head_dim == HDV && wide == (NT == 2) && p.warps == NW && !p.cluster)                                     \
+        return launch_kernel(attn_decode_q4_kernel<HDV, NT, NW, false>, grid, block, Ring<HDV, NW>::SMEM, l, a, chunks);
+#define Q4_DEC_CASE(HDV)                                                                                              \
+    if (a.kv.head_dim == HDV && p.cluster)                                                                            \
+        return launch_cluster_kernel(wide ? attn_decode_q4_kernel<HDV, 2, 8, true> : attn_decode_q4_kernel<HDV, 1, 8, true>, \
+                                     grid, block, p.n_split, Ring<HDV, 8>::SMEM, l, a, chunks);                       \
+    Q4_DEC_CASE1(HDV, 1, 8) Q4_DEC_CASE1(HDV, 1, 16) Q4_DEC_CASE1(HDV, 2, 8)
     Q4_DEC_CASE(32) Q4_DEC_CASE(64) Q4_DEC_CASE(128)
 #undef Q4_DEC_CASE
+#undef Q4_DEC_CASE1
     return cudaErrorInvalidValue;
 }
 
 cudaError_t init_attn_q4_attributes() {
     cudaError_t e = cudaSuccess;
-#define Q4_DEC_ATTR1(HDV, NT, CL)                                                              \
-    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT, CL>, Ring<HDV>::SMEM);               \
-    if (!e) e = cudaFuncSetAttribute(attn_decode_q4_kernel<HDV, NT, CL>, cudaFuncAttributePreferredSharedMemoryCarveout, \
-                                     cudaSharedmemCarveoutMaxShared);
-#define Q4_DEC_ATTR(HDV) \
-    Q4_DEC_ATTR1(HDV, 1, false) Q4_DEC_ATTR1(HDV, 2, false) Q4_DEC_ATTR1(HDV, 1, true) Q4_DEC_ATTR1(HDV, 2, true)
+#define Q4_DEC_ATTR1(HDV, NT, NWV, CL)                                                         \
+    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT, NWV, CL>, Ring<HDV, NWV>::SMEM);     \
+    if (!e) e = cudaFuncSetAttribute(attn_decode_q4_kernel<HDV, NT, NWV, CL>,                  \
+                                     cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+#define Q4_DEC_ATTR(HDV)                                                                        \
+    Q4_DEC_ATTR1(HDV, 1, 8, true) Q4_DEC_ATTR1(HDV, 1, 8, false) Q4_DEC_ATTR1(HDV, 1, 16, false) \
+    Q4_DEC_ATTR1(HDV, 2, 8, true) Q4_DEC_ATTR1(HDV, 2, 8, false)
     Q4_DEC_ATTR(32) Q4_DEC_ATTR(64) Q4_DEC_ATTR(128)
 #undef Q4_DEC_ATTR
 #undef Q4_DEC_ATTR1

@@ -341,13 +341,12 @@ cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l);
 cudaError_t launch_kv_shift_q4(const KvView &kv0, int n_layer, int seq, int p0, int n, int end, const float2 *rope,
                                const Launch &l);
 
-// Decode attention over a Q4_0 cache (AttnDecodeArgs with kv.k4 set; any T,
-// any H / Hkv).  part: attn_q4_part_floats; counters: T * Hkv * head chunks,
-// zero before the first launch and left zero.
-int attn_q4_pick_split(int T, int H, int Hkv, int n_ctx);
-int attn_q4_chunks(int H, int Hkv);
-size_t attn_q4_part_floats(int T, int H, int hd, int n_split);
-cudaError_t launch_attn_decode_q4(const AttnDecodeArgs &a, const Launch &l);
+// Decode attention over a Q4_0 cache (AttnDecodeArgs with kv.k4 set, the splits
+// and their memory chosen by the launch; any T, any H / Hkv).  scratch:
+// attn_q4_scratch_bytes of the shape, its counters at the front whatever the
+// shape: zero before the first launch, left ready for the next.
+size_t attn_q4_scratch_bytes(int T, int H, int Hkv, int hd, int n_ctx);
+cudaError_t launch_attn_decode_q4(AttnDecodeArgs a, void *scratch, const Launch &l);
 
 // Key ranges [lo, hi) of sequences to widen from a Q4_0 cache to fp16.
 struct KvSpan { int seq, lo, hi; };

@@ -130,7 +130,7 @@ struct llm_ctx {
     // scales (9/16 byte an element); decode attention's split scratch; prefill
     // widens a layer's visible rows into k16, v16 [seq][kv_head][n_pad][hd]
     bool kv_q4 = false;
-    float *q4_part = nullptr; unsigned *q4_cnt = nullptr;
+    void *q4_scratch = nullptr;
     f16 *k16 = nullptr, *v16 = nullptr;
     int n_pad = 0;
     TmaMap ak16, av16;
@@ -481,7 +481,7 @@ static void ctx_release(llm_ctx *c) {
     void *dev[] = {c->kc, c->vc, c->rope, c->rope_t, c->h, c->h2, c->ss, c->ss2, c->qf, c->x, c->qb, c->o, c->u,
                    c->gemv_part, c->gemv_cnt, c->sk_ws, c->sk_flags, c->attn_part, c->attn_cnt, c->meta_dev, c->dec_dev,
                    c->logits, c->argmax_dev, c->gen_tokens, c->err_dev,
-                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->q4_part, c->q4_cnt,
+                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->q4_scratch,
                    c->k16, c->v16};
     for (void *p : dev) if (p) cudaFree(p);
     for (int i = 0; i < 2; ++i) {
@@ -818,9 +818,7 @@ cudaError_t attn_decode(llm_ctx *c, const UbDev &u, int layer) {
     at.q = c->qf; at.kv = kv_view(c, layer); at.pos = u.pos; at.seq = u.seq; at.o = c->o; at.T = u.T; at.H = m->H;
     at.err = c->err_dev; at.window = c->swa_window;
     if (c->kv_q4) {
-        at.n_split = attn_q4_pick_split(u.T, m->H, m->Hkv, c->n_ctx);
-        at.part = c->q4_part; at.counters = c->q4_cnt;
-        return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode_q4(at, lnch_attn(c)); });
+        return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode_q4(at, c->q4_scratch, lnch_attn(c)); });
     }
     at.n_split = c->attn_split[u.T]; at.part = c->attn_part; at.counters = c->attn_cnt;
     return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode(at, lnch_attn(c)); });
@@ -1593,21 +1591,17 @@ static int32_t set_kv_q4(llm_ctx *c, bool want) {
     const size_t bytes = want ? c->kv_elems / 2 + c->kv_elems / 16 : c->kv_elems * sizeof(f16);
     const int n_pad = (c->n_ctx + 127) / 128 * 128, nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
     const size_t plane = (size_t)c->n_seq_max * m->Hkv * n_pad * m->hd * sizeof(f16);
-    size_t part = 0, cnt = 0;
-    for (int T = 1; T <= 8; ++T) {
-        part = std::max(part, attn_q4_part_floats(T, m->H, m->hd, attn_q4_pick_split(T, m->H, m->Hkv, c->n_ctx)));
-        cnt = std::max(cnt, (size_t)T * m->Hkv * attn_q4_chunks(m->H, m->Hkv));
-    }
-    void *p[7] = {nullptr};
-    const size_t need[7] = {bytes, bytes, plane, plane, part * sizeof(float), cnt * sizeof(unsigned),
-                            c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
-    const int n = want ? 7 : 2;
+    size_t scratch = 0;
+    for (int T = 1; T <= 8; ++T) scratch = std::max(scratch, attn_q4_scratch_bytes(T, m->H, m->Hkv, m->hd, c->n_ctx));
+    void *p[6] = {nullptr};
+    const size_t need[6] = {bytes, bytes, plane, plane, scratch, c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
+    const int n = want ? 6 : 2;
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) ok = !need[i] || cudaMalloc(&p[i], need[i]) == cudaSuccess;
     if (ok) {
         cudaStreamSynchronize(c->stream);
         ok = cudaMemsetAsync(p[0], 0, bytes, c->stream) == cudaSuccess && cudaMemsetAsync(p[1], 0, bytes, c->stream) == cudaSuccess &&
-             (!want || cudaMemsetAsync(p[5], 0, need[5], c->stream) == cudaSuccess);
+             (!want || cudaMemsetAsync(p[4], 0, need[4], c->stream) == cudaSuccess);
     }
     if (!ok) {
         cudaGetLastError();
@@ -1615,11 +1609,11 @@ static int32_t set_kv_q4(llm_ctx *c, bool want) {
         return fail(c, LLM_ERR_ALLOC, "KV cache reallocation failed");
     }
     cudaFree(c->kc); cudaFree(c->vc);
-    cudaFree(c->k16); cudaFree(c->v16); cudaFree(c->q4_part); cudaFree(c->q4_cnt);
+    cudaFree(c->k16); cudaFree(c->v16); cudaFree(c->q4_scratch);
     c->kc = (f16 *)p[0]; c->vc = (f16 *)p[1];
     c->k16 = (f16 *)p[2]; c->v16 = (f16 *)p[3]; c->n_pad = want ? n_pad : 0;
-    c->q4_part = (float *)p[4]; c->q4_cnt = (unsigned *)p[5];
-    if (p[6]) c->qkv = (float *)p[6];
+    c->q4_scratch = p[4];
+    if (p[5]) c->qkv = (float *)p[5];
     c->kv_q4 = want;
     make_attn_maps(c);
     drop_graphs(c);

@@ -154,9 +154,7 @@ extern "C" int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, co
 extern "C" int64_t llm_op_attn_decode_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
                                                          int32_t n_seq) {
     if (shape_error(T, H, Hkv, hd, n_ctx, n_seq) || T > DECODE_MAX_T) return LLM_ERR_INVALID;
-    const int split = attn_q4_pick_split(T, H, Hkv, n_ctx);
-    return (int64_t)(attn_q4_part_floats(T, H, hd, split) * sizeof(float) +
-                     (size_t)T * Hkv * attn_q4_chunks(H, Hkv) * sizeof(unsigned));
+    return (int64_t)attn_q4_scratch_bytes(T, H, Hkv, hd, n_ctx);
 }
 
 extern "C" int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void *v_cache, const int32_t *pos,
@@ -177,11 +175,8 @@ extern "C" int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, 
     at.q = q;
     at.kv = q4_view(k_cache, v_cache, Hkv, hd, n_ctx, n_seq);
     at.pos = pos; at.seq = seq; at.o = (f16 *)o; at.T = T; at.H = H;
-    at.n_split = attn_q4_pick_split(T, H, Hkv, n_ctx);
-    at.part = (float *)scratch;
-    at.counters = (unsigned *)(at.part + attn_q4_part_floats(T, H, hd, at.n_split));
     at.err = err; at.window = window;
-    return launched(who, launch_attn_decode_q4(at, overlapped(stream)));
+    return launched(who, launch_attn_decode_q4(at, scratch, overlapped(stream)));
 }
 
 // scratch: K, then V widened [n_seq][Hkv][padded n_ctx][hd], tiles, spans

@@ -365,6 +365,69 @@ def test_attn_decode_rows_outside(lib):
         assert np.all(np.abs(got[ok] - c.ref) <= c.tol)
 
 
+def shared(n, n_ctx, seed):
+    """Positions of n rows, among them the first, the last and short ones."""
+    pos = np.random.default_rng(seed).integers(0, n_ctx, n)
+    pos[0], pos[-1], pos[n // 2] = n_ctx - 1, 0, 15
+    return [int(p) for p in pos]
+
+
+@pytest.mark.parametrize("hd,H,Hkv,n_ctx,T,window", [
+    (128, 8, 2, 8300, 3, 0), (128, 8, 8, 8200, 2, 0), (64, 8, 2, 8200, 33, 0), (32, 2, 1, 8200, 128, 0),
+    (32, 2, 1, 8200, 129, 0), (64, 16, 2, 8300, 5, 0), (32, 40, 2, 8200, 9, 3000), (128, 4, 1, 40000, 2, 0),
+])
+def test_attn_decode_rows_share_splits(lib, hd, H, Hkv, n_ctx, T, window):
+    """Rows of unlike lengths over a long cache: each takes its share of the launch."""
+    c = Decode(lib, hd, H, Hkv, n_ctx, 2, shared(T, n_ctx, T), [i % 2 for i in range(T)], window)
+    for _ in range(2):
+        c.call()
+        c.check()
+    # equal rows, and one long row among empty ones
+    for pos in ([n_ctx - 1] * T, [1] * (T - 1) + [n_ctx - 1]):
+        c.posd.copy_(ints(pos))
+        got = []
+        for _ in range(2):
+            c.call()
+            got.append(c.o.cpu().double().numpy())
+        assert np.array_equal(*got, equal_nan=True)            # cells hidden in the first call may hold NaN
+        if pos[0] == n_ctx - 1:                                # row 0 sees what it saw before
+            assert np.all(np.abs(got[0][:1] - c.ref[:1]) <= c.tol[:1])
+    assert int(c.err) == 0
+
+
+def test_attn_decode_rows_outside_share_splits(lib):
+    pos, seq, n_ctx = [8300, 8000, -1, 20, 5, 8199], [0, 0, 1, 1, 2, -1], 8300
+    c = Decode(lib, 64, 8, 2, n_ctx, 2, [8000, 20], [0, 1])
+    q = dev(np.concatenate([np.full((1, 512), np.nan, np.float32), c.q[:1], np.zeros((1, 512), np.float32), c.q[1:],
+                            np.ones((2, 512), np.float32)]))
+    o = torch.full((6, 512), 9.0, dtype=torch.float16, device="cuda")
+    p, s = ints(pos), ints(seq)
+    scratch = torch.zeros(lib.llm_op_attn_decode_q4_0_scratch_bytes(6, 8, 2, 64, n_ctx, 2), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        c.err.zero_()
+        assert lib.llm_op_attn_decode_q4_0(q.data_ptr(), c.kc.data_ptr(), c.vc.data_ptr(), p.data_ptr(), s.data_ptr(),
+                                           o.data_ptr(), 6, 8, 2, 64, n_ctx, 2, 0, scratch.data_ptr(), scratch.numel(),
+                                           c.err.data_ptr(), stream()) == 0
+        got = o.cpu().double().numpy()
+        assert int(c.err) == 2 and np.all(got[[0, 2, 4, 5]] == 0)
+        assert np.all(np.abs(got[[1, 3]] - c.ref) <= c.tol)
+
+
+def test_attn_decode_scratch_of_any_shape(lib):
+    """One scratch, zeroed once, for calls of different shapes in turn."""
+    a = Decode(lib, 128, 32, 8, 9000, 1, [8999], [0])
+    b = Decode(lib, 64, 8, 2, 8300, 2, shared(9, 8300, 1), [i % 2 for i in range(9)])
+    d = Decode(lib, 32, 4, 2, 100, 1, [99, 3], [0, 0])
+    size = max(x.scratch.numel() for x in (a, b, d))
+    scratch = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for x in (a, b, d):
+        x.scratch = scratch
+    for x in (a, b, a, d, b, d, a):
+        x.o.fill_(9.0)
+        x.call()
+        x.check()
+
+
 def test_attn_decode_streams_and_graphs(lib):
     """Two calls at once on two streams, each with its own scratch, and a captured call replayed after its inputs moved."""
     a, b = Decode(lib, 128, 32, 8, 3000, 1, [2999], [0]), Decode(lib, 64, 8, 2, 800, 2, [799, 3], [0, 1], seed=4)
