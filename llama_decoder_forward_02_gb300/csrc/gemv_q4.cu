@@ -117,8 +117,9 @@ struct Widen {
 
 constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : 1; }
 
-// XS: x in shared memory; NST: ring stages of a warp
-template <int EPI, bool XS, int NST>
+// XS: x in shared memory; NST: ring stages of a warp; ONE: one row of x, so the
+// odd columns' sums are not kept (28672 x 4096 17.7 us, with them 18.2)
+template <int EPI, bool XS, int NST, bool ONE>
 __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a, const Plan p, const int early) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     // the warp's number from a shuffle: what follows from it is then known to be the same for its lanes
@@ -282,9 +283,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
                         mma0(s, wd.low(wg), wd.low(wh), wd.low(sg), wd.low(sh), x.x, x.z);
                         mma(s, wd.high(wg), wd.high(wh), wd.high(sg), wd.high(sh), x.y, x.w);
                         y[i][0] = fmaf(dg, s[0], y[i][0]);
-                        y[i][1] = fmaf(dg, s[1], y[i][1]);
+                        if (!ONE) y[i][1] = fmaf(dg, s[1], y[i][1]);
                         y[i][2] = fmaf(dh, s[2], y[i][2]);
-                        y[i][3] = fmaf(dh, s[3], y[i][3]);
+                        if (!ONE) y[i][3] = fmaf(dh, s[3], y[i][3]);
                     }
                 }
             }
@@ -296,8 +297,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             float *mine = sums + cu * p.red_warp + 2 * t4 * RED_COL + g;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mine[16 * i] = y[i][0]; mine[16 * i + RED_COL] = y[i][1];
-                mine[16 * i + 8] = y[i][2]; mine[16 * i + 8 + RED_COL] = y[i][3];
+                mine[16 * i] = y[i][0];
+                mine[16 * i + 8] = y[i][2];
+                if (!ONE) { mine[16 * i + RED_COL] = y[i][1]; mine[16 * i + 8 + RED_COL] = y[i][3]; }
             }
         }
         // once a tile: the readers of these sums are done before the next but one overwrites them
@@ -372,24 +374,30 @@ cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Laun
     if (a.T < 1 || a.T > 8 || ctas < 1 || a.N % row_unit(epi) || !make_plan(a.N, a.K, a.T, ctas, &p))
         return cudaErrorInvalidValue;
     const dim3 grid(ctas), block(THREADS);
-#define Q4_GEMV(E)                                                                                             \
-    if (epi == E)                                                                                              \
-        return !p.x_smem    ? launch_kernel(gemv_q4_kernel<E, false, 4>, grid, block, p.smem, l, a, p, (int)early) \
-               : p.nst == 4 ? launch_kernel(gemv_q4_kernel<E, true, 4>, grid, block, p.smem, l, a, p, (int)early)  \
-                            : launch_kernel(gemv_q4_kernel<E, true, 3>, grid, block, p.smem, l, a, p, (int)early);
+#define Q4_GEMV1(E, XS, NST)                                                                              \
+    return a.T == 1 ? launch_kernel(gemv_q4_kernel<E, XS, NST, true>, grid, block, p.smem, l, a, p, (int)early) \
+                    : launch_kernel(gemv_q4_kernel<E, XS, NST, false>, grid, block, p.smem, l, a, p, (int)early);
+#define Q4_GEMV(E)                           \
+    if (epi == E) {                          \
+        if (!p.x_smem) Q4_GEMV1(E, false, 4) \
+        if (p.nst == 4) Q4_GEMV1(E, true, 4) \
+        Q4_GEMV1(E, true, 3)                 \
+    }
     Q4_GEMV(EPI_STORE) Q4_GEMV(EPI_RESID) Q4_GEMV(EPI_SWIGLU)
 #undef Q4_GEMV
+#undef Q4_GEMV1
     return cudaErrorInvalidValue;
 }
 
 cudaError_t init_gemv_q4_attributes() {
     cudaError_t e = cudaSuccess;
-#define Q4_GEMV_ATTR(E)                                                       \
-    if (!e) e = allow_smem(gemv_q4_kernel<E, true, 4>, SMEM_CAP);             \
-    if (!e) e = allow_smem(gemv_q4_kernel<E, true, 3>, SMEM_CAP);             \
-    if (!e) e = allow_smem(gemv_q4_kernel<E, false, 4>, SMEM_CAP);
+#define Q4_GEMV_ATTR1(E, XS, NST)                                      \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, XS, NST, true>, SMEM_CAP); \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, XS, NST, false>, SMEM_CAP);
+#define Q4_GEMV_ATTR(E) Q4_GEMV_ATTR1(E, true, 4) Q4_GEMV_ATTR1(E, true, 3) Q4_GEMV_ATTR1(E, false, 4)
     Q4_GEMV_ATTR(EPI_STORE) Q4_GEMV_ATTR(EPI_RESID) Q4_GEMV_ATTR(EPI_SWIGLU)
 #undef Q4_GEMV_ATTR
+#undef Q4_GEMV_ATTR1
     return e;
 }
 
