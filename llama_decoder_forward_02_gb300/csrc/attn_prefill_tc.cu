@@ -340,6 +340,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     auto v_box = [&](int s, int i) { return base + C::V_OFF + (s * C::NB + i) * BOX; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (a.tiles_late) pdl_wait();
     // longest tiles (latest positions) first
     const AttnTile tl = a.tiles[a.n_tiles - 1 - (int)blockIdx.x];
     const int h = blockIdx.y, G = a.H / a.Hkv, j = h / G;

@@ -146,6 +146,7 @@ struct AttnPrefillTcArgs {
     f16 *o; int ldo;                        // o [rows][ldo], head h at column h*hd
     uint32_t *err;
     int window;                             // sliding window (0 = all earlier positions)
+    bool tiles_late = false;                // the kernel before this one writes the tiles
 };
 struct TmaMap;
 bool attn_prefill_tc_ok(int head_dim, bool fp8_cache);

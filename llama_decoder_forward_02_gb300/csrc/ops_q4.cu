@@ -235,7 +235,8 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
     KvSpan *dspans = (KvSpan *)(base + 2 * plane + align256((size_t)T * sizeof(AttnTile)));
     const KvView kv = q4_view(k_cache, v_cache, Hkv, hd, n_ctx, n_seq);
     cudaError_t e = cudaSuccess;
-    if (spans.size() <= KvRuns::MAX) {
+    const bool late = spans.size() <= KvRuns::MAX;    // a kernel writes the tiles, which the next may overlap
+    if (late) {
         e = launch_kv_widen_q4_runs(kv, runs, (int)spans.size(), longest, window, rows_max, dtiles, k16, v16, n_pad,
                                     overlapped(stream));
     } else {
@@ -256,7 +257,8 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
         at.tiles = dtiles; at.n_tiles = (int)tiles.size(); at.H = H; at.Hkv = Hkv; at.head_dim = hd;
         at.n_layer = 1; at.layer = 0; at.n_ctx = n_pad; at.n_seq = n_seq;
         at.o = (f16 *)o; at.ldo = H * hd; at.err = err; at.window = window;
-        e = launch_attn_prefill_tc(at, mq, mk, mv, L);
+        at.tiles_late = late;
+        e = launch_attn_prefill_tc(at, mq, mk, mv, Launch{L.stream, late, nullptr});
     } else if (!e) {
         AttnPrefillArgs at;
         at.q = (const f16 *)q;
