@@ -98,7 +98,7 @@ void llm_model_free(llm_model *m);
 /* Re-encode the model's matrices as Q8_0 or Q4_0 blocks.  Q4_0: the blocks and
  * the row layout stand with the 4-bit operators below; otherwise as Q8_0, but
  * that its rows (9 K / 16 bytes) are read by every step of 1..8 rows whose rows
- * are all outputs, 9/32 of the fp16 bytes.  Q8_0:  "LLama.cpp — how it
+ * are all outputs, 9/32 of the fp16 bytes.  Q8_0: "LLama.cpp — how it
  * works", section "The GGUF format (reference)", names Q8_0 among the
  * quantised tensor element types without giving its layout; the one taken:
  * each row of Wq, Wk, Wv, Wo, gate, up, down and the output projection is cut
@@ -584,9 +584,14 @@ int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, const int32_t
  * [T][H*hd]; any H that is a multiple of Hkv, up to 4096.  Cells outside a
  * row's visible positions may hold anything.  scratch: scratch_bytes bytes,
  * zeroed once before its first use; each call leaves it ready for the next, of
- * any shape it is large enough for, and calls that may overlap need one each.  A row whose pos
- * lies outside [0, n_ctx) or whose seq lies outside [0, n_seq) gives zeros and
- * ORs 2 into *err (DEVICE word or NULL). */
+ * any shape it is large enough for, and calls that may overlap need one each.
+ * q, the caches, o and scratch 16-byte aligned.  A row whose pos lies outside
+ * [0, n_ctx) or whose seq lies outside [0, n_seq) gives zeros and ORs 2 into
+ * *err (DEVICE word or NULL).  q, K, V and the weights enter the products with
+ * 22 bits, elements of q beyond +-65504 * sqrt(hd) / (16 log2(e)) (32,000 at
+ * head_dim 128) as that value.  The keys are split over the GPU by the rows'
+ * number and lengths: the same call gives the same bits, while a row's last
+ * bits may depend on the rows beside it. */
 int64_t llm_op_attn_decode_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
                                               int32_t n_seq);
 int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void *v_cache, const int32_t *pos,
@@ -598,9 +603,11 @@ int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void 
  * sequence seq[r] at position pos[r] and see the positions a decode row would.
  * pos, seq are HOST arrays, read before the call returns: the rows of a
  * sequence are consecutive with consecutive positions, else LLM_ERR_INVALID
- * before anything is enqueued.  o fp16 [T][H*hd].  scratch (contents need not
- * be initialised) takes the visible cells widened to fp16; calls that may
- * overlap need one each.  err: DEVICE word or NULL, ORed with 4 when a bounded
+ * before anything is enqueued.  o fp16 [T][H*hd].  K and V are rounded to fp16
+ * and the softmax weights, as over an fp16 cache, come from exponents rounded
+ * to fp16 (head_dim 64 and 128; 5e-4 of o's norm together).  q, the caches and
+ * o 16-byte aligned.  scratch (contents need not be initialised) takes the
+ * visible cells widened to fp16; calls that may overlap need one each.  err: DEVICE word or NULL, ORed with 4 when a bounded
  * wait of the kernel timed out.  For stream capture only with rows of at most
  * 64 sequences (a longer list is copied from host memory). */
 int64_t llm_op_attn_prefill_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,

@@ -3,6 +3,7 @@
 // a Q4_0 cache.  Argument checks come before any device work; nothing here
 // allocates device memory or waits for the stream.
 #include <algorithm>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -56,6 +57,7 @@ const char *shape_error(int T, int H, int Hkv, int hd, int n_ctx, int n_seq) {
     if (H > 4096) return "n_head must be at most 4096";
     if (n_ctx < 1 || n_seq < 1) return "n_ctx and n_seq must be positive";
     if (n_ctx > (1 << 30)) return "n_ctx must be at most 2^30";
+    if ((double)n_seq * Hkv * n_ctx * hd > 0x1p46) return "the cache has more than 2^46 elements";
     return nullptr;
 }
 
@@ -184,7 +186,7 @@ extern "C" int64_t llm_op_attn_prefill_q4_0_scratch_bytes(int32_t T, int32_t H, 
                                                           int32_t n_seq) {
     if (shape_error(T, H, Hkv, hd, n_ctx, n_seq)) return LLM_ERR_INVALID;
     const size_t plane = align256(cache_rows(n_seq, Hkv, padded_ctx(n_ctx)) * hd * sizeof(f16));
-    return (int64_t)(256 + 2 * plane + align256((size_t)T * sizeof(AttnTile)) + align256((size_t)n_seq * sizeof(KvSpan)));
+    return (int64_t)(256 + 2 * plane + align256((size_t)T * sizeof(AttnTile)) + align256((size_t)std::min(T, n_seq) * sizeof(KvSpan)));
 }
 
 extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void *v_cache, const int32_t *pos,
@@ -205,26 +207,33 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
     std::vector<AttnTile> tiles;
     std::vector<KvSpan> spans;
     KvRuns runs;
-    std::vector<int> span_of((size_t)n_seq, -1);
     int longest = 0;
-    for (int i = 0; i < T;) {
-        if (seq[i] < 0 || seq[i] >= n_seq) return refuse(who, "a sequence id is outside [0, n_seq)");
-        int j = i;
-        while (j < T && seq[j] == seq[i]) {
-            if (pos[j] < 0 || pos[j] >= n_ctx) return refuse(who, "a position is outside [0, n_ctx)");
-            if (j > i && pos[j] != pos[j - 1] + 1)
-                return refuse(who, "positions of a sequence's rows must be consecutive");
-            ++j;
+    try {
+        for (int i = 0; i < T;) {
+            if (seq[i] < 0 || seq[i] >= n_seq) return refuse(who, "a sequence id is outside [0, n_seq)");
+            int j = i;
+            while (j < T && seq[j] == seq[i]) {
+                if (pos[j] < 0 || pos[j] >= n_ctx) return refuse(who, "a position is outside [0, n_ctx)");
+                if (j > i && pos[j] != pos[j - 1] + 1)
+                    return refuse(who, "positions of a sequence's rows must be consecutive");
+                ++j;
+            }
+            const int lo = window > 0 && pos[i] + 1 > window ? pos[i] + 1 - window : 0, hi = pos[j - 1] + 1;
+            spans.push_back(KvSpan{seq[i], lo, hi});
+            longest = std::max(longest, hi - lo);
+            if (spans.size() <= KvRuns::MAX) runs.run[spans.size() - 1] = KvRuns::Run{i, j - i, seq[i], pos[i], (int)tiles.size()};
+            for (int r = i; r < j; r += rows_max)
+                tiles.push_back(AttnTile{r, std::min(rows_max, j - r), seq[i], pos[r], 0});
+            i = j;
         }
-        if (span_of[seq[i]] >= 0) return refuse(who, "the rows of a sequence must be consecutive");
-        span_of[seq[i]] = (int)spans.size();
-        const int lo = window > 0 && pos[i] + 1 > window ? pos[i] + 1 - window : 0, hi = pos[j - 1] + 1;
-        spans.push_back(KvSpan{seq[i], lo, hi});
-        longest = std::max(longest, hi - lo);
-        if (spans.size() <= KvRuns::MAX) runs.run[spans.size() - 1] = KvRuns::Run{i, j - i, seq[i], pos[i], (int)tiles.size()};
-        for (int r = i; r < j; r += rows_max)
-            tiles.push_back(AttnTile{r, std::min(rows_max, j - r), seq[i], pos[r], 0});
-        i = j;
+        std::vector<int> ids;
+        for (const KvSpan &s : spans) ids.push_back(s.seq);
+        std::sort(ids.begin(), ids.end());
+        if (std::adjacent_find(ids.begin(), ids.end()) != ids.end())
+            return refuse(who, "the rows of a sequence must be consecutive");
+    } catch (const std::bad_alloc &) {
+        set_global_error("llm_op_attn_prefill_q4_0: out of host memory");
+        return LLM_ERR_ALLOC;
     }
     if (cudaError_t e = init_kernel_attributes()) return launched(who, e);
     const Launch L{(cudaStream_t)stream, false, nullptr};
@@ -243,7 +252,8 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
         // copies from pageable memory: staged before the call returns
         e = cudaMemcpyAsync(dtiles, tiles.data(), tiles.size() * sizeof(AttnTile), cudaMemcpyHostToDevice, L.stream);
         if (!e) e = cudaMemcpyAsync(dspans, spans.data(), spans.size() * sizeof(KvSpan), cudaMemcpyHostToDevice, L.stream);
-        if (!e) e = launch_kv_widen_q4(kv, dspans, (int)spans.size(), longest, k16, v16, n_pad, L);
+        for (size_t i = 0; !e && i < spans.size(); i += 65535)
+            e = launch_kv_widen_q4(kv, dspans + i, (int)std::min<size_t>(65535, spans.size() - i), longest, k16, v16, n_pad, L);
     }
     if (!e && tc) {
         TmaMap mq, mk, mv;

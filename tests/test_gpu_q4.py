@@ -5,6 +5,10 @@ append, and attention over a Q4_0 cache.
 Tolerances are worst-case bounds of the arithmetic: half a step of the output
 type, and for the fp32 sums 2^-23 a step (tensor cores add by truncation) of
 the sum of magnitudes."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -411,6 +415,52 @@ def test_attn_decode_rows_outside_share_splits(lib):
         got = o.cpu().double().numpy()
         assert int(c.err) == 2 and np.all(got[[0, 2, 4, 5]] == 0)
         assert np.all(np.abs(got[[1, 3]] - c.ref) <= c.tol)
+
+
+def test_attn_decode_replayed_with_other_lengths(lib):
+    """A captured call takes its splits from the lengths it finds at the replay."""
+    a, b = (Decode(lib, 64, 8, 2, 8300, 2, shared(5, 8300, i), [0, 1, 0, 1, 0], seed=i) for i in (3, 4))
+    g = torch.cuda.CUDAGraph()
+    a.call()
+    with torch.cuda.graph(g):
+        a.call()
+    for x in (a, b):
+        for n in ("qd", "kc", "vc", "posd", "seqd"):
+            getattr(a, n).copy_(getattr(x, n))
+        a.o.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.all(np.abs(a.o.cpu().double().numpy() - x.ref) <= x.tol)
+
+
+FIRST_IN_CAPTURE = """
+import sys
+sys.path.insert(0, {root!r}); sys.path.insert(0, {tests!r})
+import torch
+import test_gpu_q4 as t
+import llama_decoder_forward_02_gb300 as lib
+d = t.Decode(lib, 64, 8, 2, {n_ctx}, 1, [40], [0])
+w = torch.zeros(64, 512, dtype=torch.float16, device="cuda")
+q, y = torch.zeros(64 * 288, dtype=torch.uint8, device="cuda"), torch.full((1, 64), 9.0, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    d.call()
+    assert lib.llm_op_quantize_q4_0(w.data_ptr(), 64, 512, q.data_ptr(), t.stream()) == 0
+    assert lib.llm_op_gemv_q4_0(q.data_ptr(), w.data_ptr(), y.data_ptr(), 64, 512, 1, 512, 64, t.stream()) == 0
+g.replay()
+d.check()
+assert not y.any()
+"""
+
+
+@pytest.mark.parametrize("n_ctx", [64, 5000])
+def test_first_calls_of_a_process_captured(lib, n_ctx):
+    """The calls' set-up of the device does not disturb a capture that runs before any other call."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_IN_CAPTURE.format(root=os.path.dirname(tests), tests=tests, n_ctx=n_ctx)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_attn_decode_scratch_of_any_shape(lib):

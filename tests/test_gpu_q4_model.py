@@ -127,6 +127,25 @@ def test_sequences_and_window(lib, shape, weights, cache):
     p.free()
 
 
+@pytest.mark.parametrize("shape,n_ctx", [(MED64, 8400), (WIDE, 4200)])
+def test_long_cache(lib, shape, n_ctx):
+    """A context whose rows share the keys' splits: sequences of unlike lengths, steps of one, two and eight rows."""
+    p = Both(lib, shape, 36, n_ctx=n_ctx, n_seq=3, n_ubatch=256, weights="q4", cache="q4")
+    lens = [400, 5, 130]
+    toks, seq = [], []
+    for s, n in enumerate(lens):
+        toks += list(synth.prompt(shape.n_vocab, 60 + s, n))
+        seq += [s] * n
+    out = np.zeros(len(toks), np.int8)
+    out[np.cumsum(lens) - 1] = 1
+    p.decode(toks, seq_id=seq, output=out)
+    for step in range(2):
+        p.decode([step], seq_id=[step])
+        p.decode([step, step + 1], seq_id=[0, 2], output=[1, 1])
+        p.decode(list(range(8)), seq_id=[0, 1, 2, 2, 1, 0, 0, 2], output=[1] * 8)
+    p.free()
+
+
 def test_generate_and_options(lib):
     """Greedy steps on the device equal the same steps one call at a time; the fp16 copies of Q4_0 weights give the
     same logits up to one rounding; both caches of the context are refused together and changed while empty only."""

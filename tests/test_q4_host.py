@@ -165,3 +165,20 @@ def test_oracle_head_norms_and_q4_model():
     h = rng.standard_normal((2, 64))
     a, b = (O.norm_operand(h, w["blk.0.attn_norm"], 1e-5, o) for o in (None, "fp16"))
     assert 0 < np.abs(a - b).max() <= np.abs(a).max() * 2.0 ** -11
+
+
+def test_cache_sizes_beyond_memory_refused():
+    """Sizes whose products pass 64 bits are refused, not wrapped."""
+    huge = (4096, 128, 1 << 30, (1 << 31) - 1)
+    assert lib.llm_op_kv_q4_0_bytes(*huge) == BAD
+    assert lib.llm_op_attn_prefill_q4_0_scratch_bytes(9, 4096, *huge) == BAD
+    assert lib.llm_op_attn_decode_q4_0_scratch_bytes(1, 4096, *huge) == BAD
+    assert lib.llm_op_kv_q4_0_bytes(1, 32, 1 << 30, 1 << 11) == 18 << 41
+
+
+def test_prefill_of_many_sequences_needs_no_table():
+    """A sequence's rows in two places are found whatever n_seq is (nothing of n_seq's size is kept on the host)."""
+    ph, sh = ((ctypes.c_int32 * 3)(*v) for v in ((0, 0, 1), (5, (1 << 31) - 2, 5)))
+    assert lib.llm_op_attn_prefill_q4_0(P, P, P, ph, sh, P, 3, 1, 1, 32, 64, (1 << 31) - 1, 0, P, 1 << 60, None,
+                                        None) == BAD
+    assert b"consecutive" in lib.llm_last_error(None)
