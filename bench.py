@@ -99,6 +99,12 @@ def kv_bytes(options):
     return next((KV_BYTES[o.partition("=")[0]] for o in options if o in ("kv_fp8=1", "kv_q4=1")), 2.0)
 
 
+def quantize(model, wtype, stream):
+    if wtype != "f16":
+        import llama_decoder_forward_02_gb300 as L
+        model.quantize({"q8_0": L.LLM_WTYPE_Q8_0, "q4_0": L.LLM_WTYPE_Q4_0}[wtype], stream=stream)
+
+
 def decode_bytes(s, positions, wb=2.0, kvb=2.0):
     """HBM bytes one decode token must move: every weight matrix once (wb B per
     element), one embedding row (fp16), the norm gains, K and V of positions
@@ -109,13 +115,13 @@ def decode_bytes(s, positions, wb=2.0, kvb=2.0):
     return sum(fixed + kvrow * (p + 1) + kvrow for p in positions)
 
 
-def decode_step_bytes(s, positions):
+def decode_step_bytes(s, positions, wb=2.0, kvb=2.0):
     """HBM bytes of one decode step over len(positions) rows (one per
-    sequence): every weight matrix once for all rows, one embedding row and
-    one fp32 logits row per row, and each row's K/V of positions 0..p read
-    and p written."""
-    kvrow = s.n_layer * s.n_head_kv * s.head_dim * 2 * 2
-    fixed = (s.n_layer * layer_matrix_params(s) + s.n_vocab * s.n_embd) * 2 + (2 * s.n_layer + 1) * s.n_embd * 2
+    sequence): every weight matrix once for all rows (wb B per element), one
+    embedding row and one fp32 logits row per row, and each row's K/V of
+    positions 0..p read and p written (kvb B per element)."""
+    kvrow = s.n_layer * s.n_head_kv * s.head_dim * 2 * kvb
+    fixed = round((s.n_layer * layer_matrix_params(s) + s.n_vocab * s.n_embd) * wb) + (2 * s.n_layer + 1) * s.n_embd * 2
     return fixed + sum(s.n_embd * 2 + s.n_vocab * 4 + kvrow * (p + 1) + kvrow for p in positions)
 
 
@@ -274,8 +280,7 @@ def run_ours(args, rank, world, local_rank):
         tensors = synth.make_weights(s, wl["seed"], dev)
     stream.synchronize()
     model = L.Model(s, tensors, stream=st)
-    if args.wtype != "f16":
-        model.quantize({"q8_0": L.LLM_WTYPE_Q8_0, "q4_0": L.LLM_WTYPE_Q4_0}[args.wtype], stream=st)
+    quantize(model, args.wtype, st)
     wb = WEIGHT_BYTES[args.wtype]
     del tensors
     torch.cuda.empty_cache()
@@ -409,6 +414,7 @@ def run_extra(name, cfg, args, world, dev, stream):
         tensors = synth.make_weights(s, cfg["seed"], dev)
     stream.synchronize()
     model = L.Model(s, tensors, stream=st)
+    quantize(model, args.wtype, st)
     del tensors
     torch.cuda.empty_cache()
     n_seq = cfg["n_seq"]
@@ -463,13 +469,16 @@ def run_extra(name, cfg, args, world, dev, stream):
     torch.cuda.empty_cache()
     hbm, tf_burst, tf_sust, peak_kind = peaks()
     pre, dec = sum(pre_ms) / steps, sum(dec_ms) / steps
-    dbytes = sum(decode_step_bytes(s, [n + k for n in lens]) for k in range(n_dec))
+    # Q8_0 rows serve one-row steps only
+    wb = 2.0 if args.wtype == "q8_0" and n_seq > 1 else WEIGHT_BYTES[args.wtype]
+    dbytes = sum(decode_step_bytes(s, [n + k for n in lens], wb, kv_bytes(args.option)) for k in range(n_dec))
     pflops = prefill_flops_seqs(s, lens, n_seq)
     return {
         "config": (f"{s.n_layer} layers, d {s.n_embd}, {s.n_head}/{s.n_head_kv} heads, head_dim {s.head_dim}, "
                    f"FFN {s.n_ff}, vocab {s.n_vocab}, {'tied' if s.tied_output else 'untied'} output; "
                    f"{n_seq} sequence(s) of {lens} prompt tokens in ubatches of {cfg['n_ubatch']} (n_ctx "
-                   f"{cfg['n_ctx']} each), then {n_dec} greedy decode steps of {n_seq} row(s); seed {cfg['seed']}"),
+                   f"{cfg['n_ctx']} each), then {n_dec} greedy decode steps of {n_seq} row(s); seed {cfg['seed']}"
+                   + (f"; weights {args.wtype}" if args.wtype != "f16" else "")),
         "steps": steps, "warmup": warm,
         "decode": {"tok_per_s": round(world * n_seq * n_dec / (dec / 1e3), 2), "ms_per_step": round(dec / n_dec, 4),
                    "hbm_roofline": {"bytes_per_step_avg": round(dbytes / n_dec), "achieved_gbs": round(dbytes / (dec / 1e3) / 1e9, 1),

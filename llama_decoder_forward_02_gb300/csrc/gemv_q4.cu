@@ -115,7 +115,7 @@ struct Widen {
     __device__ __forceinline__ uint32_t high(uint32_t w) const { return pick(w, m1, e1, 0x54805480u); }
 };
 
-constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : 1; }
+constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : epi == EPI_QKV ? 2 : 1; }
 
 // XS: x in shared memory; NST: ring stages of a warp; ONE: one row of x, so the
 // odd columns' sums are not kept (28672 x 4096 17.7 us, with them 18.2)
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     const int r0 = (int)((long long)blockIdx.x * (a.N / UNIT) / gridDim.x) * UNIT;
     const int nrows = (int)((long long)(blockIdx.x + 1) * (a.N / UNIT) / gridDim.x) * UNIT - r0;
     __shared__ float s_r[8];                         // the rows' RMSNorm factors
+    __shared__ int s_pos[8], s_seq[8];               // QKV: their cells, -1 where outside the cache
     __shared__ float s_sq[EPI == EPI_RESID ? CW : 1][8];   // sums of h^2 by row group
     const int chunks = a.K / q4::CHUNK;
     const int units = p.units, cu = warp % units, rg = warp / units, TR = RG * CW / units;
@@ -202,6 +203,13 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             r = 1.f / sqrtf(warp_sum(ss) / (float)a.K + a.eps);
         }
         if (lane == 0) s_r[warp] = r;
+        if (EPI == EPI_QKV && lane == 0) {
+            const int ps = a.pos[warp], sq = a.seq[warp];
+            const bool ok = ps >= 0 && ps < a.kv.n_ctx && sq >= 0 && sq < a.kv.n_seq;
+            if (!ok && blockIdx.x == 0) raise_error(a.err, ERRF_BAD_INDEX);
+            s_pos[warp] = ok ? ps : -1;
+            s_seq[warp] = sq;
+        }
     }
     if (XS) {
         const int per = a.K / 8, n = a.T * per;      // 16-byte pieces of x
@@ -309,10 +317,36 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         const bool in = row < nrows;
         int q = 0;
         for (int t = cu; t < a.T; t += units, ++q) {
+            float2 cs = make_float2(1.f, 0.f);       // QKV: the row pair's rotation
+            const bool cell = EPI != EPI_QKV || s_pos[t] >= 0;
+            if (EPI == EPI_QKV && in && cell && n < a.n_q + a.n_kv) {
+                const int hd = a.kv.head_dim;
+                cs = a.rope[(size_t)s_pos[t] * (hd / 2) + (n < a.n_q ? n : n - a.n_q) % hd / 2];
+            }
             float v = 0.f;
             for (int c = 0; c < units; ++c) v += sums[c * p.red_warp + t * RED_COL + lane];
             v *= s_r[t];
-            if (EPI == EPI_STORE) {
+            if (EPI == EPI_QKV) {
+                // lane pairs hold the elements of a rotation, 2i and 2i + 1
+                const float w = __shfl_xor_sync(0xffffffffu, v, 1);
+                if (n < a.n_q + a.n_kv) v = lane & 1 ? fmaf(v, cs.x, w * cs.y) : fmaf(v, cs.x, -w * cs.y);
+                const float up = __shfl_down_sync(0xffffffffu, v, 1);
+                if (in && cell) {
+                    if (n < a.n_q) {
+                        a.q_out[(size_t)t * a.n_q + n] = v;
+                    } else if (!(lane & 1)) {
+                        const bool is_k = n < a.n_q + a.n_kv;
+                        const int hd = a.kv.head_dim, c = n - a.n_q - (is_k ? 0 : a.n_kv), head = c / hd;
+                        const size_t off = (size_t)s_seq[t] * a.kv.seq_stride + ((size_t)head * a.kv.n_ctx + s_pos[t]) * hd + (c - head * hd);
+                        if (a.kv.k8) {
+                            *reinterpret_cast<uint16_t *>((is_k ? a.kv.k8 : a.kv.v8) + off) = pack_e4m3x2(v, up);
+                        } else {
+                            if (f16_bad(v) || f16_bad(up)) raise_error(a.err, ERRF_F16_RANGE);
+                            *reinterpret_cast<uint32_t *>((is_k ? a.kv.k : a.kv.v) + off) = pack_h2(v, up);
+                        }
+                    }
+                }
+            } else if (EPI == EPI_STORE) {
                 if (in) a.out[(size_t)t * a.ldo + n] = v;
             } else if (EPI == EPI_RESID) {
                 float h = 0.f;
@@ -383,7 +417,7 @@ cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Laun
         if (p.nst == 4) Q4_GEMV1(E, true, 4) \
         Q4_GEMV1(E, true, 3)                 \
     }
-    Q4_GEMV(EPI_STORE) Q4_GEMV(EPI_RESID) Q4_GEMV(EPI_SWIGLU)
+    Q4_GEMV(EPI_STORE) Q4_GEMV(EPI_RESID) Q4_GEMV(EPI_QKV) Q4_GEMV(EPI_SWIGLU)
 #undef Q4_GEMV
 #undef Q4_GEMV1
     return cudaErrorInvalidValue;
@@ -395,7 +429,7 @@ cudaError_t init_gemv_q4_attributes() {
     if (!e) e = allow_smem(gemv_q4_kernel<E, XS, NST, true>, SMEM_CAP); \
     if (!e) e = allow_smem(gemv_q4_kernel<E, XS, NST, false>, SMEM_CAP);
 #define Q4_GEMV_ATTR(E) Q4_GEMV_ATTR1(E, true, 4) Q4_GEMV_ATTR1(E, true, 3) Q4_GEMV_ATTR1(E, false, 4)
-    Q4_GEMV_ATTR(EPI_STORE) Q4_GEMV_ATTR(EPI_RESID) Q4_GEMV_ATTR(EPI_SWIGLU)
+    Q4_GEMV_ATTR(EPI_STORE) Q4_GEMV_ATTR(EPI_RESID) Q4_GEMV_ATTR(EPI_QKV) Q4_GEMV_ATTR(EPI_SWIGLU)
 #undef Q4_GEMV_ATTR
 #undef Q4_GEMV_ATTR1
     return e;

@@ -317,6 +317,10 @@ struct GemvQ4Args {
     // over its rows to ss_out[t * (CTAs of the launch, gemv_q4_ctas) + cta]
     float *hres; int ldh; const float *gain_next; f16 *xg_out; int ldxg; float *ss_out;
     f16 *u_out; int ldu;      // EPI_SWIGLU: rows as GU_GROUP interleaves gate and up
+    // EPI_QKV: rows [0, n_q) are queries, then n_kv key and n_kv value rows;
+    // queries and keys rotated, q to q_out [T][n_q], the rest to cell (seq, pos)
+    // of an fp16 or FP8 cache
+    float *q_out; int n_q, n_kv; KvView kv; const float2 *rope; const int *pos, *seq;
     uint32_t *err;
 };
 int gemv_q4_ctas(int epi, int N, int num_sms);

@@ -639,7 +639,7 @@ extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, 
     dmal((void **)&c->attn_cnt, (size_t)8 * m->Hkv * sizeof(unsigned));
     // Q4_0 steps and models with normed queries and keys store the QKV projection plainly
     c->q4_ok = m->qbuf && m->wtype == LLM_WTYPE_Q4_0;
-    if (m->nbuf || c->q4_ok) dmal((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float));
+    if (m->nbuf) dmal((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float));
     if (c->q4_ok) dmal((void **)&c->ss_q4, (size_t)8 * m->num_sms * sizeof(float));
     dmal((void **)&c->dec_dev, DEC_INTS * sizeof(int));
     dmal((void **)&c->err_dev, sizeof(uint32_t));
@@ -850,10 +850,15 @@ cudaError_t run_small_q4(llm_ctx *c, const UbDev &u) {
     };
     for (int l = 0; l < m->L; ++l) {
         const LayerW &w = m->layers[l];
-        if ((e = gemv(K_GEMV_QKV, EPI_STORE, w.q_qkv, m->n_qkv, d, c->x, true,
-                      [&](GemvQ4Args &a) { a.out = c->qkv; a.ldo = m->n_qkv; })))
+        // normed heads and the Q4_0 cache need whole heads or blocks at once, which the GEMV's epilogue does not hold
+        const bool plain = plain_qkv(c);
+        if ((e = gemv(K_GEMV_QKV, plain ? EPI_STORE : EPI_QKV, w.q_qkv, m->n_qkv, d, c->x, true, [&](GemvQ4Args &a) {
+                a.out = c->qkv; a.ldo = m->n_qkv;
+                a.q_out = c->qf; a.n_q = m->n_q; a.n_kv = m->n_kv; a.kv = kv_view(c, l);
+                a.rope = c->rope; a.pos = u.pos; a.seq = u.seq;
+            })))
             return e;
-        if ((e = qk_norm(c, u, l, false, lnch_attn(c)))) return e;
+        if (plain && (e = qk_norm(c, u, l, false, lnch_attn(c)))) return e;
         if ((e = attn_decode(c, u, l))) return e;
         if ((e = gemv(K_GEMV_O, EPI_RESID, w.q_o, d, m->n_q, c->o, false, [&](GemvQ4Args &a) { resid(a, w.ffn_norm); })))
             return e;
