@@ -33,8 +33,22 @@
 // in split order, by the cluster they form or, over long caches, by the CTA that
 // arrives last: results do not depend on timing and nothing spins.
 //
+//
+// Measured, calls in a row, 32 query and 8 kv heads of 128, and the time the
+// bytes take at the copy bandwidth: one row of 2100 keys 5.7 us (0.4), of 32000
+// keys 12.8 (5.4), eight rows of 748 to 3415 keys 10.4 (3.0).  Of the 12.8: 1.3
+// to q's fragments, 6.9 of loop (5.3 TB/s; schedulers issue in 49% of the SM's
+// clocks, ALU 41%, over the whole kernel), 0.9 for the warps' sums, 2.4 for the
+// count, the reads and the merge, 1.3 to the next call.
+//
 // Prefill: the visible rows of the ubatch's sequences are widened once to fp16
-// and the fp16 prefill attention runs on them.
+// and the fp16 prefill attention runs on them: 512 rows from position 1536 on
+// take 24.6 us, of which the attention's tensor work is 7.6 at the measured
+// rate.  A tile of it takes what its softmax takes, so widening inside it
+// would lengthen what bounds it, once for each of the G * tiles CTAs that read
+// the same keys.  Rounding d * (c - 8) to fp16 is what an fp16 cache holds; the
+// fp16 exponents of its softmax move o by as much (together 5e-4 of its norm,
+// 2e-4 of which is o's own rounding).
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -633,6 +647,8 @@ __device__ __forceinline__ uint4 widen_word(uint32_t word, float d) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// Widening reads 9/16 byte and writes two an element: bound by memory, 1.6 us at
+// the copy bandwidth for 2048 rows of 8 heads of 128.
 constexpr int WT = 256;
 
 // A thread's part of widening span sp: row block blockIdx.x, kv head blockIdx.y,

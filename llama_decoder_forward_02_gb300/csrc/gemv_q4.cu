@@ -16,7 +16,7 @@
 // codes are never rounded.  (Codes as fp16 subnormals c * 2^-24, with
 // 8 sum(x) taken off a block's sum, save the subtractions, but the tensor
 // cores truncate their addends to the largest one's exponent: y was 9e-7 off
-// instead of 4e-7, and x needed scaling and a table of sums before the first
+// instead of 1e-7, and x needed scaling and a table of sums before the first
 // product.)
 //
 // One CTA an SM owns a contiguous run of rows.  Its 16 warps are 16 / units
@@ -31,8 +31,23 @@
 // meet less often: the launcher takes the split with the fewest chunks a warp,
 // counting a meeting as a quarter of one (with 16 units throughout,
 // 128256 x 4096 took 83 us, a quarter of it in meetings).
-// (Bulk copies by a producer warp, one a row and step, took 26.7 us for
-// 28672 x 4096: about 130 clocks a copy of 1152 bytes.)
+//
+// Measured, calls in a row, one row of x where not said otherwise, and the time
+// the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 5.2 us (1.4),
+// 28672 x 4096 17.5 (9.7), 4096 x 14336 11.6 (4.9; 8 rows 12.0), 128256 x 4096
+// 57.3 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
+// 5.3, 16.1, 11.2, 11.3 and 54.5.  3 us of each go by before the first product
+// and after the last; in between the schedulers issue in 59% of their clocks
+// (ALU 46%, FMA 39%, tensor 26% of theirs) with four warps each, which wait for
+// the pipes and the shared-memory queue and hardly (0.1 of 6 warps) for memory.
+//
+// What was slower or no faster: bulk copies by a producer warp, one a row and
+// step (28672 x 4096 26.7 us: 130 clocks a copy of 1152 bytes); the columns that
+// a single row of x leaves unused taking other blocks (57.1 us for 128256 x
+// 4096, as without the odd columns' sums); two CTAs of half the warps an SM; steps
+// of 16 rows and whole chunks, whose copies run along the rows (64 lines a chunk
+// instead of 112: 55.9 us for 128256 x 4096, but 16.8 instead of 16.1 for 28672 x
+// 4096 and 11.9 instead of 11.2 for 4096 x 14336 as the forward pass runs them).
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"
@@ -73,8 +88,9 @@ bool make_plan(int N, int K, int T, int ctas, Plan *p) {
     const size_t red = (size_t)2 * CW * p->red_warp * sizeof(float);
     const size_t x = (size_t)T * (K + X_PAD) * sizeof(f16);
     // x beside four ring stages, or three (74 KB in flight on an SM, still above
-    // what the copy bandwidth needs at 1 us), where it fits; else each warp reads its fragments from L2 a
-    // step ahead: with so long a K a CTA has few row tiles to read x again for
+    // what the copy bandwidth needs at 1 us), where it fits; else each warp reads
+    // its fragments from L2 a step ahead: with so long a K a CTA has few row tiles
+    // to read x again for
     p->x_smem = x + red + ring_bytes(3) <= SMEM_CAP;
     p->nst = !p->x_smem || x + red + ring_bytes(4) <= SMEM_CAP ? 4 : 3;
     p->smem = ring_bytes(p->nst) + red + (p->x_smem ? x : 0);

@@ -14,9 +14,11 @@
 // pairs, one word of codes) a lane, so the norm's sum and a block's largest
 // magnitude are a few shuffles for several heads at once and every access is a
 // vector; a CTA takes a row, whose position, cosines and gains each lane reads
-// once.  Bound by memory: 4 bytes read and about 2 written an element.  (With
-// four elements a lane the shuffles, addresses and branches of twice as many
-// lanes took 42.7 us for 4096 rows of 48 heads, bound by issue.)
+// once.  Bound by memory: 4 bytes read and about 2 written an element.  4096
+// rows of 32 + 8 + 8 heads of 128 into an fp16 cache take 29.6 us, 76% of the
+// copy bandwidth for their 153 MB (five CTAs of 48 registers an SM; four took
+// 32.8).  With four elements a lane the shuffles, addresses and branches of
+// twice as many lanes took 42.7 us, bound by issue.
 //
 // Q4_0 codes are those of the exact values.  A float32 value carries a few
 // ulp of error from the norm and the rotation, which matters only next to a
