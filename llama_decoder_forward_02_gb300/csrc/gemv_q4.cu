@@ -61,15 +61,19 @@ constexpr int THREADS = CW * 32;
 constexpr int RG = 32;                       // rows of a warp's tile (two m16 tiles)
 constexpr int CODES = RG * 64;               // bytes of a step's codes in a warp's ring
 constexpr int SCALES = RG * 16;              // bytes of a chunk's scales
-constexpr int SC_SLOTS = 3;                  // chunks whose scales are held: NST - 1 <= 4 steps ahead touch three
-constexpr size_t ring_bytes(int nst) { return (size_t)CW * (nst * CODES + SC_SLOTS * SCALES); }
+// Ring stages of a warp: 64 KB of codes ahead on an SM.  A fourth delays x,
+// which queues behind the weights requested before it (4096 x 14336 11.6 us
+// instead of 11.0, 28672 x 4096 17.6 instead of 17.1, 8B decode 568 tok/s
+// instead of 577).
+constexpr int NST = 3;
+constexpr int SC_SLOTS = 3;                  // chunks whose scales are held: NST - 1 steps ahead touch at most three
+constexpr size_t RING_BYTES = (size_t)CW * (NST * CODES + SC_SLOTS * SCALES);
 constexpr int RED_COL = 36;                  // floats between columns of a warp's sums (bank-conflict free)
 constexpr size_t SMEM_CAP = 224 * 1024;
 constexpr int X_PAD = 32;                    // elements between rows of x in shared memory beyond K
 
 struct Plan {
     int units;           // warps that share a row tile's K
-    int nst;             // ring stages of a warp
     bool x_smem;         // x is staged in shared memory
     int red_warp;        // floats of a warp's sums of one row tile (two tiles' sums alternate)
     size_t smem;
@@ -87,13 +91,10 @@ bool make_plan(int N, int K, int T, int ctas, Plan *p) {
     p->red_warp = (T + 1) / 2 * 2 * RED_COL;
     const size_t red = (size_t)2 * CW * p->red_warp * sizeof(float);
     const size_t x = (size_t)T * (K + X_PAD) * sizeof(f16);
-    // x beside four ring stages, or three (74 KB in flight on an SM, still above
-    // what the copy bandwidth needs at 1 us), where it fits; else each warp reads
-    // its fragments from L2 a step ahead: with so long a K a CTA has few row tiles
-    // to read x again for
-    p->x_smem = x + red + ring_bytes(3) <= SMEM_CAP;
-    p->nst = !p->x_smem || x + red + ring_bytes(4) <= SMEM_CAP ? 4 : 3;
-    p->smem = ring_bytes(p->nst) + red + (p->x_smem ? x : 0);
+    // x beside the rings where it fits; else each warp reads its fragments from
+    // L2 a step ahead: with so long a K a CTA has few row tiles to read x again for
+    p->x_smem = x + red + RING_BYTES <= SMEM_CAP;
+    p->smem = RING_BYTES + red + (p->x_smem ? x : 0);
     return true;
 }
 
@@ -133,9 +134,9 @@ struct Widen {
 
 constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : epi == EPI_QKV ? 2 : 1; }
 
-// XS: x in shared memory; NST: ring stages of a warp; ONE: one row of x, so the
+// XS: x in shared memory; ONE: one row of x, so the
 // odd columns' sums are not kept (28672 x 4096 17.7 us, with them 18.2)
-template <int EPI, bool XS, int NST, bool ONE>
+template <int EPI, bool XS, bool ONE>
 __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a, const Plan p, const int early) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     // the warp's number from a shuffle: what follows from it is then known to be the same for its lanes
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     __shared__ float s_sq[EPI == EPI_RESID ? CW : 1][8];   // sums of h^2 by row group
     const int chunks = a.K / q4::CHUNK;
     const int units = p.units, cu = warp % units, rg = warp / units, TR = RG * CW / units;
-    float *red = reinterpret_cast<float *>(smem_raw + ring_bytes(NST));
+    float *red = reinterpret_cast<float *>(smem_raw + RING_BYTES);
     f16 *xs = reinterpret_cast<f16 *>(red + 2 * CW * p.red_warp);
 
     // ---- this warp's ring: rows r0 + (tile * ngroups + rg) * 32 .., chunk kc * units + cu
@@ -424,14 +425,13 @@ cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Laun
     if (a.T < 1 || a.T > 8 || ctas < 1 || a.N % row_unit(epi) || !make_plan(a.N, a.K, a.T, ctas, &p))
         return cudaErrorInvalidValue;
     const dim3 grid(ctas), block(THREADS);
-#define Q4_GEMV1(E, XS, NST)                                                                              \
-    return a.T == 1 ? launch_kernel(gemv_q4_kernel<E, XS, NST, true>, grid, block, p.smem, l, a, p, (int)early) \
-                    : launch_kernel(gemv_q4_kernel<E, XS, NST, false>, grid, block, p.smem, l, a, p, (int)early);
-#define Q4_GEMV(E)                           \
-    if (epi == E) {                          \
-        if (!p.x_smem) Q4_GEMV1(E, false, 4) \
-        if (p.nst == 4) Q4_GEMV1(E, true, 4) \
-        Q4_GEMV1(E, true, 3)                 \
+#define Q4_GEMV1(E, XS)                                                                              \
+    return a.T == 1 ? launch_kernel(gemv_q4_kernel<E, XS, true>, grid, block, p.smem, l, a, p, (int)early) \
+                    : launch_kernel(gemv_q4_kernel<E, XS, false>, grid, block, p.smem, l, a, p, (int)early);
+#define Q4_GEMV(E)                       \
+    if (epi == E) {                      \
+        if (p.x_smem) Q4_GEMV1(E, true)  \
+        Q4_GEMV1(E, false)               \
     }
     Q4_GEMV(EPI_STORE) Q4_GEMV(EPI_RESID) Q4_GEMV(EPI_QKV) Q4_GEMV(EPI_SWIGLU)
 #undef Q4_GEMV
@@ -441,10 +441,10 @@ cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Laun
 
 cudaError_t init_gemv_q4_attributes() {
     cudaError_t e = cudaSuccess;
-#define Q4_GEMV_ATTR1(E, XS, NST)                                      \
-    if (!e) e = allow_smem(gemv_q4_kernel<E, XS, NST, true>, SMEM_CAP); \
-    if (!e) e = allow_smem(gemv_q4_kernel<E, XS, NST, false>, SMEM_CAP);
-#define Q4_GEMV_ATTR(E) Q4_GEMV_ATTR1(E, true, 4) Q4_GEMV_ATTR1(E, true, 3) Q4_GEMV_ATTR1(E, false, 4)
+#define Q4_GEMV_ATTR1(E, XS)                                      \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, XS, true>, SMEM_CAP); \
+    if (!e) e = allow_smem(gemv_q4_kernel<E, XS, false>, SMEM_CAP);
+#define Q4_GEMV_ATTR(E) Q4_GEMV_ATTR1(E, true) Q4_GEMV_ATTR1(E, false)
     Q4_GEMV_ATTR(EPI_STORE) Q4_GEMV_ATTR(EPI_RESID) Q4_GEMV_ATTR(EPI_QKV) Q4_GEMV_ATTR(EPI_SWIGLU)
 #undef Q4_GEMV_ATTR
 #undef Q4_GEMV_ATTR1
