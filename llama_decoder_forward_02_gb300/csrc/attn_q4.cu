@@ -35,11 +35,14 @@
 //
 //
 // Measured, calls in a row, 32 query and 8 kv heads of 128, and the time the
-// bytes take at the copy bandwidth: one row of 2100 keys 5.7 us (0.4), of 32000
-// keys 12.8 (5.4), eight rows of 748 to 3415 keys 10.4 (3.0).  Of the 12.8: 1.3
+// bytes take at the copy bandwidth: one row of 2100 keys 4.7 us (0.4), of 32000
+// keys 12.9 (5.4), eight rows of 748 to 3415 keys 9.9 (3.0).  Of the 12.9: 1.3
 // to q's fragments, 6.9 of loop (5.3 TB/s; schedulers issue in 49% of the SM's
 // clocks, ALU 41%, over the whole kernel), 0.9 for the warps' sums, 2.4 for the
-// count, the reads and the merge, 1.3 to the next call.
+// count, the reads and the merge, 1.4 to the next call.  In a cluster each split
+// sends its share to the rank that merges it before the one barrier they meet
+// at; reading it there after the barrier, with a second one to leave by, took
+// 0.7 more.
 //
 // Prefill: the visible rows of the ubatch's sequences are widened once to fp16
 // and the fp16 prefill attention runs on them: 512 rows from position 1536 on
@@ -67,7 +70,7 @@ constexpr int MAX_SPLIT = ATTN_DECODE_MAX_SPLIT;
 constexpr int MIN_GRP = 8;               // groups of a split, at least
 constexpr int MERGE_AHEAD = 40;          // splits whose partials a merging thread asks for at once
 constexpr int MAX_CLUSTER = 8;           // splits merged in a cluster
-constexpr int CLUSTER_CTX = 4096;        // longest cache whose splits always are one cluster
+constexpr int CLUSTER_CTX = 8192;        // longest cache whose splits always are one cluster
 constexpr int BALANCE_T = 128;           // most rows that share the splits of a launch ...
 constexpr int BALANCE_UNITS = 2048;      // ... and most (row, kv head, chunk)s, each of which has a counter
 constexpr int SMS = 152;                 // of the one GPU this library is compiled for: scratch sizes follow from it
@@ -83,8 +86,10 @@ struct Ring {
     static constexpr size_t MERGE = (size_t)NW * GC * (HD + 2) * sizeof(float);
     static constexpr size_t QFRAG = (size_t)2 * NB * (32 * 16 + 16);      // q's fragments, two tiles at most
     static constexpr size_t WGT = BYTES > MERGE ? BYTES : MERGE;          // split weights, after the rings or the results
-    static constexpr size_t TAIL = (size_t)GC * (MAX_SPLIT > HD + 2 ? MAX_SPLIT : HD + 2) * sizeof(float);   // or a cluster's records
-    static constexpr size_t SMEM = BYTES + QFRAG > WGT + TAIL ? BYTES + QFRAG : WGT + TAIL;
+    static constexpr size_t SMEM = BYTES + QFRAG > WGT + GC * MAX_SPLIT * sizeof(float) ? BYTES + QFRAG : WGT + GC * MAX_SPLIT * sizeof(float);
+    // a cluster's splits send a CTA its share of their results behind all that, where another may still be reading q
+    static constexpr size_t INBOX = (BYTES + QFRAG > MERGE ? BYTES + QFRAG : MERGE) + 15 & ~(size_t)15;
+    static constexpr size_t SMEM_CL = INBOX + (size_t)GC * (HD / 2) * sizeof(float4);
     // byte offset of word block `part` (4 NB bytes, lane t4 of a K row) of row r
     __device__ static __forceinline__ int at(int r, int part) {
         if (HD == 128) return r * ROW + ((part ^ ((r >> 1) & 3)) << 4);
@@ -325,6 +330,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     }
 #pragma unroll
     for (int i = 0; i < NST - 1; ++i) request();
+    if constexpr (CL) cluster_arrive_relaxed();       // started: the others may write to this CTA once they have waited
     if (warp < NT * NB) {
         const int u = warp;
         const float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -499,9 +505,12 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     __syncthreads();
     // records of a split: numerators, sum, maximum
     const bool one = !CL && n_eff == 1;
-    float *rec = reinterpret_cast<float *>(smem_raw + R::WGT);             // CL: this CTA's records, [GC][REC]
-    float *part = CL ? rec : a.part + ((size_t)h0 * a.n_split + blockIdx.x) * REC;
-    const size_t part_head = CL ? REC : (size_t)a.n_split * REC;
+    float *part = a.part + ((size_t)h0 * a.n_split + blockIdx.x) * REC;
+    const size_t part_head = (size_t)a.n_split * REC;
+    // CL: rank r merges the (head, dimension pair)s [r share, (r + 1) share) of all ranks' records
+    float4 *inbox = reinterpret_cast<float4 *>(smem_raw + R::INBOX);       // [rank][share]
+    const int share = gn * (HD / 2) / (CL ? a.n_split : 1);
+    if constexpr (CL) cluster_wait();
     for (int i = tid; i < gn * (HD / 2); i += THREADS) {
         const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
         float2 num = make_float2(0.f, 0.f);
@@ -514,7 +523,13 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
             num.y += v.y;
             den += ws[HD];
         }
-        if (one) {
+        if constexpr (CL) {
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, s_max[w][h]);
+            const int r = i / share;
+            dsmem_st_f32x4(dsmem(inbox + sp * share + (i - r * share), (uint32_t)r), make_float4(num.x, num.y, den, M));
+        } else if (one) {
             const float inv = den > 0.f ? 1.f / den : 0.f;
             *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(num.x * inv, num.y * inv);
         } else {
@@ -530,37 +545,26 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     }
     if (one) return;
     if constexpr (CL) {
-        // rank r merges its share of the (head, dimension pair)s from every rank's records, in split order
-        const int ranks = (int)gridDim.x, n = gn * (HD / 2);
         cluster_sync();
-        for (int i = sp * n / ranks + tid; i < (sp + 1) * n / ranks; i += THREADS) {
-            const int h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
-            float2 num[MAX_CLUSTER], lm[MAX_CLUSTER];
+        for (int k = tid; k < share; k += THREADS) {
+            const int i = sp * share + k, h = i / (HD / 2), d = 2 * (i - h * (HD / 2));
+            float4 v[MAX_CLUSTER];
 #pragma unroll
-            for (int p = 0; p < MAX_CLUSTER; ++p) {
-                num[p] = make_float2(0.f, 0.f);
-                lm[p] = make_float2(0.f, -INFINITY);
-                if (p < ranks) {
-                    const uint32_t at = dsmem(rec + h * REC, (uint32_t)p);
-                    num[p] = dsmem_ld_f32x2(at + 4u * d);
-                    lm[p] = dsmem_ld_f32x2(at + 4u * HD);
-                }
-            }
+            for (int p = 0; p < MAX_CLUSTER; ++p) v[p] = p < a.n_split ? inbox[p * share + k] : make_float4(0.f, 0.f, 0.f, -INFINITY);
             float M = -INFINITY, den = 0.f;
             float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int p = 0; p < MAX_CLUSTER; ++p) M = fmaxf(M, lm[p].y);
+            for (int p = 0; p < MAX_CLUSTER; ++p) M = fmaxf(M, v[p].w);
 #pragma unroll
             for (int p = 0; p < MAX_CLUSTER; ++p) {
-                const float f = lm[p].y == -INFINITY ? 0.f : exp2_fast(lm[p].y - M);
-                acc.x = fmaf(f, num[p].x, acc.x);
-                acc.y = fmaf(f, num[p].y, acc.y);
-                den = fmaf(f, lm[p].x, den);
+                const float f = v[p].w == -INFINITY ? 0.f : exp2_fast(v[p].w - M);
+                acc.x = fmaf(f, v[p].x, acc.x);
+                acc.y = fmaf(f, v[p].y, acc.y);
+                den = fmaf(f, v[p].z, den);
             }
             const float inv = den > 0.f ? 1.f / den : 0.f;
             *reinterpret_cast<uint32_t *>(a.o + ((size_t)t * a.H + h0 + h) * HD + d) = pack_h2(acc.x * inv, acc.y * inv);
         }
-        cluster_sync();                               // no CTA leaves while another reads its records
         return;
     }
     __syncthreads();
@@ -716,22 +720,21 @@ __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, co
 
 // How the keys are split.
 //
-// Short caches and many rows: every (row, kv head, chunk) has the same number
-// of splits, a power of two up to MAX_CLUSTER, and they are one cluster; about
-// two CTAs of 8 warps an SM in all.  The merge inside a cluster costs about a
-// microsecond less than the one through memory (one row of 2100 keys, 8 kv
-// heads of 128: 5.7 us, 6.3 in 16 splits through memory; eight rows of 4000
-// keys 12.9 and 14.7).
+// Caches of up to CLUSTER_CTX positions and many rows: every (row, kv head,
+// chunk) has the same number of splits, a power of two up to MAX_CLUSTER, and
+// they are one cluster; about two CTAs of 8 warps an SM in all.  The merge
+// inside a cluster costs a good microsecond less than the one through memory
+// (8 kv heads of 128: one row of 2100 keys 4.7 us, 6.3 in 16 splits through
+// memory; of 4000 keys 5.5 and 6.7; of 8000 keys 7.5 both; eight rows of 4000
+// keys 12.1 and 14.7).
 //
-// Long caches: the rows share the splits by their lengths (find_split), merged
-// through memory.  One or two rows of 8 kv heads get one CTA of 16 warps an SM,
-// more rows two of 8.  One row of 8000 keys 7.6 us (a cluster of eight 8.2), of
-// 32000 keys 12.8 (two CTAs of 8 warps, 32 splits: 14.8, as 104 SMs had two of
-// them and 48 one; 38 splits 15.9 for their merge); two rows of 8000 and 5000
-// keys 9.1 (clusters 10.0); eight rows of 1000 to 30000 keys 32 us (clusters of
-// four, whose CTAs wait for the longest row's, 56).  Eight rows of 4000 keys in
-// a cache of 8192 still are faster as clusters, so more than two rows share
-// from 2 CLUSTER_CTX positions on.
+// Longer caches: the rows share the splits by their lengths (find_split),
+// merged through memory.  One or two rows of 8 kv heads get one CTA of 16 warps
+// an SM, more rows two of 8.  One row of 32000 keys 12.9 us (two CTAs of 8
+// warps, 32 splits: 14.8, as 104 SMs had two of them and 48 one; 38 splits
+// 15.9 for their merge); four rows of 2000 to 16000 keys 13.9; eight rows of
+// 1000 to 30000 keys 32 (clusters of four, whose CTAs wait for the longest
+// row's, 56).
 namespace {
 
 int chunks_of(int H, int Hkv) { return (H / Hkv + GC - 1) / GC; }
@@ -743,7 +746,7 @@ Plan plan_of(int T, int H, int Hkv, int n_ctx) {
     const long long most = std::max(1, n_ctx / (MIN_GRP * KG) + (n_ctx % (MIN_GRP * KG) > 0));   // splits of a row
     const bool wide = H / Hkv > 4;
     Plan p;
-    p.cluster = n_ctx <= (8 * units <= SMS ? 1 : 2) * CLUSTER_CTX || T > BALANCE_T || units > BALANCE_UNITS || (long long)T * n_ctx > 1ll << 34;
+    p.cluster = n_ctx <= CLUSTER_CTX || T > BALANCE_T || units > BALANCE_UNITS || (long long)T * n_ctx > 1ll << 34;
     if (p.cluster) {
         long long s = std::min((wide ? 1ll : 2ll) * SMS / units, most);
         s = std::min(std::max(s, 1ll), (long long)MAX_CLUSTER);
@@ -782,7 +785,7 @@ cudaError_t launch_attn_decode_q4(AttnDecodeArgs a, void *scratch, const Launch 
 #define Q4_DEC_CASE(HDV)                                                                                              \
     if (a.kv.head_dim == HDV && p.cluster)                                                                            \
         return launch_cluster_kernel(wide ? attn_decode_q4_kernel<HDV, 2, 8, true> : attn_decode_q4_kernel<HDV, 1, 8, true>, \
-                                     grid, block, p.n_split, Ring<HDV, 8>::SMEM, l, a, chunks);                       \
+                                     grid, block, p.n_split, Ring<HDV, 8>::SMEM_CL, l, a, chunks);                       \
     Q4_DEC_CASE1(HDV, 1, 8) Q4_DEC_CASE1(HDV, 1, 16) Q4_DEC_CASE1(HDV, 2, 8)
     Q4_DEC_CASE(32) Q4_DEC_CASE(64) Q4_DEC_CASE(128)
 #undef Q4_DEC_CASE
@@ -793,7 +796,7 @@ cudaError_t launch_attn_decode_q4(AttnDecodeArgs a, void *scratch, const Launch 
 cudaError_t init_attn_q4_attributes() {
     cudaError_t e = cudaSuccess;
 #define Q4_DEC_ATTR1(HDV, NT, NWV, CL)                                                         \
-    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT, NWV, CL>, Ring<HDV, NWV>::SMEM);     \
+    if (!e) e = allow_smem(attn_decode_q4_kernel<HDV, NT, NWV, CL>, CL ? Ring<HDV, NWV>::SMEM_CL : Ring<HDV, NWV>::SMEM); \
     if (!e) e = cudaFuncSetAttribute(attn_decode_q4_kernel<HDV, NT, NWV, CL>,                  \
                                      cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 #define Q4_DEC_ATTR(HDV)                                                                        \

@@ -33,21 +33,22 @@
 // 128256 x 4096 took 83 us, a quarter of it in meetings).
 //
 // Measured, calls in a row, one row of x where not said otherwise, and the time
-// the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 5.2 us (1.4),
-// 28672 x 4096 17.5 (9.7), 4096 x 14336 11.6 (4.9; 8 rows 12.0), 128256 x 4096
-// 57.3 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
-// 5.3, 16.1, 11.2, 11.3 and 54.5.  3 us of each go by before the first product
+// the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 5.1 us (1.4),
+// 28672 x 4096 17.1 (9.7), 4096 x 14336 11.0 (4.9; 8 rows 12.1), 128256 x 4096
+// 56.8 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
+// 5.2, 16.4, 11.1, 11.3 and 55.5.  3 us of each go by before the first product
 // and after the last; in between the schedulers issue in 59% of their clocks
 // (ALU 46%, FMA 39%, tensor 26% of theirs) with four warps each, which wait for
 // the pipes and the shared-memory queue and hardly (0.1 of 6 warps) for memory.
 //
 // What was slower or no faster: bulk copies by a producer warp, one a row and
-// step (28672 x 4096 26.7 us: 130 clocks a copy of 1152 bytes); the columns that
-// a single row of x leaves unused taking other blocks (57.1 us for 128256 x
-// 4096, as without the odd columns' sums); two CTAs of half the warps an SM; steps
-// of 16 rows and whole chunks, whose copies run along the rows (64 lines a chunk
-// instead of 112: 55.9 us for 128256 x 4096, but 16.8 instead of 16.1 for 28672 x
-// 4096 and 11.9 instead of 11.2 for 4096 x 14336 as the forward pass runs them).
+// step (28672 x 4096 26.7 us: 130 clocks a copy of 1152 bytes); the columns that a
+// single row of x leaves unused taking other blocks (57.1 us for 128256 x 4096, as
+// without the odd columns' sums, 57.2); two CTAs of half the warps an SM; steps of
+// 16 rows and whole chunks, whose copies run along the rows (64 lines a chunk
+// instead of 112; with four stages each 55.9 instead of 57.3 us for 128256 x 4096,
+// but 16.8 instead of 16.1 for 28672 x 4096 and 11.9 instead of 11.2 for 4096 x
+// 14336 with the early requests).
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"

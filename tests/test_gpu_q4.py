@@ -454,7 +454,7 @@ assert not y.any()
 """
 
 
-@pytest.mark.parametrize("n_ctx", [64, 5000])
+@pytest.mark.parametrize("n_ctx", [64, 9000])
 def test_first_calls_of_a_process_captured(lib, n_ctx):
     """The calls' set-up of the device does not disturb a capture that runs before any other call."""
     tests = os.path.dirname(os.path.abspath(__file__))

@@ -127,7 +127,7 @@ def test_sequences_and_window(lib, shape, weights, cache):
     p.free()
 
 
-@pytest.mark.parametrize("shape,n_ctx", [(MED64, 8400), (WIDE, 4200)])
+@pytest.mark.parametrize("shape,n_ctx", [(MED64, 8400), (WIDE, 8400)])
 def test_long_cache(lib, shape, n_ctx):
     """A context whose rows share the keys' splits: sequences of unlike lengths, steps of one, two and eight rows."""
     p = Both(lib, shape, 36, n_ctx=n_ctx, n_seq=3, n_ubatch=256, weights="q4", cache="q4")
