@@ -209,6 +209,21 @@ def test_fp8_cache_with_norms(lib):
     p.free()
 
 
+@pytest.mark.parametrize("shape", [MED32, MED64, MED128])
+def test_fp8_cache_of_q4_model(lib, shape):
+    """Q4_0 weights with the FP8 cache: the append of the GEMV's own epilogue, for one and several rows and sequences."""
+    p = Both(lib, shape, 37, n_ctx=128, n_seq=2, weights="q4")
+    p.ctx.set_option("kv_fp8", 1)
+    p.oc.cache.store = "e4m3"
+    p.decode(synth.prompt(shape.n_vocab, 37, 60))
+    for tok in (3, 4):
+        p.decode([tok])
+    p.decode([5, 6, 7], seq_id=[1, 1, 0], output=[1, 1, 1])
+    p.decode(list(range(8)), seq_id=[0, 1] * 4, output=[1] * 8)
+    p.decode([9], seq_id=[1])
+    p.free()
+
+
 def test_qk_norm_arguments(lib):
     t = synth.make_weights(MED64, 1, "cpu")
     m = lib.Model(MED64, {k: v.cuda() for k, v in t.items()}, stream=stream())
