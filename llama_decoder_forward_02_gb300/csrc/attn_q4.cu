@@ -88,7 +88,7 @@ struct Ring {
     static constexpr size_t WGT = BYTES > MERGE ? BYTES : MERGE;          // split weights, after the rings or the results
     static constexpr size_t SMEM = BYTES + QFRAG > WGT + GC * MAX_SPLIT * sizeof(float) ? BYTES + QFRAG : WGT + GC * MAX_SPLIT * sizeof(float);
     // a cluster's splits send a CTA its share of their results behind all that, where another may still be reading q
-    static constexpr size_t INBOX = (BYTES + QFRAG > MERGE ? BYTES + QFRAG : MERGE) + 15 & ~(size_t)15;
+    static constexpr size_t INBOX = ((BYTES + QFRAG > MERGE ? BYTES + QFRAG : MERGE) + 15) & ~(size_t)15;
     static constexpr size_t SMEM_CL = INBOX + (size_t)GC * (HD / 2) * sizeof(float4);
     // byte offset of word block `part` (4 NB bytes, lane t4 of a K row) of row r
     __device__ static __forceinline__ int at(int r, int part) {

@@ -213,22 +213,35 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     // ---- x: column g of the N side is row g of x (columns from T on repeat row 0, their sums are not stored)
     const f16 *xp = a.x;
     int ldx = a.ldx;
-    if (warp < a.T) {
-        float r = 1.f;
-        if (a.ss_in) {
-            float ss = 0.f;
-            for (int i = lane; i < a.n_ss_in; i += 32) ss += a.ss_in[(size_t)warp * a.n_ss_in + i];
-            r = 1.f / sqrtf(warp_sum(ss) / (float)a.K + a.eps);
+    // a row's sums of squares and cell are asked for at once, x right behind them, and all are waited for together
+    constexpr int SSQ = 8;
+    float part[SSQ];
+    int ps = 0, sq = 0;
+    const bool stats = warp < a.T;
+    if (stats) {
+        if (EPI == EPI_QKV) { ps = a.pos[warp]; sq = a.seq[warp]; }
+#pragma unroll
+        for (int j = 0; j < SSQ; ++j) {
+            const int i = lane + 32 * j;
+            part[j] = a.ss_in && i < a.n_ss_in ? a.ss_in[(size_t)warp * a.n_ss_in + i] : 0.f;
         }
-        if (lane == 0) s_r[warp] = r;
+    }
+    auto finish_stats = [&]() {
+        if (!stats) return;
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < SSQ; ++j) ss += part[j];
+        if (a.ss_in)
+            for (int i = lane + 32 * SSQ; i < a.n_ss_in; i += 32) ss += a.ss_in[(size_t)warp * a.n_ss_in + i];
+        ss = warp_sum(ss);
+        if (lane == 0) s_r[warp] = a.ss_in ? 1.f / sqrtf(ss / (float)a.K + a.eps) : 1.f;
         if (EPI == EPI_QKV && lane == 0) {
-            const int ps = a.pos[warp], sq = a.seq[warp];
             const bool ok = ps >= 0 && ps < a.kv.n_ctx && sq >= 0 && sq < a.kv.n_seq;
             if (!ok && blockIdx.x == 0) raise_error(a.err, ERRF_BAD_INDEX);
             s_pos[warp] = ok ? ps : -1;
             s_seq[warp] = sq;
         }
-    }
+    };
     if (XS) {
         const int per = a.K / 8, n = a.T * per;      // 16-byte pieces of x
         constexpr int HOLD = 4;                      // pieces a thread asks for before the ring's first steps
@@ -249,12 +262,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         for (int i = tid + HOLD * THREADS; i < n; i += THREADS) put(i, piece(i));
         ldx = a.K + X_PAD;
         xp = xs;
-        __syncthreads();
-    } else {
-        if (!early)
-            for (int j = 0; j < NST - 1; ++j) request(j & 1);
-        __syncthreads();
+    } else if (!early) {
+        for (int j = 0; j < NST - 1; ++j) request(j & 1);
     }
+    finish_stats();
+    __syncthreads();
     xp += (size_t)(g < a.T ? g : 0) * ldx + cu * q4::CHUNK + 8 * t4;
     uint4 bx[4];                                     // !XS: the next step's x
     auto load_x = [&](int k) {
@@ -270,6 +282,24 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     uint32_t cslot = 0, sslot = 0;
     const uint8_t *wr = ring + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4), *dr = ring + NST * CODES + g * 16;
     for (int tile = 0; tile < ntiles; ++tile) {
+        // what the epilogue adds to this lane's row, for the warp's first row of x, is asked for ahead of the products
+        const int row = (tile * (CW / units) + rg) * RG + lane, n = r0 + row;
+        const bool in = row < nrows;
+        auto turn = [&](int t) {                     // QKV: the row pair's rotation
+            const int hd = a.kv.head_dim;
+            return EPI == EPI_QKV && in && s_pos[t] >= 0 && n < a.n_q + a.n_kv
+                       ? a.rope[(size_t)s_pos[t] * (hd / 2) + (n < a.n_q ? n : n - a.n_q) % hd / 2]
+                       : make_float2(1.f, 0.f);
+        };
+        float2 cs = make_float2(1.f, 0.f);
+        float h0 = 0.f, gain = 0.f;
+        if (cu < a.T) {
+            if (EPI == EPI_QKV) cs = turn(cu);
+            if (EPI == EPI_RESID && in) {
+                h0 = a.hres[(size_t)cu * a.ldh + n];
+                if (a.xg_out) gain = a.gain_next[n];
+            }
+        }
         float y[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
@@ -331,15 +361,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         // once a tile: the readers of these sums are done before the next but one overwrites them
         if (units > 1) asm volatile("bar.sync %0, %1;" :: "r"(rg + 1), "r"(units * 32) : "memory");
         else __syncwarp();
-        const int row = (tile * (CW / units) + rg) * RG + lane, n = r0 + row;
-        const bool in = row < nrows;
         int q = 0;
         for (int t = cu; t < a.T; t += units, ++q) {
-            float2 cs = make_float2(1.f, 0.f);       // QKV: the row pair's rotation
-            const bool cell = EPI != EPI_QKV || s_pos[t] >= 0;
-            if (EPI == EPI_QKV && in && cell && n < a.n_q + a.n_kv) {
-                const int hd = a.kv.head_dim;
-                cs = a.rope[(size_t)s_pos[t] * (hd / 2) + (n < a.n_q ? n : n - a.n_q) % hd / 2];
+            if (t != cu) {
+                if (EPI == EPI_QKV) cs = turn(t);
+                if (EPI == EPI_RESID && in) h0 = a.hres[(size_t)t * a.ldh + n];
             }
             float v = 0.f;
             for (int c = 0; c < units; ++c) v += sums[c * p.red_warp + t * RED_COL + lane];
@@ -349,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
                 const float w = __shfl_xor_sync(0xffffffffu, v, 1);
                 if (n < a.n_q + a.n_kv) v = lane & 1 ? fmaf(v, cs.x, w * cs.y) : fmaf(v, cs.x, -w * cs.y);
                 const float up = __shfl_down_sync(0xffffffffu, v, 1);
-                if (in && cell) {
+                if (in && s_pos[t] >= 0) {
                     if (n < a.n_q) {
                         a.q_out[(size_t)t * a.n_q + n] = v;
                     } else if (!(lane & 1)) {
@@ -369,10 +395,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             } else if (EPI == EPI_RESID) {
                 float h = 0.f;
                 if (in) {
-                    h = a.hres[(size_t)t * a.ldh + n] + v;
+                    h = h0 + v;
                     a.hres[(size_t)t * a.ldh + n] = h;
                     if (a.xg_out) {
-                        const float xg = h * a.gain_next[n];
+                        const float xg = h * gain;
                         if (f16_bad(xg)) raise_error(a.err, ERRF_F16_RANGE);
                         a.xg_out[(size_t)t * a.ldxg + n] = f2h(xg);
                     }
