@@ -253,8 +253,10 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     const int j = blockIdx.y / chunks, ck = blockIdx.y - j * chunks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int Hkv = a.kv.n_kv_head, G = a.H / Hkv, h0 = j * G + ck * GC, gn = min(GC, G - ck * GC);
-    pdl_wait();
-    pdl_trigger();
+    if (!a.early) {
+        pdl_wait();
+        pdl_trigger();
+    }
     int sp = blockIdx.x, t = blockIdx.z, pos, seq, n_eff;
     Row rw;
     int len;                                          // groups of a split
@@ -266,7 +268,10 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
         n_eff = a.n_split;                            // all stay for the cluster's barriers
     } else {
         sp = find_split(a, blockIdx.x, lane, t, rw, pos, seq, len, n_eff);
-        if (sp < 0) return;
+        if (sp < 0) {
+            if (a.early) pdl_wait();                  // no CTA leaves before the kernel ahead is done
+            return;
+        }
     }
     if (!rw.ok && tid == 0 && sp == 0 && blockIdx.y == 0) raise_error(a.err, ERRF_BAD_INDEX);
     const long long at = (long long)sp * len * KG;    // first key of the split
@@ -321,6 +326,15 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     float *q8 = reinterpret_cast<float *>(qf + NT * NB * 32);              // [NT * NB][4]: 8 sum(q) * 2^-20 of the columns' head
     const float scale = 16.f * 1.4426950408889634f / sqrtf((float)HD);
     static_assert(NT * NB <= NW, "a warp makes one block's fragments");
+    int asked = 0;                                    // groups requested
+    if (a.early) {                                    // cells that no row of this launch's batch was appended to
+        while (asked < NST - 1 && kb + KG * (warp + NW * asked) + KG <= pos + 1 - a.T) {
+            request();
+            ++asked;
+        }
+        pdl_wait();
+        pdl_trigger();
+    }
     float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
     if (warp < NT * NB && 4 * (warp / NB) + (g >> 1) < gn) {
         const float4 *qp = reinterpret_cast<const float4 *>(a.q + ((size_t)t * a.H + h0 + 4 * (warp / NB) + (g >> 1)) * HD +
@@ -329,7 +343,8 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
         x1 = __ldcg(qp + 1);                          // ring's burst, behind which it would wait 2 us
     }
 #pragma unroll
-    for (int i = 0; i < NST - 1; ++i) request();
+    for (int i = 0; i < NST - 1; ++i)
+        if (i >= asked) request();
     if constexpr (CL) cluster_arrive_relaxed();       // started: the others may write to this CTA once they have waited
     if (warp < NT * NB) {
         const int u = warp;

@@ -113,6 +113,9 @@ struct AttnDecodeArgs {
     unsigned *counters;        // [T][Hkv]
     uint32_t *err;
     int window = 0;            // sliding window: keys with pos - W < key <= pos (0 = all)
+    // Q4_0 cache: pos, seq and the keys of cells up to pos - T were written
+    // before the kernel that precedes this one, and may be read before its end
+    bool early = false;
 };
 // Most sequence splits per (row, kv head) the decode-attention kernel takes.
 constexpr int ATTN_DECODE_MAX_SPLIT = 128;
@@ -339,6 +342,7 @@ struct QkNormArgs {
     KvView kv;
     int T, H;
     uint32_t *err;
+    bool early = false;        // pos, seq and rope were written before the kernel that precedes this one
 };
 cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l);
 // launch_kv_shift of a Q4_0 cache: keys are rotated as the values they stand

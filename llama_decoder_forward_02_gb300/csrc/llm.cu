@@ -809,6 +809,7 @@ cudaError_t qk_norm(llm_ctx *c, const UbDev &u, int layer, bool prefill, const L
     n.rope = c->rope; n.pos = u.pos; n.seq = u.seq;
     n.q32 = prefill ? nullptr : c->qf; n.q16 = prefill ? c->qb : nullptr;
     n.kv = kv_view(c, layer); n.T = u.T; n.H = m->H; n.err = c->err_dev;
+    n.early = true;                                   // positions and table stand since before the QKV projection
     return timed(c, K_QK_NORM, [&] { return launch_qk_norm_rope(n, L); });
 }
 
@@ -818,6 +819,7 @@ cudaError_t attn_decode(llm_ctx *c, const UbDev &u, int layer) {
     at.q = c->qf; at.kv = kv_view(c, layer); at.pos = u.pos; at.seq = u.seq; at.o = c->o; at.T = u.T; at.H = m->H;
     at.err = c->err_dev; at.window = c->swa_window;
     if (c->kv_q4) {
+        at.early = true;                              // the rows of the step were appended by the kernel just before
         return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode_q4(at, c->q4_scratch, lnch_attn(c)); });
     }
     at.n_split = c->attn_split[u.T]; at.part = c->attn_part; at.counters = c->attn_cnt;

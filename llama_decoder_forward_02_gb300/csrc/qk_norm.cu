@@ -135,13 +135,16 @@ __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const
     const int t = blockIdx.x;
     int h0 = ((int)blockIdx.y * (THREADS / 32) + warp) * PER;        // the warp's first head
     const int step = (int)gridDim.y * (THREADS / 32) * PER;
-    pdl_wait();
-    pdl_trigger();
-    if (h0 >= heads) return;                          // whole warps
     const float *row = a.qkv + (size_t)t * a.ld + e0;
     // every lane stays for the shuffles; heads past the last repeat it and store nothing
+    const float *first = row + (size_t)min(h0 + lane / L, heads - 1) * HD;
     float next[E];
-    load8(next, row + (size_t)min(h0 + lane / L, heads - 1) * HD);
+    if (!a.early) {
+        pdl_wait();
+        pdl_trigger();
+        if (h0 >= heads) return;                      // whole warps
+        load8(next, first);
+    }
     const int pos = a.pos[t], seq = a.seq[t];
     const bool ok = pos >= 0 && pos < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
     float2 turn[E / 2];
@@ -151,6 +154,12 @@ __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const
         if (ok) v = *reinterpret_cast<const float4 *>(a.rope + (size_t)pos * (HD / 2) + e0 / 2 + e);
         turn[e] = make_float2(v.x, v.y);
         turn[e + 1] = make_float2(v.z, v.w);
+    }
+    if (a.early) {
+        pdl_wait();
+        pdl_trigger();
+        if (h0 >= heads) return;
+        load8(next, first);
     }
     if (!ok && h0 == 0 && lane == 0) raise_error(a.err, ERRF_BAD_INDEX);
     bool out_of_range = false;

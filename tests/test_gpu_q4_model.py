@@ -224,6 +224,25 @@ def test_fp8_cache_of_q4_model(lib, shape):
     p.free()
 
 
+@pytest.mark.parametrize("weights,n_ctx", [("q4", 600), (None, 600), ("q4", 8300)])
+def test_overlapped_launches_change_nothing(lib, weights, n_ctx):
+    """The norm's and the attention's launches overlap the kernels before them and read what stands since before those:
+    the same bits as without the overlap, over steps of one and several rows, replayed and not."""
+    a, b = (Both(lib, MED128, 38, n_ctx=n_ctx, n_seq=3, weights=weights, cache="q4", norms="qk") for _ in range(2))
+    b.ctx.set_option("pdl_attn", 0)
+    b.ctx.set_option("graphs", 0)
+    toks = synth.prompt(MED128.n_vocab, 38, 300)
+    for x in (a, b):
+        assert x.ctx.decode(toks, seq_id=[0] * 200 + [1] * 90 + [2] * 10, output=[0] * 299 + [1]) == 0
+    for step in range(30):
+        for rows in ([step % 3], [0, 1, 1], [0, 1, 2, 2, 2, 1, 0, 0]):
+            for x in (a, b):
+                assert x.ctx.decode([(7 * step + i) % 500 for i in range(len(rows))], seq_id=rows, output=[1] * len(rows)) == 0
+            assert np.array_equal(a.logits(), b.logits()), (step, rows)
+    a.free()
+    b.free()
+
+
 def test_qk_norm_arguments(lib):
     t = synth.make_weights(MED64, 1, "cpu")
     m = lib.Model(MED64, {k: v.cuda() for k, v in t.items()}, stream=stream())
