@@ -34,9 +34,9 @@
 //
 // Measured, calls in a row, one row of x where not said otherwise, and the time
 // the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 5.1 us (1.4),
-// 28672 x 4096 17.1 (9.7), 4096 x 14336 11.0 (4.9; 8 rows 12.1), 128256 x 4096
-// 56.8 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
-// 5.2, 16.4, 11.1, 11.3 and 55.5.  3 us of each go by before the first product
+// 28672 x 4096 16.9 (9.7), 4096 x 14336 11.0 (4.9; 8 rows 11.8), 128256 x 4096
+// 56.6 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
+// 5.4, 16.5, 11.1, 11.7 and 55.1.  3 us of each go by before the first product
 // and after the last; in between the schedulers issue in 59% of their clocks
 // (ALU 46%, FMA 39%, tensor 26% of theirs) with four warps each, which wait for
 // the pipes and the shared-memory queue and hardly (0.1 of 6 warps) for memory.
@@ -48,7 +48,9 @@
 // 16 rows and whole chunks, whose copies run along the rows (64 lines a chunk
 // instead of 112; with four stages each 55.9 instead of 57.3 us for 128256 x 4096,
 // but 16.8 instead of 16.1 for 28672 x 4096 and 11.9 instead of 11.2 for 4096 x
-// 14336 with the early requests).
+// 14336 with the early requests); the chunks that 16 warps share unevenly (56 of a
+// K of 14336) cut into halves (11.8 instead of 11.0: a step that may be either half
+// is scheduled worse than the two of a chunk).
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"
