@@ -76,20 +76,24 @@ constexpr size_t SMEM_CAP = 224 * 1024;
 constexpr int X_PAD = 32;                    // elements between rows of x in shared memory beyond K
 
 struct Plan {
-    int units;           // warps that share a row tile's K
+    int log_units;       // units = 2^log_units warps share a row tile's K
+    int run, longer;     // a CTA's rows: run row units, one more for the first `longer` CTAs
     bool x_smem;         // x is staged in shared memory
     int red_warp;        // floats of a warp's sums of one row tile (two tiles' sums alternate)
     size_t smem;
 };
 
 // false: K is not a positive multiple of 256
-bool make_plan(int N, int K, int T, int ctas, Plan *p) {
+bool make_plan(int N, int K, int T, int ctas, int unit, Plan *p) {
     if (K < q4::CHUNK || K % q4::CHUNK) return false;
-    const int chunks = K / q4::CHUNK, rows = (N + ctas - 1) / ctas, tiles = (rows + RG - 1) / RG;
+    p->run = N / unit / ctas;
+    p->longer = N / unit % ctas;
+    const int chunks = K / q4::CHUNK, rows = (p->run + (p->longer > 0)) * unit, tiles = (rows + RG - 1) / RG;
     long long best = 0;
-    for (int u = CW; u >= 1; u /= 2) {
+    for (int lu = 4; lu >= 0; --lu) {
+        const int u = 1 << lu;
         const long long mine = (tiles + CW / u - 1) / (CW / u), cost = mine * (4LL * ((chunks + u - 1) / u) + 1);
-        if (u == CW || cost < best) { best = cost; p->units = u; }
+        if (u == CW || cost < best) { best = cost; p->log_units = lu; }
     }
     p->red_warp = (T + 1) / 2 * 2 * RED_COL;
     const size_t red = (size_t)2 * CW * p->red_warp * sizeof(float);
@@ -145,19 +149,21 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     // the warp's number from a shuffle: what follows from it is then known to be the same for its lanes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     constexpr int UNIT = row_unit(EPI);              // rows kept together
-    const int r0 = (int)((long long)blockIdx.x * (a.N / UNIT) / gridDim.x) * UNIT;
-    const int nrows = (int)((long long)(blockIdx.x + 1) * (a.N / UNIT) / gridDim.x) * UNIT - r0;
+    // no divisions here: a CTA that starts when its SM falls free has all this ahead of its first product
+    const int bx0 = (int)blockIdx.x, r0 = (bx0 * p.run + min(bx0, p.longer)) * UNIT;
+    const int nrows = (p.run + (bx0 < p.longer)) * UNIT;
     __shared__ float s_r[8];                         // the rows' RMSNorm factors
     __shared__ int s_pos[8], s_seq[8];               // QKV: their cells, -1 where outside the cache
     __shared__ float s_sq[EPI == EPI_RESID ? CW : 1][8];   // sums of h^2 by row group
     const int chunks = a.K / q4::CHUNK;
-    const int units = p.units, cu = warp % units, rg = warp / units, TR = RG * CW / units;
+    const int lu = p.log_units, units = 1 << lu, cu = warp & (units - 1), rg = warp >> lu, TR = RG * CW >> lu;
+    static_assert(RG * CW == 512, "TR = 2^(9 - lu)");
     float *red = reinterpret_cast<float *>(smem_raw + RING_BYTES);
     f16 *xs = reinterpret_cast<f16 *>(red + 2 * CW * p.red_warp);
 
     // ---- this warp's ring: rows r0 + (tile * ngroups + rg) * 32 .., chunk kc * units + cu
-    const int my_kc = cu < chunks ? (chunks - cu + units - 1) / units : 0;          // this warp's chunks of a row tile
-    const int ntiles = nrows > rg * RG ? (nrows - rg * RG + TR - 1) / TR : 0;       // its row group's tiles
+    const int my_kc = (chunks - cu + units - 1) >> lu;                                // this warp's chunks of a row tile
+    const int ntiles = nrows > rg * RG ? (nrows - rg * RG + TR - 1) >> (9 - lu) : 0;   // its row group's tiles
     uint8_t *ring = smem_raw + (size_t)warp * (NST * CODES + SC_SLOTS * SCALES);
     const uint32_t row_bytes = (uint32_t)chunks * q4::CHUNK_BYTES;
     // source of the next chunk to request (the warp's) and this lane's offsets from it: rows g, g + 8, .. of the codes
@@ -248,9 +254,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         const int per = a.K / 8, n = a.T * per;      // 16-byte pieces of x
         constexpr int HOLD = 4;                      // pieces a thread asks for before the ring's first steps
         uint4 held[HOLD];
-        auto piece = [&](int i) { return *reinterpret_cast<const uint4 *>(a.x + (size_t)(i / per) * a.ldx + (i % per) * 8); };
+        auto piece = [&](int i) {
+            return *reinterpret_cast<const uint4 *>(ONE ? a.x + 8 * i : a.x + (size_t)(i / per) * a.ldx + (i % per) * 8);
+        };
         auto put = [&](int i, const uint4 &u) {
-            *reinterpret_cast<uint4 *>(xs + (size_t)(i / per) * (a.K + X_PAD) + (i % per) * 8) = u;
+            *reinterpret_cast<uint4 *>(ONE ? xs + 8 * i : xs + (size_t)(i / per) * (a.K + X_PAD) + (i % per) * 8) = u;
         };
 #pragma unroll
         for (int j = 0; j < HOLD; ++j)
@@ -285,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     const uint8_t *wr = ring + g * 64 + ((t4 ^ ((g >> 1) & 3)) << 4), *dr = ring + NST * CODES + g * 16;
     for (int tile = 0; tile < ntiles; ++tile) {
         // what the epilogue adds to this lane's row, for the warp's first row of x, is asked for ahead of the products
-        const int row = (tile * (CW / units) + rg) * RG + lane, n = r0 + row;
+        const int row = (tile * (CW >> lu) + rg) * RG + lane, n = r0 + row;
         const bool in = row < nrows;
         auto turn = [&](int t) {                     // QKV: the row pair's rotation
             const int hd = a.kv.head_dim;
@@ -433,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
         __syncthreads();
         if (tid < a.T) {
             float v = 0.f;
-            for (int k = 0; k < CW / units; ++k) v += s_sq[k][tid];
+            for (int k = 0; k < CW >> lu; ++k) v += s_sq[k][tid];
             a.ss_out[(size_t)tid * gridDim.x + blockIdx.x] = v;
         }
     }
@@ -451,7 +459,7 @@ int gemv_q4_ctas(int epi, int N, int num_sms) {
 cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Launch &l, bool early) {
     Plan p;
     const int ctas = gemv_q4_ctas(epi, a.N, num_sms);
-    if (a.T < 1 || a.T > 8 || ctas < 1 || a.N % row_unit(epi) || !make_plan(a.N, a.K, a.T, ctas, &p))
+    if (a.T < 1 || a.T > 8 || ctas < 1 || a.N % row_unit(epi) || !make_plan(a.N, a.K, a.T, ctas, row_unit(epi), &p))
         return cudaErrorInvalidValue;
     const dim3 grid(ctas), block(THREADS);
 #define Q4_GEMV1(E, XS)                                                                              \
