@@ -139,7 +139,7 @@ struct Widen {
     __device__ __forceinline__ uint32_t high(uint32_t w) const { return pick(w, m1, e1, 0x54805480u); }
 };
 
-constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : epi == EPI_QKV ? 2 : 1; }
+constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : epi == EPI_QKV ? q4::BLOCK : 1; }
 
 // XS: x in shared memory; ONE: one row of x, so the
 // odd columns' sums are not kept (28672 x 4096 17.7 us, with them 18.2)
@@ -382,10 +382,32 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             v *= s_r[t];
             if (EPI == EPI_QKV) {
                 // lane pairs hold the elements of a rotation, 2i and 2i + 1
-                const float w = __shfl_xor_sync(0xffffffffu, v, 1);
+                const float w = __shfl_xor_sync(0xffffffffu, v, 1), x = v;
                 if (n < a.n_q + a.n_kv) v = lane & 1 ? fmaf(v, cs.x, w * cs.y) : fmaf(v, cs.x, -w * cs.y);
                 const float up = __shfl_down_sync(0xffffffffu, v, 1);
-                if (in && s_pos[t] >= 0) {
+                if (a.kv.k4 && n >= a.n_q) {         // the warp's 32 rows are one block: whole blocks are kept together
+                    const bool is_k = n < a.n_q + a.n_kv;
+                    float d;
+                    int code;
+                    if (__any_sync(0xffffffffu, q4::encode_lane(v, d, code))) {
+                        // next to a border: from float64 (a value is exact as it is)
+                        const double wy = (double)w * cs.y, u = is_k ? (double)x * cs.x + (lane & 1 ? wy : -wy) : (double)x;
+                        double d64;
+                        q4::encode_lane(u, d64, code);
+                        d = (float)d64;
+                    }
+                    uint32_t word = (uint32_t)code << q4::shift_of(lane & 7);
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+                    if (s_pos[t] >= 0) {
+                        if (f16_bad(v)) raise_error(a.err, ERRF_F16_RANGE);
+                        const int hd = a.kv.head_dim, c = n - a.n_q - (is_k ? 0 : a.n_kv), head = c / hd, blk = (c - head * hd) / 32;
+                        const size_t row = (size_t)s_seq[t] * a.kv.seq_stride + ((size_t)head * a.kv.n_ctx + s_pos[t]) * hd;
+                        if ((lane & 7) == 0)
+                            reinterpret_cast<uint32_t *>((is_k ? a.kv.k4 : a.kv.v4) + row / 2)[(lane >> 3) * (hd / 32) + blk] = word;
+                        if (lane == 0) (is_k ? a.kv.kd : a.kv.vd)[row / 32 + blk] = f2h(d);
+                    }
+                } else if (in && s_pos[t] >= 0) {
                     if (n < a.n_q) {
                         a.q_out[(size_t)t * a.n_q + n] = v;
                     } else if (!(lane & 1)) {

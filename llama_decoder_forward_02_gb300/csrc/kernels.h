@@ -322,7 +322,7 @@ struct GemvQ4Args {
     f16 *u_out; int ldu;      // EPI_SWIGLU: rows as GU_GROUP interleaves gate and up
     // EPI_QKV: rows [0, n_q) are queries, then n_kv key and n_kv value rows;
     // queries and keys rotated, q to q_out [T][n_q], the rest to cell (seq, pos)
-    // of an fp16 or FP8 cache
+    // of the cache; head_dim a multiple of 32
     float *q_out; int n_q, n_kv; KvView kv; const float2 *rope; const int *pos, *seq;
     uint32_t *err;
 };

@@ -852,8 +852,8 @@ cudaError_t run_small_q4(llm_ctx *c, const UbDev &u) {
     };
     for (int l = 0; l < m->L; ++l) {
         const LayerW &w = m->layers[l];
-        // normed heads and the Q4_0 cache need whole heads or blocks at once, which the GEMV's epilogue does not hold
-        const bool plain = plain_qkv(c);
+        // normed heads need whole heads at once, which the GEMV's epilogue does not hold; a Q4_0 block it does
+        const bool plain = m->nbuf;
         if ((e = gemv(K_GEMV_QKV, plain ? EPI_STORE : EPI_QKV, w.q_qkv, m->n_qkv, d, c->x, true, [&](GemvQ4Args &a) {
                 a.out = c->qkv; a.ldo = m->n_qkv;
                 a.q_out = c->qf; a.n_q = m->n_q; a.n_kv = m->n_kv; a.kv = kv_view(c, l);

@@ -44,5 +44,35 @@ __device__ __forceinline__ int code_of(R v, R d) {
     return c < 0 ? 0 : c > 15 ? 15 : c;
 }
 
+// Whether q = v / d in float32, next to the integer k, lies so near a code
+// border that its last bits could decide: |q| <= 8 with a relative error below
+// 24 * 2^-24 (a norm, a rotation and the quotient) is 1.2e-5 off at most.
+__device__ __forceinline__ bool near_border(float q, float k) {
+    constexpr float NEAR = 2e-5f;
+    return fabsf(fabsf(q - k) - 0.5f) < NEAR || q > 8.f - NEAR;
+}
+
+// The code of a lane's element u of the block that its warp holds, and the
+// block's scale.  Returns whether R does not settle the code.
+template <class R>
+__device__ __forceinline__ bool encode_lane(R u, R &d, int &code) {
+    R top = fabs(u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const R other = __shfl_xor_sync(0xffffffffu, top, o);
+        top = other > top ? other : top;
+    }
+    const unsigned has = __ballot_sync(0xffffffffu, fabs(u) == top);     // the first of that magnitude gives the sign
+    d = __shfl_sync(0xffffffffu, u, has ? __ffs(has) - 1 : 0) * R(-0.125);
+    if constexpr (sizeof(R) == 4) {
+        const float q = d != 0.f ? u * __frcp_rn(d) : 0.f, k = rintf(q);
+        code = min(max((int)k + 8, 0), 15);
+        return d != 0.f && (!(fabsf(d) > 1e-30f) || near_border(q, k));
+    } else {
+        code = code_of(u, d);
+        return false;
+    }
+}
+
 }  // namespace q4
 }  // namespace llm

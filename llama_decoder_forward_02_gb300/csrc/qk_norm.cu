@@ -22,8 +22,8 @@
 //
 // Q4_0 codes are those of the exact values.  A float32 value carries a few
 // ulp of error from the norm and the rotation, which matters only next to a
-// border between two codes; a row with an element within NEAR of one (about
-// one row in 200) is encoded again from float64 arithmetic.
+// border between two codes; a row with an element next to one (about one row in
+// 200) is encoded again from float64 arithmetic.
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"
@@ -33,9 +33,6 @@ namespace llm {
 namespace {
 
 constexpr int THREADS = 256;
-// Distance from a code border, in codes, under which float32 does not settle
-// the code: |v / d| <= 8 with a relative error below 24 * 2^-24 gives 1.2e-5.
-constexpr float NEAR = 2e-5f;
 
 __device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }         // 2 ulp
 __device__ __forceinline__ double inv_sqrt(double v) { return 1.0 / sqrt(v); }
@@ -96,7 +93,7 @@ __device__ __forceinline__ bool encode(const R (&u)[E], int lane, R &d, uint32_t
         for (int e = 0; e < E; ++e) {
             const float q = u[e] * inv, k = rintf(q);            // in [-8, 8]: the top itself is at -8
             word |= (uint32_t)min(max((int)k + 8, 0), 15) << q4::shift_of(e);
-            near |= fabsf(fabsf(q - k) - 0.5f) < NEAR || q > 8.f - NEAR;
+            near |= q4::near_border(q, k);
         }
     } else {
 #pragma unroll
