@@ -390,11 +390,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
                     float d;
                     int code;
                     if (__any_sync(0xffffffffu, q4::encode_lane(v, d, code))) {
-                        // next to a border: from float64 (a value is exact as it is)
-                        const double wy = (double)w * cs.y, u = is_k ? (double)x * cs.x + (lane & 1 ? wy : -wy) : (double)x;
-                        double d64;
-                        q4::encode_lane(u, d64, code);
-                        d = (float)d64;
+                        // next to a border: from the exact products (a value is exact as it is)
+                        const float up = fabsf(d) > q4::TINY ? 1.f : q4::RAISE, xs = x * up, ws = (lane & 1 ? w : -w) * up;
+                        q4::encode_lane(is_k ? q4::two_prod(xs, cs.x) + q4::two_prod(ws, cs.y) : q4::Pair{xs, 0.f}, d, code);
+                        d /= up;
                     }
                     uint32_t word = (uint32_t)code << q4::shift_of(lane & 7);
 #pragma unroll

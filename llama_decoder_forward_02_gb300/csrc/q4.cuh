@@ -31,16 +31,69 @@ constexpr int BLOCK = 32;                // elements of a block
 constexpr int CHUNK = 256;               // elements of a weight chunk
 constexpr int CHUNK_BYTES = 144;         // ... its codes (2 x 64 bytes), then 8 fp16 scales
 
+// scales at and below which a product's remainder leaves float32's range, and a
+// factor that brings such a block back
+constexpr float TINY = 1e-30f, RAISE = 0x1p96f;
+
 // bits of element e of an eight-element word
 __host__ __device__ constexpr int shift_of(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
 
-// The code of v in a block of scale d (unrounded).  |v / d| <= 8; R is float
-// where v is exact, double where a caller resolves a value next to a border.
-template <class R>
-__device__ __forceinline__ int code_of(R v, R d) {
-    if (d == R(0)) return 8;
-    const R q = v / d;
-    int c = (int)rint(q) + 8;
+// The code of v in a block of scale d (unrounded), v exact.  |v / d| <= 8.
+__device__ __forceinline__ int code_of(float v, float d) {
+    if (d == 0.f) return 8;
+    const int c = (int)rintf(v / d) + 8;
+    return c < 0 ? 0 : c > 15 ? 15 : c;
+}
+
+// Values next to a code border are settled in pairs of floats, h + l with l at
+// most half an ulp of h: sums and products of floats are exact as pairs (Knuth's
+// two-sum, a product and its FMA remainder), those of pairs good to 2^-44, and
+// this GPU's float64 units are a sixtieth of its float32 ones (a warp that
+// resolved its borders in float64 took 6.5 us).
+struct Pair { float h, l; };
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair two_prod(float a, float b) {
+    const float p = __fmul_rn(a, b);
+    return Pair{p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Pair settle(float h, float l) {          // |l| well below |h|
+    const float s = __fadd_rn(h, l);
+    return Pair{s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    const Pair s = two_sum(a.h, b.h);
+    return settle(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Pair operator*(Pair a, float b) {
+    const Pair p = two_prod(a.h, b);
+    return settle(p.h, __fmaf_rn(a.l, b, p.l));
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    const Pair p = two_prod(a.h, b.h);
+    return settle(p.h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.l, b.h, p.l)));
+}
+__device__ __forceinline__ Pair magnitude(Pair a) { return a.h < 0.f ? Pair{-a.h, -a.l} : a; }
+// of two magnitudes
+__device__ __forceinline__ bool larger(Pair a, Pair b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+__device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
+    return Pair{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+}
+__device__ __forceinline__ Pair shfl(Pair a, int from) {
+    return Pair{__shfl_sync(0xffffffffu, a.h, from), __shfl_sync(0xffffffffu, a.l, from)};
+}
+
+// The code of v: which side of the border b nearest to v / d it lies on is the
+// sign of v - b d.  On the border the even integer.
+__device__ __forceinline__ int code_of(Pair v, Pair d) {
+    if (d.h == 0.f) return 8;
+    const float q = v.h * __frcp_rn(d.h), k = rintf(q), b = q >= k ? k + 0.5f : k - 0.5f;
+    const Pair p = two_prod(b, d.h);
+    const float t = __fadd_rn(__fsub_rn(__fsub_rn(v.h, p.h), p.l), __fmaf_rn(-b, d.l, v.l));
+    const int lo = (int)floorf(b);
+    const int c = 8 + (t == 0.f ? lo + (lo & 1) : lo + ((t > 0.f) == (d.h > 0.f)));
     return c < 0 ? 0 : c > 15 ? 15 : c;
 }
 
@@ -53,25 +106,33 @@ __device__ __forceinline__ bool near_border(float q, float k) {
 }
 
 // The code of a lane's element u of the block that its warp holds, and the
-// block's scale.  Returns whether R does not settle the code.
-template <class R>
-__device__ __forceinline__ bool encode_lane(R u, R &d, int &code) {
-    R top = fabs(u);
+// block's scale.  Returns whether float32 does not settle the code.
+__device__ __forceinline__ bool encode_lane(float u, float &d, int &code) {
+    float top = fabsf(u);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const R other = __shfl_xor_sync(0xffffffffu, top, o);
+        const float other = __shfl_xor_sync(0xffffffffu, top, o);
         top = other > top ? other : top;
     }
-    const unsigned has = __ballot_sync(0xffffffffu, fabs(u) == top);     // the first of that magnitude gives the sign
-    d = __shfl_sync(0xffffffffu, u, has ? __ffs(has) - 1 : 0) * R(-0.125);
-    if constexpr (sizeof(R) == 4) {
-        const float q = d != 0.f ? u * __frcp_rn(d) : 0.f, k = rintf(q);
-        code = min(max((int)k + 8, 0), 15);
-        return d != 0.f && (!(fabsf(d) > 1e-30f) || near_border(q, k));
-    } else {
-        code = code_of(u, d);
-        return false;
+    const unsigned has = __ballot_sync(0xffffffffu, fabsf(u) == top);     // the first of that magnitude gives the sign
+    d = __shfl_sync(0xffffffffu, u, has ? __ffs(has) - 1 : 0) * -0.125f;
+    const float q = d != 0.f ? u * __frcp_rn(d) : 0.f, k = rintf(q);
+    code = min(max((int)k + 8, 0), 15);
+    return d != 0.f && (!(fabsf(d) > TINY) || near_border(q, k));
+}
+// ... of the pair u, whose remainder is lost below TINY: the caller scales.
+__device__ __forceinline__ void encode_lane(Pair u, float &d, int &code) {
+    Pair top = magnitude(u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Pair other = shfl_xor(top, o);
+        if (larger(other, top)) top = other;
     }
+    const Pair mine = magnitude(u);
+    const unsigned has = __ballot_sync(0xffffffffu, mine.h == top.h && mine.l == top.l);
+    const Pair m = shfl(u, has ? __ffs(has) - 1 : 0), d2{m.h * -0.125f, m.l * -0.125f};
+    code = code_of(u, d2);
+    d = d2.h;
 }
 
 }  // namespace q4

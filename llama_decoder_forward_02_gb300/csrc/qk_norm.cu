@@ -23,7 +23,7 @@
 // Q4_0 codes are those of the exact values.  A float32 value carries a few
 // ulp of error from the norm and the rotation, which matters only next to a
 // border between two codes; a row with an element next to one (about one row in
-// 200) is encoded again from float64 arithmetic.
+// 200) is encoded again from pairs of floats (2^-42).
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"
@@ -34,11 +34,8 @@ namespace {
 
 constexpr int THREADS = 256;
 
-__device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }         // 2 ulp
-__device__ __forceinline__ double inv_sqrt(double v) { return 1.0 / sqrt(v); }
-
-template <int W, class R>
-__device__ __forceinline__ R group_sum(R v) {
+template <int W>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -46,72 +43,112 @@ __device__ __forceinline__ R group_sum(R v) {
 
 constexpr int E = 8;                      // elements of a lane
 
-// The head's values after norm and rotation, in R.
-template <int HD, class R>
+// The head's values after norm and rotation.
+template <int HD>
 __device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
-                                          bool turn, float eps, R (&u)[E]) {
+                                          bool turn, float eps, float (&u)[E]) {
     // the shuffles run for every lane: heads without a norm share the warp
-    R ss = R(0);
+    float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) ss += R(x[e]) * R(x[e]);
+    for (int e = 0; e < E; ++e) ss += x[e] * x[e];
     ss = group_sum<HD / E>(ss);
-    const R r = inv_sqrt(ss / R(HD) + R(eps));
+    const float r = rsqrtf(ss / (float)HD + eps);                    // 2 ulp
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-        const R a = norm ? R(x[e]) * r * R(gain[e]) : R(x[e]), b = norm ? R(x[e + 1]) * r * R(gain[e + 1]) : R(x[e + 1]);
+        const float a = norm ? x[e] * r * gain[e] : x[e], b = norm ? x[e + 1] * r * gain[e + 1] : x[e + 1];
         const float2 c = cs[e / 2];
-        u[e] = turn ? a * R(c.x) - b * R(c.y) : a;
-        u[e + 1] = turn ? a * R(c.y) + b * R(c.x) : b;
+        u[e] = turn ? a * c.x - b * c.y : a;
+        u[e + 1] = turn ? a * c.y + b * c.x : b;
+    }
+}
+
+// ... times up (a power of two) as pairs, good to 2^-42.
+template <int HD>
+__device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
+                                          bool turn, float eps, float up, q4::Pair (&u)[E]) {
+    q4::Pair r{0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) r = r + q4::two_prod(x[e], x[e]);
+#pragma unroll
+    for (int o = HD / E / 2; o > 0; o >>= 1) r = r + q4::shfl_xor(r, o);
+    // 1 / sqrt(v) by one Newton step from float32's
+    const q4::Pair v = q4::Pair{r.h / (float)HD, r.l / (float)HD} + q4::Pair{eps, 0.f};
+    const float r0 = rsqrtf(v.h);
+    const q4::Pair one = v * r0 * r0;
+    r = q4::settle(r0, 0.5f * r0 * __fsub_rn(__fsub_rn(1.f, one.h), one.l));
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        q4::Pair a{x[e] * up, 0.f}, b{x[e + 1] * up, 0.f};
+        if (norm) {
+            a = q4::two_prod(x[e], gain[e] * up) * r;
+            b = q4::two_prod(x[e + 1], gain[e + 1] * up) * r;
+        }
+        const float2 c = cs[e / 2];
+        u[e] = turn ? a * c.x + b * -c.y : a;
+        u[e + 1] = turn ? a * c.y + b * c.x : b;
     }
 }
 
 // The codes of a lane's elements and the scale of its block (4 lanes).
-// Returns whether a value lies so near a border that R does not settle it.
-template <class R>
-__device__ __forceinline__ bool encode(const R (&u)[E], int lane, R &d, uint32_t &word) {
-    R m = u[0];
+// Returns whether a value lies so near a border that float32 does not settle it.
+__device__ __forceinline__ bool encode(const float (&u)[E], int lane, float &d, uint32_t &word) {
+    float m = u[0];
 #pragma unroll
     for (int e = 1; e < E; ++e)
-        if (fabs(u[e]) > fabs(m)) m = u[e];
-    R top = fabs(m);
+        if (fabsf(u[e]) > fabsf(m)) m = u[e];
+    float top = fabsf(m);
 #pragma unroll
     for (int o = 2; o > 0; o >>= 1) {
-        const R other = __shfl_xor_sync(0xffffffffu, top, o);
+        const float other = __shfl_xor_sync(0xffffffffu, top, o);
         top = other > top ? other : top;
     }
     // the first element of that magnitude gives the sign
-    const unsigned has = __ballot_sync(0xffffffffu, fabs(m) == top) >> (lane & ~3) & 0xfu;
-    m = __shfl_sync(0xffffffffu, m, (lane & ~3) + (has ? __ffs(has) - 1 : 0));
-    d = m * R(-0.125);
-    bool near = false;
+    const unsigned has = __ballot_sync(0xffffffffu, fabsf(m) == top) >> (lane & ~3) & 0xfu;
+    d = __shfl_sync(0xffffffffu, m, (lane & ~3) + (has ? __ffs(has) - 1 : 0)) * -0.125f;
+    // the quotients by one reciprocal; scales that it does not reach are left to the exact form
+    const float inv = d != 0.f ? __frcp_rn(d) : 0.f;
+    bool near = d != 0.f && !(fabsf(d) > q4::TINY);
     word = 0;
-    if constexpr (sizeof(R) == 4) {
-        // the quotients by one reciprocal; scales that it does not reach are left to float64
-        const float inv = d != 0.f ? __frcp_rn(d) : 0.f;
-        near = d != 0.f && !(fabsf(d) > 1e-30f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float q = u[e] * inv, k = rintf(q);            // in [-8, 8]: the top itself is at -8
-            word |= (uint32_t)min(max((int)k + 8, 0), 15) << q4::shift_of(e);
-            near |= q4::near_border(q, k);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) word |= (uint32_t)q4::code_of(u[e], d) << q4::shift_of(e);
+    for (int e = 0; e < E; ++e) {
+        const float q = u[e] * inv, k = rintf(q);                // in [-8, 8]: the top itself is at -8
+        word |= (uint32_t)min(max((int)k + 8, 0), 15) << q4::shift_of(e);
+        near |= q4::near_border(q, k);
     }
     return near;
+}
+__device__ __forceinline__ void encode(const q4::Pair (&u)[E], int lane, float &d, uint32_t &word) {
+    q4::Pair m = u[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e)
+        if (q4::larger(q4::magnitude(u[e]), q4::magnitude(m))) m = u[e];
+    const q4::Pair mine = q4::magnitude(m);
+    q4::Pair top = mine;
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {
+        const q4::Pair other = q4::shfl_xor(top, o);
+        if (q4::larger(other, top)) top = other;
+    }
+    const unsigned has = __ballot_sync(0xffffffffu, mine.h == top.h && mine.l == top.l) >> (lane & ~3) & 0xfu;
+    m = q4::shfl(m, (lane & ~3) + (has ? __ffs(has) - 1 : 0));
+    const q4::Pair d2{m.h * -0.125f, m.l * -0.125f};
+    word = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) word |= (uint32_t)q4::code_of(u[e], d2) << q4::shift_of(e);
+    d = d2.h;
 }
 
 // The word and scale of the exact values.
 template <int HD>
 __device__ __forceinline__ void encode_exact(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
                                              bool turn, float eps, const float (&u)[E], bool used, int lane, float &d, uint32_t &word) {
-    const bool near = encode<float>(u, lane, d, word);
+    const bool near = encode(u, lane, d, word);
     if (__any_sync(0xffffffffu, near && used)) {
-        double u64[E], d64;
-        transform<HD, double>(x, gain, cs, norm, turn, eps, u64);
-        encode<double>(u64, lane, d64, word);
-        d = (float)d64;
+        const float up = fabsf(d) > q4::TINY || d == 0.f ? 1.f : q4::RAISE;     // the same for the lanes of a block
+        q4::Pair u2[E];
+        transform<HD>(x, gain, cs, norm, turn, eps, up, u2);
+        encode(u2, lane, d, word);
+        d /= up;
     }
 }
 
@@ -122,7 +159,7 @@ __device__ __forceinline__ void load8(float (&v)[E], const float *p) {
 }
 
 // grid (row, part): part p of gridDim.y takes the warps' heads p, p + parts, ..
-// Q4: the cache is Q4_0 (its float64 path would take registers from the others).
+// Q4: the cache is Q4_0 (its exact path would take registers from the others).
 // Four or five CTAs an SM keep the loads in flight.
 template <int HD, bool Q4>
 __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const QkNormArgs a) {
@@ -175,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const
             for (int e = 0; e < E; ++e) gain[e] = 1.f;
         }
         float u[E];
-        transform<HD, float>(x, gain, turn, gp != nullptr, is_q || is_k, a.eps, u);
+        transform<HD>(x, gain, turn, gp != nullptr, is_q || is_k, a.eps, u);
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) bad |= f16_bad(u[e]);
@@ -251,7 +288,7 @@ __global__ void __launch_bounds__(SHIFT_THREADS) kv_shift_q4_kernel(KvView kv, i
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = (float)((int)((w >> q4::shift_of(e)) & 15u) - 8) * d;     // exact
         uint32_t out;
-        transform<HD, float>(x, gain, back, false, true, 0.f, u);
+        transform<HD>(x, gain, back, false, true, 0.f, u);
         encode_exact<HD>(x, gain, back, false, true, 0.f, u, true, lane, nd, out);
         __syncthreads();
         if (in) {
