@@ -797,8 +797,8 @@ cudaError_t debug_copy(llm_ctx *c, const UbDev &u, int layer, const float *h, in
 }
 
 // Whether the QKV projection's rows are stored plainly for a kernel of its own
-// that norms, rotates and appends: normed queries and keys, and a Q4_0 cache,
-// need a whole head at once.
+// that norms, rotates and appends: normed queries and keys need a whole head at
+// once, a Q4_0 cache a block (which the GEMV over Q4_0 rows has, run_small_q4).
 bool plain_qkv(const llm_ctx *c) { return c->m->nbuf || c->kv_q4; }
 
 cudaError_t qk_norm(llm_ctx *c, const UbDev &u, int layer, bool prefill, const Launch &L) {

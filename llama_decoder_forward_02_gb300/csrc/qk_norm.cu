@@ -7,8 +7,8 @@
 // apply it between the projection and the rotation):
 //   u = x * gain / sqrt(mean(x^2) + eps),  (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
 // on adjacent pairs.  A model without such gains skips the norm; it comes here
-// when its cache is Q4_0, whose blocks need 32 neighbouring elements at once,
-// which no projection epilogue holds.
+// when its cache is Q4_0, whose blocks need 32 neighbouring elements at once: of
+// the projections' epilogues only that of the GEMV over Q4_0 rows holds them.
 //
 // head_dim / 8 lanes take one head of one row, eight elements (four rotation
 // pairs, one word of codes) a lane, so the norm's sum and a block's largest
@@ -19,6 +19,8 @@
 // copy bandwidth for their 153 MB (five CTAs of 48 registers an SM; four took
 // 32.8).  With four elements a lane the shuffles, addresses and branches of
 // twice as many lanes took 42.7 us, bound by issue.
+//
+// Into a Q4_0 cache 512 rows take 7.2 us (4.8 into an fp16 one), 8 rows 3.7.
 //
 // Q4_0 codes are those of the exact values.  A float32 value carries a few
 // ulp of error from the norm and the rotation, which matters only next to a

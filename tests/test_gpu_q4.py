@@ -218,6 +218,42 @@ def test_append_codes_at_borders(lib):
     assert np.array_equal(c[0, 0, :T], rc) and np.array_equal(d[0, 0, :T], rd) and int(err) == 0
 
 
+@pytest.mark.parametrize("hd,scale", [(128, 1.0), (64, 3e-32), (32, 700.0), (64, 2e-36)])
+def test_append_rotated_codes_at_borders(lib, hd, scale):
+    """Keys whose rotated values lie within float32's rounding of a code border: the exact value's side counts."""
+    rng = np.random.default_rng(hd)
+    Hkv, T, n_ctx = 2, 96, 128
+    table = rope_table(n_ctx, hd)
+    pos = np.arange(T)
+    cs = table.astype(np.float64)[pos][:, None].repeat(Hkv, 1)                      # [T][Hkv][hd / 2][2]
+    x = (rng.uniform(-1, 1, (T, Hkv, hd)) * scale).astype(np.float32)
+    x[..., 0::32] *= 40                                                             # a block's largest
+    c, s = cs[..., 0], cs[..., 1]
+    rot = lambda v: (v[..., 0::2] * c - v[..., 1::2] * s, v[..., 0::2] * s + v[..., 1::2] * c)  # noqa: E731
+    for _ in range(2):
+        even, odd = rot(x.astype(np.float64))
+        full = np.stack([even, odd], -1).reshape(T, Hkv, hd // 32, 32)
+        top = np.take_along_axis(full, np.abs(full).argmax(-1)[..., None], -1)
+        d = np.repeat((top / -8).reshape(T, Hkv, -1), 16, -1)
+        border = (rng.integers(-8, 7, d.shape) + 0.5) * d
+        a = ((border + x[..., 1::2].astype(np.float64) * s) / c).astype(np.float32)
+        keep = (np.arange(hd // 2) % 16 == 0) | (np.abs(c) < 0.3) | (np.abs(a) > 30 * scale)
+        x[..., 0::2] = np.where(keep, x[..., 0::2], a)
+    H = 2
+    qkv = np.zeros((T, (H + 2 * Hkv) * hd), np.float32)
+    qkv[:, H * hd:(H + Hkv) * hd] = x.reshape(T, -1)
+    kc, vc = (torch.zeros(lib.llm_op_kv_q4_0_bytes(Hkv, hd, n_ctx, 1), dtype=torch.uint8, device="cuda") for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run_qk(lib, qkv, qkv.shape[1], None, None, 1e-5, table, pos, [0] * T, 0, kc, vc, 2, H, Hkv, hd, n_ctx, 1, err)
+    ref = qk_reference(qkv, None, None, 1e-5, table, pos, H, Hkv, hd)[1]
+    rc, rd = O.quantize_q4_0(ref)
+    exact = np.abs(ref.reshape(T, Hkv, -1, 32) / np.repeat(np.abs(ref.reshape(T, Hkv, -1, 32)).max(-1, keepdims=True), 32, -1) * 8)
+    assert (np.abs(exact % 1 - 0.5) < 1e-6).mean() > 0.2                            # the borders are met
+    got, gd = unpack_cache(kc.cpu().numpy(), 1, Hkv, n_ctx, hd)
+    assert np.array_equal(got[0, :, :T], rc.swapaxes(0, 1)) and int(err) == 0
+    assert np.all(np.abs(gd[0, :, :T].astype(float) - rd.swapaxes(0, 1).astype(float)) <= np.abs(rd.swapaxes(0, 1)) * 2.0 ** -10 + 2.0 ** -24)
+
+
 @pytest.mark.parametrize("kt", [0, 2])
 def test_rows_outside_the_cache_and_range(lib, kt):
     """Rows whose cell does not exist are reported and append nothing; so is a value beyond fp16; other rows are as usual."""
