@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     constexpr int NB = R::NB, REC = HD + 2, THREADS = NW * 32;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ int s_last;
-    const int j = blockIdx.y / chunks, ck = blockIdx.y - j * chunks;
+    const int j = chunks == 1 ? blockIdx.y : blockIdx.y / chunks, ck = blockIdx.y - j * chunks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const int Hkv = a.kv.n_kv_head, G = a.H / Hkv, h0 = j * G + ck * GC, gn = min(GC, G - ck * GC);
     if (!a.early) {
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
         pos = a.pos[t];
         seq = a.seq[t];
         rw = row_keys(a, pos, seq);
-        len = max(MIN_GRP, (rw.groups() + a.n_split - 1) / a.n_split);
+        len = max(MIN_GRP, (rw.groups() + a.n_split - 1) >> (31 - __clz(a.n_split)));
         n_eff = a.n_split;                            // all stay for the cluster's barriers
     } else {
         sp = find_split(a, blockIdx.x, lane, t, rw, pos, seq, len, n_eff);
@@ -740,8 +740,9 @@ __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, co
 // they are one cluster; about two CTAs of 8 warps an SM in all.  The merge
 // inside a cluster costs a good microsecond less than the one through memory
 // (8 kv heads of 128: one row of 2100 keys 4.7 us, 6.3 in 16 splits through
-// memory; of 4000 keys 5.5 and 6.7; of 8000 keys 7.5 both; eight rows of 4000
-// keys 12.1 and 14.7).
+// memory; of 4000 keys 5.5 and 6.7; of 8000 keys 7.4 and 7.5; eight rows of 4000
+// keys 11.9 and 14.7).  Clusters of sixteen take 5.4 for the 2100 keys and 7.7
+// for the 8000.
 //
 // Longer caches: the rows share the splits by their lengths (find_split),
 // merged through memory.  One or two rows of 8 kv heads get one CTA of 16 warps
