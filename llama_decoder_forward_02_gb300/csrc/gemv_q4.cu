@@ -384,7 +384,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
                 if (EPI == EPI_RESID && in) h0 = a.hres[(size_t)t * a.ldh + n];
             }
             float v = 0.f;
-            for (int c = 0; c < units; ++c) v += sums[c * p.red_warp + t * RED_COL + lane];
+            if (units >= 4) {
+                float v4[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int c = 0; c < units; c += 4)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v4[k] += sums[(c + k) * p.red_warp + t * RED_COL + lane];
+                v = (v4[0] + v4[1]) + (v4[2] + v4[3]);
+            } else {
+                for (int c = 0; c < units; ++c) v += sums[c * p.red_warp + t * RED_COL + lane];
+            }
             v *= s_r[t];
             if (EPI == EPI_QKV) {
                 // lane pairs hold the elements of a rotation, 2i and 2i + 1
@@ -455,7 +463,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
             }
         }
     }
-    if (EPI == EPI_RESID && a.xg_out) {
+    if (EPI == EPI_RESID && a.xg_out && units == CW) {
+        // one row group: the warp of a row of x holds the CTA's sum
+        if (cu < a.T && lane == 0) a.ss_out[(size_t)cu * gridDim.x + blockIdx.x] = ssq[0];
+    } else if (EPI == EPI_RESID && a.xg_out) {
         // this CTA's sums of squares of the new h, in a fixed order
         int q = 0;
         for (int t = cu; t < a.T; t += units, ++q) {
