@@ -39,10 +39,10 @@
 // own, and whole tiles alone are worth 2%.
 //
 // Measured, calls in a row, one row of x where not said otherwise, and the time
-// the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 5.1 us (1.4),
-// 28672 x 4096 16.9 (9.7), 4096 x 14336 11.0 (4.9; 8 rows 11.8), 128256 x 4096
+// the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 4.5 us (1.4),
+// 28672 x 4096 16.7 (9.7), 4096 x 14336 10.2 (4.9; 8 rows 11.5), 128256 x 4096
 // 56.6 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
-// 5.4, 16.5, 11.1, 11.7 and 55.1.  3 us of each go by before the first product
+// 4.4, 15.4, 9.8, 10.6 and 55.2.  2.5 us of each go by before the first product
 // and after the last; in between the schedulers issue in 59% of their clocks
 // (ALU 46%, FMA 39%, tensor 26% of theirs) with four warps each, which wait for
 // the pipes and the shared-memory queue and hardly (0.1 of 6 warps) for memory.
@@ -56,7 +56,9 @@
 // but 16.8 instead of 16.1 for 28672 x 4096 and 11.9 instead of 11.2 for 4096 x
 // 14336 with the early requests); the chunks that 16 warps share unevenly (56 of a
 // K of 14336) cut into halves (11.8 instead of 11.0: a step that may be either half
-// is scheduled worse than the two of a chunk).
+// is scheduled worse than the two of a chunk); one kernel for all epilogues, its
+// products kept in the instruction cache (8B decode 662 tok/s instead of 676); one
+// m16 tile where the second has no rows (663).
 #include "common.cuh"
 #include "launch.cuh"
 #include "q4.cuh"
@@ -242,13 +244,15 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     }
     auto finish_stats = [&]() {
         if (!stats) return;
-        float ss = 0.f;
+        float r = 1.f;
+        if (a.ss_in) {
+            float ss = 0.f;
 #pragma unroll
-        for (int j = 0; j < SSQ; ++j) ss += part[j];
-        if (a.ss_in)
+            for (int j = 0; j < SSQ; ++j) ss += part[j];
             for (int i = lane + 32 * SSQ; i < a.n_ss_in; i += 32) ss += a.ss_in[(size_t)warp * a.n_ss_in + i];
-        ss = warp_sum(ss);
-        if (lane == 0) s_r[warp] = a.ss_in ? 1.f / sqrtf(ss / (float)a.K + a.eps) : 1.f;
+            r = 1.f / sqrtf(warp_sum(ss) / (float)a.K + a.eps);
+        }
+        if (lane == 0) s_r[warp] = r;
         if (EPI == EPI_QKV && lane == 0) {
             const bool ok = ps >= 0 && ps < a.kv.n_ctx && sq >= 0 && sq < a.kv.n_seq;
             if (!ok && blockIdx.x == 0) raise_error(a.err, ERRF_BAD_INDEX);
