@@ -344,8 +344,7 @@ int32_t llm_debug_fail_alloc(int32_t n);
  *                  fp16 (default); allowed only while every sequence is empty
  *                  (the cache is reallocated);
  *   "kv_q4"        1 = the KV cache holds Q4_0 blocks (the 4-bit operators below
- *                  have the layout; 9/32 of the fp16 cache's bytes, plus one
- *                  layer's rows in fp16 that prefill widens into), 0 = fp16
+ *                  have the layout; 9/32 of the fp16 cache's bytes), 0 = fp16
  *                  (default); allowed only while every sequence is empty, and not
  *                  together with kv_fp8; a failed call changes nothing;
  *   "gemv_q4"      1 = steps of 1..8 rows of a Q4_0 model read its Q4_0 rows
@@ -373,7 +372,7 @@ int64_t llm_kernel_launches(const llm_ctx *c);
  * LLM_KERNEL_CLASSES-1), the summed duration in milliseconds, the launch count
  * and a static name ("gemv_gateup_swiglu", "attn_decode", ...); it returns
  * LLM_ERR_INVALID past the last class. */
-#define LLM_KERNEL_CLASSES 18
+#define LLM_KERNEL_CLASSES 17
 int32_t llm_kernel_timing(llm_ctx *c, int32_t enable);
 int32_t llm_kernel_time(llm_ctx *c, int32_t kernel, double *total_ms, int64_t *count, const char **name);
 
@@ -499,8 +498,8 @@ int32_t llm_op_attn_decode_noalloc(const float *q, const void *k_cache, const vo
 /* --------------------------------------------------------------------------
  * 4-bit operators: Q4_0 weights, a Q4_0 cache, and the per-head query/key norm
  * that feeds it.  None of these calls allocates or waits: each enqueues its
- * kernels on `stream` and returns, so they can be captured into a CUDA graph
- * (the prefill attention as it says).  Pointers belong to the current device.
+ * kernels on `stream` and returns, so they can be captured into a CUDA graph.
+ * Pointers belong to the current device.
  *
  * Q4_0 blocks ("LLama.cpp — how it works" names four-bit types in "The GGUF
  * format (reference)" and a quantised cache in "KV-cache" without a layout;
@@ -603,13 +602,14 @@ int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void 
  * sequence seq[r] at position pos[r] and see the positions a decode row would.
  * pos, seq are HOST arrays, read before the call returns: the rows of a
  * sequence are consecutive with consecutive positions, else LLM_ERR_INVALID
- * before anything is enqueued.  o fp16 [T][H*hd].  K and V are rounded to fp16
- * and the softmax weights, as over an fp16 cache, come from exponents rounded
- * to fp16 (head_dim 64 and 128; 5e-4 of o's norm together).  q, the caches and
- * o 16-byte aligned.  scratch (contents need not be initialised) takes the
- * visible cells widened to fp16; calls that may overlap need one each.  err: DEVICE word or NULL, ORed with 4 when a bounded
- * wait of the kernel timed out.  For stream capture only with rows of at most
- * 64 sequences (a longer list is copied from host memory). */
+ * before anything is enqueued.  o fp16 [T][H*hd].  q, K and V enter the products
+ * exactly and the softmax weights with 22 bits (below 2^-21 of the row's largest
+ * with 2^-31 of it); sums are fp32.  A visible cell whose scale stands for values
+ * beyond fp16's range (more than 8188, an infinity or a NaN) makes the heads that
+ * see it NaN; cells that a row does not see may hold anything.  q, the caches and
+ * o 16-byte aligned.  scratch, scratch_bytes: not used, may be NULL and 0 (kept, with
+ * the size they used to need, for programs written against them).  err: DEVICE word
+ * or NULL, ORed with 4 when a bounded wait of the kernel timed out. */
 int64_t llm_op_attn_prefill_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
                                                int32_t n_seq);
 int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void *v_cache, const int32_t *pos,

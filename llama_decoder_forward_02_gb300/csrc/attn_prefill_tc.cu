@@ -56,6 +56,7 @@
 #include "tma.cuh"
 #include "cluster.cuh"
 #include "gemm_tc_common.cuh"
+#include "attn_tc.cuh"
 
 namespace llm {
 
@@ -65,6 +66,7 @@ using tcg::sdesc;
 using tcg::tc_fence_after;
 using tcg::tc_fence_before;
 using tcg::tmem_ld32;
+using namespace tca;
 
 constexpr int BQ = 128, BKEY = 128, FA_THREADS = 384;   // 2 + 8 + 2 warps
 constexpr int SM_WARPS = 8;                                   // softmax warps (2-9)
@@ -96,60 +98,6 @@ struct FaCfg {
         (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(BQ >> 4) << 24);
 };
 
-__device__ __forceinline__ void mma1(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-        :: "r"(tmem), "l"(a), "l"(b), "r"(idesc), "r"(accum) : "memory");
-}
-// The same with A in tensor memory (P: lane = row, 32-bit column j = the fp16
-// pair of keys 2j, 2j + 1; a K = 16 step reads 8 columns).
-__device__ __forceinline__ void mma1_ts(uint32_t tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accum) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        :: "r"(tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum) : "memory");
-}
-__device__ __forceinline__ void commit1(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
-}
-// Shared-memory descriptor of an MN-major operand (the MN dimension
-// contiguous) in the 128-byte-swizzle layout: atoms of 64 MN elements x 8 K
-// rows; `lbo` bytes between 64-element MN blocks, 1024 bytes between 8-row K
-// groups.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// One 32-bit value per lane to / from a TMEM column (the softmax halves
-// exchange their row maxima and sums through columns of an idle S buffer).
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" :: "r"(taddr), "r"(__float_as_uint(v)) : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-    uint32_t v;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-    return __uint_as_float(v);
-}
 // 2^x of an fp16 pair on the special-function unit (two results an op)
 __device__ __forceinline__ uint32_t ex2_h2(uint32_t x) {
     uint32_t y;
@@ -163,11 +111,6 @@ __device__ __forceinline__ float add_h2_f32(uint32_t p, float acc) {
         "fma.rn.f32.f16 %0, lo, one, %0;\n\tfma.rn.f32.f16 %0, hi, one, %0;\n\t}"
         : "+f"(acc) : "r"(p));
     return acc;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 // The softmax warps (2-9) of a query tile: two threads per row, each on 64
 // keys of every 128-key tile (see the kernel comment).  s_full(b) / pv_done(pb)
@@ -340,7 +283,6 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     auto v_box = [&](int s, int i) { return base + C::V_OFF + (s * C::NB + i) * BOX; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a.tiles_late) pdl_wait();
     // longest tiles (latest positions) first
     const AttnTile tl = a.tiles[a.n_tiles - 1 - (int)blockIdx.x];
     const int h = blockIdx.y, G = a.H / a.Hkv, j = h / G;

@@ -1,10 +1,10 @@
-// Attention over a Q4_0 cache ("LLama.cpp — how it works", "KV-cache": a
+// Decode attention over a Q4_0 cache ("LLama.cpp — how it works", "KV-cache": a
 // quantised cache where memory is short; the attention itself as in
 // attn_decode.cu): for each row t and query head h, o = softmax(q K^T /
 // sqrt(hd)) V over the visible positions of sequence seq[t], K and V standing
 // for d * (c - 8) (q4.cuh).
 //
-// Decode.  Bound by HBM reads of K and V: 9/8 bytes a (key, element), which
+// Bound by HBM reads of K and V: 9/8 bytes a (key, element), which
 // leaves an SM about 100 clocks for 16 keys of 128 elements at the copy
 // bandwidth.  Widening every code on the CUDA cores costs more than that, so
 // the codes go to mma.sync as they are, the fp16 subnormals that masking a
@@ -43,15 +43,6 @@
 // sends its share to the rank that merges it before the one barrier they meet
 // at; reading it there after the barrier, with a second one to leave by, took
 // 0.7 more.
-//
-// Prefill: the visible rows of the ubatch's sequences are widened once to fp16
-// and the fp16 prefill attention runs on them: 512 rows from position 1536 on
-// take 24.6 us, of which the attention's tensor work is 7.6 at the measured
-// rate.  A tile of it takes what its softmax takes, so widening inside it
-// would lengthen what bounds it, once for each of the G * tiles CTAs that read
-// the same keys.  Rounding d * (c - 8) to fp16 is what an fp16 cache holds; the
-// fp16 exponents of its softmax move o by as much (together 5e-4 of its norm,
-// 2e-4 of which is o's own rounding).
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -666,49 +657,7 @@ __device__ __forceinline__ uint4 widen_word(uint32_t word, float d) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Widening reads 9/16 byte and writes two an element: bound by memory, 1.6 us at
-// the copy bandwidth for 2048 rows of 8 heads of 128.
 constexpr int WT = 256;
-
-// A thread's part of widening span sp: row block blockIdx.x, kv head blockIdx.y,
-// one word of K and of V.
-__device__ __forceinline__ void widen_span(const KvView &kv, const KvSpan &sp, f16 *k16, f16 *v16, int n_pad) {
-    const int hd = kv.head_dim, wpr = hd / 8, nb = hd / 32;      // words of a row, blocks of a row
-    const int r0 = sp.lo / 128 * 128, r1 = (sp.hi + 127) / 128 * 128;
-    const int row = r0 + (int)(blockIdx.x * (WT / wpr) + threadIdx.x / wpr), w = threadIdx.x % wpr;
-    if (row >= r1) return;
-    const size_t dst = (((size_t)sp.seq * kv.n_kv_head + blockIdx.y) * n_pad + row) * hd + 32 * (w % nb) + 8 * (w / nb);
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-    if (row >= sp.lo && row < sp.hi) {
-        const size_t e = (size_t)sp.seq * kv.seq_stride + ((size_t)blockIdx.y * kv.n_ctx + row) * hd;
-        k = widen_word(reinterpret_cast<const uint32_t *>(kv.k4 + e / 2)[w], hf(kv.kd[e / 32 + w % nb]));
-        v = widen_word(reinterpret_cast<const uint32_t *>(kv.v4 + e / 2)[w], hf(kv.vd[e / 32 + w % nb]));
-    }
-    *reinterpret_cast<uint4 *>(k16 + dst) = k;
-    *reinterpret_cast<uint4 *>(v16 + dst) = v;
-}
-
-__global__ void __launch_bounds__(WT) kv_widen_q4_kernel(const KvView kv, const KvSpan *spans, f16 *k16, f16 *v16,
-                                                         int n_pad) {
-    pdl_wait();
-    pdl_trigger();
-    widen_span(kv, spans[blockIdx.z], k16, v16, n_pad);
-}
-
-// The same for runs of rows passed by value, which also leaves their tiles of
-// at most tile_rows rows in device memory: no copy from the host is needed.
-__global__ void __launch_bounds__(WT) kv_widen_q4_runs_kernel(const KvView kv, const KvRuns runs, int window, int tile_rows,
-                                                              AttnTile *tiles, f16 *k16, f16 *v16, int n_pad) {
-    pdl_wait();
-    pdl_trigger();
-    const KvRuns::Run r = runs.run[blockIdx.z];
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = threadIdx.x; i * tile_rows < r.n_rows; i += WT)
-            tiles[r.tile0 + i] = AttnTile{r.row0 + i * tile_rows, min(tile_rows, r.n_rows - i * tile_rows), r.seq,
-                                          r.pos0 + i * tile_rows, 0};
-    const int lo = window > 0 && r.pos0 + 1 > window ? r.pos0 + 1 - window : 0;
-    widen_span(kv, KvSpan{r.seq, lo, r.pos0 + r.n_rows}, k16, v16, n_pad);
-}
 
 __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, const f16 *scales, const KvView kv,
                                                         const int *pos, const int *seq, f16 *out, int T, uint32_t *err) {
@@ -822,25 +771,6 @@ cudaError_t init_attn_q4_attributes() {
 #undef Q4_DEC_ATTR
 #undef Q4_DEC_ATTR1
     return e;
-}
-
-cudaError_t launch_kv_widen_q4(const KvView &kv, const KvSpan *spans, int n_spans, int max_rows, f16 *k16, f16 *v16,
-                               int n_pad, const Launch &l) {
-    if (n_spans < 1) return cudaSuccess;
-    if (n_spans > 65535 || kv.n_kv_head > 65535 || n_pad % 128 || n_pad < kv.n_ctx || !kv.k4) return cudaErrorInvalidValue;
-    // a span touches at most max_rows / 128 + 2 tiles of 128 rows
-    const int rows = (max_rows / 128 + 2) * 128, per = WT / (kv.head_dim / 8);
-    return launch_kernel(kv_widen_q4_kernel, dim3((rows + per - 1) / per, kv.n_kv_head, n_spans), dim3(WT), 0, l, kv,
-                         spans, k16, v16, n_pad);
-}
-
-cudaError_t launch_kv_widen_q4_runs(const KvView &kv, const KvRuns &runs, int n_runs, int max_rows, int window,
-                                    int tile_rows, AttnTile *tiles, f16 *k16, f16 *v16, int n_pad, const Launch &l) {
-    if (n_runs < 1 || n_runs > KvRuns::MAX || kv.n_kv_head > 65535 || n_pad % 128 || n_pad < kv.n_ctx || !kv.k4)
-        return cudaErrorInvalidValue;
-    const int rows = (max_rows / 128 + 2) * 128, per = WT / (kv.head_dim / 8);
-    return launch_kernel(kv_widen_q4_runs_kernel, dim3((rows + per - 1) / per, kv.n_kv_head, n_runs), dim3(WT), 0, l, kv,
-                         runs, window, tile_rows, tiles, k16, v16, n_pad);
 }
 
 cudaError_t launch_kv_rows_q4(const uint8_t *codes, const f16 *scales, const KvView &kv, const int *pos,

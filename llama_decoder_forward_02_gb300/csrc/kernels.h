@@ -149,7 +149,6 @@ struct AttnPrefillTcArgs {
     f16 *o; int ldo;                        // o [rows][ldo], head h at column h*hd
     uint32_t *err;
     int window;                             // sliding window (0 = all earlier positions)
-    bool tiles_late = false;                // the kernel before this one writes the tiles
 };
 struct TmaMap;
 bool attn_prefill_tc_ok(int head_dim, bool fp8_cache);
@@ -357,22 +356,18 @@ cudaError_t launch_kv_shift_q4(const KvView &kv0, int n_layer, int seq, int p0, 
 size_t attn_q4_scratch_bytes(int T, int H, int Hkv, int hd, int n_ctx);
 cudaError_t launch_attn_decode_q4(AttnDecodeArgs a, void *scratch, const Launch &l);
 
-// Key ranges [lo, hi) of sequences to widen from a Q4_0 cache to fp16.
-struct KvSpan { int seq, lo, hi; };
-// Widen the spans' rows of both caches into k16, v16, laid out
-// [n_seq][Hkv][n_pad][hd] (n_pad a multiple of 128): rows [lo, hi) as the
-// values they stand for, the other rows of the 128-row tiles they touch zero.
-cudaError_t launch_kv_widen_q4(const KvView &kv, const KvSpan *spans, int n_spans, int max_rows, f16 *k16, f16 *v16,
-                               int n_pad, const Launch &l);
-// The same for runs of rows of one sequence each (n_rows rows from pos0 on,
-// rows row0.. of the batch), passed by value; it also writes their attention
-// tiles (of at most tile_rows rows, a run's from tiles[tile0] on).
+// Prefill attention over a Q4_0 cache (AttnPrefillArgs with kv.k4 set): on tcgen05
+// with mQ, the map of q (boxes of 128 rows x 64; head_dim 64 or 128), else on
+// mma.sync.  Tiles of at most attn_prefill_q4_rows rows come from memory
+// (a.tiles), or, where that is null, from runs passed by value: n_rows rows of
+// one sequence from pos0 on, rows row0.. of the batch, whose tiles are tile0.. .
 struct KvRuns {
     static constexpr int MAX = 64;
     struct Run { int row0, n_rows, seq, pos0, tile0; } run[MAX];
 };
-cudaError_t launch_kv_widen_q4_runs(const KvView &kv, const KvRuns &runs, int n_runs, int max_rows, int window,
-                                    int tile_rows, AttnTile *tiles, f16 *k16, f16 *v16, int n_pad, const Launch &l);
+bool attn_prefill_q4_tc_ok(int head_dim);
+int attn_prefill_q4_rows(bool tc);
+cudaError_t launch_attn_prefill_q4(const AttnPrefillArgs &a, const KvRuns *runs, int n_runs, const TmaMap *mQ, const Launch &l);
 // out[t][j][:] = the values of row pos[t], kv head j of sequence seq[t].
 cudaError_t launch_kv_rows_q4(const uint8_t *codes, const f16 *scales, const KvView &kv, const int *pos,
                               const int *seq, f16 *out, int T, uint32_t *err, const Launch &l);

@@ -33,6 +33,7 @@ cudaError_t init_sample_attributes();
 cudaError_t init_gemv_stream_attributes();
 cudaError_t init_gemv_q4_attributes();
 cudaError_t init_attn_q4_attributes();
+cudaError_t init_attn_prefill_q4_attributes();
 
 // Kernel attributes (dynamic shared-memory limits, carveouts) take effect on
 // the device that is current when they are set, so they are set once per
@@ -57,6 +58,7 @@ cudaError_t init_kernel_attributes() {
         if (!e) e = init_gemv_stream_attributes();
         if (!e) e = init_gemv_q4_attributes();
         if (!e) e = init_attn_q4_attributes();
+        if (!e) e = init_attn_prefill_q4_attributes();
         status[dev] = e;
         done[dev] = true;
     }
@@ -108,12 +110,12 @@ struct llm_model {
 enum KId {
     K_EMBED, K_GATHER, K_GEMV_QKV, K_ATTN_DECODE, K_GEMV_O, K_GEMV_GATEUP, K_GEMV_DOWN,
     K_GEMV_LMHEAD, K_GEMM_QKV, K_ATTN_PREFILL, K_GEMM_O, K_GEMM_GATEUP, K_GEMM_DOWN, K_GEMM_LMHEAD,
-    K_ARGMAX, K_COPY, K_QK_NORM, K_KV_WIDEN, K_COUNT
+    K_ARGMAX, K_COPY, K_QK_NORM, K_COUNT
 };
 static const char *const KNAME[K_COUNT] = {
     "embed", "gather_rows", "gemv_qkv_rope_kv", "attn_decode", "gemv_o_resid", "gemv_gateup_swiglu",
     "gemv_down_resid", "gemv_lm_head", "gemm_qkv_rope_kv", "attn_prefill", "gemm_o_resid", "gemm_gateup_swiglu",
-    "gemm_down_resid", "gemm_lm_head", "argmax", "copy", "qk_norm_rope_kv", "kv_widen"};
+    "gemm_down_resid", "gemm_lm_head", "argmax", "copy", "qk_norm_rope_kv"};
 
 struct KtRec { int id; cudaEvent_t a, b; };
 
@@ -127,13 +129,9 @@ struct llm_ctx {
     size_t kv_elems = 0;                      // elements of each of kc, vc
     bool kv_fp8 = false;                      // kc, vc hold FP8 E4M3 (one byte an element)
     // Q4_0 cache (option "kv_q4"): kc, vc hold a plane of codes, then one of
-    // scales (9/16 byte an element); decode attention's split scratch; prefill
-    // widens a layer's visible rows into k16, v16 [seq][kv_head][n_pad][hd]
+    // scales (9/16 byte an element); decode attention's split scratch
     bool kv_q4 = false;
     void *q4_scratch = nullptr;
-    f16 *k16 = nullptr, *v16 = nullptr;
-    int n_pad = 0;
-    TmaMap ak16, av16;
     float *qkv = nullptr;          // QKV projection rows [n_ubatch][n_qkv], where a kernel of its own norms, rotates and appends
     float *ss_q4 = nullptr;        // Q4_0 steps: per-CTA sums of h^2 [8][num_sms]
     float2 *rope = nullptr;
@@ -481,8 +479,7 @@ static void ctx_release(llm_ctx *c) {
     void *dev[] = {c->kc, c->vc, c->rope, c->rope_t, c->h, c->h2, c->ss, c->ss2, c->qf, c->x, c->qb, c->o, c->u,
                    c->gemv_part, c->gemv_cnt, c->sk_ws, c->sk_flags, c->attn_part, c->attn_cnt, c->meta_dev, c->dec_dev,
                    c->logits, c->argmax_dev, c->gen_tokens, c->err_dev,
-                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->q4_scratch,
-                   c->k16, c->v16};
+                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->q4_scratch};
     for (void *p : dev) if (p) cudaFree(p);
     for (int i = 0; i < 2; ++i) {
         if (c->meta_host[i]) cudaFreeHost(c->meta_host[i]);
@@ -509,13 +506,8 @@ static void make_attn_maps(llm_ctx *c) {
     const long long rows = (long long)c->n_seq_max * m->L * m->Hkv * c->n_ctx;
     const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
     if (c->kv_q4) {
-        // the widened rows of one layer
-        const long long rows16 = (long long)c->n_seq_max * m->Hkv * c->n_pad;
         c->attn_pair_ok = false;
-        c->attn_tc_ok = attn_prefill_tc_ok(m->hd, false) && rows16 < (1ll << 31) &&
-                        make_operand_map(&c->aq, c->qb, nub, m->n_q, 128) &&
-                        make_operand_map(&c->ak16, c->k16, (int)rows16, m->hd, 128) &&
-                        make_operand_map(&c->av16, c->v16, (int)rows16, m->hd, 128);
+        c->attn_tc_ok = attn_prefill_q4_tc_ok(m->hd) && make_operand_map(&c->aq, c->qb, nub, m->n_q, 128);
         return;
     }
     c->attn_tc_ok = !c->kv_fp8 && attn_prefill_tc_ok(m->hd, false) && rows < (1ll << 31) &&
@@ -711,8 +703,6 @@ struct UbDev {
     int n_tiles;
     const AttnTile *tiles128; // up to 128 rows each (tcgen05 prefill attention)
     int n_tiles128;
-    const KvSpan *spans;      // Q4_0 cache: the sequences' visible rows (prefill widens them)
-    int n_spans, max_span;
     int T, n_out;
     int out_base;             // first logits row of this ubatch
     int ub_index;
@@ -1031,29 +1021,15 @@ GemmArgs gemm_base(llm_ctx *c, const f16 *A, const f16 *W, int M, int N, int K) 
     return g;
 }
 
-// Prefill attention of a Q4_0 cache: the layer's visible rows widened to fp16,
-// then the fp16 attention on them (its tiles say that no key is ready before).
+// Prefill attention of a Q4_0 cache, out of its codes.
 cudaError_t attn_prefill_q4(llm_ctx *c, const UbDev &u, const KvView &kv) {
-    const llm_model *m = c->m;
-    const Launch L = lnch_prefill(c);
-    cudaError_t e = timed(c, K_KV_WIDEN, [&] {
-        return launch_kv_widen_q4(kv, u.spans, u.n_spans, u.max_span, c->k16, c->v16, c->n_pad, L);
-    });
-    if (e) return e;
-    if (c->attn_tc_ok && c->attn_mode > 0) {
-        AttnPrefillTcArgs at;
-        at.tiles = u.tiles128; at.n_tiles = u.n_tiles128; at.H = m->H; at.Hkv = m->Hkv; at.head_dim = m->hd;
-        at.n_layer = 1; at.layer = 0; at.n_ctx = c->n_pad; at.n_seq = c->n_seq_max;
-        at.o = c->o; at.ldo = m->n_q; at.err = c->err_dev; at.window = c->swa_window;
-        return timed(c, K_ATTN_PREFILL, [&] { return launch_attn_prefill_tc(at, c->aq, c->ak16, c->av16, L); });
-    }
+    const bool tc = c->attn_tc_ok && c->attn_mode > 0;
     AttnPrefillArgs at;
-    at.q = c->qb;
-    at.kv.k = c->k16; at.kv.v = c->v16;
-    at.kv.seq_stride = (long long)m->Hkv * c->n_pad * m->hd;
-    at.kv.n_ctx = c->n_pad; at.kv.n_seq = c->n_seq_max; at.kv.head_dim = m->hd; at.kv.n_kv_head = m->Hkv;
-    at.tiles = u.tiles; at.n_tiles = u.n_tiles; at.o = c->o; at.H = m->H; at.err = c->err_dev; at.window = c->swa_window;
-    return timed(c, K_ATTN_PREFILL, [&] { return launch_attn_prefill(at, L); });
+    at.q = c->qb; at.kv = kv; at.o = c->o; at.H = c->m->H; at.err = c->err_dev; at.window = c->swa_window;
+    at.tiles = tc ? u.tiles128 : u.tiles; at.n_tiles = tc ? u.n_tiles128 : u.n_tiles;
+    return timed(c, K_ATTN_PREFILL, [&] {
+        return launch_attn_prefill_q4(at, nullptr, 0, tc ? &c->aq : nullptr, lnch_prefill(c));
+    });
 }
 
 // Prefill-sized ubatch: tensor-core GEMMs and tiled causal attention.  Each
@@ -1225,22 +1201,6 @@ cudaError_t launch_decode_graph(llm_ctx *c, int T) {
     return cudaGraphLaunch(c->graph[T], c->stream);
 }
 
-// The sequences of ubatch rows [s0, s1) with the cells their rows see: from the
-// first row's window on, up to the last row.
-int build_spans(const std::vector<int32_t> &seq, const std::vector<int32_t> &pos, int s0, int s1, int window,
-                std::vector<KvSpan> &out) {
-    out.clear();
-    for (int i = s0; i < s1; ++i) {
-        size_t k = 0;
-        while (k < out.size() && out[k].seq != seq[i]) ++k;
-        const int lo = window > 0 && pos[i] + 1 > window ? pos[i] + 1 - window : 0;
-        if (k == out.size()) out.push_back(KvSpan{seq[i], lo, pos[i] + 1});
-        out[k].lo = std::min(out[k].lo, lo);
-        out[k].hi = std::max(out[k].hi, pos[i] + 1);
-    }
-    return (int)out.size();
-}
-
 // The attention tiles of ubatch rows [s0, s1): runs of at most max_rows rows
 // of one sequence (consecutive positions); kv_ready is the sequence's first
 // position in the ubatch, below which its keys were cached before it.
@@ -1293,9 +1253,6 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
         const int nub = (int)p.ub_start.size() - 1;
         std::vector<size_t> off_tok(nub), off_rows(nub), off_tiles(nub), off_tiles128(nub);
         std::vector<int> n_tiles(nub), n_tiles128(nub), n_out(nub);
-        // Q4_0 cache: the visible cells of each ubatch's sequences
-        std::vector<std::vector<KvSpan>> spans(c->kv_q4 ? nub : 0);
-        std::vector<size_t> off_spans(nub);
         constexpr size_t TILE_INTS = sizeof(AttnTile) / sizeof(int);
         size_t ints = 3 * (size_t)p.n;
         for (int k = 0; k < nub; ++k) {
@@ -1309,10 +1266,6 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             ints = align_up(ints, 4);
             off_tiles[k] = ints; ints += (size_t)n_tiles[k] * TILE_INTS;
             off_tiles128[k] = ints; ints += (size_t)n_tiles128[k] * TILE_INTS;
-            if (c->kv_q4) {
-                off_spans[k] = ints;
-                ints += build_spans(p.seq, p.pos, s0, s1, c->swa_window, spans[k]) * (sizeof(KvSpan) / sizeof(int));
-            }
         }
         if (c->meta_cap < ints) {
             CK(cudaStreamSynchronize(c->stream));
@@ -1342,12 +1295,6 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             for (int i = s0; i < s1; ++i) if (p.out[i]) rows[r++] = i - s0;
             build_tiles(p.seq, p.pos, s0, s1, 64, reinterpret_cast<AttnTile *>(hs + off_tiles[k]));
             build_tiles(p.seq, p.pos, s0, s1, 128, reinterpret_cast<AttnTile *>(hs + off_tiles128[k]));
-            if (c->kv_q4) {
-                memcpy(hs + off_spans[k], spans[k].data(), spans[k].size() * sizeof(KvSpan));
-                // every key the attention reads comes from the widening just before it
-                for (int i = 0; i < n_tiles[k]; ++i) reinterpret_cast<AttnTile *>(hs + off_tiles[k])[i].kv_ready = 0;
-                for (int i = 0; i < n_tiles128[k]; ++i) reinterpret_cast<AttnTile *>(hs + off_tiles128[k])[i].kv_ready = 0;
-            }
         }
         CK(cudaMemcpyAsync(c->meta_dev, hs, ints * sizeof(int), cudaMemcpyHostToDevice, c->stream));
         CK(cudaEventRecord(c->meta_ev[slot], c->stream));
@@ -1365,12 +1312,6 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             u.n_tiles = n_tiles[k];
             u.tiles128 = reinterpret_cast<const AttnTile *>(c->meta_dev + off_tiles128[k]);
             u.n_tiles128 = n_tiles128[k];
-            u.spans = nullptr; u.n_spans = u.max_span = 0;
-            if (c->kv_q4) {
-                u.spans = reinterpret_cast<const KvSpan *>(c->meta_dev + off_spans[k]);
-                u.n_spans = (int)spans[k].size();
-                for (const KvSpan &sp : spans[k]) u.max_span = std::max(u.max_span, sp.hi - sp.lo);
-            }
             u.out_base = out_base;
             u.ub_index = k;
             out_base += n_out[k];
@@ -1596,19 +1537,18 @@ extern "C" int32_t llm_debug_hidden(llm_ctx *c, float *dst, int32_t max_rows, in
 static int32_t set_kv_q4(llm_ctx *c, bool want) {
     const llm_model *m = c->m;
     const size_t bytes = want ? c->kv_elems / 2 + c->kv_elems / 16 : c->kv_elems * sizeof(f16);
-    const int n_pad = (c->n_ctx + 127) / 128 * 128, nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
-    const size_t plane = (size_t)c->n_seq_max * m->Hkv * n_pad * m->hd * sizeof(f16);
+    const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
     size_t scratch = 0;
     for (int T = 1; T <= 8; ++T) scratch = std::max(scratch, attn_q4_scratch_bytes(T, m->H, m->Hkv, m->hd, c->n_ctx));
-    void *p[6] = {nullptr};
-    const size_t need[6] = {bytes, bytes, plane, plane, scratch, c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
-    const int n = want ? 6 : 2;
+    void *p[4] = {nullptr};
+    const size_t need[4] = {bytes, bytes, scratch, c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
+    const int n = want ? 4 : 2;
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) ok = !need[i] || cudaMalloc(&p[i], need[i]) == cudaSuccess;
     if (ok) {
         cudaStreamSynchronize(c->stream);
         ok = cudaMemsetAsync(p[0], 0, bytes, c->stream) == cudaSuccess && cudaMemsetAsync(p[1], 0, bytes, c->stream) == cudaSuccess &&
-             (!want || cudaMemsetAsync(p[4], 0, need[4], c->stream) == cudaSuccess);
+             (!want || cudaMemsetAsync(p[2], 0, need[2], c->stream) == cudaSuccess);
     }
     if (!ok) {
         cudaGetLastError();
@@ -1616,11 +1556,10 @@ static int32_t set_kv_q4(llm_ctx *c, bool want) {
         return fail(c, LLM_ERR_ALLOC, "KV cache reallocation failed");
     }
     cudaFree(c->kc); cudaFree(c->vc);
-    cudaFree(c->k16); cudaFree(c->v16); cudaFree(c->q4_scratch);
+    cudaFree(c->q4_scratch);
     c->kc = (f16 *)p[0]; c->vc = (f16 *)p[1];
-    c->k16 = (f16 *)p[2]; c->v16 = (f16 *)p[3]; c->n_pad = want ? n_pad : 0;
-    c->q4_scratch = p[4];
-    if (p[5]) c->qkv = (float *)p[5];
+    c->q4_scratch = p[2];
+    if (p[3]) c->qkv = (float *)p[3];
     c->kv_q4 = want;
     make_attn_maps(c);
     drop_graphs(c);

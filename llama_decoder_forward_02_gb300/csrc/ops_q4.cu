@@ -181,12 +181,14 @@ extern "C" int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, 
     return launched(who, launch_attn_decode_q4(at, scratch, overlapped(stream)));
 }
 
-// scratch: K, then V widened [n_seq][Hkv][padded n_ctx][hd], tiles, spans
+// Not used any more (the kernels widen what they read themselves): two fp16
+// planes [n_seq][Hkv][padded n_ctx][hd] and the row lists, as programs written
+// for them size it.
 extern "C" int64_t llm_op_attn_prefill_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
                                                           int32_t n_seq) {
     if (shape_error(T, H, Hkv, hd, n_ctx, n_seq)) return LLM_ERR_INVALID;
     const size_t plane = align256(cache_rows(n_seq, Hkv, padded_ctx(n_ctx)) * hd * sizeof(f16));
-    return (int64_t)(256 + 2 * plane + align256((size_t)T * sizeof(AttnTile)) + align256((size_t)std::min(T, n_seq) * sizeof(KvSpan)));
+    return (int64_t)(256 + 2 * plane + align256((size_t)T * sizeof(AttnTile)));
 }
 
 extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void *v_cache, const int32_t *pos,
@@ -197,17 +199,13 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
     if (!q || !k_cache || !v_cache || !pos || !seq || !o) return refuse(who, "a pointer is NULL");
     if (const char *why = shape_error(T, H, Hkv, hd, n_ctx, n_seq)) return refuse(who, why);
     if (window < 0) return refuse(who, "window must not be negative");
-    if (!scratch || scratch_bytes < llm_op_attn_prefill_q4_0_scratch_bytes(T, H, Hkv, hd, n_ctx, n_seq))
-        return refuse(who, "scratch is NULL or smaller than llm_op_attn_prefill_q4_0_scratch_bytes");
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16))
         return refuse(who, "q, the caches and o must be 16-byte aligned");
-    const int n_pad = padded_ctx(n_ctx);
-    const bool tc = attn_prefill_tc_ok(hd, false) && (long long)n_seq * Hkv * n_pad < (1ll << 31);
-    const int rows_max = tc ? 128 : 64;
-    std::vector<AttnTile> tiles;
-    std::vector<KvSpan> spans;
-    KvRuns runs;
-    int longest = 0;
+    (void)scratch;
+    (void)scratch_bytes;
+    const bool tc = attn_prefill_q4_tc_ok(hd);
+    const int rows_max = attn_prefill_q4_rows(tc);
+    std::vector<KvRuns::Run> runs;
     try {
         for (int i = 0; i < T;) {
             if (seq[i] < 0 || seq[i] >= n_seq) return refuse(who, "a sequence id is outside [0, n_seq)");
@@ -218,16 +216,11 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
                     return refuse(who, "positions of a sequence's rows must be consecutive");
                 ++j;
             }
-            const int lo = window > 0 && pos[i] + 1 > window ? pos[i] + 1 - window : 0, hi = pos[j - 1] + 1;
-            spans.push_back(KvSpan{seq[i], lo, hi});
-            longest = std::max(longest, hi - lo);
-            if (spans.size() <= KvRuns::MAX) runs.run[spans.size() - 1] = KvRuns::Run{i, j - i, seq[i], pos[i], (int)tiles.size()};
-            for (int r = i; r < j; r += rows_max)
-                tiles.push_back(AttnTile{r, std::min(rows_max, j - r), seq[i], pos[r], 0});
+            runs.push_back(KvRuns::Run{i, j - i, seq[i], pos[i], 0});
             i = j;
         }
         std::vector<int> ids;
-        for (const KvSpan &s : spans) ids.push_back(s.seq);
+        for (const KvRuns::Run &r : runs) ids.push_back(r.seq);
         std::sort(ids.begin(), ids.end());
         if (std::adjacent_find(ids.begin(), ids.end()) != ids.end())
             return refuse(who, "the rows of a sequence must be consecutive");
@@ -236,47 +229,26 @@ extern "C" int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, 
         return LLM_ERR_ALLOC;
     }
     if (cudaError_t e = init_kernel_attributes()) return launched(who, e);
-    const Launch L{(cudaStream_t)stream, false, nullptr};
-    const size_t plane = align256(cache_rows(n_seq, Hkv, n_pad) * hd * sizeof(f16));
-    char *base = (char *)align256((size_t)scratch);
-    f16 *k16 = (f16 *)base, *v16 = (f16 *)(base + plane);
-    AttnTile *dtiles = (AttnTile *)(base + 2 * plane);
-    KvSpan *dspans = (KvSpan *)(base + 2 * plane + align256((size_t)T * sizeof(AttnTile)));
-    const KvView kv = q4_view(k_cache, v_cache, Hkv, hd, n_ctx, n_seq);
-    cudaError_t e = cudaSuccess;
-    const bool late = spans.size() <= KvRuns::MAX;    // a kernel writes the tiles, which the next may overlap
-    if (late) {
-        e = launch_kv_widen_q4_runs(kv, runs, (int)spans.size(), longest, window, rows_max, dtiles, k16, v16, n_pad,
-                                    overlapped(stream));
-    } else {
-        // copies from pageable memory: staged before the call returns
-        e = cudaMemcpyAsync(dtiles, tiles.data(), tiles.size() * sizeof(AttnTile), cudaMemcpyHostToDevice, L.stream);
-        if (!e) e = cudaMemcpyAsync(dspans, spans.data(), spans.size() * sizeof(KvSpan), cudaMemcpyHostToDevice, L.stream);
-        for (size_t i = 0; !e && i < spans.size(); i += 65535)
-            e = launch_kv_widen_q4(kv, dspans + i, (int)std::min<size_t>(65535, spans.size() - i), longest, k16, v16, n_pad, L);
+    TmaMap mq;
+    if (tc && !make_operand_map(&mq, (const f16 *)q, T, H * hd, 128)) {
+        set_global_error("llm_op_attn_prefill_q4_0: TMA descriptor creation failed");
+        return LLM_ERR_COMPUTE;
     }
-    if (!e && tc) {
-        TmaMap mq, mk, mv;
-        const int rows = n_seq * Hkv * n_pad;
-        if (!make_operand_map(&mq, (const f16 *)q, T, H * hd, 128) || !make_operand_map(&mk, k16, rows, hd, 128) ||
-            !make_operand_map(&mv, v16, rows, hd, 128)) {
-            set_global_error("llm_op_attn_prefill_q4_0: TMA descriptor creation failed");
-            return LLM_ERR_COMPUTE;
+    AttnPrefillArgs at;
+    at.q = (const f16 *)q;
+    at.kv = q4_view(k_cache, v_cache, Hkv, hd, n_ctx, n_seq);
+    at.tiles = nullptr; at.o = (f16 *)o; at.H = H; at.err = err; at.window = window;
+    // the runs go with the launch, as many as one takes at a time
+    for (size_t i = 0; i < runs.size();) {
+        KvRuns part;
+        int n = 0;
+        at.n_tiles = 0;
+        for (; n < KvRuns::MAX && i < runs.size(); ++n, ++i) {
+            part.run[n] = runs[i];
+            part.run[n].tile0 = at.n_tiles;
+            at.n_tiles += (runs[i].n_rows + rows_max - 1) / rows_max;
         }
-        AttnPrefillTcArgs at;
-        at.tiles = dtiles; at.n_tiles = (int)tiles.size(); at.H = H; at.Hkv = Hkv; at.head_dim = hd;
-        at.n_layer = 1; at.layer = 0; at.n_ctx = n_pad; at.n_seq = n_seq;
-        at.o = (f16 *)o; at.ldo = H * hd; at.err = err; at.window = window;
-        at.tiles_late = late;
-        e = launch_attn_prefill_tc(at, mq, mk, mv, Launch{L.stream, late, nullptr});
-    } else if (!e) {
-        AttnPrefillArgs at;
-        at.q = (const f16 *)q;
-        at.kv.k = k16; at.kv.v = v16;
-        at.kv.seq_stride = (long long)Hkv * n_pad * hd;
-        at.kv.n_ctx = n_pad; at.kv.n_seq = n_seq; at.kv.head_dim = hd; at.kv.n_kv_head = Hkv;
-        at.tiles = dtiles; at.n_tiles = (int)tiles.size(); at.o = (f16 *)o; at.H = H; at.err = err; at.window = window;
-        e = launch_attn_prefill(at, L);
+        if (cudaError_t e = launch_attn_prefill_q4(at, &part, n, tc ? &mq : nullptr, overlapped(stream))) return launched(who, e);
     }
-    return launched(who, e);
+    return LLM_OK;
 }
