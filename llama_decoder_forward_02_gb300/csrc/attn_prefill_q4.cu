@@ -100,36 +100,20 @@ __device__ __forceinline__ bool tile_bad(const AttnTile &tl, const KvView &kv, i
 __device__ __forceinline__ uint32_t beyond(uint32_t d) { return ((d & 0x7FFF7FFFu) + 0x10001000u) & 0x80008000u; }
 
 // The eight values of a word of codes with scale dd (in both halves) as hi and
-// lo fp16 numbers, exactly: c - 8 through the fp16 patterns of 1024 + c and
-// 64 + c, a rounded product, and the remainder by FMA.  Masks and biases are
-// held in registers that the compiler cannot see through: one logic instruction
-// takes one constant as an immediate.
-struct Widen {
-    uint32_t m0, e0, m1, e1;
-    __device__ __forceinline__ Widen() {
-        asm volatile("mov.b32 %0, 0x000F000F;\n\tmov.b32 %1, 0x64006400;\n\tmov.b32 %2, 0x00F000F0;\n\tmov.b32 %3, 0x54005400;"
-                     : "=r"(m0), "=r"(e0), "=r"(m1), "=r"(e1));
-    }
-    __device__ __forceinline__ static __half2 pick(uint32_t w, uint32_t m, uint32_t e, uint32_t bias) {
-        uint32_t v;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(m), "r"(e));       // (w & m) | e
-        return __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&bias));
-    }
-    __device__ __forceinline__ void split(uint32_t w, __half2 dd, uint4 &hi, uint4 &lo) const {
-        const uint32_t w8 = w >> 8;
-        const __half2 c[4] = {pick(w, m0, e0, 0x64086408u), pick(w, m1, e1, 0x54805480u), pick(w8, m0, e0, 0x64086408u),
-                              pick(w8, m1, e1, 0x54805480u)};
-        uint32_t h[4], l[4];
+// lo fp16 numbers, exactly: a rounded product, and its remainder by FMA.
+__device__ __forceinline__ void split_word(const q4::Widen &wd, uint32_t w, __half2 dd, uint4 &hi, uint4 &lo) {
+    const uint32_t w8 = w >> 8, c[4] = {wd.low(w), wd.high(w), wd.low(w8), wd.high(w8)};
+    uint32_t h[4], l[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 v = __hmul2_rn(c[i], dd), r = __hfma2(c[i], dd, __hneg2(v));
-            h[i] = *reinterpret_cast<const uint32_t *>(&v);
-            l[i] = *reinterpret_cast<const uint32_t *>(&r);
-        }
-        hi = make_uint4(h[0], h[1], h[2], h[3]);
-        lo = make_uint4(l[0], l[1], l[2], l[3]);
+    for (int i = 0; i < 4; ++i) {
+        const __half2 ci = *reinterpret_cast<const __half2 *>(&c[i]);
+        const __half2 v = __hmul2_rn(ci, dd), r = __hfma2(ci, dd, __hneg2(v));
+        h[i] = *reinterpret_cast<const uint32_t *>(&v);
+        l[i] = *reinterpret_cast<const uint32_t *>(&r);
     }
-};
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -237,7 +221,7 @@ struct Widener {
     uint32_t base, bar;
     volatile int *abort;
     uint32_t *err;
-    Widen wd;
+    q4::Widen wd;
 
     // first key row (of its 128-key tile) and 64-column half of the warp's share of unit `half` of a tile
     template <bool K>
@@ -298,8 +282,8 @@ struct Widener {
 #pragma unroll
         for (int i = 0; i < WT; ++i) {
             uint4 h0, l0, h1, l1;
-            wd.split(x.w[i].x, dup_lo(x.d[i]), h0, l0);
-            wd.split(x.w[i].y, dup_hi(x.d[i]), h1, l1);
+            split_word(wd, x.w[i].x, dup_lo(x.d[i]), h0, l0);
+            split_word(wd, x.w[i].y, dup_hi(x.d[i]), h1, l1);
             st_shared(c0 + 1024u * i, h0);
             st_shared(c0 + 1024u * i + QBOX, l0);
             st_shared(c1 + 1024u * i, h1);
@@ -653,7 +637,7 @@ __global__ void __launch_bounds__(M_THREADS) attn_prefill_q4_kernel(const AttnPr
             }
         }
     };
-    const Widen wd;
+    const q4::Widen wd;
     auto put = [&]() {
 #pragma unroll
         for (int i = 0; i < TASKS; ++i) {
@@ -665,11 +649,11 @@ __global__ void __launch_bounds__(M_THREADS) attn_prefill_q4_kernel(const AttnPr
             for (int b = 0; b < NB; ++b) {
                 uint4 hi, lw;
                 const int at = Swz<HD>::off(r, 4 * b + part);
-                wd.split(kw[i][b], dup_lo(kd[i][b]), hi, lw);
+                split_word(wd, kw[i][b], dup_lo(kd[i][b]), hi, lw);
                 if (nan && b == 0) hi.x = 0x7FFF7FFFu;
                 *reinterpret_cast<uint4 *>(Kh + at) = hi;
                 *reinterpret_cast<uint4 *>(Kl + at) = lw;
-                wd.split(vw[i][b], dup_lo(beyond(vd[i][b]) ? 0u : vd[i][b]), hi, lw);
+                split_word(wd, vw[i][b], dup_lo(beyond(vd[i][b]) ? 0u : vd[i][b]), hi, lw);
                 *reinterpret_cast<uint4 *>(Vh + at) = hi;
                 *reinterpret_cast<uint4 *>(Vl + at) = lw;
             }

@@ -7,8 +7,8 @@
 // Bound by HBM reads of K and V: 9/8 bytes a (key, element), which
 // leaves an SM about 100 clocks for 16 keys of 128 elements at the copy
 // bandwidth.  Widening every code on the CUDA cores costs more than that, so
-// the codes go to mma.sync as they are, the fp16 subnormals that masking a
-// word leaves (q4.cuh):
+// the codes go to mma.sync (q4.cuh): K's as the fp16 subnormals c * 2^-24 that
+// masking a word leaves, V's as c - 8.
 //   * S^T = K q^T with 16 keys as the M side.  A block of 32 dimensions is one
 //     fp32 sum of two mma (the second's q divided by 16 for the nibbles that
 //     stand four bits higher), less 8 sum(q) of the block, made once, for the
@@ -20,8 +20,12 @@
 //     again as two fp16 numbers; neighbouring keys' halves of a word are put
 //     together by one byte permute.  S^T comes out with keys along the lanes'
 //     rows and w is wanted with heads there: a register transpose of the warp
-//     (movmatrix) for each block.  The offset is taken off at the end,
-//     8 * sum(w).
+//     (movmatrix) for each block.  w is held times a power of two that brings
+//     the largest |d| a warp has met to 2^14 .. 2^15, so that both parts stay
+//     normal numbers down to 2^-28 of it whatever V's size.  (With V's codes as
+//     subnormals too and 8 sum(w) taken off at the end, w times 8: the parts'
+//     rounding came in as error * c instead of error * (c - 8), and w of V near
+//     1e-3 lost it altogether, 9.4e-4 of o's norm.)
 // So neither q, K, V nor the weights are rounded to fewer than 22 bits on the
 // way to the fp32 sums; only o is.
 //
@@ -32,7 +36,6 @@
 // passes it.  Splits over the keys leave (numerators, sum, max) and are merged
 // in split order, by the cluster they form or, over long caches, by the CTA that
 // arrives last: results do not depend on timing and nothing spins.
-//
 //
 // Measured, calls in a row, 32 query and 8 kv heads of 128, and the time the
 // bytes take at the copy bandwidth: one row of 2100 keys 4.7 us (0.4), of 32000
@@ -368,14 +371,17 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
         }
     constexpr float UNDO = 1048576.f;                 // 2^24 of the codes over the 16 of q
 
-    // sums of the lane's head(s) 4 n + t4: O^T tiles of 16 dimensions (two a block), weights, offsets
-    float o[NT][NB][2][4], m[NT], l[NT], sw[NT][NB];
+    // sums of the lane's head(s) 4 n + t4: O^T tiles of 16 dimensions (two a block), weights
+    float o[NT][NB][2][4], m[NT], l[NT];
+    // o is held sig times as large, a power of two that brings this warp's largest |d| of V to 2^14 or more; one of
+    // top or more lowers it
+    float sig = 0x1p39f, unsig = 0x1p-39f, top = 0x1p-24f;
+    const q4::Widen wd;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = -INFINITY; l[n] = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            sw[n][b] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][b][0][e] = o[n][b][1][e] = 0.f;
         }
@@ -420,7 +426,10 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
             }
         }
         // m and s in units of 2^-20 (the codes' 2^-24 and the 16 of q)
-        bool raise = false;
+        float dmax = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) dmax = fmaxf(dmax, fmaxf(fabsf(dv[0][b]), fabsf(dv[1][b])));
+        bool raise = dmax >= top;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             s[n][0] = in0 ? s[n][0] : -INFINITY;
@@ -428,6 +437,16 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
             raise |= fmaxf(s[n][0], s[n][1]) > m[n];
         }
         if (__any_sync(0xffffffffu, raise)) {
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(dmax));     // of floats from 0 on
+            float drop = 1.f;
+            if (most >= __float_as_uint(top)) {
+                // 2^(e - 127) .. 2^(e - 126): sig = 2^(141 - e) from then on
+                const uint32_t e = min(most >> 23, 253u);
+                top = __uint_as_float((e + 1) << 23);
+                sig = __uint_as_float((268 - e) << 23);
+                drop = sig * unsig;
+                unsig = __uint_as_float((e - 14) << 23);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float mx = fmaxf(s[n][0], s[n][1]);
@@ -437,22 +456,23 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
                 const float f = mx == -INFINITY ? 1.f : exp2f((m[n] - mx) * UNDO);
                 m[n] = mx;
                 l[n] *= f;
+                const float fo = f * drop;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    sw[n][b] *= f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { o[n][b][0][e] *= f; o[n][b][1][e] *= f; }
+                    for (int e = 0; e < 4; ++e) { o[n][b][0][e] *= fo; o[n][b][1][e] *= fo; }
                 }
             }
         }
-        // weights, 8 times as large: w <= 8 * 8188 (the largest scale) still is an fp16 number
         float p[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float base = m[n] == -INFINITY ? 0.f : fmaf(m[n], -UNDO, 3.f);
-            p[n][0] = exp2_fast(fmaf(s[n][0], UNDO, base));
-            p[n][1] = exp2_fast(fmaf(s[n][1], UNDO, base));
+            const float m0 = m[n] == -INFINITY ? 0.f : m[n];
+            p[n][0] = exp2_fast((s[n][0] - m0) * UNDO);
+            p[n][1] = exp2_fast((s[n][1] - m0) * UNDO);
             l[n] += p[n][0] + p[n][1];
+            p[n][0] *= sig;
+            p[n][1] *= sig;
         }
         uint32_t vw[4][NB];
 #pragma unroll
@@ -461,13 +481,14 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
         for (int b = 0; b < NB; ++b) {
             const uint32_t u = __byte_perm(vw[0][b], vw[1][b], sel), v = __byte_perm(vw[2][b], vw[3][b], sel);
             const uint32_t u8 = u >> 8, v8 = v >> 8;
+            const uint32_t ul = wd.low(u), uh = wd.high(u), ul8 = wd.low(u8), uh8 = wd.high(u8);
+            const uint32_t vl = wd.low(v), vh = wd.high(v), vl8 = wd.low(v8), vh8 = wd.high(v8);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float w0 = p[n][0] * dv[0][b], w1 = p[n][1] * dv[1][b];
-                sw[n][b] += w0 + w1;
                 const uint32_t b0 = transpose8x8(two_halves(w0)), b1 = transpose8x8(two_halves(w1));
-                mma_acc(o[n][b][0], u & 0x000F000Fu, u8 & 0x000F000Fu, v & 0x000F000Fu, v8 & 0x000F000Fu, b0, b1);
-                mma_acc(o[n][b][1], u & 0x00F000F0u, u8 & 0x00F000F0u, v & 0x00F000F0u, v8 & 0x00F000F0u, b0, b1);
+                mma_acc(o[n][b][0], ul, ul8, vl, vl8, b0, b1);
+                mma_acc(o[n][b][1], uh, uh8, vh, vh8, b0, b1);
             }
         }
         valid -= NW * KG;
@@ -495,17 +516,14 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);
         if (g == 0) ws[HD] = l[n] * f;
-        const float f1 = 16777216.f * f, f16 = 1048576.f * f, f8 = -8.f * f;
+        const float f1 = f * unsig;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) sw[n][b] += __shfl_xor_sync(0xffffffffu, sw[n][b], x);
             float *d = ws + 32 * b + 8 * (g >> 1) + (g & 1);
-            const float o8 = f8 * sw[n][b];
-            d[0] = fmaf(o[n][b][0][0] + o[n][b][0][1], f1, o8);
-            d[4] = fmaf(o[n][b][0][2] + o[n][b][0][3], f1, o8);
-            d[2] = fmaf(o[n][b][1][0] + o[n][b][1][1], f16, o8);
-            d[6] = fmaf(o[n][b][1][2] + o[n][b][1][3], f16, o8);
+            d[0] = (o[n][b][0][0] + o[n][b][0][1]) * f1;
+            d[4] = (o[n][b][0][2] + o[n][b][0][3]) * f1;
+            d[2] = (o[n][b][1][0] + o[n][b][1][1]) * f1;
+            d[6] = (o[n][b][1][2] + o[n][b][1][3]) * f1;
         }
     }
     __syncthreads();

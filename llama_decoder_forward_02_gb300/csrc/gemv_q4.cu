@@ -127,26 +127,6 @@ __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// c - 8 of the codes at bits 0 and 16 / at bits 4 and 20, as an fp16 pair.  One
-// LOP3 takes at most one constant as an immediate, so the masks and biases are
-// kept in registers the compiler cannot see through (with immediates it emits
-// two: 20% more instructions in all).
-struct Widen {
-    uint32_t m0, e0, m1, e1;
-    __device__ __forceinline__ Widen() {
-        asm volatile("mov.b32 %0, 0x000F000F;\n\tmov.b32 %1, 0x64006400;\n\tmov.b32 %2, 0x00F000F0;\n\tmov.b32 %3, 0x54005400;"
-                     : "=r"(m0), "=r"(e0), "=r"(m1), "=r"(e1));
-    }
-    __device__ __forceinline__ static uint32_t pick(uint32_t w, uint32_t m, uint32_t e, uint32_t bias) {
-        uint32_t v;
-        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(m), "r"(e));       // (w & m) | e
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&bias));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-    __device__ __forceinline__ uint32_t low(uint32_t w) const { return pick(w, m0, e0, 0x64086408u); }
-    __device__ __forceinline__ uint32_t high(uint32_t w) const { return pick(w, m1, e1, 0x54805480u); }
-};
-
 constexpr int row_unit(int epi) { return epi == EPI_SWIGLU ? 2 * GU_GROUP : epi == EPI_QKV ? q4::BLOCK : 1; }
 
 // XS: x in shared memory; ONE: one row of x, so the
@@ -295,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemv_q4_kernel(const GemvQ4Args a,
     };
     if (!XS && my_kc * ntiles > 0) load_x(0);
 
-    const Widen wd;
+    const q4::Widen wd;
     float ssq[EPI == EPI_RESID ? 8 : 1];             // RESID: this warp's sums of h^2, by its rows of x in turn
 #pragma unroll
     for (float &v : ssq) v = 0.f;
