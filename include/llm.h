@@ -586,11 +586,12 @@ int32_t llm_op_kv_rows_q4_0(const void *cache, const int32_t *pos, const int32_t
  * any shape it is large enough for, and calls that may overlap need one each.
  * q, the caches, o and scratch 16-byte aligned.  A row whose pos lies outside
  * [0, n_ctx) or whose seq lies outside [0, n_seq) gives zeros and ORs 2 into
- * *err (DEVICE word or NULL).  q, K, V and the weights enter the products with
- * 22 bits, elements of q beyond +-65504 * sqrt(hd) / (16 log2(e)) (32,000 at
- * head_dim 128) as that value.  The keys are split over the GPU by the rows'
- * number and lengths: the same call gives the same bits, while a row's last
- * bits may depend on the rows beside it. */
+ * *err (DEVICE word or NULL).  q enters the products with 22 bits (2^-39 of
+ * its head's largest element where that is more), K and V exactly, the weights
+ * with 22 bits, sums are fp32; a head with an element of q of 2^117 or more gives
+ * NaN.  The keys are split over the GPU by the rows' number and lengths: the same
+ * call gives the same bits, while a row's last bits may depend on the rows beside
+ * it. */
 int64_t llm_op_attn_decode_q4_0_scratch_bytes(int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
                                               int32_t n_seq);
 int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void *v_cache, const int32_t *pos,

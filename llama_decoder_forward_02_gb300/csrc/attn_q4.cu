@@ -14,8 +14,9 @@
 //     stand four bits higher), less 8 sum(q) of the block, made once, for the
 //     offset, and scaled by the key's d in fp32.
 //   * The N side has 8 columns and a kv head rarely 8 query heads, so each
-//     head takes two: q as the sum of two fp16 numbers (22 bits), and so its
-//     weights.  Four heads fill a column tile, larger groups take NT = 2.
+//     head takes two: q, times a power of two that brings its head's largest
+//     element to 2^14 .. 2^15, as the sum of two fp16 numbers (22 bits), and so
+//     its weights.  Four heads fill a column tile, larger groups take NT = 2.
 //   * O^T += V^T w with 16 dimensions as the M side and w = p * d[key][block],
 //     again as two fp16 numbers; neighbouring keys' halves of a word are put
 //     together by one byte permute.  S^T comes out with keys along the lanes'
@@ -313,12 +314,12 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     };
     // ---- q as the N side: column g of tile n is half g % 2 of head 4 n + g / 2.
     // The fragments are the same for every warp: each makes some blocks' and
-    // leaves them in shared memory.  q * log2(e) / sqrt(hd), times 16 for the
-    // nibbles at bits 0 and 8 and as it is for those four bits higher; values
-    // beyond fp16's range count as its end.
+    // leaves them in shared memory.  q times the power of two that brings its
+    // head's largest element to 2^14 .. 2^15, as it is for the nibbles at bits 0
+    // and 8 and divided by 16 for those four bits higher.
     uint4 *qf = reinterpret_cast<uint4 *>(smem_raw + R::BYTES);            // [NT * NB][32]
-    float *q8 = reinterpret_cast<float *>(qf + NT * NB * 32);              // [NT * NB][4]: 8 sum(q) * 2^-20 of the columns' head
-    const float scale = 16.f * 1.4426950408889634f / sqrtf((float)HD);
+    float *q8 = reinterpret_cast<float *>(qf + NT * NB * 32);              // [NT * NB][4]: 8 sum(q) * 2^-24 of the columns' head
+    __shared__ float s_qmax[NT * NB][4];                                   // a block's largest |q| by head
     static_assert(NT * NB <= NW, "a warp makes one block's fragments");
     int asked = 0;                                    // groups requested
     if (a.early) {                                    // cells that no row of this launch's batch was appended to
@@ -340,14 +341,30 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     for (int i = 0; i < NST - 1; ++i)
         if (i >= asked) request();
     if constexpr (CL) cluster_arrive_relaxed();       // started: the others may write to this CTA once they have waited
+    const float qv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    if (warp < NT * NB) {
+        float most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(qv[e]));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        if (t4 == 0 && !(g & 1)) s_qmax[warp][g >> 1] = most;
+    }
+    __syncthreads();
+    // exponent of the largest element of a head: 2^(e - 127) .. 2^(e - 126)
+    auto q_exp = [&](int n, int h) {
+        float most = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) most = fmaxf(most, s_qmax[n * NB + b][h]);
+        return (int)min(max(__float_as_uint(most) >> 23, 14u), 243u);
+    };
     if (warp < NT * NB) {
         const int u = warp;
-        const float v[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        const float up = __uint_as_float((uint32_t)(268 - q_exp(warp / NB, g >> 1)) << 23);      // 2^(141 - e)
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float x = v[e] * scale;
-            x = x > 65504.f ? 65504.f : x < -65504.f ? -65504.f : x;          // a NaN stays one
+            const float x = qv[e] * up;
             const uint32_t two = two_halves((e & 2) ? x * 0.0625f : x);   // elements 2, 3, 6, 7: nibbles four bits up
             h[e] = g & 1 ? two >> 16 : two & 0xFFFFu;
         }
@@ -369,7 +386,11 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
             qb[n][b][0] = f.x; qb[n][b][1] = f.y; qb[n][b][2] = f.z; qb[n][b][3] = f.w;
             off[n][b] = q8[(n * NB + b) * 4 + t4];
         }
-    constexpr float UNDO = 1048576.f;                 // 2^24 of the codes over the 16 of q
+    // from the sums to scores in base 2: the 2^24 of the codes, q's power of two, log2(e) / sqrt(hd)
+    float undo[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        undo[n] = __uint_as_float((uint32_t)(q_exp(n, t4) + 10) << 23) * (1.4426950408889634f / sqrtf((float)HD));
 
     // sums of the lane's head(s) 4 n + t4: O^T tiles of 16 dimensions (two a block), weights
     float o[NT][NB][2][4], m[NT], l[NT];
@@ -425,7 +446,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
                 s[n][1] = fmaf(dk[1][b], (c[2] + c[3]) + off[n][b], s[n][1]);
             }
         }
-        // m and s in units of 2^-20 (the codes' 2^-24 and the 16 of q)
+        // m and s in units of 1 / undo
         float dmax = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) dmax = fmaxf(dmax, fmaxf(fabsf(dv[0][b]), fabsf(dv[1][b])));
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
                 mx = fmaxf(mx, m[n]);
-                const float f = mx == -INFINITY ? 1.f : exp2f((m[n] - mx) * UNDO);
+                const float f = mx == -INFINITY ? 1.f : exp2f((m[n] - mx) * undo[n]);
                 m[n] = mx;
                 l[n] *= f;
                 const float fo = f * drop;
@@ -468,8 +489,8 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float m0 = m[n] == -INFINITY ? 0.f : m[n];
-            p[n][0] = exp2_fast((s[n][0] - m0) * UNDO);
-            p[n][1] = exp2_fast((s[n][1] - m0) * UNDO);
+            p[n][0] = exp2_fast((s[n][0] - m0) * undo[n]);
+            p[n][1] = exp2_fast((s[n][1] - m0) * undo[n]);
             l[n] += p[n][0] + p[n][1];
             p[n][0] *= sig;
             p[n][1] *= sig;
@@ -503,7 +524,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
     __shared__ float s_max[NW][GC];
     if (g == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s_max[warp][4 * n + t4] = m[n] * UNDO;
+        for (int n = 0; n < NT; ++n) s_max[warp][4 * n + t4] = m[n] * undo[n];
     }
     __syncthreads();
 #pragma unroll
@@ -511,7 +532,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 && NW == 8 ? 2 : 1) attn_deco
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, s_max[w][4 * n + t4]);
-        const float f = m[n] == -INFINITY ? 0.f : exp2_fast(m[n] * UNDO - M);
+        const float f = m[n] == -INFINITY ? 0.f : exp2_fast(m[n] * undo[n] - M);
         float *ws = wst + ((size_t)warp * GC + 4 * n + t4) * REC;
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], x);

@@ -3,7 +3,8 @@ whatever the sizes of q, K and V.
 
 Tolerances.  A score sums a block's codes and its offset 8 sum(q) in six steps of
 2^-23 of magnitudes up to (15 + 8) sum |q|, times d, and the blocks in as many
-steps; q enters with 22 bits, each of two parts half a step off.  A weight takes
+steps; q enters with 22 bits, or two parts of half a subnormal step each, 2^-39 of
+its head's largest element.  A weight takes
 2^-21 (two parts and the exponential) and the rounding of its exponent, 2^-22 of
 the largest score in base 2, twice.  Its products with V's scale are held to 2^-38
 of the largest scale, times |c - 8| <= 8 and the number of cells.  O sums 16 keys
@@ -57,6 +58,9 @@ class Decode:
             mag = max(mag, 23 * np.einsum("jgb,jcb->jgc", qb, kdz[seq[t]]).max() / np.sqrt(hd))
             qk = max(qk, np.einsum("jgd,jcd->jgc", np.abs(q[t]).reshape(Hkv, G, hd), kz[seq[t]]).max() / np.sqrt(hd))
         top = qk * 1.4426950408889634
+        low = 2.0 ** -38 * np.abs(q).max(-1, keepdims=True) * np.ones(hd)
+        for t in range(T):
+            qk = max(qk, 2.0 ** 21 * np.einsum("jgd,jcd->jgc", low[t].reshape(Hkv, G, hd), kz[seq[t]]).max() / np.sqrt(hd))
         w = (6 + hd // 32) * U32 * mag + 2.0 ** -21 * qk + 2.0 ** -21 + 2.0 ** -21 * top + (n_ctx / 128 + 160) * U32
         mean = reference(q, k, vz, pos, seq, Hkv, window)
         seen = np.minimum(np.array(pos) + 1, window) if window else np.array(pos) + 1
@@ -99,3 +103,59 @@ def test_cells_of_unlike_sizes(lib, hd, H, Hkv):
     """V's scales grow and shrink along the cache, a factor of 1e4 apart."""
     Decode(lib, hd, H, Hkv, mixed=True, **LONG).check()
     Decode(lib, hd, H, Hkv, mixed=True, dominant=True, window=900, **SHORT).check()
+
+
+@pytest.mark.parametrize("hd,H,Hkv", [(128, 8, 2), (64, 12, 1), (32, 4, 2)])
+@pytest.mark.parametrize("qs,ks", [(1e5, 1e-5), (4e4, 4e-5), (1e-6, 2000.0), (1e-30, 1.0), (1e30, 0.0)])
+def test_sizes_of_q(lib, hd, H, Hkv, qs, ks):
+    """Queries far beyond fp16's range, and far below it, over keys that make their scores ordinary ones."""
+    for where in (LONG, SHORT):
+        Decode(lib, hd, H, Hkv, qs=qs, ks=ks, **where).check()
+
+
+def test_heads_of_unlike_queries(lib):
+    """Each head's queries are held by their own largest: a head of zeros, tiny ones, huge ones, and one whose largest
+    element meets keys of zero."""
+    hd, H, Hkv = 64, 8, 2
+    c = Decode(lib, hd, H, Hkv, qs=0.0, **SHORT)
+    rng = np.random.default_rng(5)
+    n_seq, n_ctx = 2, SHORT["n_ctx"]
+    (kc, kd), (vc, vd) = (make_cache(rng, n_seq, Hkv, n_ctx, hd, np.ones((n_seq, n_ctx), bool)) for _ in range(2))
+    kc[..., 7] = 8                                              # keys' element 7: 0
+    kd = (kd * 1e-2).astype(np.float16)
+    q = rng.standard_normal((2, H, hd)) * np.array([0.0, 1e-20, 1e2, 3e3, 1.0, 1e2, 1e-3, 1e2])[None, :, None]
+    q[:, 5, 7] = 1e6
+    q = q.astype(np.float32)
+    k, v = O.dequantize_q4_0(kc, kd), O.dequantize_q4_0(vc, vd)
+    q64 = q.astype(np.float64)
+    ref = reference(q64, k, v, SHORT["pos"], SHORT["seq"], Hkv, 0)
+    qb = np.abs(q64).reshape(2, Hkv, 4, 2, 32).sum(-1)
+    # by head: the bound of the head of this file
+    mag = 23 * np.stack([np.einsum("jgb,jcb->jgc", qb[t], np.abs(kd[t].astype(np.float64))).max(-1).reshape(-1) for t in range(2)]) / 8
+    qk = np.stack([np.einsum("jgd,jcd->jgc", (np.abs(q64[t]) + 2.0 ** -17 * np.abs(q64[t]).max(-1, keepdims=True)).reshape(
+        Hkv, 4, hd), np.abs(k[t])).max(-1).reshape(-1) for t in range(2)]) / 8
+    w = 8 * U32 * mag + 2.0 ** -20 * qk * 1.5 + 2.0 ** -21 + (n_ctx / 128 + 160) * U32
+    off = 2 * w[..., None] * reference(q64, k, np.abs(v), SHORT["pos"], SHORT["seq"], Hkv, 0)
+    off = off + 2.0 ** -35 * np.abs(vd.astype(np.float64)).max() * (np.array(SHORT["pos"]) + 1)[:, None, None]
+    c.ref, c.tol = ref, half_step(np.abs(ref) + off) + off
+    c.qd, c.kc, c.vc = dev(q.reshape(2, -1)), dev(pack_cache(kc, kd)), dev(pack_cache(vc, vd))
+    c.check()
+
+
+@pytest.mark.parametrize("odd", [2.0 ** 118, np.inf, np.nan])
+def test_queries_out_of_range_stay_in_their_head(lib, odd):
+    c = Decode(lib, 128, 8, 2, **SHORT)
+    q = c.qd.cpu().numpy()
+    q[0, 3 * 128 + 40] = odd
+    c.qd.copy_(torch.from_numpy(q))
+    want = c.ref.copy()
+    c.ref[0, 3] = 0.0
+    c.tol[0, 3] = np.inf
+    T, H, Hkv, hd, n_ctx, n_seq = c.shape
+    assert lib.llm_op_attn_decode_q4_0(c.qd.data_ptr(), c.kc.data_ptr(), c.vc.data_ptr(), c.posd.data_ptr(), c.seqd.data_ptr(),
+                                       c.o.data_ptr(), T, H, Hkv, hd, n_ctx, n_seq, 0, c.scratch.data_ptr(), c.scratch.numel(),
+                                       c.err.data_ptr(), stream()) == 0
+    got = c.o.cpu().double().numpy().reshape(want.shape)
+    assert np.all(np.isnan(got[0, 3]))
+    got[0, 3] = 0.0
+    assert np.all(np.abs(got - c.ref) <= c.tol)
