@@ -141,6 +141,17 @@ int32_t llm_model_set_qk_norm(llm_model *m, const void *const *q_norm, const voi
  * context keeps a reference to `m`, which must outlive it. */
 int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, int32_t n_ubatch,
                      void *stream, llm_ctx **out);
+
+/* llm_kv_alloc with a cache of another element type from the start (the options
+ * "kv_fp8" and "kv_q4" change it later, and need room for the fp16 cache first):
+ * LLM_KV_F16 as llm_kv_alloc, LLM_KV_E4M3 half its bytes, LLM_KV_Q4_0 9/32 of
+ * them (the layouts stand with those options and the 4-bit operators).
+ * LLM_ERR_INVALID for another kv_type; else as llm_kv_alloc. */
+#define LLM_KV_F16 0
+#define LLM_KV_E4M3 1
+#define LLM_KV_Q4_0 2
+int32_t llm_kv_alloc_typed(llm_model *m, int32_t n_ctx, int32_t n_seq_max, int32_t n_ubatch, int32_t kv_type,
+                           void *stream, llm_ctx **out);
 void llm_kv_free(llm_ctx *c);
 
 /* The batch of one llm_decode call ("llama_batch", one sequence id per
@@ -285,7 +296,8 @@ const char *llm_last_error(const llm_ctx *c);
 int32_t llm_debug_hidden(llm_ctx *c, float *dst, int32_t max_rows, int32_t max_ubatches);
 
 /* Tests of the failure paths.  llm_debug_fail_alloc(n): in the next
- * llm_kv_alloc call (only), its device allocation number n (0-based, in the
+ * llm_kv_alloc or llm_kv_alloc_typed call, or the next change of option
+ * "kv_q4" (that call only), its device allocation number n (0-based, in the
  * order the call makes them) fails as if the device were out of memory, so
  * the call returns LLM_ERR_ALLOC after releasing what it had allocated; -1
  * disarms.  Process-wide; returns LLM_ERR_INVALID for n < -1. */
@@ -346,7 +358,9 @@ int32_t llm_debug_fail_alloc(int32_t n);
  *   "kv_q4"        1 = the KV cache holds Q4_0 blocks (the 4-bit operators below
  *                  have the layout; 9/32 of the fp16 cache's bytes), 0 = fp16
  *                  (default); allowed only while every sequence is empty, and not
- *                  together with kv_fp8; a failed call changes nothing;
+ *                  together with kv_fp8; both caches stand during the change, and
+ *                  a failed call changes nothing (llm_kv_alloc_typed makes the
+ *                  Q4_0 cache alone);
  *   "gemv_q4"      1 = steps of 1..8 rows of a Q4_0 model read its Q4_0 rows
  *                  (default); 0 = its fp16 copies;
  *   "swa_window"   sliding-window attention ("KV Cache" of the pages): a query at
@@ -562,9 +576,6 @@ int64_t llm_op_kv_q4_0_bytes(int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_s
  * LLM_ERR_INVALID before anything is enqueued (reason in llm_last_error(NULL)). */
 #define LLM_Q_F32 0
 #define LLM_Q_F16 1
-#define LLM_KV_F16 0
-#define LLM_KV_E4M3 1
-#define LLM_KV_Q4_0 2
 int32_t llm_op_qk_norm_rope(const float *qkv, int32_t ld, const float *q_gain, const float *k_gain, float eps,
                             const float *rope, const int32_t *pos, const int32_t *seq, void *q, int32_t q_type,
                             void *k_cache, void *v_cache, int32_t kv_type, int32_t T, int32_t H, int32_t Hkv,

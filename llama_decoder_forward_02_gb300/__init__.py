@@ -68,6 +68,7 @@ llm_model_free = _proto("llm_model_free", None, c_vp)
 llm_model_quantize = _proto("llm_model_quantize", c_i32, c_vp, c_i32, c_vp)
 llm_model_set_qk_norm = _proto("llm_model_set_qk_norm", c_i32, c_vp, ctypes.POINTER(c_vp), ctypes.POINTER(c_vp), c_vp)
 llm_kv_alloc = _proto("llm_kv_alloc", c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, ctypes.POINTER(c_vp))
+llm_kv_alloc_typed = _proto("llm_kv_alloc_typed", c_i32, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, ctypes.POINTER(c_vp))
 llm_kv_free = _proto("llm_kv_free", None, c_vp)
 llm_decode = _proto("llm_decode", c_i32, c_vp, ctypes.POINTER(llm_batch))
 llm_get_logits = _proto("llm_get_logits", c_vp, c_vp, c_i32p)
@@ -243,10 +244,11 @@ class Model:
 class Context:
     """Owns an llm_ctx handle; methods marshal to the C calls of the same name."""
 
-    def __init__(self, model: Model, n_ctx: int, n_seq_max: int = 1, n_ubatch: int = 512, stream=0):
+    def __init__(self, model: Model, n_ctx: int, n_seq_max: int = 1, n_ubatch: int = 512, stream=0,
+                 kv_type: int = LLM_KV_F16):
         self.model = model
         h = c_vp()
-        check(llm_kv_alloc(model.handle, n_ctx, n_seq_max, n_ubatch, c_vp(stream), ctypes.byref(h)))
+        check(llm_kv_alloc_typed(model.handle, n_ctx, n_seq_max, n_ubatch, kv_type, c_vp(stream), ctypes.byref(h)))
         self.handle = h
 
     def decode(self, tokens=None, pos=None, seq_id=None, output=None, token_dev_ptr=None, n_tokens=None):

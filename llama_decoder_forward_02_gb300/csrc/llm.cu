@@ -538,8 +538,21 @@ static int attn_pick_split(const llm_model *m, int T, int n_ctx) {
     return s < 1 ? 1 : s;
 }
 
+// Bytes of each of kc and vc holding elements of type LLM_KV_*.
+static size_t cache_bytes(size_t elems, int type) {
+    return type == LLM_KV_F16 ? elems * sizeof(f16) : type == LLM_KV_E4M3 ? elems : elems / 2 + elems / 16;
+}
+
+// Bytes of the Q4_0 decode attention's scratch for steps of up to 8 rows.
+static size_t q4_scratch_bytes(const llm_model *m, int n_ctx) {
+    size_t n = 0;
+    for (int T = 1; T <= 8; ++T) n = std::max(n, attn_q4_scratch_bytes(T, m->H, m->Hkv, m->hd, n_ctx));
+    return n;
+}
+
 // Allocation-failure injection for tests (llm_debug_fail_alloc): the device
-// allocation of that index in the next llm_kv_alloc fails; -1 = none.
+// allocation of that index in the next llm_kv_alloc, or the next change of the
+// cache's type, fails; -1 = none.
 static int g_fail_alloc = -1;
 
 extern "C" int32_t llm_debug_fail_alloc(int32_t n) {
@@ -550,6 +563,11 @@ extern "C" int32_t llm_debug_fail_alloc(int32_t n) {
 
 extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, int32_t n_ubatch, void *stream,
                                 llm_ctx **out) {
+    return llm_kv_alloc_typed(m, n_ctx, n_seq_max, n_ubatch, LLM_KV_F16, stream, out);
+}
+
+extern "C" int32_t llm_kv_alloc_typed(llm_model *m, int32_t n_ctx, int32_t n_seq_max, int32_t n_ubatch, int32_t kv_type,
+                                      void *stream, llm_ctx **out) {
     llm_ctx *nc = nullptr;
     const int inject = g_fail_alloc;      // armed for this call only
     g_fail_alloc = -1;
@@ -557,6 +575,8 @@ extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, 
     *out = nullptr;
     if (!m || n_ctx < 1 || n_seq_max < 1 || n_ubatch < 1 || n_ubatch > 4096)
         return fail(nc, LLM_ERR_INVALID, "invalid context arguments");
+    if (kv_type != LLM_KV_F16 && kv_type != LLM_KV_E4M3 && kv_type != LLM_KV_Q4_0)
+        return fail(nc, LLM_ERR_INVALID, "unknown cache type");
     llm_ctx *c = new llm_ctx();
     c->m = m;
     m->n_contexts++;
@@ -585,8 +605,12 @@ extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, 
     };
     const size_t kv_elems = (size_t)n_seq_max * m->L * m->Hkv * n_ctx * hd;
     c->kv_elems = kv_elems;
-    dmal((void **)&c->kc, kv_elems * sizeof(f16));
-    dmal((void **)&c->vc, kv_elems * sizeof(f16));
+    c->kv_fp8 = kv_type == LLM_KV_E4M3;
+    c->kv_q4 = kv_type == LLM_KV_Q4_0;
+    const size_t kv_bytes = cache_bytes(kv_elems, kv_type), q4_scratch = c->kv_q4 ? q4_scratch_bytes(m, n_ctx) : 0;
+    dmal((void **)&c->kc, kv_bytes);
+    dmal((void **)&c->vc, kv_bytes);
+    if (c->kv_q4) dmal(&c->q4_scratch, q4_scratch);
     dmal((void **)&c->rope, (size_t)n_ctx * (hd / 2) * sizeof(float2));
     dmal((void **)&c->rope_t, (size_t)n_ctx * (hd / 2) * sizeof(float2));
     dmal((void **)&c->h, (size_t)nub * d * sizeof(float));
@@ -629,9 +653,10 @@ extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, 
     c->attn_part_floats = ap;
     dmal((void **)&c->attn_part, ap * sizeof(float));
     dmal((void **)&c->attn_cnt, (size_t)8 * m->Hkv * sizeof(unsigned));
-    // Q4_0 steps and models with normed queries and keys store the QKV projection plainly
     c->q4_ok = m->qbuf && m->wtype == LLM_WTYPE_Q4_0;
-    if (m->nbuf) dmal((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float));
+    // where a kernel of its own norms, rotates and appends: normed queries and keys, and a Q4_0 cache unless the GEMV
+    // over Q4_0 rows encodes
+    if (m->nbuf || c->kv_q4) dmal((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float));
     if (c->q4_ok) dmal((void **)&c->ss_q4, (size_t)8 * m->num_sms * sizeof(float));
     dmal((void **)&c->dec_dev, DEC_INTS * sizeof(int));
     dmal((void **)&c->err_dev, sizeof(uint32_t));
@@ -679,8 +704,9 @@ extern "C" int32_t llm_kv_alloc(llm_model *m, int32_t n_ctx, int32_t n_seq_max, 
                    gemv_stream_ok(EPI_SWIGLU, 2 * m->F_pad, d, m->num_sms) &&
                    gemv_stream_ok(EPI_RESID, d, m->F_pad, m->num_sms) && gemv_stream_ok(EPI_STORE, m->V, d, m->num_sms);
     c->stream_q8 = q8_plans_ok(c);
-    if (!e) e = cudaMemsetAsync(c->kc, 0, kv_elems * sizeof(f16), c->stream);
-    if (!e) e = cudaMemsetAsync(c->vc, 0, kv_elems * sizeof(f16), c->stream);
+    if (!e) e = cudaMemsetAsync(c->kc, 0, kv_bytes, c->stream);
+    if (!e) e = cudaMemsetAsync(c->vc, 0, kv_bytes, c->stream);
+    if (!e && q4_scratch) e = cudaMemsetAsync(c->q4_scratch, 0, q4_scratch, c->stream);
     if (!e) e = cudaStreamSynchronize(c->stream);
     if (e) {
         ctx_release(c);
@@ -1533,18 +1559,18 @@ extern "C" int32_t llm_debug_hidden(llm_ctx *c, float *dst, int32_t max_rows, in
 }
 
 // Swap the (empty) cache for one of the other element type.  Everything the new
-// one needs is allocated first: a failure changes nothing.
+// one needs is allocated while the old one stands: a failure changes nothing.
 static int32_t set_kv_q4(llm_ctx *c, bool want) {
     const llm_model *m = c->m;
-    const size_t bytes = want ? c->kv_elems / 2 + c->kv_elems / 16 : c->kv_elems * sizeof(f16);
+    const int inject = g_fail_alloc;      // armed for this call only
+    g_fail_alloc = -1;
+    const size_t bytes = cache_bytes(c->kv_elems, want ? LLM_KV_Q4_0 : LLM_KV_F16);
     const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
-    size_t scratch = 0;
-    for (int T = 1; T <= 8; ++T) scratch = std::max(scratch, attn_q4_scratch_bytes(T, m->H, m->Hkv, m->hd, c->n_ctx));
     void *p[4] = {nullptr};
-    const size_t need[4] = {bytes, bytes, scratch, c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
+    const size_t need[4] = {bytes, bytes, q4_scratch_bytes(m, c->n_ctx), c->qkv ? 0 : (size_t)nub * m->n_qkv * sizeof(float)};
     const int n = want ? 4 : 2;
     bool ok = true;
-    for (int i = 0; i < n && ok; ++i) ok = !need[i] || cudaMalloc(&p[i], need[i]) == cudaSuccess;
+    for (int i = 0; i < n && ok; ++i) ok = !need[i] || (i != inject && cudaMalloc(&p[i], need[i]) == cudaSuccess);
     if (ok) {
         cudaStreamSynchronize(c->stream);
         ok = cudaMemsetAsync(p[0], 0, bytes, c->stream) == cudaSuccess && cudaMemsetAsync(p[1], 0, bytes, c->stream) == cudaSuccess &&

@@ -146,7 +146,7 @@ def test_heads_of_unlike_queries(lib):
 def test_queries_out_of_range_stay_in_their_head(lib, odd):
     c = Decode(lib, 128, 8, 2, **SHORT)
     q = c.qd.cpu().numpy()
-    q[0, 3 * 128 + 40] = odd
+    q[0, 3, 40] = odd
     c.qd.copy_(torch.from_numpy(q))
     want = c.ref.copy()
     c.ref[0, 3] = 0.0

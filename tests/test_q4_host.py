@@ -182,3 +182,11 @@ def test_prefill_of_many_sequences_needs_no_table():
     assert lib.llm_op_attn_prefill_q4_0(P, P, P, ph, sh, P, 3, 1, 1, 32, 64, (1 << 31) - 1, 0, P, 1 << 60, None,
                                         None) == BAD
     assert b"consecutive" in lib.llm_last_error(None)
+
+
+def test_cache_type_refused():
+    out = ctypes.c_void_p(123)
+    assert lib.llm_kv_alloc_typed(None, 64, 1, 16, lib.LLM_KV_Q4_0, None, ctypes.byref(out)) == BAD and out.value is None
+    for kv in (-1, 3):
+        assert lib.llm_kv_alloc_typed(P, 64, 1, 16, kv, None, ctypes.byref(out)) == BAD and b"cache type" in why()
+    assert lib.llm_kv_alloc_typed(P, 64, 1, 16, lib.LLM_KV_Q4_0, None, None) == BAD
