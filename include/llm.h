@@ -297,7 +297,7 @@ int32_t llm_debug_hidden(llm_ctx *c, float *dst, int32_t max_rows, int32_t max_u
 
 /* Tests of the failure paths.  llm_debug_fail_alloc(n): in the next
  * llm_kv_alloc or llm_kv_alloc_typed call, or the next change of option
- * "kv_q4" (that call only), its device allocation number n (0-based, in the
+ * "kv_q4" or "kv_fp8" (that call only), its device allocation number n (0-based, in the
  * order the call makes them) fails as if the device were out of memory, so
  * the call returns LLM_ERR_ALLOC after releasing what it had allocated; -1
  * disarms.  Process-wide; returns LLM_ERR_INVALID for n < -1. */
@@ -354,7 +354,9 @@ int32_t llm_debug_fail_alloc(int32_t n);
  *   "kv_fp8"       1 = the KV cache holds FP8 E4M3 elements (nearest, saturating
  *                  at +-448, no scale; half the bytes of the fp16 cache), 0 =
  *                  fp16 (default); allowed only while every sequence is empty
- *                  (the cache is reallocated);
+ *                  (the cache is freed and allocated anew; where that fails with
+ *                  LLM_ERR_ALLOC, calls that use the cache do too until the option
+ *                  succeeds);
  *   "kv_q4"        1 = the KV cache holds Q4_0 blocks (the 4-bit operators below
  *                  have the layout; 9/32 of the fp16 cache's bytes), 0 = fp16
  *                  (default); allowed only while every sequence is empty, and not

@@ -231,6 +231,9 @@ static int32_t fail(llm_ctx *c, int32_t code, const char *what, cudaError_t e = 
     return code;
 }
 
+// what a failed change of option "kv_fp8" leaves, until one succeeds
+static const char *const NO_CACHE = "the context has no KV cache (a change of kv_fp8 failed)";
+
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ============================================================== model
@@ -1250,6 +1253,7 @@ int build_tiles(const std::vector<int32_t> &seq, const std::vector<int32_t> &pos
 
 extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
     if (!c || !b) return fail(c, LLM_ERR_INVALID, "ctx or batch is NULL");
+    if (!c->kc) return fail(c, LLM_ERR_ALLOC, NO_CACHE);
     const llm_model *m = c->m;
     BatchPlan p;
     const int rc = plan_batch(*b, m->V, c->n_ctx, c->n_seq_max, c->n_ubatch, c->seq_next, p);
@@ -1429,6 +1433,7 @@ extern "C" int32_t llm_sample(llm_ctx *c, const llm_sampling *s, const float *u,
 extern "C" int32_t llm_generate(llm_ctx *c, int32_t seq_id, int32_t n_steps, int32_t *tokens_out) {
     if (!c || !tokens_out || n_steps < 1) return fail(c, LLM_ERR_INVALID, "invalid generate arguments");
     if (seq_id < 0 || seq_id >= c->n_seq_max) return fail(c, LLM_ERR_INVALID, "invalid seq_id");
+    if (!c->kc) return fail(c, LLM_ERR_ALLOC, NO_CACHE);
     if (c->n_outputs < 1) return fail(c, LLM_ERR_INVALID, "no logits to start from");
     if (c->seq_next[seq_id] + n_steps > c->n_ctx) { c->last_error = "sequence would pass n_ctx"; return LLM_NO_KV_ROOM; }
     if (c->gemv_max_rows < 1) return fail(c, LLM_ERR_INVALID, "decode kernels disabled");
@@ -1632,16 +1637,21 @@ extern "C" int32_t llm_set_option(llm_ctx *c, const char *key, int32_t value) {
         for (int s = 0; s < c->n_seq_max; ++s)
             if (c->seq_next[s] != 0) return fail(c, LLM_ERR_INVALID, "kv_fp8 needs an empty cache (llm_seq_clear)");
         const bool want = value != 0;
-        if (want == c->kv_fp8) return LLM_OK;
+        if (want == c->kv_fp8 && c->kc) return LLM_OK;
         if (c->kv_q4) return fail(c, LLM_ERR_INVALID, "the cache is Q4_0 (kv_q4)");
-        const size_t bytes = c->kv_elems * (want ? 1 : sizeof(f16));
+        const int inject = g_fail_alloc;      // armed for this call only
+        g_fail_alloc = -1;
+        const size_t bytes = cache_bytes(c->kv_elems, want ? LLM_KV_E4M3 : LLM_KV_F16);
         cudaStreamSynchronize(c->stream);
         cudaFree(c->kc); cudaFree(c->vc);
         c->kc = c->vc = nullptr;
-        if (cudaMalloc((void **)&c->kc, bytes) != cudaSuccess || cudaMalloc((void **)&c->vc, bytes) != cudaSuccess ||
-            cudaMemsetAsync(c->kc, 0, bytes, c->stream) != cudaSuccess ||
+        if (inject == 0 || cudaMalloc((void **)&c->kc, bytes) != cudaSuccess || inject == 1 ||
+            cudaMalloc((void **)&c->vc, bytes) != cudaSuccess || cudaMemsetAsync(c->kc, 0, bytes, c->stream) != cudaSuccess ||
             cudaMemsetAsync(c->vc, 0, bytes, c->stream) != cudaSuccess) {
             cudaGetLastError();
+            // no cache: the calls that use one refuse until this option succeeds
+            cudaFree(c->kc); cudaFree(c->vc);
+            c->kc = c->vc = nullptr;
             return fail(c, LLM_ERR_ALLOC, "KV cache reallocation failed");
         }
         c->kv_fp8 = want;
@@ -1655,6 +1665,7 @@ extern "C" int32_t llm_set_option(llm_ctx *c, const char *key, int32_t value) {
             if (c->seq_next[s] != 0) return fail(c, LLM_ERR_INVALID, "kv_q4 needs an empty cache (llm_seq_clear)");
         if ((value != 0) == c->kv_q4) return LLM_OK;
         if (c->kv_fp8) return fail(c, LLM_ERR_INVALID, "the cache is FP8 (kv_fp8)");
+        if (!c->kc) return fail(c, LLM_ERR_ALLOC, NO_CACHE);
         return set_kv_q4(c, value != 0);
     }
     if (!strcmp(key, "gemv_q4")) {

@@ -129,3 +129,30 @@ def test_failed_change_changes_nothing(lib):
     check(None)
     ctx.free()
     m.free()
+
+
+def test_failed_change_to_fp8_leaves_no_cache_to_use(lib):
+    """The FP8 change frees the old cache first: where it fails, the calls that would use a cache refuse, and a later
+    change brings one back."""
+    m, om = make_model(lib, MED64, 55)
+    ctx = lib.Context(m, 64, 1, 16, stream=stream())
+    prompt = synth.prompt(MED64.n_vocab, 55, 30)
+    assert ctx.decode(prompt) == 0 and ctx.decode([5]) == 0      # a captured step over the cache that goes
+    ctx.synchronize()
+    out = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for n in (0, 1):
+        ctx.seq_clear(0)
+        assert lib.llm_debug_fail_alloc(n) == 0
+        with pytest.raises(lib.LlmError):
+            ctx.set_option("kv_fp8", 1)
+        for call in (lambda: ctx.decode([5]), lambda: ctx.decode(prompt), lambda: ctx.generate(0, 4, out.data_ptr()),
+                     lambda: ctx.set_option("kv_q4", 1), lambda: ctx.seq_shift(0, 0, 1)):
+            with pytest.raises(lib.LlmError):
+                call()
+        ctx.set_option("kv_fp8", 0)
+        oc = O.Context(om, 64, 1, 16)
+        for toks in (prompt, [5]):
+            assert ctx.decode(toks) == 0 and oc.decode(toks) == 0
+            compare_logits(logits(lib, ctx, MED64), oc.logits)
+    ctx.free()
+    m.free()
