@@ -97,8 +97,8 @@ void llm_model_free(llm_model *m);
 
 /* Re-encode the model's matrices as Q8_0 or Q4_0 blocks.  Q4_0: the blocks and
  * the row layout stand with the 4-bit operators below; otherwise as Q8_0, but
- * that its rows (9 K / 16 bytes) are read by every step of 1..8 rows whose rows
- * are all outputs, 9/32 of the fp16 bytes.  Q8_0: "LLama.cpp — how it
+ * that its rows (9 K / 16 bytes) are read by every step of 1..8 rows, 9/32 of the
+ * fp16 bytes.  Q8_0: "LLama.cpp — how it
  * works", section "The GGUF format (reference)", names Q8_0 among the
  * quantised tensor element types without giving its layout; the one taken:
  * each row of Wq, Wk, Wv, Wo, gate, up, down and the output projection is cut

@@ -134,6 +134,7 @@ struct llm_ctx {
     void *q4_scratch = nullptr;
     float *qkv = nullptr;          // QKV projection rows [n_ubatch][n_qkv], where a kernel of its own norms, rotates and appends
     float *ss_q4 = nullptr;        // Q4_0 steps: per-CTA sums of h^2 [8][num_sms]
+    float *logits_q4 = nullptr;    // ... and the logits of all rows where only some are outputs
     float2 *rope = nullptr;
     float2 *rope_t = nullptr;      // the same table position-minor [hd / 2][n_ctx] (prefill QKV epilogue)
     // workspaces
@@ -482,7 +483,7 @@ static void ctx_release(llm_ctx *c) {
     void *dev[] = {c->kc, c->vc, c->rope, c->rope_t, c->h, c->h2, c->ss, c->ss2, c->qf, c->x, c->qb, c->o, c->u,
                    c->gemv_part, c->gemv_cnt, c->sk_ws, c->sk_flags, c->attn_part, c->attn_cnt, c->meta_dev, c->dec_dev,
                    c->logits, c->argmax_dev, c->gen_tokens, c->err_dev,
-                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->q4_scratch};
+                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->logits_q4, c->q4_scratch};
     for (void *p : dev) if (p) cudaFree(p);
     for (int i = 0; i < 2; ++i) {
         if (c->meta_host[i]) cudaFreeHost(c->meta_host[i]);
@@ -660,7 +661,10 @@ extern "C" int32_t llm_kv_alloc_typed(llm_model *m, int32_t n_ctx, int32_t n_seq
     // where a kernel of its own norms, rotates and appends: normed queries and keys, and a Q4_0 cache unless the GEMV
     // over Q4_0 rows encodes
     if (m->nbuf || c->kv_q4) dmal((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float));
-    if (c->q4_ok) dmal((void **)&c->ss_q4, (size_t)8 * m->num_sms * sizeof(float));
+    if (c->q4_ok) {
+        dmal((void **)&c->ss_q4, (size_t)8 * m->num_sms * sizeof(float));
+        dmal((void **)&c->logits_q4, (size_t)8 * m->V * sizeof(float));
+    }
     dmal((void **)&c->dec_dev, DEC_INTS * sizeof(int));
     dmal((void **)&c->err_dev, sizeof(uint32_t));
     if (ok) {
@@ -845,7 +849,7 @@ cudaError_t attn_decode(llm_ctx *c, const UbDev &u, int layer) {
     return timed(c, K_ATTN_DECODE, [&] { return launch_attn_decode(at, lnch_attn(c)); });
 }
 
-// Steps of 1-8 output rows of a Q4_0 model, out of its Q4_0 rows.  As in the
+// Steps of 1-8 rows of a Q4_0 model, out of its Q4_0 rows.  As in the
 // prefill, the kernel that last updates h also writes f16(h * gain) of the next
 // norm and sums of h^2; the GEMV that reads them scales its products.
 cudaError_t run_small_q4(llm_ctx *c, const UbDev &u) {
@@ -890,17 +894,32 @@ cudaError_t run_small_q4(llm_ctx *c, const UbDev &u) {
         const float *next = l + 1 < m->L ? m->layers[l + 1].attn_norm : m->output_norm;
         if ((e = gemv(K_GEMV_DOWN, EPI_RESID, w.q_down, d, m->F_pad, c->u, false, [&](GemvQ4Args &a) { resid(a, next); })))
             return e;
-        if ((e = debug_copy(c, u, l, c->h, T))) return e;
+        if (l == m->L - 1 && u.out_rows && c->dbg) {
+            // the last layer's hidden rows are those of the outputs
+            if (u.n_out == 0) break;
+            if ((e = launch_gather_rows(c->h, u.out_rows, u.n_out, d, c->h2, nullptr, nullptr, lnch(c)))) return e;
+            if ((e = debug_copy(c, u, l, c->h2, u.n_out))) return e;
+        } else if ((e = debug_copy(c, u, l, c->h, T))) {
+            return e;
+        }
     }
-    return gemv(K_GEMV_LMHEAD, EPI_STORE, m->q_out, m->V, d, c->x, true, [&](GemvQ4Args &a) {
-        a.out = c->logits + (size_t)u.out_base * m->V;
-        a.ldo = m->V;
+    if (u.n_out == 0) return cudaSuccess;
+    // the same weights are read for one row as for all: where only some are outputs, theirs are picked out
+    float *logits = c->logits + (size_t)u.out_base * m->V;
+    if ((e = gemv(K_GEMV_LMHEAD, EPI_STORE, m->q_out, m->V, d, c->x, true, [&](GemvQ4Args &a) {
+            a.out = u.out_rows ? c->logits_q4 : logits;
+            a.ldo = m->V;
+        })))
+        return e;
+    if (!u.out_rows) return cudaSuccess;
+    return timed(c, K_GATHER, [&] {
+        return launch_gather_rows(c->logits_q4, u.out_rows, u.n_out, m->V, logits, nullptr, nullptr, lnch(c));
     });
 }
 
 // Decode-sized ubatch (1..8 rows): GEMV kernels and split attention.
 cudaError_t run_small(llm_ctx *c, const UbDev &u) {
-    if (c->q4_ok && c->use_q4 && !u.out_rows && u.n_out == u.T) return run_small_q4(c, u);
+    if (c->q4_ok && c->use_q4) return run_small_q4(c, u);
     const llm_model *m = c->m;
     const int d = m->d, T = u.T;
     const Launch L = lnch(c);

@@ -119,3 +119,39 @@ def test_overlapped_launches_change_nothing(lib, shape, weights, cache, norms, n
     a.free()
     b.free()
     m.free()
+
+
+@pytest.mark.parametrize("cache,norms", [("q4", ""), (None, "qk")])
+def test_output_rows_do_not_change_a_step(lib, cache, norms):
+    """A step of several rows gives a row the same bits whichever rows are outputs, leaves the same cache, and hands out
+    the hidden rows of the outputs; a step without outputs counts too."""
+    shape = MED128
+    m, _ = make(lib, shape, 64, "q4", norms)
+    a, b = (lib.Context(m, 100, 2, 16, stream=stream(), kv_type=lib.LLM_KV_Q4_0 if cache else lib.LLM_KV_F16) for _ in range(2))
+    prompt = synth.prompt(shape.n_vocab, 64, 20)
+    for c in (a, b):
+        assert c.decode(prompt) == 0
+    hidden = [torch.zeros((1, shape.n_layer, 8, shape.n_embd), device="cuda") for _ in range(2)]
+    for out in ([0, 1], [1, 0, 1, 1, 0, 0, 0, 1], [0, 0, 1, 0, 0], [0, 0, 0]):
+        n = len(out)
+        toks, seq = list(range(7, 7 + n)), [0, 1, 1, 0, 0, 0, 1, 0][:n]
+        for c, o, h in ((a, [1] * n, hidden[0]), (b, out, hidden[1])):
+            if n in (8, 3):
+                lib.check(lib.llm_debug_hidden(c.handle, h.data_ptr(), 8, 1), c.handle)
+            assert c.decode(toks, seq_id=seq, output=o) == 0
+            c.synchronize()
+            if n in (8, 3):
+                lib.check(lib.llm_debug_hidden(c.handle, None, 0, 0), c.handle)
+        rows = [i for i in range(n) if out[i]]
+        if rows:
+            assert np.array_equal(lib.logits_numpy(a, shape.n_vocab)[rows], lib.logits_numpy(b, shape.n_vocab))
+        if n == 8:
+            assert torch.equal(hidden[0][:, :-1], hidden[1][:, :-1])
+            assert torch.equal(hidden[0][:, -1, rows], hidden[1][:, -1, :len(rows)]) and not hidden[1][:, -1, len(rows):].any()
+    for c in (a, b):
+        assert c.decode([3]) == 0
+        c.synchronize()
+    assert np.array_equal(lib.logits_numpy(a, shape.n_vocab), lib.logits_numpy(b, shape.n_vocab))
+    for c in (a, b):
+        c.free()
+    m.free()
