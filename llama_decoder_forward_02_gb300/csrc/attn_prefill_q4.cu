@@ -34,16 +34,19 @@
 // far below the maximum stay normal fp16 numbers (below 2^-21 of it their parts
 // step by 2^-31 of it).
 //
-// Bound by the tensor cores: 40 MMAs a key tile where the fp16 cache's kernel
-// has 16.  512 rows of 32 heads of 128 from position 1536 on, 8 kv heads: 37.9
-// us, of which the MMAs alone are 31.6, softmax and MMAs without the widening
-// 35.0.  (With both parts rounded to fp16, read back from a widened copy: 24.6.)
-// On the way there: one branch for each row's bounds in the widening 76 us;
-// four widening warps, one a scheduler, which issue every fourth clock at best,
-// 64; eight 46; descriptors by a whole warp, so that they stay in uniform
-// registers, 44; K and V widened by warps of their own, the next unit asked for
-// only once this one's registers are read (a wait for older loads is one for
-// newer ones too), 41; a third S buffer 39; 128 registers for the softmax 38.
+// Bound by the tensor cores and the shared memory that feeds them: 40 MMAs a key
+// tile where the fp16 cache's kernel has 16, 224 KB read by them and 128 KB
+// written by the widening.  512 rows of 32 heads of 128 from position 1536 on, 8
+// kv heads: 37.6 us; a key tile takes 1.94 us, without the widening 1.86, without
+// exponentials 1.62, the MMAs alone 1.60.  (With both parts rounded to fp16, read
+// back from a widened copy: 24.4 us and 1.06 a tile.)  On the way there: a branch
+// for each row's bounds in the widening 76 us; four widening warps, one a
+// scheduler, which issue every fourth clock at best, 64; eight 46; descriptors by a
+// whole warp, so that they stay in uniform registers, 44; K and V widened by warps
+// of their own, the next unit asked for only once this one's registers are read,
+// 41; a third S buffer 39; 128 registers for the softmax 38.  No faster: polls that
+// sleep; the next unit's codes asked for ahead of this one's widening (2.1 us a
+// tile); both units of K waited for ahead of S (1.91).
 //
 // The mma.sync kernel (head_dim 32, and wherever the other does not apply) takes
 // 64 rows a CTA and 64 keys a tile with the same split and widening.
@@ -141,23 +144,8 @@ __device__ __forceinline__ bool elect_one() {
     return is != 0;
 }
 
-// mbar_wait whose polls sleep up to a microsecond each: 18 warps wait here, and
-// polls that come back at once were 20% of the instructions issued.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err) {
-    for (uint32_t i = 0; i < WAIT_LIMIT; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000u) : "memory");
-        if (ok) return true;
-        if (*abort) return false;
-    }
-    raise_error(err, ERRF_WAIT_TIMEOUT);
-    *abort = 1;
-    return false;
-}
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err) {
-    return __all_sync(0xffffffffu, wait(bar, parity, abort, err));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
 }
 
 constexpr int BQ = 128, BKEY = 128;
