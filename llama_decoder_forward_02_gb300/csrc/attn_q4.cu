@@ -38,12 +38,14 @@
 // in split order, by the cluster they form or, over long caches, by the CTA that
 // arrives last: results do not depend on timing and nothing spins.
 //
-// Measured, calls in a row, 32 query and 8 kv heads of 128, and the time the
-// bytes take at the copy bandwidth: one row of 2100 keys 4.7 us (0.4), of 32000
-// keys 12.9 (5.4), eight rows of 748 to 3415 keys 9.9 (3.0).  Of the 12.9: 1.3
-// to q's fragments, 6.9 of loop (5.3 TB/s; schedulers issue in 49% of the SM's
-// clocks, ALU 41%, over the whole kernel), 0.9 for the warps' sums, 2.4 for the
-// count, the reads and the merge, 1.4 to the next call.  In a cluster each split
+// Measured, calls in a row in a captured graph, 32 query and 8 kv heads of 128,
+// and the time the bytes take at the copy bandwidth: one row of 2100 keys 4.4 us
+// (0.4), of 32000 keys 12.4 (5.4), eight rows of 748 to 3415 keys 10.1 (3.0); with
+// V's codes as subnormals too and weights times 8 they were 4.4, 12.0 and 9.6.  Of
+// the 12.0, which calls from C stretched to 12.9: 1.3 to q's fragments, 6.9 of loop
+// (5.3 TB/s), 0.9 for the warps' sums, 2.4 for the count, the reads and the merge,
+// 1.4 to the next call.  The schedulers issue in 54% of the SM's clocks (ALU 43%)
+// over the whole kernel.  In a cluster each split
 // sends its share to the rank that merges it before the one barrier they meet
 // at; reading it there after the barrier, with a second one to leave by, took
 // 0.7 more.
@@ -722,6 +724,9 @@ __global__ void __launch_bounds__(WT) kv_rows_q4_kernel(const uint8_t *codes, co
 }  // namespace
 
 // How the keys are split.
+//
+// (The times below were taken side by side, calls from C, before weights kept 22
+// bits for V of any size; they are 3 to 5% more since.)
 //
 // Caches of up to CLUSTER_CTX positions and many rows: every (row, kv head,
 // chunk) has the same number of splits, a power of two up to MAX_CLUSTER, and

@@ -9,11 +9,9 @@
 // and fp16-pair instructions take 2 and FFMA 1): 16 weight rows are the M side,
 // the rows of x the N side (its other columns are not used).  A word of eight
 // codes becomes four fragment registers by one shift and, for each, one logic
-// instruction and one exact fp16 subtraction: (w & 0x000F000F) | 0x64006400
-// reads 1024 + c in both halves, (w & 0x00F000F0) | 0x54005400 reads 64 + c,
-// and less 1032 and 72 that is c - 8.  Each block of 32 k is one sum of 32
-// exact products in fp32, scaled by d in fp32 and added in fp32: x and the
-// codes are never rounded.  (Codes as fp16 subnormals c * 2^-24, with
+// instruction and one exact fp16 subtraction, which leave c - 8 (q4::Widen).
+// Each block of 32 k is one sum of 32 exact products in fp32, scaled by d in
+// fp32 and added in fp32: x and the codes are never rounded.  (Codes as fp16 subnormals c * 2^-24, with
 // 8 sum(x) taken off a block's sum, save the subtractions, but the tensor
 // cores truncate their addends to the largest one's exponent: y was 9e-7 off
 // instead of 1e-7, and x needed scaling and a table of sums before the first
@@ -38,14 +36,13 @@
 // decode step of the 8B shape that is 2.3 us a layer less than a kernel of its
 // own, and whole tiles alone are worth 2%.
 //
-// Measured, calls in a row, one row of x where not said otherwise, and the time
-// the bytes take at the copy bandwidth (6.79 TB/s): 4096 x 4096 4.5 us (1.4),
-// 28672 x 4096 16.7 (9.7), 4096 x 14336 10.2 (4.9; 8 rows 11.5), 128256 x 4096
-// 56.6 (43.5; 5.2 TB/s).  With the weights requested before the dependency wait
-// 4.4, 15.4, 9.8, 10.6 and 55.2.  2.5 us of each go by before the first product
-// and after the last; in between the schedulers issue in 59% of their clocks
-// (ALU 46%, FMA 39%, tensor 26% of theirs) with four warps each, which wait for
-// the pipes and the shared-memory queue and hardly (0.1 of 6 warps) for memory.
+// Measured, calls in a row in a captured graph, one row of x where not said
+// otherwise, and the time the bytes take at the copy bandwidth (6.79 TB/s): 4096 x
+// 4096 4.3 us (1.4), 28672 x 4096 14.8 (9.7), 4096 x 14336 with 8 rows 10.5 (4.9),
+// 128256 x 4096 55.5 (43.5; 5.3 TB/s).  2.5 us of each go by before the first
+// product and after the last; in between (128256 x 4096) the schedulers issue in
+// 60% of their clocks (ALU 47%, FMA 40%, tensor 27% of theirs) with four warps
+// each, which wait for the pipes and the shared-memory queue and hardly for memory.
 //
 // What was slower or no faster: bulk copies by a producer warp, one a row and
 // step (28672 x 4096 26.7 us: 130 clocks a copy of 1152 bytes); the columns that a

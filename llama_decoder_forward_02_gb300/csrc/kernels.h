@@ -305,7 +305,7 @@ size_t q4_0_row_bytes(int K);
 cudaError_t launch_quantize_q4_0(f16 *w, int N, int K, uint8_t *q4, bool write_back, cudaStream_t st);
 
 // y[t][n] = r[t] * sum_k W[n][k] x[t][k] with Q4_0 rows W, t < T <= 8, and
-// what becomes of y (EPI_STORE, EPI_RESID or EPI_SWIGLU).
+// what becomes of y (EPI_STORE, EPI_RESID, EPI_SWIGLU or EPI_QKV).
 struct GemvQ4Args {
     const uint8_t *W;         // [N] rows of q4_0_row_bytes(K)
     int N, K, T;

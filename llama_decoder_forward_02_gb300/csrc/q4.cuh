@@ -16,10 +16,10 @@
 // in bits 4 i.., element 8 t + 2 i + 1 in bits 16 + 4 i...  So one AND with
 // 0x000F000F leaves two neighbouring elements in the halves of a register,
 // which is how an mma.sync fragment wants them, and the 4 NB bytes that lane t
-// of a fragment row needs are contiguous.  The ANDed halves are used as they
-// are: as fp16 bit patterns they are the subnormals c * 2^-24 (or, for the
-// nibbles at bits 4 and 20, c * 2^-20), which the tensor cores multiply
-// exactly.
+// of a fragment row needs are contiguous.  Decode attention uses K's ANDed
+// halves as they are: as fp16 bit patterns they are the subnormals c * 2^-24 (or,
+// for the nibbles at bits 4 and 20, c * 2^-20), which the tensor cores multiply
+// exactly.  Everything else reads c - 8 (Widen).
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
