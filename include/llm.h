@@ -535,8 +535,9 @@ int32_t llm_op_attn_decode_noalloc(const float *q, const void *k_cache, const vo
  * ------------------------------------------------------------------------*/
 
 /* Q4_0 encoding of the fp16 matrix W [N][K] into out (N rows of 9 K / 16
- * bytes), both 16-byte aligned; W is only read.  LLM_ERR_INVALID for a null
- * or misaligned pointer, N < 1 or a K that is not a positive multiple of 256. */
+ * bytes), both 16-byte aligned; W is only read and finite (a NaN counts as 0, an
+ * infinity makes its block's scale one).  LLM_ERR_INVALID for a null or
+ * misaligned pointer, N < 1 or a K that is not a positive multiple of 256. */
 int32_t llm_op_quantize_q4_0(const void *W, int32_t N, int32_t K, void *out, void *stream);
 
 /* y[t][n] = sum over blocks b of d[n][b] * sum over k in b of
@@ -555,7 +556,8 @@ int64_t llm_op_kv_q4_0_bytes(int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_s
 /* Queries and keys normed per head and rotated, keys and values appended to
  * the cache, in one pass over the QKV projection's output: for row t < T and
  * each query or key head x of it, u = x * gain / sqrt(mean(x^2) + eps) (the
- * head itself where its gain pointer is NULL), then the rotation of pairs
+ * head itself where its gain pointer is NULL; squares are summed in fp32, so
+ * elements of a normed head stay below 1e18), then the rotation of pairs
  * (u[2i], u[2i+1]) by rope[pos[t]][i] = (cos, sin).  Values are appended as
  * they are.
  *   qkv     fp32 [T][ld]: H query heads, Hkv key heads, Hkv value heads of hd
