@@ -633,6 +633,123 @@ int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void 
                                  int32_t n_ctx, int32_t n_seq, int32_t window, void *scratch, int64_t scratch_bytes,
                                  uint32_t *err, void *stream);
 
+/* --------------------------------------------------------------------------
+ * Drafted decoding: rotary positions in every layout and scaling, attention of
+ * trees of drafted tokens, and the acceptance of a tree's path.  None of these
+ * calls allocates or waits: each enqueues its kernels on `stream` and returns, so
+ * they can be captured into a CUDA graph.  Pointers belong to the current
+ * device and are DEVICE pointers unless stated.
+ *
+ * Trees.  A call takes n_tree trees (1..4096), at most one of a sequence.  Tree
+ * i has the consecutive rows row0[i] .. row0[i + 1] - 1 of the call (row0 int32
+ * [n_tree + 1], ascending, within [0, T]), its nodes 0, 1, ..; at most max_nodes
+ * (1..256) of them, none being allowed.  Node j stands in cell base[i] + j of
+ * sequence seq[i]'s cache; the cells before base[i] are the sequence's earlier
+ * positions.  Rows that belong to no tree are left as they are.  A tree with
+ * rows outside [0, T), more than max_nodes nodes, cells outside [0, n_ctx) or a
+ * sequence outside [0, n_seq) ORs 2 into *err (DEVICE word or NULL).
+ * ------------------------------------------------------------------------*/
+
+/* cos and sin of positions: out fp32 [n_pos][n_rot / 2][2] holds, for position
+ * pos0 + i and pair j, m cos(a) and m sin(a) of the angle a = (pos0 + i) * f_j,
+ * angles in 64 bits.  With f = theta^(-2 j / n_rot), f_j is by `scaling`
+ *   LLM_ROPE_NONE    f
+ *   LLM_ROPE_LINEAR  f / factor
+ *   LLM_ROPE_BANDS   f * k + f / factor * (1 - k), k = (t - slow) / (fast - slow)
+ *                    clamped to [0, 1], t = n_ctx_orig * f / (2 pi) the turns of
+ *                    the pair in the trained context
+ *   LLM_ROPE_RAMP    the same with k = 1 - (j - lo) / max(hi - lo, 0.001) clamped,
+ *                    lo and hi the (fractional) pairs that turn fast and slow
+ *                    times, n_rot ln(n_ctx_orig / (2 pi turns)) / (2 ln theta),
+ *                    rounded down and up and clamped to [0, n_rot - 1]
+ * and m = attn_factor, or where that is 0 the scaling's own: 0.1 ln(factor) + 1
+ * with LLM_ROPE_RAMP, else 1.  rope: HOST struct, read before the call returns.
+ * LLM_ERR_INVALID (reason in llm_last_error(NULL)) unless n_rot is a multiple of
+ * 8 in [8, 128], theta > 1, factor >= 1 (where scaled), 0 < slow < fast and
+ * n_ctx_orig >= 1 (bands and ramp), attn_factor >= 0, 0 <= pos0, n_pos >= 1, pos0 +
+ * n_pos <= 2^30 and out is 16-byte aligned.  `layout` is checked, and not used. */
+#define LLM_ROPE_PAIRS 0
+#define LLM_ROPE_HALVES 1
+#define LLM_ROPE_NONE 0
+#define LLM_ROPE_LINEAR 1
+#define LLM_ROPE_BANDS 2
+#define LLM_ROPE_RAMP 3
+typedef struct {
+    float theta;
+    int32_t n_rot, layout, scaling;
+    float factor, slow, fast;
+    int32_t n_ctx_orig;
+    float attn_factor;
+} llm_rope;
+int32_t llm_op_rope_table(const llm_rope *rope, int32_t pos0, int32_t n_pos, float *out, void *stream);
+
+/* llm_op_qk_norm_rope with the rotation in every layout, and cells that need not
+ * be positions (nodes of a tree that share one).  The first n_rot elements of
+ * each query and key head (a multiple of 8 up to head_dim) turn, the others stay:
+ * LLM_ROPE_PAIRS elements 2 i and 2 i + 1, LLM_ROPE_HALVES elements i and
+ * i + n_rot / 2, by the angles of rope fp32 [n_pos][n_rot / 2][2], row pos[t].
+ * K and V of row t go to cell cell[t] of sequence seq[t] (cell NULL: cell
+ * pos[t]); rows of one call have distinct (seq, cell).  A row whose pos lies
+ * outside [0, n_pos), its cell outside [0, n_ctx) or its seq outside [0, n_seq)
+ * is treated as a row outside the cache there; the other arguments too are
+ * those of that call. */
+int32_t llm_op_rope_kv(const float *qkv, int32_t ld, const float *q_gain, const float *k_gain, float eps,
+                       const float *rope, int32_t n_pos, int32_t n_rot, int32_t layout, const int32_t *pos,
+                       const int32_t *cell, const int32_t *seq, void *q, int32_t q_type, void *k_cache, void *v_cache,
+                       int32_t kv_type, int32_t T, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq,
+                       uint32_t *err, void *stream);
+
+/* Attention of the nodes of trees over their sequences' caches: for row t of
+ * tree i and query head h, o[t][h] = softmax_c(q[t][h] . K[c] / sqrt(hd)) V[c]
+ * over the cells c < base[i], with window > 0 those c > pos[t] - window, and the
+ * cells base[i] + j, j below the tree's nodes, whose bit j % 32 of word j / 32 of
+ * mask[t] is set (a node's ancestors and itself, or any others).  A row that sees
+ * nothing is zero.
+ *   q, o     fp16 [T][H * hd]; o is written for the rows of trees only (zeros for a
+ *            tree that does not fit, as far as its rows lie within [0, T) and
+ *            max_nodes)
+ *   mask     uint32 [T][(max_nodes + 31) / 32]
+ *   pos      int32 [T], or NULL where window is 0
+ *   k_cache, v_cache  one layer [n_seq][Hkv][n_ctx][hd], fp16 (LLM_KV_F16) or FP8
+ *            (LLM_KV_E4M3), fewer than 2^31 - 1000 rows
+ *   scratch  scratch_bytes bytes, zeroed once before its first use; each call leaves
+ *            it ready for the next, of any shape it is large enough for, and calls
+ *            that may overlap need one each
+ * q, K and V enter the products exactly and the softmax weights with 22 bits (below
+ * 2^-21 of the row's largest with 2^-31 of it); sums are fp32.  A visible cell with an infinity or a NaN
+ * gives the heads that see it values that are not finite; cells that a row does
+ * not see may hold anything.  head_dim 32, 64 or 128; any H that is a multiple of
+ * Hkv, up to 4096, with n_tree * Hkv * ceil(max_nodes * H / Hkv / 128) at most 65535;
+ * q, the caches, o and scratch 16-byte aligned; else LLM_ERR_INVALID before
+ * anything is enqueued.  *err is ORed with 4 when a bounded wait of the kernel
+ * timed out. */
+int64_t llm_op_attn_tree_scratch_bytes(int32_t n_tree, int32_t max_nodes, int32_t H, int32_t Hkv, int32_t hd,
+                                       int32_t n_ctx);
+int32_t llm_op_attn_tree(const void *q, const void *k_cache, const void *v_cache, const int32_t *row0,
+                         const int32_t *seq, const int32_t *base, const uint32_t *mask, const int32_t *pos, void *o,
+                         int32_t T, int32_t n_tree, int32_t max_nodes, int32_t H, int32_t Hkv, int32_t hd, int32_t n_ctx,
+                         int32_t n_seq, int32_t kv_type, int32_t window, void *scratch, int64_t scratch_bytes,
+                         uint32_t *err, void *stream);
+
+/* The path of each tree that its targets accept, and the move of its cells.
+ * token[t] is the drafted token of row t, parent[t] the node it was drafted
+ * after (-1 for node 0, else a lower node of its tree), target[t] the token that
+ * the model picks after it (llm_op_sample of the row's logits).  Node 0 stands;
+ * after a node that stands its child whose token is the node's target stands too,
+ * the lowest of several.  For tree i the nodes that stand go to path[i] (int32
+ * [n_tree][max_nodes], the rest -1), their number to n_accept[i], the target of
+ * the last to next[i], and the keys and values of cells base[i] + path[i][j] to
+ * cells base[i] + j, in every layer and kv head: caches [n_seq][n_layer][Hkv]
+ * [n_ctx][hd] of kv_type (Q4_0: the codes of all, then the scales of all), V as K.
+ * Other cells keep their values.  A tree without nodes accepts none (next -1);
+ * one that does not fit, or with a parent that is not a lower node, accepts none
+ * and ORs 2 into *err.  n_layer * Hkv at most 65535; caches 16-byte aligned. */
+int32_t llm_op_tree_accept(const int32_t *token, const int32_t *parent, const int32_t *target, const int32_t *row0,
+                           const int32_t *seq, const int32_t *base, void *k_cache, void *v_cache, int32_t kv_type,
+                           int32_t *path, int32_t *n_accept, int32_t *next, int32_t T, int32_t n_tree,
+                           int32_t max_nodes, int32_t n_layer, int32_t Hkv, int32_t hd, int32_t n_ctx, int32_t n_seq,
+                           uint32_t *err, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

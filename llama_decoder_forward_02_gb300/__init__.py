@@ -19,6 +19,8 @@ LLM_BATCH_TOKENS_ON_DEVICE = 1
 LLM_WTYPE_Q8_0, LLM_WTYPE_Q4_0 = 1, 2
 LLM_Q_F32, LLM_Q_F16 = 0, 1
 LLM_KV_F16, LLM_KV_E4M3, LLM_KV_Q4_0 = 0, 1, 2
+LLM_ROPE_PAIRS, LLM_ROPE_HALVES = 0, 1
+LLM_ROPE_NONE, LLM_ROPE_LINEAR, LLM_ROPE_BANDS, LLM_ROPE_RAMP = 0, 1, 2, 3
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with llama_decoder_forward_02_gb300.build.build()")
@@ -52,6 +54,11 @@ class llm_batch(ctypes.Structure):
 class llm_sampling(ctypes.Structure):
     _fields_ = [("temperature", c_f32), ("top_k", c_i32), ("top_p", c_f32), ("min_p", c_f32),
                 ("repeat_penalty", c_f32), ("penalty_last_n", c_i32)]
+
+
+class llm_rope(ctypes.Structure):
+    _fields_ = [("theta", c_f32), ("n_rot", c_i32), ("layout", c_i32), ("scaling", c_i32), ("factor", c_f32),
+                ("slow", c_f32), ("fast", c_f32), ("n_ctx_orig", c_i32), ("attn_factor", c_f32)]
 
 
 def _proto(name, res, *args):
@@ -121,6 +128,13 @@ _attn_q4_args = [c_vp] * 6 + [c_i32] * 7 + [c_vp, c_i64, c_vp, c_vp]
 llm_op_attn_decode_q4_0 = _proto("llm_op_attn_decode_q4_0", c_i32, *_attn_q4_args)
 llm_op_attn_prefill_q4_0 = _proto("llm_op_attn_prefill_q4_0", c_i32, *_attn_q4_args)
 
+llm_op_rope_table = _proto("llm_op_rope_table", c_i32, ctypes.POINTER(llm_rope), c_i32, c_i32, c_vp, c_vp)
+llm_op_rope_kv = _proto("llm_op_rope_kv", c_i32, c_vp, c_i32, c_vp, c_vp, c_f32, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
+                        c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp)
+llm_op_attn_tree_scratch_bytes = _proto("llm_op_attn_tree_scratch_bytes", c_i64, *[c_i32] * 6)
+llm_op_attn_tree = _proto("llm_op_attn_tree", c_i32, *[c_vp] * 9, *[c_i32] * 10, c_vp, c_i64, c_vp, c_vp)
+llm_op_tree_accept = _proto("llm_op_tree_accept", c_i32, *[c_vp] * 8, c_i32, *[c_vp] * 3, *[c_i32] * 8, c_vp, c_vp)
+
 EXPORTED = [n for n in dir() if n.startswith("llm_") and callable(globals()[n]) and
             not isinstance(globals()[n], type)]
 
@@ -138,6 +152,14 @@ def check(code, handle=None):
 
 
 # ---------------------------------------------------------------- marshalling helpers
+
+def rope(theta, n_rot, layout=LLM_ROPE_PAIRS, scaling=LLM_ROPE_NONE, factor=1.0, slow=1.0, fast=None, n_ctx_orig=0,
+         attn_factor=0.0) -> llm_rope:
+    """llm_rope; `fast` as usual for the scaling where not given (4 turns with bands, 32 with a ramp)."""
+    if fast is None:
+        fast = 4.0 if scaling == LLM_ROPE_BANDS else 32.0
+    return llm_rope(theta, n_rot, layout, scaling, factor, slow, fast, n_ctx_orig, attn_factor)
+
 
 def hparams(shape) -> llm_hparams:
     """llm_hparams from any object with the Llama hyper-parameter fields."""

@@ -331,17 +331,22 @@ cudaError_t launch_gemv_q4(int epi, const GemvQ4Args &a, int num_sms, const Laun
 
 // Per-head RMSNorm (gains may be null: no norm) and rotation of the query and
 // key heads of qkv rows [T][ld] (H query, Hkv key, Hkv value heads), q to q32
-// or q16 [T][H * hd], keys and values appended to the cache kv.
+// or q16 [T][H * hd], keys and values to cells cell[t] (null: pos[t]) of the
+// cache kv.  The first n_rot elements of a head turn (a multiple of 8; 0: all),
+// as adjacent pairs or as halves, by the table's row pos[t] of n_pos (0: n_ctx).
 struct QkNormArgs {
     const float *qkv; int ld;
     const float *q_gain, *k_gain; float eps;
-    const float2 *rope;        // [n_ctx][hd / 2]
+    const float2 *rope;        // [n_pos][n_rot / 2]
     const int *pos, *seq;
     float *q32; f16 *q16;
     KvView kv;
     int T, H;
     uint32_t *err;
-    bool early = false;        // pos, seq and rope were written before the kernel that precedes this one
+    bool early = false;        // pos, cell, seq and rope were written before the kernel that precedes this one
+    const int *cell = nullptr;
+    int n_pos = 0, n_rot = 0;
+    bool halves = false;
 };
 cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l);
 // launch_kv_shift of a Q4_0 cache: keys are rotated as the values they stand
@@ -371,5 +376,57 @@ cudaError_t launch_attn_prefill_q4(const AttnPrefillArgs &a, const KvRuns *runs,
 // out[t][j][:] = the values of row pos[t], kv head j of sequence seq[t].
 cudaError_t launch_kv_rows_q4(const uint8_t *codes, const f16 *scales, const KvView &kv, const int *pos,
                               const int *seq, f16 *out, int T, uint32_t *err, const Launch &l);
+
+// ------------------------------------------------------------------ rotary tables
+enum { ROPE_NONE = 0, ROPE_LINEAR = 1, ROPE_BANDS = 2, ROPE_RAMP = 3 };
+struct RopeSpec {
+    float theta;
+    int n_rot;                 // elements of a head that turn (even)
+    int scaling;               // ROPE_*
+    float factor;              // how far frequencies are stretched
+    float slow, fast;          // turns in n_ctx_orig positions: at most slow stretched, from fast on kept
+    int n_ctx_orig;
+    float attn_factor;         // factor of cos and sin; 0: the scaling's own
+};
+// Radians a position of the n_rot / 2 pairs, and the factor of cos and sin.
+void rope_frequencies(const RopeSpec &r, double *f, double *scale);
+// out[i][j] = factor * (cos, sin)((pos0 + i) * frequency j), i < n_pos.
+cudaError_t launch_rope_table(const RopeSpec &r, int pos0, int n_pos, float2 *out, const Launch &l);
+
+// ------------------------------------------------------------------ trees of drafted tokens
+// Rows row0[i] .. row0[i + 1] - 1 are the nodes of tree i, at most max_nodes, in
+// cells base[i] .. of sequence seq[i]'s cache.  A tree that does not fit (rows
+// outside T, cells outside n_ctx, another sequence) raises ERRF_BAD_INDEX.
+constexpr int TREE_MAX_NODES = 256;
+struct AttnTreeArgs {
+    const f16 *q;              // [T][H*hd], after RoPE
+    KvView kv;                 // fp16 or E4M3
+    const int *row0, *seq, *base;
+    const uint32_t *mask;      // [T][words]: bit j = cell base + j is seen
+    const int *pos;            // [T], read where window > 0
+    f16 *o;                    // [T][H*hd]
+    int T, n_tree, max_nodes, words, H, window;
+    void *scratch;
+    uint32_t *err;
+    long long map_row0 = 0;    // the layer's first row in the caches' maps
+};
+size_t attn_tree_scratch_bytes(int n_tree, int max_nodes, int H, int Hkv, int hd, int n_ctx);
+// mK, mV: maps of the fp16 caches (boxes of 128 rows x 64), unused with E4M3
+cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap *mK, const TmaMap *mV, const Launch &l);
+
+// Path of a tree that its targets accept, and the move of its cells (tree_accept.cu).
+enum { TREE_KV_F16 = 0, TREE_KV_E4M3 = 1, TREE_KV_Q4_0 = 2 };       // as LLM_KV_*
+struct TreeAcceptArgs {
+    const int *token, *parent, *target;       // [T]
+    const int *row0, *seq, *base;
+    void *k, *v;               // caches [n_seq][heads][n_ctx][hd]
+    int kv_type;
+    int *path, *n_accept, *next;              // [n_tree][max_nodes], [n_tree], [n_tree]
+    int T, n_tree, max_nodes;
+    int heads;                 // layers * kv heads
+    int head_dim, n_ctx, n_seq;
+    uint32_t *err;
+};
+cudaError_t launch_tree_accept(const TreeAcceptArgs &a, const Launch &l);
 
 }  // namespace llm

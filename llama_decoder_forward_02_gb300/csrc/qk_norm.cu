@@ -64,20 +64,26 @@ __device__ __forceinline__ void transform(const float (&x)[E], const float (&gai
     }
 }
 
-// ... times up (a power of two) as pairs, good to 2^-42.
+// 1 / sqrt(mean(x^2) + eps) of the head as a pair.
 template <int HD>
-__device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
-                                          bool turn, float eps, float up, q4::Pair (&u)[E]) {
+__device__ __forceinline__ q4::Pair inverse_norm(const float (&x)[E], float eps) {
     q4::Pair r{0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < E; ++e) r = r + q4::two_prod(x[e], x[e]);
 #pragma unroll
     for (int o = HD / E / 2; o > 0; o >>= 1) r = r + q4::shfl_xor(r, o);
-    // 1 / sqrt(v) by one Newton step from float32's
+    // one Newton step from float32's
     const q4::Pair v = q4::Pair{r.h / (float)HD, r.l / (float)HD} + q4::Pair{eps, 0.f};
     const float r0 = rsqrtf(v.h);
     const q4::Pair one = v * r0 * r0;
-    r = q4::settle(r0, 0.5f * r0 * __fsub_rn(__fsub_rn(1.f, one.h), one.l));
+    return q4::settle(r0, 0.5f * r0 * __fsub_rn(__fsub_rn(1.f, one.h), one.l));
+}
+
+// ... times up (a power of two) as pairs, good to 2^-42.
+template <int HD>
+__device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
+                                          bool turn, float eps, float up, q4::Pair (&u)[E]) {
+    const q4::Pair r = inverse_norm<HD>(x, eps);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
         q4::Pair a{x[e] * up, 0.f}, b{x[e + 1] * up, 0.f};
@@ -89,6 +95,89 @@ __device__ __forceinline__ void transform(const float (&x)[E], const float (&gai
         u[e] = turn ? a * c.x + b * -c.y : a;
         u[e + 1] = turn ? a * c.y + b * c.x : b;
     }
+}
+
+// Rotation by halves: element e < half of a head turns with element e + half,
+// half = n_rot / 2 a multiple of 4.  A lane's partners are whole groups of four
+// elements in other lanes of the head, fetched after the norm (shuffles; reading
+// them again from memory would also need their gains).
+struct Halves {
+    int src[2];               // the lane that holds the partners of elements 0-3 and of 4-7
+    bool upper[2];            // ... as its elements 4-7
+    bool turns[2];            // inside the first n_rot elements
+    bool first[2];            // below half
+    bool whole;               // half is a multiple of 8: the lane's eight partners are another lane's eight
+    __device__ __forceinline__ Halves(int n_rot, int sub, int lane) {
+        const int h4 = n_rot / 8;                     // half in groups of four
+        whole = h4 % 2 == 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int at = 2 * sub + g;
+            first[g] = at < h4;
+            turns[g] = at < 2 * h4;
+            const int to = !turns[g] ? at : first[g] ? at + h4 : at - h4;
+            src[g] = lane - sub + to / 2;
+            upper[g] = to & 1;
+        }
+    }
+    template <typename V>
+    __device__ __forceinline__ void partners(const V (&a)[E], V (&y)[E]) const {
+        if (whole) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = shuffle(a[e], src[0]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const V lo = shuffle(a[e & 3], src[e >> 2]), hi = shuffle(a[(e & 3) + 4], src[e >> 2]);
+                y[e] = upper[e >> 2] ? hi : lo;
+            }
+        }
+    }
+    // cosine and signed sine of the lane's elements
+    __device__ __forceinline__ void turn(const float2 *row, bool ok, int sub, int n_rot, float2 (&cs)[E]) const {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int i = 4 * (2 * sub + g) - (first[g] ? 0 : n_rot / 2);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+                if (ok && turns[g]) v = *reinterpret_cast<const float4 *>(row + i + e);
+                cs[4 * g + e] = make_float2(v.x, first[g] ? -v.y : v.y);
+                cs[4 * g + e + 1] = make_float2(v.z, first[g] ? -v.w : v.w);
+            }
+        }
+    }
+
+private:
+    static __device__ __forceinline__ float shuffle(float v, int from) { return __shfl_sync(0xffffffffu, v, from); }
+    static __device__ __forceinline__ q4::Pair shuffle(const q4::Pair &v, int from) { return q4::shfl(v, from); }
+};
+
+template <int HD>
+__device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E], const Halves &hv,
+                                          bool norm, bool turn, float eps, float (&u)[E]) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss += x[e] * x[e];
+    ss = group_sum<HD / E>(ss);
+    const float r = rsqrtf(ss / (float)HD + eps);
+    float a[E], y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = norm ? x[e] * r * gain[e] : x[e];
+    hv.partners(a, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) u[e] = turn && hv.turns[e >> 2] ? a[e] * cs[e].x + y[e] * cs[e].y : a[e];
+}
+template <int HD>
+__device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E], const Halves &hv,
+                                          bool norm, bool turn, float eps, float up, q4::Pair (&u)[E]) {
+    const q4::Pair r = inverse_norm<HD>(x, eps);
+    q4::Pair a[E], y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = norm ? q4::two_prod(x[e], gain[e] * up) * r : q4::Pair{x[e] * up, 0.f};
+    hv.partners(a, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e) u[e] = turn && hv.turns[e >> 2] ? a[e] * cs[e].x + y[e] * cs[e].y : a[e];
 }
 
 // The codes of a lane's elements and the scale of its block (4 lanes).
@@ -140,15 +229,14 @@ __device__ __forceinline__ void encode(const q4::Pair (&u)[E], int lane, float &
     d = d2.h;
 }
 
-// The word and scale of the exact values.
-template <int HD>
-__device__ __forceinline__ void encode_exact(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
-                                             bool turn, float eps, const float (&u)[E], bool used, int lane, float &d, uint32_t &word) {
+// The word and scale of the exact values; exact(up, u2) gives them times up as pairs.
+template <typename Exact>
+__device__ __forceinline__ void encode_exact(const float (&u)[E], bool used, int lane, float &d, uint32_t &word, Exact &&exact) {
     const bool near = encode(u, lane, d, word);
     if (__any_sync(0xffffffffu, near && used)) {
         const float up = fabsf(d) > q4::TINY || d == 0.f ? 1.f : q4::RAISE;     // the same for the lanes of a block
         q4::Pair u2[E];
-        transform<HD>(x, gain, cs, norm, turn, eps, up, u2);
+        exact(up, u2);
         encode(u2, lane, d, word);
         d /= up;
     }
@@ -162,9 +250,11 @@ __device__ __forceinline__ void load8(float (&v)[E], const float *p) {
 
 // grid (row, part): part p of gridDim.y takes the warps' heads p, p + parts, ..
 // Q4: the cache is Q4_0 (its exact path would take registers from the others).
-// Four or five CTAs an SM keep the loads in flight.
-template <int HD, bool Q4>
-__global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const QkNormArgs a) {
+// HALF: rotation by halves instead of adjacent pairs.
+// Four or five CTAs an SM keep the loads in flight (three by halves, whose
+// partners and signed sines take registers).
+template <int HD, bool Q4, bool HALF>
+__global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_kernel(const QkNormArgs a) {
     constexpr int L = HD / E, PER = 32 / L;           // lanes of a head, heads of a warp at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, e0 = E * sub;
     const int Hkv = a.kv.n_kv_head, heads = a.H + 2 * Hkv;
@@ -181,15 +271,21 @@ __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const
         if (h0 >= heads) return;                      // whole warps
         load8(next, first);
     }
-    const int pos = a.pos[t], seq = a.seq[t];
-    const bool ok = pos >= 0 && pos < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
-    float2 turn[E / 2];
+    const int pos = a.pos[t], cell = a.cell[t], seq = a.seq[t];
+    const bool ok = pos >= 0 && pos < a.n_pos && cell >= 0 && cell < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
+    const Halves hv(a.n_rot, sub, lane);
+    const bool mine = HALF || e0 < a.n_rot;           // by pairs a lane turns whole or not at all
+    const float2 *angles = a.rope + (size_t)(ok ? pos : 0) * (a.n_rot / 2);
+    float2 turn[HALF ? E : E / 2];
+    if constexpr (HALF) hv.turn(angles, ok, sub, a.n_rot, turn);
+    else {
 #pragma unroll
-    for (int e = 0; e < E / 2; e += 2) {
-        float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
-        if (ok) v = *reinterpret_cast<const float4 *>(a.rope + (size_t)pos * (HD / 2) + e0 / 2 + e);
-        turn[e] = make_float2(v.x, v.y);
-        turn[e + 1] = make_float2(v.z, v.w);
+        for (int e = 0; e < E / 2; e += 2) {
+            float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+            if (ok && mine) v = *reinterpret_cast<const float4 *>(angles + e0 / 2 + e);
+            turn[e] = make_float2(v.x, v.y);
+            turn[e + 1] = make_float2(v.z, v.w);
+        }
     }
     if (a.early) {
         pdl_wait();
@@ -214,7 +310,8 @@ __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const
             for (int e = 0; e < E; ++e) gain[e] = 1.f;
         }
         float u[E];
-        transform<HD>(x, gain, turn, gp != nullptr, is_q || is_k, a.eps, u);
+        if constexpr (HALF) transform<HD>(x, gain, turn, hv, gp != nullptr, is_q || is_k, a.eps, u);
+        else transform<HD>(x, gain, turn, gp != nullptr, (is_q || is_k) && mine, a.eps, u);
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) bad |= f16_bad(u[e]);
@@ -233,11 +330,14 @@ __global__ void __launch_bounds__(THREADS, Q4 ? 4 : 5) qk_norm_rope_kernel(const
         const bool put = in && ok && !is_q;
         if (!__any_sync(0xffffffffu, put)) continue;             // a warp of query heads
         const int j = h - a.H - (is_k ? 0 : Hkv);
-        const size_t base = put ? (size_t)seq * a.kv.seq_stride + ((size_t)j * a.kv.n_ctx + pos) * HD : 0;
+        const size_t base = put ? (size_t)seq * a.kv.seq_stride + ((size_t)j * a.kv.n_ctx + cell) * HD : 0;
         if (Q4) {
             float d;
             uint32_t word;
-            encode_exact<HD>(x, gain, turn, gp != nullptr, is_k, a.eps, u, put, lane, d, word);
+            encode_exact(u, put, lane, d, word, [&](float up, q4::Pair (&u2)[E]) {
+                if constexpr (HALF) transform<HD>(x, gain, turn, hv, gp != nullptr, is_k, a.eps, up, u2);
+                else transform<HD>(x, gain, turn, gp != nullptr, is_k && mine, a.eps, up, u2);
+            });
             if (put) {
                 out_of_range |= bad;
                 const int blk = sub >> 2, tt = sub & 3;
@@ -291,7 +391,8 @@ __global__ void __launch_bounds__(SHIFT_THREADS) kv_shift_q4_kernel(KvView kv, i
         for (int e = 0; e < E; ++e) x[e] = (float)((int)((w >> q4::shift_of(e)) & 15u) - 8) * d;     // exact
         uint32_t out;
         transform<HD>(x, gain, back, false, true, 0.f, u);
-        encode_exact<HD>(x, gain, back, false, true, 0.f, u, true, lane, nd, out);
+        encode_exact(u, true, lane, nd, out,
+                     [&](float up, q4::Pair (&u2)[E]) { transform<HD>(x, gain, back, false, true, 0.f, up, u2); });
         __syncthreads();
         if (in) {
             kw[dst * (HD / 8) + at] = out;
@@ -323,16 +424,26 @@ cudaError_t launch_kv_shift_q4(const KvView &kv0, int n_layer, int seq, int p0, 
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_qk_norm_rope(const QkNormArgs &a, const Launch &l) {
+template <int HD>
+static cudaError_t launch_qk(const QkNormArgs &a, dim3 grid, const Launch &l) {
+    const dim3 block(THREADS);
+    if (a.halves)
+        return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<HD, true, true> : qk_norm_rope_kernel<HD, false, true>, grid, block, 0, l, a);
+    return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<HD, true, false> : qk_norm_rope_kernel<HD, false, false>, grid, block, 0, l, a);
+}
+
+cudaError_t launch_qk_norm_rope(const QkNormArgs &a0, const Launch &l) {
+    QkNormArgs a = a0;
     const int hd = a.kv.head_dim, heads = a.H + 2 * a.kv.n_kv_head;
-    if (a.T < 1 || (!a.q32 && !a.q16) || (hd != 32 && hd != 64 && hd != 128)) return cudaErrorInvalidValue;
+    if (!a.cell) a.cell = a.pos;
+    if (!a.n_rot) a.n_rot = hd;
+    if (!a.n_pos) a.n_pos = a.kv.n_ctx;
+    if (a.T < 1 || (!a.q32 && !a.q16) || (hd != 32 && hd != 64 && hd != 128) || a.n_rot % 8 || a.n_rot < 8 || a.n_rot > hd)
+        return cudaErrorInvalidValue;
     // few rows: the heads of a row spread over several CTAs; many: one CTA a row
     const int per = 32 / (hd / E) * (THREADS / 32), parts = (heads + per - 1) / per;      // heads a CTA takes at once
-    const dim3 grid(a.T, (long long)a.T * parts > 4 * 152 ? 1 : parts), block(THREADS);
-    if (hd == 32) return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<32, true> : qk_norm_rope_kernel<32, false>, grid, block, 0, l, a);
-    if (hd == 64) return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>, grid, block, 0, l, a);
-    if (hd == 128) return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>, grid, block, 0, l, a);
-    return cudaErrorInvalidValue;
+    const dim3 grid(a.T, (long long)a.T * parts > 4 * 152 ? 1 : parts);
+    return hd == 32 ? launch_qk<32>(a, grid, l) : hd == 64 ? launch_qk<64>(a, grid, l) : launch_qk<128>(a, grid, l);
 }
 
 }  // namespace llm
