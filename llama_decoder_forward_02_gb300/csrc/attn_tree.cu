@@ -6,79 +6,706 @@
 // over the cells c < base[i] (with a window those c > pos[t] - window) and the
 // cells base[i] + j whose bit j of mask[t] is set.  A row that sees nothing is zero.
 //
-// One warp takes a row and query head, a lane a key of 32.
+// The rows of a tree that share a kv head, its nodes times the query heads of the
+// group, see the same earlier cells: 128 of them are one tile of tcgen05.mma, which
+// reads each K and V tile of 128 keys once for all of them.  The keys are split over
+// the CTAs of a cluster, and where there are still SMs left over several clusters.
+//
+// Precision.  q, K and V are fp16 (an E4M3 value is one exactly); a weight p = 2^x,
+// x in fp32, enters O as two fp16 numbers of 22 bits together.  Rounded to one, o is
+// off by 1.4 times its own rounding.  The running maximum is raised, and O rescaled,
+// only when a tile's maximum passes it by 8 in base 2; weights are kept 2^7 times as
+// large, so that those far below the maximum stay normal fp16 numbers.
+//
+// A CTA: warps 0-7 softmax (two threads a row, 64 keys each), 8-11 bring K and
+// 12-15 V (fp16: one lane each by TMA; E4M3: all widen), 16 issues S = q K^T, 17
+// O += P V.  Tensor memory: three S buffers of 128 columns, P in the place of the
+// S it came from (of each 32 columns 16 of high pairs, 16 of low pairs), O.
+//
+// Joining: a CTA sends its rows of O, their maxima and sums to the ranks that own
+// them (rows / cluster size each), one cluster barrier later every rank joins its
+// rows.  With several clusters a rank leaves its rows in memory and the last one to
+// come joins them, in the clusters' order whichever it is.
+//
+// Cells that a row does not see may hold anything: a masked score is replaced, and
+// in tiles that not every row sees whole, V is read over before its product: rows
+// outside the tree's cells become zero, and a value that is not finite makes the
+// rows that see its cell NaN and is zero for the others.
+//
+// Every mbarrier wait is bounded; on a timeout the CTA raises ERRF_WAIT_TIMEOUT,
+// waits (bounded) for its own copies in flight, takes part in the cluster's barriers
+// and frees its tensor memory.  The shared memory of a CTA leaves no room for another
+// that allocates tensor memory, so the allocation never waits.
+#include <cuda.h>
+
+#include "attn_tc.cuh"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.cuh"
+#include "tma.cuh"
 
 namespace llm {
 
 namespace {
 
-constexpr int WARPS = 4;
+using tcg::sdesc;
+using tcg::tc_fence_after;
+using tcg::tc_fence_before;
+using tcg::tmem_ld32;
+using namespace tca;
 
+constexpr float LIFT = 7.f;                  // weights are kept 2^LIFT times as large
+constexpr float RESCALE_LOG2 = 8.f;          // raise the running maximum only past this margin
+constexpr int BQ = 128, BKEY = 128;
+constexpr int SM_WARPS = 8, K_WARP = 8, V_WARP = 12, W_WARPS = 4, S_WARP = 16, PV_WARP = 17;
+constexpr int THREADS = 20 * 32;             // five warpgroups; the last two warps only make up the number
+// Registers a thread: 96 at launch (640 threads), then by warpgroup: 2 x 128 + 2 x 72 + 80 = 480 of 480
+constexpr int L_REGS = 96, SM_REGS = 128, W_REGS = 72, I_REGS = 80;
+constexpr uint32_t BOX = 128 * 128;          // bytes of one 128-row x 64-column fp16 box
+constexpr int NS = 3;                        // S buffers
+constexpr uint32_t TMEM_COLS = 512;          // S_b / P_b [128 b, 128 b + 128), O [384, 384 + HD)
+constexpr int MAX_CLUSTER = 8;
+constexpr int SLOTS = 64;                    // (group, cluster) results that go through memory
+constexpr int COUNTERS = 1024;
+
+// HD: head_dim as the tiles hold it (head_dim 32: 64, the rest zeros).
+template <int HD>
+struct Cfg {
+    static constexpr int NBX = HD / 64;                         // 64-column boxes of a row
+    static constexpr int ST = HD == 128 ? 2 : 5;                // stages of each ring
+    static constexpr uint32_t TILE = NBX * BOX;
+    static constexpr uint32_t K_OFF = TILE;
+    static constexpr uint32_t V_OFF = K_OFF + ST * TILE;
+    static constexpr uint32_t RECV_OFF = V_OFF + ST * TILE;     // rows of O from the other ranks
+    static constexpr uint32_t RECV = BQ * HD * 4 / MAX_CLUSTER * (MAX_CLUSTER - 1);
+    static constexpr uint32_t ML_OFF = RECV_OFF + RECV;         // their maxima and sums [rank][row][2]
+    static constexpr uint32_t X_OFF = ML_OFF + BQ * 8;          // the halves' exchange [2][half][row]
+    static constexpr uint32_t BAR_OFF = X_OFF + 2 * 2 * BQ * 4;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + 256;
+    static constexpr size_t SMEM = MISC_OFF + 128;
+    static constexpr uint32_t O_COL = NS * BKEY;
+    // kind::f16 instruction descriptors: D fp32 (bit 4), A and B fp16, M = 128
+    // (M >> 4 at bit 24), N >> 3 at bit 17; bit 16 marks B as MN-major
+    static constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(BKEY >> 3) << 17) | ((uint32_t)(BQ >> 4) << 24);
+    static constexpr uint32_t IDESC_O =
+        (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(BQ >> 4) << 24);
+    // barriers, in units of eight bytes
+    static constexpr int B_Q = 0, B_S_FULL = 1, B_P_FULL = B_S_FULL + NS, B_PV_DONE = B_P_FULL + NS,
+                         B_K_FULL = B_PV_DONE + NS, B_K_EMPTY = B_K_FULL + ST, B_V_FULL = B_K_EMPTY + ST,
+                         B_V_EMPTY = B_V_FULL + ST, B_COUNT = B_V_EMPTY + ST;
+    static_assert(8 * B_COUNT <= 256, "barriers");
+    // more than half of an SM's shared memory, and so much that no other kernel with tensor memory fits beside
+    static_assert(SMEM <= 227 * 1024 && SMEM >= 190 * 1024, "one CTA an SM");
+};
+
+// Shared words behind the barriers.
+struct Misc {
+    int abort;
+    uint32_t tmem;
+    int lo_min, lo_max;                       // the rows' first visible cells
+    uint32_t bad[3][4];                       // keys of a tile whose V is not finite, three tiles in turn
+    int last;
+};
+static_assert(sizeof(Misc) <= 128, "shared words");
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+    return is != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// A 16-byte chunk of a row of a box, as TMA's 128-byte swizzle places it.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int chunk) {
+    return tile + (uint32_t)(chunk >> 3) * BOX + (uint32_t)row * 128u + (uint32_t)(((chunk & 7) ^ (row & 7)) << 4);
+}
+// Two weights as hi and lo fp16 pairs: the low 13 mantissa bits are split off exactly.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const float ah = __uint_as_float(__float_as_uint(a) & 0xFFFFE000u), bh = __uint_as_float(__float_as_uint(b) & 0xFFFFE000u);
+    hi = pack_h2(ah, bh);
+    lo = pack_h2(a - ah, b - bh);
+}
+__device__ __forceinline__ bool not_finite(uint32_t h2) {
+    return (h2 & 0x7C00u) == 0x7C00u || (h2 & 0x7C000000u) == 0x7C000000u;
+}
+
+// The tree of a group of rows and what of it lies in the call and the cache.
+struct Tree {
+    int r0, n, seq, base;                     // n: nodes whose rows are written
+    bool ok;
+    __device__ __forceinline__ Tree(const AttnTreeArgs &a, int i) {
+        r0 = a.row0[i];
+        n = a.row0[i + 1] - r0;
+        seq = a.seq[i];
+        base = a.base[i];
+        ok = r0 >= 0 && n >= 0 && n <= a.max_nodes && r0 <= a.T - n && seq >= 0 && seq < a.kv.n_seq && base >= 0 &&
+             base <= a.kv.n_ctx - n;
+        n = min(max(n, 0), a.max_nodes);
+    }
+};
+
+// Which of the keys k0 .. k0 + 63 a row sees: those from lo to base, and by the bits
+// of its mask those from base to end.
+__device__ __forceinline__ unsigned long long visible(int k0, int lo, int base, int end, const uint32_t *mask, int words) {
+    unsigned long long v = 0;
+    const int a0 = max(lo - k0, 0), a1 = min(base - k0, 64);
+    if (a1 > a0) v = (~0ull >> (64 - (a1 - a0))) << a0;
+    const int j0 = k0 - base, nb = min(end - k0, 64);
+    if (j0 > -64 && nb > 0) {
+        const int i0 = j0 >> 5, sh = j0 & 31;
+        auto word = [&](int i) { return i >= 0 && i < words ? __ldcg(mask + i) : 0u; };
+        const uint32_t w0 = word(i0), w1 = word(i0 + 1), w2 = word(i0 + 2);
+        const unsigned long long t = (unsigned long long)__funnelshift_r(w1, w2, sh) << 32 | __funnelshift_r(w0, w1, sh);
+        v |= t & (~0ull >> (64 - nb));
+    }
+    return v;
+}
+
+// Brings a head's E4M3 rows as fp16 tiles, four warps for K or for V: a lane takes 16
+// elements of a row, eight lanes that write at once four pieces of two rows, which the
+// swizzle spreads over all banks.  Rows outside [lo, end) are zero.
+template <int HD>
+__device__ __forceinline__ void widen_tile(const uint8_t *head, int hd, int key0, int lo, int end, uint32_t tile, int ww, int lane) {
+    constexpr int NBX = Cfg<HD>::NBX, N = 4 * NBX;
+    const int piece = lane & 3, r8 = lane >> 2;
+    uint4 x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int key = key0 + ww * 32 + i / NBX * 8 + r8, at = (i % NBX) * 64 + piece * 16;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (key >= lo && key < end && at < hd) x[i] = __ldcg(reinterpret_cast<const uint4 *>(head + (size_t)key * hd + at));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = ww * 32 + i / NBX * 8 + r8, c = (i % NBX) * 8 + piece * 2;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[2 * j] = e4m3x2_to_h2((uint16_t)w[j]);
+            h[2 * j + 1] = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
+        }
+        st_shared(chunk_at(tile, row, c), make_uint4(h[0], h[1], h[2], h[3]));
+        st_shared(chunk_at(tile, row, c + 1), make_uint4(h[4], h[5], h[6], h[7]));
+    }
+}
+
+// grid (splits, (tree, kv head, row tile)); the splits are clusters of `cs` CTAs.
 template <int HD, bool F8>
-__global__ void __launch_bounds__(WARPS * 32) attn_tree_kernel(const AttnTreeArgs a) {
-    __shared__ float qs[WARPS][HD];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(THREADS, 1)
+attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnTreeArgs a,
+                 const int row_tiles, const int cs) {
+    using C = Cfg<HD>;
+    constexpr int NBX = C::NBX, ST = C::ST;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base_sm = smem_u32(smem_raw);
+    Misc &misc = *reinterpret_cast<Misc *>(smem_raw + C::MISC_OFF);
+    float *const xch = reinterpret_cast<float *>(smem_raw + C::X_OFF);
+    float2 *const ml = reinterpret_cast<float2 *>(smem_raw + C::ML_OFF);
+    const uint32_t bar = base_sm + C::BAR_OFF;
+    auto s_full = [&](int b) { return bar + 8u * (C::B_S_FULL + b); };
+    auto p_full = [&](int b) { return bar + 8u * (C::B_P_FULL + b); };        // P_t written
+    auto pv_done = [&](int b) { return bar + 8u * (C::B_PV_DONE + b); };      // O += P_t V_t done
+    auto k_full = [&](int s) { return bar + 8u * (C::B_K_FULL + s); };
+    auto k_empty = [&](int s) { return bar + 8u * (C::B_K_EMPTY + s); };
+    auto v_full = [&](int s) { return bar + 8u * (C::B_V_FULL + s); };
+    auto v_empty = [&](int s) { return bar + 8u * (C::B_V_EMPTY + s); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort = &misc.abort;
+
+    cluster_arrive_relaxed();                            // started: the others may write here once they have waited
+    if (tid == 0) {
+        mbar_init(bar + 8u * C::B_Q, SM_WARPS);
+        for (int b = 0; b < NS; ++b) {
+            mbar_init(s_full(b), 1);
+            mbar_init(p_full(b), SM_WARPS);
+            mbar_init(pv_done(b), 1);
+        }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(k_full(s), F8 ? W_WARPS : 1);
+            mbar_init(k_empty(s), 1);
+            mbar_init(v_full(s), F8 ? W_WARPS : 1);
+            mbar_init(v_empty(s), 1);
+        }
+        misc.abort = 0;
+        misc.lo_min = a.kv.n_ctx;
+        misc.lo_max = 0;
+        for (int i = 0; i < 12; ++i) misc.bad[i / 4][i % 4] = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == S_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(&misc.tmem)), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc.tmem;
     pdl_wait();
     pdl_trigger();
-    const int tree = blockIdx.y, Hkv = a.kv.n_kv_head;
-    const int r0 = a.row0[tree], n = a.row0[tree + 1] - r0, seq = a.seq[tree], base = a.base[tree];
-    const bool ok = r0 >= 0 && n >= 0 && n <= a.max_nodes && r0 <= a.T - n && seq >= 0 && seq < a.kv.n_seq && base >= 0 &&
-                    base <= a.kv.n_ctx - n;
-    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, ERRF_BAD_INDEX);
-    const int item = blockIdx.x * WARPS + warp, node = item / a.H, h = item % a.H, t = r0 + node;
-    if (node >= min(n, a.max_nodes) || t < 0 || t >= a.T) return;
-    f16 *o = a.o + ((size_t)t * a.H + h) * HD;
-    if (!ok) {
-        for (int d = lane; d < HD; d += 32) o[d] = f2h(0.f);
-        return;
+
+    const int hd = a.kv.head_dim, Hkv = a.kv.n_kv_head, G = a.H / Hkv;
+    const int group = blockIdx.y, mt = group % row_tiles, j = group / row_tiles % Hkv;
+    const Tree tr(a, group / row_tiles / Hkv);
+    const int rows = min(max(tr.n * G - mt * BQ, 0), BQ);          // rows of this tile
+    const int base = tr.base, end = tr.base + tr.n;
+    if (!tr.ok && mt == 0 && j == 0 && blockIdx.x == 0 && tid == 0) raise_error(a.err, ERRF_BAD_INDEX);
+    // thread r (and r + 128) of the softmax has row r: query head j G + g of node `node`
+    const int r = tid & (BQ - 1), node = (mt * BQ + r) / G, g = (mt * BQ + r) - node * G;
+    const bool row_ok = r < rows && tr.ok;
+    int lo = 0;
+    if (warp < SM_WARPS && row_ok) {
+        if (a.window > 0) lo = min(max(a.pos[tr.r0 + node] - a.window + 1, 0), base);
+        if (warp < SM_WARPS / 2) {
+            atomicMin(&misc.lo_min, lo);
+            atomicMax(&misc.lo_max, lo);
+        }
     }
-    const float c = 1.4426950408889634f / sqrtf((float)HD);
-    for (int d = lane; d < HD; d += 32) qs[warp][d] = hf(a.q[((size_t)t * a.H + h) * HD + d]) * c;
+    __syncthreads();
+    const int lo_min = misc.lo_min, lo_max = misc.lo_max;
+    // this CTA's tiles of 128 keys
+    const int first = lo_min / BKEY, all = tr.ok && rows > 0 ? (end + BKEY - 1) / BKEY - first : 0;
+    const int S = gridDim.x, split = blockIdx.x;
+    const int kt0 = first + (int)((long long)all * split / S), nt = first + (int)((long long)all * (split + 1) / S) - kt0;
+
+    if (warp < SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(SM_REGS));
+    else if (warp < S_WARP) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(W_REGS));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(I_REGS));
+
+    float m_run = -INFINITY, l_row = 0.f;
+    bool have = false;                                   // O holds this CTA's sums
+    if (nt == 0) {
+        // nothing to do: on to the joining
+    } else if (warp < SM_WARPS) {
+        constexpr int HK = BKEY / 2;
+        const int quarter = warp & 3, hf = warp >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t o_col = C::O_COL + hf * (HD / 2);     // this half's O columns
+        const bool active = quarter * 32 < rows;             // the warp's lanes hold rows
+        // q: this half's chunks of the row (rows past the last are zero)
+        {
+            const f16 *src = a.q + ((size_t)(tr.r0 + node) * a.H + (size_t)j * G + g) * hd;
+            uint4 x[HD / 16];
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+                const int c = hf * (HD / 16) + i;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row_ok && 8 * c < hd) x[i] = __ldcg(reinterpret_cast<const uint4 *>(src) + c);
+            }
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) st_shared(chunk_at(base_sm, r, hf * (HD / 16) + i), x[i]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + 8u * C::B_Q);
+        }
+        const float c = 1.4426950408889634f / sqrtf((float)hd);
+        // the other half's value of the same row; two buffers in turn, so that a half one tile ahead does not overwrite
+        // what the other has not read
+        auto exchange = [&](int turn, float v) {
+            float *x = xch + (turn & 1) * 2 * BQ + r;
+            x[hf * BQ] = v;
+            named_sync(1 + quarter, 64);
+            return x[(hf ^ 1) * BQ];
+        };
+        float l_run = 0.f;
+        // ok stays uniform over each warp, and every softmax thread runs all nt
+        // iterations, so the named barriers (which have no time limit) are always
+        // reached by all their threads; after a timeout the iterations only pass them
+        bool ok = true;
+        int b = 0, round = 0, edges = 0;                     // t % NS, t / NS
+        for (int t = 0; t < nt; ++t, b = b + 1 == NS ? 0 : b + 1, round += b == 0) {
+            const int tile0 = (kt0 + t) * BKEY, key0 = tile0 + hf * HK;
+            const uint32_t s_col = lane_base + b * BKEY + hf * HK;
+            const bool edge = tile0 + BKEY > base || tile0 < lo_max;       // not every row sees the whole tile
+            unsigned long long vis = ~0ull, nan = 0ull;
+            if (edge) {
+                vis = row_ok ? visible(key0, lo, base, end, a.mask + (size_t)(tr.r0 + node) * a.words, a.words) : 0ull;
+                // two threads a key read over its V
+                const int sl = t % ST, key = tid >> 1, part = tid & 1;
+                // the softmax may be ahead of V by more than its ring: the stage's tile before must have landed, or this
+                // wait would take the one before that for its own
+                if (ST <= NS && t >= ST) ok = ok && warp_wait(pv_done((t - ST) % NS), (t - ST) / NS & 1, abort, a.err);
+                ok = ok && warp_wait(v_full(sl), t / ST & 1, abort, a.err);
+                if (ok) {
+                    const bool in = tile0 + key >= lo_min && tile0 + key < end;
+                    const uint32_t tile = base_sm + C::V_OFF + sl * C::TILE;
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < HD / 16; ++i) {
+                        const uint4 x = ld_shared(chunk_at(tile, key, part * (HD / 16) + i));
+                        odd |= not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+                    }
+                    if (!in || odd) {
+#pragma unroll
+                        for (int i = 0; i < HD / 16; ++i) st_shared(chunk_at(tile, key, part * (HD / 16) + i), make_uint4(0u, 0u, 0u, 0u));
+                        if (in) atomicOr(&misc.bad[edges % 3][key >> 5], 1u << (key & 31));
+                    }
+                    fence_proxy_async();
+                }
+                named_sync(5, SM_WARPS * 32);
+                const uint32_t *bad = misc.bad[edges % 3];
+                nan = vis & ((unsigned long long)bad[2 * hf + 1] << 32 | bad[2 * hf]);
+                // the set of the tile before has been read by all, and serves the tile after the next
+                if (tid < 4) misc.bad[(edges + 2) % 3][tid] = 0u;
+                ++edges;
+            }
+            ok = ok && warp_wait(s_full(b), round & 1, abort, a.err);
+            if (!active) {
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(p_full(b));
+                continue;
+            }
+            float s[HK];
+            float mx = -INFINITY;
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < HK / 32; ++q) {
+                    uint32_t v[32];
+                    tmem_ld32(s_col + q * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[q * 32 + i] = __uint_as_float(v[i]);
+                }
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < HK; ++i)
+                        if (!(vis >> i & 1)) s[i] = -INFINITY;
+                    if (nan) {
+#pragma unroll
+                        for (int i = 0; i < HK; ++i)
+                            if (nan >> i & 1) s[i] = __uint_as_float(0x7FFFFFFFu);
+                    }
+                }
+                float m8[8];                                 // half-row maximum as a tree of 8 chains
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m8[i] = s[i];
+#pragma unroll
+                for (int i = 8; i < HK; ++i) m8[i & 7] = fmaxf(m8[i & 7], s[i]);
+                mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            }
+            mx = fmaxf(mx, exchange(t, mx));
+            if (!ok) continue;
+            float factor = 1.f;
+            const bool raise = mx != -INFINITY && (m_run == -INFINITY || (mx - m_run) * c > RESCALE_LOG2);
+            if (raise) {
+                factor = m_run == -INFINITY ? 0.f : ex2((m_run - mx) * c);
+                m_run = mx;
+            }
+            const float m0 = m_run == -INFINITY ? 0.f : m_run;
+            // a raised maximum rescales O, which P_{t-1} V_{t-1} must have finished
+            if (t >= 1 && __any_sync(0xffffffffu, raise)) {
+                ok = warp_wait(pv_done(b == 0 ? NS - 1 : b - 1), (b == 0 ? round - 1 : round) & 1, abort, a.err);
+                if (!ok) continue;
+                tc_fence_after();
+#pragma unroll 1
+                for (int q = 0; q < HD / 64; ++q) {
+                    uint32_t v[32];
+                    tmem_ld32(lane_base + o_col + q * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * factor);
+                    tmem_st32(lane_base + o_col + q * 32, v);
+                }
+            }
+            // the weights of 32 keys over the columns of S they came from: 16 of hi pairs, 16 of lo pairs
+            float rs8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rs8[i] = 0.f;
+#pragma unroll
+            for (int q = 0; q < HK / 32; ++q) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = ex2(fmaf(s[32 * q + 2 * i] - m0, c, LIFT)), p1 = ex2(fmaf(s[32 * q + 2 * i + 1] - m0, c, LIFT));
+                    rs8[(2 * i) & 7] += p0;
+                    rs8[(2 * i + 1) & 7] += p1;
+                    split_pair(p0, p1, p[i], p[16 + i]);
+                }
+                tmem_st32(s_col + 32 * q, p);
+            }
+            l_run = l_run * factor + (((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(b));
+        }
+        if (active) l_row = l_run + exchange(nt, l_run);
+        have = ok && warp_wait(pv_done((nt - 1) % NS), (nt - 1) / NS & 1, abort, a.err);
+        tc_fence_after();
+    } else if (warp < S_WARP) {
+        // ---- K and V tiles
+        const bool k = warp < V_WARP;
+        const int ww = warp - (k ? K_WARP : V_WARP);
+        const uint32_t ring = base_sm + (k ? C::K_OFF : C::V_OFF);
+        const uint32_t full = bar + 8u * (k ? C::B_K_FULL : C::B_V_FULL), empty = bar + 8u * (k ? C::B_K_EMPTY : C::B_V_EMPTY);
+        if constexpr (F8) {
+            const uint8_t *head = (k ? a.kv.k8 : a.kv.v8) + (size_t)tr.seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * hd;
+            for (int t = 0; t < nt; ++t) {
+                const int sl = t % ST, use = t / ST;
+                if (use > 0 && !warp_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
+                widen_tile<HD>(head, hd, (kt0 + t) * BKEY, lo_min, end, ring + sl * C::TILE, ww, lane);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + 8u * sl);
+            }
+        } else if (ww == 0 && lane == 0) {
+            const int row = (int)(a.map_row0 + (long long)tr.seq * (a.kv.seq_stride / hd) + (long long)j * a.kv.n_ctx);
+            int t = 0;
+            for (; t < nt; ++t) {
+                const int sl = t % ST, use = t / ST;
+                if (use > 0 && !mbar_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
+                mbar_expect_tx(full + 8u * sl, C::TILE);
+                for (int i = 0; i < NBX; ++i)
+                    tma_load_2d(ring + sl * C::TILE + i * BOX, k ? &tmK : &tmV, full + 8u * sl, i * 64, row + (kt0 + t) * BKEY);
+            }
+            // after a timeout: wait (bounded) for the copies in flight before the memory is released
+            for (int u = max(t - ST, 0); u < t && *abort; ++u)
+                for (uint32_t i = 0; i < WAIT_LIMIT && !mbar_try_wait(full + 8u * (u % ST), u / ST & 1); ++i) {
+                }
+        }
+    } else if (warp == S_WARP) {
+        // ---- S_t = q K_t^T into buffer t % NS, once the P that took the place of the S before has been read.  The whole
+        // warp walks the loop, so that addresses and descriptors stay uniform; the elected lane issues.
+        const bool leader = elect_one();
+        bool ok = warp_wait(bar + 8u * C::B_Q, 0, abort, a.err);
+        const uint64_t q_desc = sdesc(base_sm), k_desc = sdesc(base_sm + C::K_OFF);
+        for (int t = 0; ok && t < nt; ++t) {
+            const int b = t % NS, sl = t % ST;
+            if (t >= NS && !warp_wait(pv_done(b), (t / NS - 1) & 1, abort, a.err)) break;
+            if (!warp_wait(k_full(sl), t / ST & 1, abort, a.err)) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+                for (int f = 0; f < NBX; ++f) {
+                    const uint64_t qd = q_desc + (uint32_t)f * (BOX >> 4), kd = k_desc + (uint32_t)sl * (C::TILE >> 4) + (uint32_t)f * (BOX >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma1(tmem + b * BKEY, qd + 2 * kk, kd + 2 * kk, C::IDESC_S, (f | kk) != 0);
+                }
+                commit1(k_empty(sl));
+                commit1(s_full(b));
+            }
+            __syncwarp();
+        }
+    } else if (warp == PV_WARP) {
+        // ---- O (+)= P_t V_t once the softmax has written P_t (and rescaled O)
+        const bool leader = elect_one();
+        const uint32_t o_acc = tmem + C::O_COL;
+        const uint64_t v_desc = sdesc_mn(base_sm + C::V_OFF, BOX);
+        for (int t = 0; t < nt; ++t) {
+            const int b = t % NS, sl = t % ST;
+            if (!warp_wait(p_full(b), t / NS & 1, abort, a.err)) break;
+            if (!warp_wait(v_full(sl), t / ST & 1, abort, a.err)) break;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t vd = v_desc + (uint32_t)sl * (C::TILE >> 4);
+#pragma unroll
+                for (int kk = 0; kk < BKEY / 16; ++kk) {
+                    // 16 keys: 8 columns of P's hi pairs, 16 on their lo pairs, among the 32 of their 32 keys
+                    const uint32_t p = tmem + b * BKEY + kk / 2 * 32 + kk % 2 * 8;
+                    mma1_ts(o_acc, p, vd + kk * (2048 >> 4), C::IDESC_O, (t | kk) != 0);
+                    mma1_ts(o_acc, p + 16, vd + kk * (2048 >> 4), C::IDESC_O, 1);
+                }
+                commit1(v_empty(sl));
+                commit1(pv_done(b));
+            }
+            __syncwarp();
+        }
+    }
+
+    // Back to the registers of the launch, for what follows is every warp's.  The others take theirs only after the
+    // softmax has taken and returned its own: before, theirs could be the ones that it waits for.
     __syncwarp();
-    const size_t row = (size_t)seq * a.kv.seq_stride + (size_t)(h / (a.H / Hkv)) * a.kv.n_ctx * HD;
-    auto value = [&](const f16 *p, const uint8_t *p8, size_t e) {
-        return F8 ? h2lo(e4m3x2_to_h2(p8[e])) : hf(p[e]);
+    if (warp < SM_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L_REGS));
+    __syncthreads();
+    if (warp >= SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L_REGS));
+
+    // ---- joining.  Row r belongs to rank r / share; what it is sent lies in its shared memory, its own part over
+    // its K tiles, which all products have read.
+    const int rank = cs > 1 ? (int)cluster_rank() : 0, share = max((rows + cs - 1) / cs, 1);
+    cluster_wait();                                      // the others have started
+    auto part_at = [&](int of, int to) {                 // where rank `to` has the rows of rank `of`
+        return of == to ? C::K_OFF : C::RECV_OFF + (uint32_t)((of < to ? of : of - 1) * share) * (HD * 4);
     };
-    const int lo = a.window > 0 ? max(0, min(a.pos[t] - a.window + 1, base)) : 0;
-    float m = -INFINITY, l = 0.f, acc[HD / 32] = {0.f};
-    for (int k0 = lo; k0 < base + n; k0 += 32) {
-        const int k = k0 + lane, j = k - base;
-        const bool seen = k < base + n && (j < 0 || (a.mask[(size_t)t * a.words + j / 32] >> (j & 31) & 1u));
-        float s = -INFINITY;
-        if (seen) {
-            s = 0.f;
-            for (int d = 0; d < HD; ++d) s = fmaf(qs[warp][d], value(a.kv.k, a.kv.k8, row + (size_t)k * HD + d), s);
-        }
-        const float mn = fmaxf(m, warp_max(s)), f = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float p = seen ? exp2f(s - mn) : 0.f;
-        l = l * f + warp_sum(p);
-        m = mn;
-        for (int i = 0; i < HD / 32; ++i) acc[i] *= f;
-        for (int q = 0; q < 32; ++q) {
-            const float pq = __shfl_sync(0xffffffffu, p, q);
-            if (!__shfl_sync(0xffffffffu, (int)seen, q)) continue;
-            for (int i = 0; i < HD / 32; ++i)
-                acc[i] = fmaf(pq, value(a.kv.v, a.kv.v8, row + (size_t)(k0 + q) * HD + lane + 32 * i), acc[i]);
+    if (warp < SM_WARPS && r < rows) {
+        const int hf = warp >> 2, to = r / share, at = r - to * share;
+        if (hf == 0) {
+            const uint32_t dst = dsmem(ml + rank * share + at, to);
+            dsmem_st_u64(dst, (unsigned long long)__float_as_uint(l_row) << 32 | __float_as_uint(m_run));
         }
     }
-    for (int i = 0; i < HD / 32; ++i) o[lane + 32 * i] = f2h(l == 0.f ? 0.f : acc[i] / l);
+    if (warp < SM_WARPS && (warp & 3) * 32 < rows && have) {       // whole warps: the loads from tensor memory are the warp's
+        const int hf = warp >> 2, to = min(r / share, cs - 1), at = r - to * share;
+        const uint32_t dst = dsmem(smem_raw + part_at(rank, to), to) + (uint32_t)at * (HD * 4);
+#pragma unroll 1
+        for (int q = 0; q < HD / 64; ++q) {
+            uint32_t v[32];
+            tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::O_COL + hf * (HD / 2) + q * 32, v);
+            if (r < rows && hf * (HD / 2) < hd) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int chunk = hf * (HD / 8) + q * 8 + i;
+                    dsmem_st_f32x4(dst + (uint32_t)((chunk ^ (at & 7)) << 4),
+                                   make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                               __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp == S_WARP) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+
+    const int my_rows = min(share, rows - rank * share), per = hd / 4, clusters = S / cs, mine = split / cs;
+    const float c = 1.4426950408889634f / sqrtf((float)hd);
+    unsigned *const counters = reinterpret_cast<unsigned *>(a.scratch);
+    float *const slots = reinterpret_cast<float *>(counters + COUNTERS);
+    auto slot_o = [&](int ci, int row) { return slots + ((size_t)(group * clusters + ci) * BQ + row) * (HD + 4); };
+    auto store = [&](int row, int chunk, const float4 &v) {
+        const int at = mt * BQ + row, nd = at / G, t = tr.r0 + nd;
+        if (t >= 0 && t < a.T)
+            *reinterpret_cast<uint2 *>(a.o + ((size_t)t * a.H + (size_t)j * G + (at - nd * G)) * hd + 4 * chunk) =
+                make_uint2(pack_h2(v.x, v.y), pack_h2(v.z, v.w));
+    };
+    for (int i = tid; i < my_rows * per; i += THREADS) {
+        const int at = i / per, chunk = i - at * per;
+        float M = -INFINITY, L = 0.f;
+        for (int s = 0; s < cs; ++s) M = fmaxf(M, ml[s * share + at].x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < cs; ++s) {
+            const float2 v = ml[s * share + at];
+            if (v.y == 0.f) continue;                    // that rank saw nothing of the row
+            const float f = ex2((v.x - M) * c);
+            const float4 x = *reinterpret_cast<const float4 *>(smem_raw + part_at(s, rank) + (uint32_t)at * (HD * 4) + ((chunk ^ (at & 7)) << 4));
+            L = fmaf(f, v.y, L);
+            o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
+        }
+        const int row = rank * share + at;
+        if (clusters == 1) {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            store(row, chunk, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        } else {
+            float *dst = slot_o(mine, row);
+            __stcg(reinterpret_cast<float4 *>(dst) + chunk, o);
+            if (chunk == 0) __stcg(reinterpret_cast<float2 *>(dst + HD), make_float2(M, L));
+        }
+    }
+    if (clusters == 1) return;
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        unsigned *cnt = counters + group * cs + rank;
+        const bool last = atomicAdd(cnt, 1u) == (unsigned)clusters - 1;
+        if (last) *cnt = 0u;                             // ready for the next call
+        __threadfence();
+        misc.last = last;
+    }
+    __syncthreads();
+    if (!misc.last) return;
+    for (int i = tid; i < my_rows * per; i += THREADS) {
+        const int at = i / per, chunk = i - at * per, row = rank * share + at;
+        float M = -INFINITY, L = 0.f;
+        for (int s = 0; s < clusters; ++s) M = fmaxf(M, __ldcg(slot_o(s, row) + HD));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < clusters; ++s) {
+            const float *src = slot_o(s, row);
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + HD));
+            if (v.y == 0.f) continue;
+            const float f = ex2((v.x - M) * c);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(src) + chunk);
+            L = fmaf(f, v.y, L);
+            o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        store(row, chunk, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+}
+
+// Clusters of 2, 4 and 8 CTAs that a device holds at once.
+constexpr int MAX_DEV = 64;
+int max_clusters[MAX_DEV][MAX_CLUSTER + 1];
+
+// CTAs of a cluster and clusters of a group: the split that keeps most SMs busy, of
+// equals the one with the larger clusters (a join in shared memory costs less than
+// one through memory); every split has a tile where the cache is full.
+struct Plan { int cs, clusters; };
+Plan plan(int groups, int n_ctx) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEV) dev = 0;
+    const int tiles = (n_ctx + BKEY - 1) / BKEY;
+    Plan best{1, 1};
+    for (int cs = MAX_CLUSTER; cs >= 2; cs /= 2) {
+        if (groups > max_clusters[dev][cs] || cs > tiles) continue;
+        int k = max_clusters[dev][cs] / groups;
+        if (k > tiles / cs) k = tiles / cs;
+        if (k > SLOTS / groups) k = SLOTS / groups;
+        if (k < 1) k = 1;
+        if (cs * k > best.cs * best.clusters) best = Plan{cs, k};
+    }
+    return best;
 }
 
 }  // namespace
 
-size_t attn_tree_scratch_bytes(int, int, int, int, int, int) { return 16; }
+size_t attn_tree_scratch_bytes(int, int, int, int, int hd, int) {
+    return COUNTERS * sizeof(unsigned) + (size_t)SLOTS * BQ * ((hd == 128 ? 128 : 64) + 4) * sizeof(float);
+}
 
-cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap *, const TmaMap *, const Launch &l) {
-    const dim3 grid((a.max_nodes * a.H + WARPS - 1) / WARPS, a.n_tree), block(WARPS * 32);
+cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap *mK, const TmaMap *mV, const Launch &l) {
+    const int hd = a.kv.head_dim, Hkv = a.kv.n_kv_head;
+    if (Hkv < 1 || a.H % Hkv || (!a.kv.k8 && (!mK || !mV))) return cudaErrorInvalidValue;
+    const int row_tiles = (a.max_nodes * (a.H / Hkv) + BQ - 1) / BQ, groups = a.n_tree * Hkv * row_tiles;
+    if (groups > 65535) return cudaErrorInvalidValue;
+    const Plan p = plan(groups, a.kv.n_ctx);
+    static const CUtensorMap none = {};
+    const CUtensorMap &k = mK ? *reinterpret_cast<const CUtensorMap *>(mK) : none, &v = mV ? *reinterpret_cast<const CUtensorMap *>(mV) : none;
+    const dim3 grid(p.cs * p.clusters, groups), block(THREADS);
     const bool f8 = a.kv.k8;
-    switch (a.kv.head_dim) {
-        case 32: return launch_kernel(f8 ? attn_tree_kernel<32, true> : attn_tree_kernel<32, false>, grid, block, 0, l, a);
-        case 64: return launch_kernel(f8 ? attn_tree_kernel<64, true> : attn_tree_kernel<64, false>, grid, block, 0, l, a);
-        case 128: return launch_kernel(f8 ? attn_tree_kernel<128, true> : attn_tree_kernel<128, false>, grid, block, 0, l, a);
-    }
+    if (hd == 128)
+        return launch_cluster_kernel(f8 ? attn_tree_kernel<128, true> : attn_tree_kernel<128, false>, grid, block, p.cs,
+                                     Cfg<128>::SMEM, l, k, v, a, row_tiles, p.cs);
+    if (hd == 64 || hd == 32)
+        return launch_cluster_kernel(f8 ? attn_tree_kernel<64, true> : attn_tree_kernel<64, false>, grid, block, p.cs,
+                                     Cfg<64>::SMEM, l, k, v, a, row_tiles, p.cs);
     return cudaErrorInvalidValue;
+}
+
+cudaError_t init_attn_tree_attributes() {
+    cudaError_t e = allow_smem(attn_tree_kernel<128, false>, Cfg<128>::SMEM);
+    if (!e) e = allow_smem(attn_tree_kernel<128, true>, Cfg<128>::SMEM);
+    if (!e) e = allow_smem(attn_tree_kernel<64, false>, Cfg<64>::SMEM);
+    if (!e) e = allow_smem(attn_tree_kernel<64, true>, Cfg<64>::SMEM);
+    int dev = 0;
+    if (!e) e = cudaGetDevice(&dev);
+    if (e || dev < 0 || dev >= MAX_DEV) return e;
+    for (int cs = 2; cs <= MAX_CLUSTER; cs *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(cs);
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = Cfg<128>::SMEM;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = cs;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, attn_tree_kernel<128, false>, &cfg))) return e;
+        max_clusters[dev][cs] = n;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace llm

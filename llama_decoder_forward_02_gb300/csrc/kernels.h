@@ -209,6 +209,9 @@ struct GemmArgs {
 // operand [rows][cols], boxes of box_rows x 64 with 128-byte swizzle.
 struct alignas(64) TmaMap { uint64_t opaque[16]; };
 bool make_operand_map(TmaMap *m, const f16 *ptr, int rows, int cols, int box_rows);
+// An fp16 cache [rows][head_dim] in boxes of 128 rows x 64; of head_dim 32 the
+// other half of a box reads zeros.
+bool make_cache_map(TmaMap *m, const f16 *ptr, long long rows, int head_dim);
 // The tcgen05/TMEM GEMM on CTA pairs (cta_group::2): 256 x bn tiles, bn in
 // {128, 192, 256}; mA boxes 128 x 64 over A [>=M][K], mB boxes of bn / 2 x 64
 // over W [N][K].

@@ -34,6 +34,7 @@ cudaError_t init_gemv_stream_attributes();
 cudaError_t init_gemv_q4_attributes();
 cudaError_t init_attn_q4_attributes();
 cudaError_t init_attn_prefill_q4_attributes();
+cudaError_t init_attn_tree_attributes();
 
 // Kernel attributes (dynamic shared-memory limits, carveouts) take effect on
 // the device that is current when they are set, so they are set once per
@@ -59,6 +60,7 @@ cudaError_t init_kernel_attributes() {
         if (!e) e = init_gemv_q4_attributes();
         if (!e) e = init_attn_q4_attributes();
         if (!e) e = init_attn_prefill_q4_attributes();
+        if (!e) e = init_attn_tree_attributes();
         status[dev] = e;
         done[dev] = true;
     }

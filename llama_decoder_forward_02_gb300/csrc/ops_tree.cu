@@ -133,7 +133,14 @@ extern "C" int32_t llm_op_attn_tree(const void *q, const void *k_cache, const vo
     a.row0 = row0; a.seq = seq; a.base = base; a.mask = mask; a.pos = pos; a.o = (f16 *)o;
     a.T = T; a.n_tree = n_tree; a.max_nodes = max_nodes; a.words = (max_nodes + 31) / 32; a.H = H; a.window = window;
     a.scratch = scratch; a.err = err;
-    return launched(who, launch_attn_tree(a, nullptr, nullptr, overlapped(stream)));
+    TmaMap mk, mv;
+    const bool f16_cache = kv_type == LLM_KV_F16;
+    const long long rows = (long long)n_seq * Hkv * n_ctx;
+    if (f16_cache && (!make_cache_map(&mk, a.kv.k, rows, hd) || !make_cache_map(&mv, a.kv.v, rows, hd))) {
+        set_global_error("llm_op_attn_tree: TMA descriptor creation failed");
+        return LLM_ERR_COMPUTE;
+    }
+    return launched(who, launch_attn_tree(a, f16_cache ? &mk : nullptr, f16_cache ? &mv : nullptr, overlapped(stream)));
 }
 
 extern "C" int32_t llm_op_tree_accept(const int32_t *token, const int32_t *parent, const int32_t *target,

@@ -302,6 +302,16 @@ def test_long_context(lib, hd, kt):
     t.check(norm=False)
 
 
+@pytest.mark.parametrize("hd,H,kt", [(128, 16, 0), (64, 16, 0), (32, 16, 0), (128, 8, 1), (64, 32, 1)])
+@pytest.mark.parametrize("n", [3, 10, 24])
+def test_many_tiles_a_split(lib, hd, H, kt, n):
+    """Groups enough that a split has several tiles, with few rows and with many."""
+    trees = [(1900 - 77 * i, 1 + (i * 5) % 23) for i in range(n)]
+    t = Trees(lib, hd, H, 8, trees, 2000, kt, seed=n, spare=2)
+    t.run()
+    t.check()
+
+
 def test_many_trees(lib):
     """More groups than the GPU holds at once, some trees without nodes."""
     trees = [(37 * i % 400, i % 7) for i in range(90)]
