@@ -131,6 +131,35 @@ int32_t llm_model_quantize(llm_model *m, int32_t wtype, void *stream);
  * LLM_ERR_COMPUTE as llm_model_create.  Runs on `stream` and synchronizes it. */
 int32_t llm_model_set_qk_norm(llm_model *m, const void *const *q_norm, const void *const *k_norm, void *stream);
 
+/* Give the model another rotation than whole heads in adjacent pairs with
+ * unscaled frequencies of hparams.rope_theta: the first rope->n_rot elements of
+ * each query and key head turn (the others stay), LLM_ROPE_PAIRS elements 2 i and
+ * 2 i + 1 or LLM_ROPE_HALVES elements i and i + n_rot / 2, with the frequencies
+ * and the factor of cos and sin that llm_op_rope_table gives for `rope` (theta is
+ * rope's, hparams' is not used).  Every call of its contexts then rotates so,
+ * llm_seq_shift included.  Call it once, before llm_model_quantize,
+ * llm_model_set_qk_norm and any context.  Halves: the rows of Wq and Wk (later
+ * the norms' gains) are brought into the order in which they turn as pairs, so that
+ * K caches hold their elements in that order.  LLM_ERR_INVALID (nothing changed)
+ * for a NULL model, a rotation that llm_op_rope_table refuses or with n_rot above
+ * head_dim, a second call or a call too late; LLM_ERR_COMPUTE if a launch fails,
+ * after which the model's weights are undefined and it should be freed.  Runs on
+ * `stream` and synchronizes it. */
+#define LLM_ROPE_PAIRS 0
+#define LLM_ROPE_HALVES 1
+#define LLM_ROPE_NONE 0
+#define LLM_ROPE_LINEAR 1
+#define LLM_ROPE_BANDS 2
+#define LLM_ROPE_RAMP 3
+typedef struct {
+    float theta;
+    int32_t n_rot, layout, scaling;
+    float factor, slow, fast;
+    int32_t n_ctx_orig;
+    float attn_factor;
+} llm_rope;
+int32_t llm_model_set_rope(llm_model *m, const llm_rope *rope, void *stream);
+
 /* Create a context ("llama_new_context"): an fp16 KV cache of n_ctx positions
  * for each of n_seq_max sequences and every layer, laid out
  * [seq][layer][kv_head][pos][head_dim] for K and for V; activation
@@ -187,6 +216,43 @@ typedef struct {
  * the stream reaches that point (llm_synchronize, or any later call that
  * reads them to the host). */
 int32_t llm_decode(llm_ctx *c, const llm_batch *b);
+
+/* A step over trees of drafted tokens.  Tree i has n_nodes[i] nodes (1..256), in
+ * batch order: token[] their tokens, parent[] the node of the same tree each was
+ * drafted after, -1 for node 0 (the last token picked for the sequence) and a
+ * lower node for the others.  All arrays are HOST memory, token and parent
+ * with one entry a node of all trees.  Tree i belongs to sequence seq_id[i] (NULL:
+ * sequence i), no two to the same.
+ * llm_decode_tree runs all nodes through the model in one ubatch: a node sees its
+ * sequence's cached positions, its ancestors and itself, and its position is
+ * seq_pos_max + 1 plus its depth.  The nodes' K and V stand behind the cached
+ * positions; seq_pos_max does not change.  Every node's logits are kept in batch
+ * order (llm_get_logits_ith(i), llm_get_argmax, llm_sample).
+ * llm_tree_accept then takes target[] (HOST), the token picked after each node
+ * (llm_get_argmax's or llm_sample's output): node 0 stands, after a node that
+ * stands its child whose token is the node's target, the lowest of several.  The
+ * keys and values of the nodes that stand are moved behind the cached positions
+ * and the sequence continues after them: it holds the same as if their tokens
+ * had been decoded one by one.  HOST outputs, each may be NULL: path[] one entry a
+ * node in batch order, for tree i the nodes that stand from its first entry on,
+ * then -1; n_accept[i] their number; next[i] the target of the last, node 0 of the
+ * sequence's next tree.  Any call in between that changes a cache (llm_decode,
+ * llm_generate, llm_seq_clear, llm_seq_shift) drops the tree; the logits stay
+ * until the next call that makes some, but llm_generate does not start from
+ * those of a tree.  Asynchronous like llm_decode.  Return codes as llm_decode:
+ * LLM_NO_KV_ROOM (nothing written) if a tree's nodes would pass n_ctx;
+ * LLM_ERR_INVALID for an invalid batch, more nodes than n_ubatch, a Q4_0 cache, or
+ * llm_tree_accept without a tree that waits.  The first llm_decode_tree of a
+ * context allocates its workspace (LLM_ERR_ALLOC if that fails). */
+typedef struct {
+    int32_t n_trees;
+    const int32_t *n_nodes;
+    const int32_t *seq_id;
+    const int32_t *token;
+    const int32_t *parent;
+} llm_tree_batch;
+int32_t llm_decode_tree(llm_ctx *c, const llm_tree_batch *b);
+int32_t llm_tree_accept(llm_ctx *c, const int32_t *target, int32_t *path, int32_t *n_accept, int32_t *next);
 
 /* DEVICE pointer to the logits of the last llm_decode / llm_generate:
  * fp32 [n_outputs][n_vocab], rows in batch order.  Owned by the context and
@@ -274,6 +340,12 @@ int32_t llm_seq_shift(llm_ctx *c, int32_t seq_id, int32_t p0, int32_t n_discard)
 int32_t llm_batch_check(int32_t n_vocab, int32_t n_ctx, int32_t n_seq_max, int32_t n_ubatch,
                         const int32_t *seq_pos_max, const llm_batch *b, int32_t *pos_out,
                         int32_t *out_index, int32_t *ubatch_starts, int32_t *n_ubatches);
+
+/* Host-only check of a batch of trees, as llm_batch_check: fills, when not NULL, the
+ * HOST arrays pos_out and cell_out (one entry a node) and returns the code
+ * llm_decode_tree would, as far as the batch and the cache's fill decide it. */
+int32_t llm_tree_check(int32_t n_vocab, int32_t n_ctx, int32_t n_seq_max, int32_t n_ubatch, const int32_t *seq_pos_max,
+                       const llm_tree_batch *b, int32_t *pos_out, int32_t *cell_out);
 
 /* Wait for the context's stream; return LLM_ERR_COMPUTE if a CUDA error
  * occurred or a kernel raised the error flag (the flag is then cleared),
@@ -388,7 +460,7 @@ int64_t llm_kernel_launches(const llm_ctx *c);
  * LLM_KERNEL_CLASSES-1), the summed duration in milliseconds, the launch count
  * and a static name ("gemv_gateup_swiglu", "attn_decode", ...); it returns
  * LLM_ERR_INVALID past the last class. */
-#define LLM_KERNEL_CLASSES 17
+#define LLM_KERNEL_CLASSES 19
 int32_t llm_kernel_timing(llm_ctx *c, int32_t enable);
 int32_t llm_kernel_time(llm_ctx *c, int32_t kernel, double *total_ms, int64_t *count, const char **name);
 
@@ -668,19 +740,6 @@ int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void 
  * 8 in [8, 128], theta > 1, factor >= 1 (where scaled), 0 < slow < fast and
  * n_ctx_orig >= 1 (bands and ramp), attn_factor >= 0, 0 <= pos0, n_pos >= 1, pos0 +
  * n_pos <= 2^30 and out is 16-byte aligned.  `layout` is checked, and not used. */
-#define LLM_ROPE_PAIRS 0
-#define LLM_ROPE_HALVES 1
-#define LLM_ROPE_NONE 0
-#define LLM_ROPE_LINEAR 1
-#define LLM_ROPE_BANDS 2
-#define LLM_ROPE_RAMP 3
-typedef struct {
-    float theta;
-    int32_t n_rot, layout, scaling;
-    float factor, slow, fast;
-    int32_t n_ctx_orig;
-    float attn_factor;
-} llm_rope;
 int32_t llm_op_rope_table(const llm_rope *rope, int32_t pos0, int32_t n_pos, float *out, void *stream);
 
 /* llm_op_qk_norm_rope with the rotation in every layout, and cells that need not

@@ -61,6 +61,10 @@ class llm_rope(ctypes.Structure):
                 ("slow", c_f32), ("fast", c_f32), ("n_ctx_orig", c_i32), ("attn_factor", c_f32)]
 
 
+class llm_tree_batch(ctypes.Structure):
+    _fields_ = [("n_trees", c_i32), ("n_nodes", c_i32p), ("seq_id", c_i32p), ("token", c_i32p), ("parent", c_i32p)]
+
+
 def _proto(name, res, *args):
     f = getattr(_lib, name)
     f.restype = res
@@ -74,10 +78,15 @@ llm_model_create = _proto("llm_model_create", c_i32, ctypes.POINTER(llm_hparams)
 llm_model_free = _proto("llm_model_free", None, c_vp)
 llm_model_quantize = _proto("llm_model_quantize", c_i32, c_vp, c_i32, c_vp)
 llm_model_set_qk_norm = _proto("llm_model_set_qk_norm", c_i32, c_vp, ctypes.POINTER(c_vp), ctypes.POINTER(c_vp), c_vp)
+llm_model_set_rope = _proto("llm_model_set_rope", c_i32, c_vp, ctypes.POINTER(llm_rope), c_vp)
 llm_kv_alloc = _proto("llm_kv_alloc", c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, ctypes.POINTER(c_vp))
 llm_kv_alloc_typed = _proto("llm_kv_alloc_typed", c_i32, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, ctypes.POINTER(c_vp))
 llm_kv_free = _proto("llm_kv_free", None, c_vp)
 llm_decode = _proto("llm_decode", c_i32, c_vp, ctypes.POINTER(llm_batch))
+llm_decode_tree = _proto("llm_decode_tree", c_i32, c_vp, ctypes.POINTER(llm_tree_batch))
+llm_tree_accept = _proto("llm_tree_accept", c_i32, c_vp, c_i32p, c_i32p, c_i32p, c_i32p)
+llm_tree_check = _proto("llm_tree_check", c_i32, c_i32, c_i32, c_i32, c_i32, c_i32p, ctypes.POINTER(llm_tree_batch), c_i32p,
+                        c_i32p)
 llm_get_logits = _proto("llm_get_logits", c_vp, c_vp, c_i32p)
 llm_get_logits_ith = _proto("llm_get_logits_ith", c_vp, c_vp, c_i32)
 llm_get_argmax = _proto("llm_get_argmax", c_i32, c_vp, c_i32p, c_i32)
@@ -209,6 +218,14 @@ def batch(tokens=None, pos=None, seq_id=None, output=None, n_tokens=None, token_
     return llm_batch(n, tok_p, pos_p, seq_p, out_p, flags), keep
 
 
+def tree_batch(n_nodes, token, parent, seq_id=None):
+    """llm_tree_batch from host sequences.  Returns the struct and the arrays it references (keep both alive)."""
+    if len(token) != sum(n_nodes) or len(parent) != sum(n_nodes) or (seq_id is not None and len(seq_id) != len(n_nodes)):
+        raise ValueError("one token and one parent a node, one seq_id a tree")
+    ptrs, keep = zip(*(_arr(ctypes.c_int32, v) for v in (n_nodes, seq_id, token, parent)))
+    return llm_tree_batch(len(n_nodes), *ptrs), keep
+
+
 class _DeviceArray:
     """A raw device pointer exposed through __cuda_array_interface__."""
 
@@ -257,6 +274,10 @@ class Model:
                 raise ValueError("one gain tensor a layer")
         check(llm_model_set_qk_norm(self.handle, ptrs(q_norm), ptrs(k_norm), c_vp(stream)))
 
+    def set_rope(self, r: llm_rope, stream=0):
+        """llm_model_set_rope."""
+        check(llm_model_set_rope(self.handle, ctypes.byref(r), c_vp(stream)))
+
     def free(self):
         if self.handle:
             llm_model_free(self.handle)
@@ -277,6 +298,28 @@ class Context:
         b, keep = batch(tokens, pos, seq_id, output, n_tokens=n_tokens, token_dev_ptr=token_dev_ptr)
         rc = llm_decode(self.handle, ctypes.byref(b))
         return check(rc, self.handle)
+
+    def decode_tree(self, n_nodes, token, parent, seq_id=None):
+        """llm_decode_tree of trees with n_nodes[i] nodes each, tokens and parents in batch order."""
+        b, keep = tree_batch(n_nodes, token, parent, seq_id)
+        rc = check(llm_decode_tree(self.handle, ctypes.byref(b)), self.handle)
+        if rc == LLM_OK:
+            self.tree_nodes = list(n_nodes)
+        return rc
+
+    def tree_accept(self, target):
+        """llm_tree_accept: for each tree the nodes that stand and the next token."""
+        nodes = getattr(self, "tree_nodes", [])
+        if len(target) != sum(nodes):
+            raise ValueError("one target a node of the last decode_tree")
+        t = (c_i32 * max(len(target), 1))(*[int(v) for v in target])
+        path, count, nxt = ((c_i32 * max(n, 1))() for n in (len(target), len(nodes), len(nodes)))
+        check(llm_tree_accept(self.handle, t, path, count, nxt), self.handle)
+        out, r = [], 0
+        for n, a, x in zip(nodes, count, nxt):
+            out.append((list(path[r:r + a]), x))
+            r += n
+        return out
 
     def logits_ptr(self):
         n = ctypes.c_int32(0)

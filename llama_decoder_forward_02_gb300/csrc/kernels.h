@@ -286,6 +286,11 @@ cudaError_t launch_widen_bf16(const bf16 *src, float *dst, int n, cudaStream_t s
 // beyond the fp16 range raise ERRF_BAD_INDEX in *err.
 cudaError_t launch_convert_rows(const bf16 *src, int src_ld, f16 *dst, int dst_ld, int rows, int cols,
                                 uint32_t *err, cudaStream_t st);
+// Rows of heads [heads][hd][cols] whose first n_rot elements turn as halves,
+// brought in place into the order in which they turn as adjacent pairs: rows
+// 2 i and 2 i + 1 become what rows i and i + n_rot / 2 were.
+cudaError_t launch_pair_rows(f16 *rows, int heads, int hd, int n_rot, int cols, cudaStream_t st);
+cudaError_t launch_pair_rows(float *rows, int heads, int hd, int n_rot, int cols, cudaStream_t st);
 cudaError_t launch_repack_gate_up(const bf16 *gate, const bf16 *up, int F, int F_pad, int d, f16 *dst,
                                   uint32_t *err, cudaStream_t st);
 // Copy the hidden state rows into the diagnostic buffer.
@@ -393,8 +398,9 @@ struct RopeSpec {
 };
 // Radians a position of the n_rot / 2 pairs, and the factor of cos and sin.
 void rope_frequencies(const RopeSpec &r, double *f, double *scale);
-// out[i][j] = factor * (cos, sin)((pos0 + i) * frequency j), i < n_pos.
-cudaError_t launch_rope_table(const RopeSpec &r, int pos0, int n_pos, float2 *out, const Launch &l);
+// out[i][j] = factor * (cos, sin)((pos0 + i) * frequency j), i < n_pos, j < width,
+// (1, 0) from j = n_rot / 2 on; out_t (or null) the same position-minor [width][n_pos].
+cudaError_t launch_rope_table(const RopeSpec &r, int pos0, int n_pos, int width, float2 *out, float2 *out_t, const Launch &l);
 
 // ------------------------------------------------------------------ trees of drafted tokens
 // Rows row0[i] .. row0[i + 1] - 1 are the nodes of tree i, at most max_nodes, in

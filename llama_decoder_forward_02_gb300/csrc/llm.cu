@@ -35,6 +35,8 @@ cudaError_t init_gemv_q4_attributes();
 cudaError_t init_attn_q4_attributes();
 cudaError_t init_attn_prefill_q4_attributes();
 cudaError_t init_attn_tree_attributes();
+const char *rope_error(const llm_rope *r, int hd);
+RopeSpec rope_spec(const llm_rope &r);
 
 // Kernel attributes (dynamic shared-memory limits, carveouts) take effect on
 // the device that is current when they are set, so they are set once per
@@ -103,6 +105,10 @@ struct llm_model {
     uint8_t *qbuf = nullptr;           // Q8_0 or Q4_0 rows of every decode matrix
     const uint8_t *q_out = nullptr;    // ... of the output projection
     float *nbuf = nullptr;             // query and key gains of every layer (llm_model_set_qk_norm)
+    // llm_model_set_rope: the rotation of its contexts' tables.  Halves are adjacent pairs here: the rows of Wq
+    // and Wk (and the gains) are brought into that order, which attention does not see.
+    bool has_rope = false;
+    llm_rope rope = {};
     int num_sms = 0;
     int device = 0;
     int n_contexts = 0;
@@ -112,12 +118,14 @@ struct llm_model {
 enum KId {
     K_EMBED, K_GATHER, K_GEMV_QKV, K_ATTN_DECODE, K_GEMV_O, K_GEMV_GATEUP, K_GEMV_DOWN,
     K_GEMV_LMHEAD, K_GEMM_QKV, K_ATTN_PREFILL, K_GEMM_O, K_GEMM_GATEUP, K_GEMM_DOWN, K_GEMM_LMHEAD,
-    K_ARGMAX, K_COPY, K_QK_NORM, K_COUNT
+    K_ARGMAX, K_COPY, K_QK_NORM, K_ATTN_TREE, K_TREE_ACCEPT, K_COUNT
 };
 static const char *const KNAME[K_COUNT] = {
     "embed", "gather_rows", "gemv_qkv_rope_kv", "attn_decode", "gemv_o_resid", "gemv_gateup_swiglu",
     "gemv_down_resid", "gemv_lm_head", "gemm_qkv_rope_kv", "attn_prefill", "gemm_o_resid", "gemm_gateup_swiglu",
-    "gemm_down_resid", "gemm_lm_head", "argmax", "copy", "qk_norm_rope_kv"};
+    "gemm_down_resid", "gemm_lm_head", "argmax", "copy", "qk_norm_rope_kv",
+    "attn_tree", "tree_accept"};
+static_assert(K_COUNT == LLM_KERNEL_CLASSES, "llm.h says how many classes there are");
 
 struct KtRec { int id; cudaEvent_t a, b; };
 
@@ -139,6 +147,14 @@ struct llm_ctx {
     float *logits_q4 = nullptr;    // ... and the logits of all rows where only some are outputs
     float2 *rope = nullptr;
     float2 *rope_t = nullptr;      // the same table position-minor [hd / 2][n_ctx] (prefill QKV epilogue)
+    float2 *rope_unit = nullptr;   // the table without the factor of cos and sin, where the model's rotation has one (context shift)
+    // trees of drafted tokens (llm_decode_tree): scratch of their attention, the caches' maps, and the step that waits
+    // for llm_tree_accept
+    void *tree_scratch = nullptr;
+    TmaMap tree_k, tree_v;
+    bool tree_maps = false;
+    TreePlan tree;                 // n == 0: none waits
+    bool tree_logits = false;      // the logits are those of a tree
     // workspaces
     float *h = nullptr, *h2 = nullptr, *ss = nullptr, *ss2 = nullptr, *qf = nullptr;
     f16 *xg = nullptr;                        // one-row steps: f16(h * the next norm gain) [d]
@@ -403,12 +419,40 @@ extern "C" int32_t llm_model_set_qk_norm(llm_model *m, const void *const *q_norm
         cudaFree(buf);
         return fail(c, LLM_ERR_COMPUTE, "query and key gain copy", e);
     }
+    if (m->has_rope && m->rope.layout == LLM_ROPE_HALVES) {
+        if (!e) e = launch_pair_rows(buf, 2 * m->L, hd, m->rope.n_rot, 1, st);
+        if (!e) e = cudaStreamSynchronize(st);
+        if (e) {
+            cudaFree(buf);
+            return fail(c, LLM_ERR_COMPUTE, "query and key gain order", e);
+        }
+    }
     cudaFree(m->nbuf);
     m->nbuf = buf;
     for (int l = 0; l < m->L; ++l) {
         m->layers[l].q_norm = q_norm ? buf + (size_t)2 * l * hd : nullptr;
         m->layers[l].k_norm = k_norm ? buf + (size_t)2 * l * hd + hd : nullptr;
     }
+    return LLM_OK;
+}
+
+extern "C" int32_t llm_model_set_rope(llm_model *m, const llm_rope *rope, void *stream) {
+    llm_ctx *c = nullptr;
+    if (!m) return fail(c, LLM_ERR_INVALID, "model is NULL");
+    if (const char *why = rope_error(rope, m->hd)) return fail(c, LLM_ERR_INVALID, why);
+    if (m->n_contexts) return fail(c, LLM_ERR_INVALID, "the model has live contexts");
+    if (m->has_rope) return fail(c, LLM_ERR_INVALID, "the model's rotation is set already");
+    if (m->wtype || m->nbuf) return fail(c, LLM_ERR_INVALID, "llm_model_set_rope comes before llm_model_quantize and llm_model_set_qk_norm");
+    if (rope->layout == LLM_ROPE_HALVES) {
+        cudaStream_t st = (cudaStream_t)stream;
+        cudaError_t e = cudaSuccess;
+        for (int l = 0; l < m->L && !e; ++l)
+            e = launch_pair_rows(m->layers[l].wqkv, m->H + m->Hkv, m->hd, rope->n_rot, m->d, st);
+        if (!e) e = cudaStreamSynchronize(st);
+        if (e) return fail(c, LLM_ERR_COMPUTE, "order of the query and key rows", e);
+    }
+    m->rope = *rope;
+    m->has_rope = true;
     return LLM_OK;
 }
 
@@ -485,7 +529,8 @@ static void ctx_release(llm_ctx *c) {
     void *dev[] = {c->kc, c->vc, c->rope, c->rope_t, c->h, c->h2, c->ss, c->ss2, c->qf, c->x, c->qb, c->o, c->u,
                    c->gemv_part, c->gemv_cnt, c->sk_ws, c->sk_flags, c->attn_part, c->attn_cnt, c->meta_dev, c->dec_dev,
                    c->logits, c->argmax_dev, c->gen_tokens, c->err_dev,
-                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->logits_q4, c->q4_scratch};
+                   c->samp_dev, c->xg, c->ss_cta, c->x2, c->ss32, c->ss32b, c->qkv, c->ss_q4, c->logits_q4, c->q4_scratch,
+                   c->rope_unit, c->tree_scratch};
     for (void *p : dev) if (p) cudaFree(p);
     for (int i = 0; i < 2; ++i) {
         if (c->meta_host[i]) cudaFreeHost(c->meta_host[i]);
@@ -511,6 +556,8 @@ static void make_attn_maps(llm_ctx *c) {
     const llm_model *m = c->m;
     const long long rows = (long long)c->n_seq_max * m->L * m->Hkv * c->n_ctx;
     const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
+    c->tree_maps = !c->kv_q4 && !c->kv_fp8 && make_cache_map(&c->tree_k, c->kc, rows, m->hd) &&
+                   make_cache_map(&c->tree_v, c->vc, rows, m->hd);
     if (c->kv_q4) {
         c->attn_pair_ok = false;
         c->attn_tc_ok = attn_prefill_q4_tc_ok(m->hd) && make_operand_map(&c->aq, c->qb, nub, m->n_q, 128);
@@ -619,6 +666,11 @@ extern "C" int32_t llm_kv_alloc_typed(llm_model *m, int32_t n_ctx, int32_t n_seq
     if (c->kv_q4) dmal(&c->q4_scratch, q4_scratch);
     dmal((void **)&c->rope, (size_t)n_ctx * (hd / 2) * sizeof(float2));
     dmal((void **)&c->rope_t, (size_t)n_ctx * (hd / 2) * sizeof(float2));
+    if (m->has_rope) {
+        double f[64], scale;
+        rope_frequencies(rope_spec(m->rope), f, &scale);
+        if (scale != 1.0) dmal((void **)&c->rope_unit, (size_t)n_ctx * (hd / 2) * sizeof(float2));
+    }
     dmal((void **)&c->h, (size_t)nub * d * sizeof(float));
     dmal((void **)&c->h2, (size_t)nub * d * sizeof(float));
     dmal((void **)&c->xg, (size_t)d * sizeof(f16));
@@ -690,18 +742,30 @@ extern "C" int32_t llm_kv_alloc_typed(llm_model *m, int32_t n_ctx, int32_t n_seq
         return fail(nc, LLM_ERR_COMPUTE, "TMA descriptor creation failed");
     }
     make_attn_maps(c);
-    // RoPE table: angle = pos * theta^(-2i/hd), in double precision
-    std::vector<float2> tab((size_t)n_ctx * (hd / 2));
-    for (int pidx = 0; pidx < n_ctx; ++pidx)
+    cudaError_t e = cudaSuccess;
+    std::vector<float2> tab, tab_t;
+    if (m->has_rope) {
+        const Launch l{c->stream, false, nullptr};
+        RopeSpec r = rope_spec(m->rope);
+        e = launch_rope_table(r, 0, n_ctx, hd / 2, c->rope, c->rope_t, l);
+        r.attn_factor = 1.f;
+        if (!e && c->rope_unit) e = launch_rope_table(r, 0, n_ctx, hd / 2, c->rope_unit, nullptr, l);
+    } else {
+        // RoPE table: angle = pos * theta^(-2i/hd), in double precision
+        tab.resize((size_t)n_ctx * (hd / 2));
+        tab_t.resize(tab.size());
         for (int i = 0; i < hd / 2; ++i) {
-            const double ang = (double)pidx * std::pow((double)m->hp.rope_theta, -2.0 * i / hd);
-            tab[(size_t)pidx * (hd / 2) + i] = make_float2((float)std::cos(ang), (float)std::sin(ang));
+            const double f = std::pow((double)m->hp.rope_theta, -2.0 * i / hd);
+            for (int pidx = 0; pidx < n_ctx; ++pidx) {
+                const double ang = (double)pidx * f;
+                const float2 cs = make_float2((float)std::cos(ang), (float)std::sin(ang));
+                tab[(size_t)pidx * (hd / 2) + i] = cs;
+                tab_t[(size_t)i * n_ctx + pidx] = cs;
+            }
         }
-    std::vector<float2> tab_t(tab.size());
-    for (int pidx = 0; pidx < n_ctx; ++pidx)
-        for (int i = 0; i < hd / 2; ++i) tab_t[(size_t)i * n_ctx + pidx] = tab[(size_t)pidx * (hd / 2) + i];
-    cudaError_t e = cudaMemcpyAsync(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice, c->stream);
-    if (!e) e = cudaMemcpyAsync(c->rope_t, tab_t.data(), tab_t.size() * sizeof(float2), cudaMemcpyHostToDevice, c->stream);
+        e = cudaMemcpyAsync(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice, c->stream);
+        if (!e) e = cudaMemcpyAsync(c->rope_t, tab_t.data(), tab_t.size() * sizeof(float2), cudaMemcpyHostToDevice, c->stream);
+    }
     if (!e) e = cudaMemsetAsync(c->gemv_cnt, 0, cnt * sizeof(unsigned), c->stream);
     if (!e) e = cudaMemsetAsync(c->sk_flags, 0, (size_t)2 * gemm_pair_max_clusters() * sizeof(unsigned), c->stream);
     if (!e) e = cudaMemsetAsync(c->attn_cnt, 0, (size_t)8 * m->Hkv * sizeof(unsigned), c->stream);
@@ -731,6 +795,13 @@ extern "C" void llm_kv_free(llm_ctx *c) { ctx_release(c); }
 
 namespace {
 
+// The trees of a step: a cell for each row, and what their attention reads.
+struct TreeDev {
+    const int *cell, *row0, *seq, *base;
+    const uint32_t *mask;
+    int n_tree, max_nodes, words;
+};
+
 struct UbDev {
     const int *tok, *pos, *seq;
     const int *out_rows;      // rows of the ubatch that are outputs (n_out entries), or NULL = all
@@ -741,6 +812,7 @@ struct UbDev {
     int T, n_out;
     int out_base;             // first logits row of this ubatch
     int ub_index;
+    const TreeDev *tree;      // or null
 };
 
 Launch lnch(llm_ctx *c) { return Launch{c->stream, c->use_pdl && !c->ktime, &c->launches}; }
@@ -823,8 +895,9 @@ cudaError_t debug_copy(llm_ctx *c, const UbDev &u, int layer, const float *h, in
 
 // Whether the QKV projection's rows are stored plainly for a kernel of its own
 // that norms, rotates and appends: normed queries and keys need a whole head at
-// once, a Q4_0 cache a block (which the GEMV over Q4_0 rows has, run_small_q4).
-bool plain_qkv(const llm_ctx *c) { return c->m->nbuf || c->kv_q4; }
+// once, a Q4_0 cache a block (which the GEMV over Q4_0 rows has, run_small_q4),
+// and nodes of a tree stand in cells that are not their positions.
+bool plain_qkv(const llm_ctx *c, const UbDev &u) { return c->m->nbuf || c->kv_q4 || u.tree; }
 
 cudaError_t qk_norm(llm_ctx *c, const UbDev &u, int layer, bool prefill, const Launch &L) {
     const llm_model *m = c->m;
@@ -832,13 +905,27 @@ cudaError_t qk_norm(llm_ctx *c, const UbDev &u, int layer, bool prefill, const L
     n.qkv = c->qkv; n.ld = m->n_qkv;
     n.q_gain = m->layers[layer].q_norm; n.k_gain = m->layers[layer].k_norm; n.eps = m->hp.rms_eps;
     n.rope = c->rope; n.pos = u.pos; n.seq = u.seq;
+    if (u.tree) { n.cell = u.tree->cell; prefill = true; }        // the attention of trees takes fp16 queries
     n.q32 = prefill ? nullptr : c->qf; n.q16 = prefill ? c->qb : nullptr;
     n.kv = kv_view(c, layer); n.T = u.T; n.H = m->H; n.err = c->err_dev;
     n.early = true;                                   // positions and table stand since before the QKV projection
     return timed(c, K_QK_NORM, [&] { return launch_qk_norm_rope(n, L); });
 }
 
+cudaError_t attn_tree(llm_ctx *c, const UbDev &u, int layer, const Launch &L) {
+    const llm_model *m = c->m;
+    AttnTreeArgs a;
+    a.q = c->qb; a.kv = kv_view(c, layer); a.o = c->o; a.H = m->H; a.T = u.T;
+    a.row0 = u.tree->row0; a.seq = u.tree->seq; a.base = u.tree->base; a.mask = u.tree->mask; a.pos = u.pos;
+    a.n_tree = u.tree->n_tree; a.max_nodes = u.tree->max_nodes; a.words = u.tree->words; a.window = c->swa_window;
+    a.scratch = c->tree_scratch; a.err = c->err_dev;
+    a.map_row0 = (long long)layer * m->Hkv * c->n_ctx;
+    const bool maps = !c->kv_fp8;
+    return timed(c, K_ATTN_TREE, [&] { return launch_attn_tree(a, maps ? &c->tree_k : nullptr, maps ? &c->tree_v : nullptr, L); });
+}
+
 cudaError_t attn_decode(llm_ctx *c, const UbDev &u, int layer) {
+    if (u.tree) return attn_tree(c, u, layer, lnch_attn(c));
     const llm_model *m = c->m;
     AttnDecodeArgs at;
     at.q = c->qf; at.kv = kv_view(c, layer); at.pos = u.pos; at.seq = u.seq; at.o = c->o; at.T = u.T; at.H = m->H;
@@ -878,7 +965,7 @@ cudaError_t run_small_q4(llm_ctx *c, const UbDev &u) {
     for (int l = 0; l < m->L; ++l) {
         const LayerW &w = m->layers[l];
         // normed heads need whole heads at once, which the GEMV's epilogue does not hold; a Q4_0 block it does
-        const bool plain = m->nbuf;
+        const bool plain = m->nbuf || u.tree;
         if ((e = gemv(K_GEMV_QKV, plain ? EPI_STORE : EPI_QKV, w.q_qkv, m->n_qkv, d, c->x, true, [&](GemvQ4Args &a) {
                 a.out = c->qkv; a.ldo = m->n_qkv;
                 a.q_out = c->qf; a.n_q = m->n_q; a.n_kv = m->n_kv; a.kv = kv_view(c, l);
@@ -973,7 +1060,7 @@ cudaError_t run_small(llm_ctx *c, const UbDev &u) {
             }
         }
         if (stream && l > 0) take_x(a);                                // h * attn_norm from the down GEMV
-        if (plain_qkv(c)) {
+        if (plain_qkv(c, u)) {
             a.out = c->qkv; a.ldo = m->n_qkv;
             if ((e = timed(c, K_GEMV_QKV, [&] { return gv(PRO_NORM, EPI_STORE, a, akb); }))) return e;
             if ((e = qk_norm(c, u, l, false, lnch_attn(c)))) return e;
@@ -1109,7 +1196,7 @@ cudaError_t run_large(llm_ctx *c, const UbDev &u) {
         const KvView kv = kv_view(c, l);
         GemmArgs g = gemm_base(c, c->x, w.wqkv, T, m->n_qkv, d);
         norm_in(g);
-        if (plain_qkv(c)) {
+        if (plain_qkv(c, u)) {
             g.C = c->qkv; g.ldc = m->n_qkv;
             if ((e = timed(c, K_GEMM_QKV, [&] { return gemm(c, EPI_STORE, g, c->ax, w.mqkv); }))) return e;
             if ((e = qk_norm(c, u, l, true, L))) return e;
@@ -1118,7 +1205,9 @@ cudaError_t run_large(llm_ctx *c, const UbDev &u) {
             g.rope_t = c->rope_t; g.rope_n = c->n_ctx;
             if ((e = timed(c, K_GEMM_QKV, [&] { return gemm(c, EPI_QKV, g, c->ax, w.mqkv); }))) return e;
         }
-        if (c->kv_q4) {
+        if (u.tree) {
+            if ((e = attn_tree(c, u, l, L))) return e;
+        } else if (c->kv_q4) {
             if ((e = attn_prefill_q4(c, u, kv))) return e;
         } else if (c->attn_tc_ok && c->attn_mode > 0) {
             AttnPrefillTcArgs at;
@@ -1226,6 +1315,22 @@ int *staging(llm_ctx *c, size_t ints) {
     return c->meta_host[s];
 }
 
+// Room for a step's metadata on the device.
+int32_t reserve_meta(llm_ctx *c, size_t ints) {
+    if (c->meta_cap >= ints) return LLM_OK;
+    CK(cudaStreamSynchronize(c->stream));
+    if (c->meta_dev) cudaFree(c->meta_dev);
+    c->meta_dev = nullptr;
+    const size_t cap = align_up(ints, 4096);
+    if (cudaMalloc(&c->meta_dev, cap * sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        c->meta_cap = 0;
+        return fail(c, LLM_ERR_ALLOC, "metadata allocation failed");
+    }
+    c->meta_cap = cap;
+    return LLM_OK;
+}
+
 // Capture (once) and launch the decode graph for T rows whose metadata sits in dec_dev.
 cudaError_t launch_decode_graph(llm_ctx *c, int T) {
     if (!c->graph[T]) {
@@ -1318,18 +1423,7 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             off_tiles[k] = ints; ints += (size_t)n_tiles[k] * TILE_INTS;
             off_tiles128[k] = ints; ints += (size_t)n_tiles128[k] * TILE_INTS;
         }
-        if (c->meta_cap < ints) {
-            CK(cudaStreamSynchronize(c->stream));
-            if (c->meta_dev) cudaFree(c->meta_dev);
-            c->meta_dev = nullptr;
-            const size_t cap = align_up(ints, 4096);
-            if (cudaMalloc(&c->meta_dev, cap * sizeof(int)) != cudaSuccess) {
-                cudaGetLastError();
-                c->meta_cap = 0;
-                return fail(c, LLM_ERR_ALLOC, "metadata allocation failed");
-            }
-            c->meta_cap = cap;
-        }
+        if (const int32_t rc = reserve_meta(c, ints)) return rc;
         int *hs = staging(c, ints);
         if (!hs) return fail(c, LLM_ERR_ALLOC, "pinned staging allocation failed");
         const int slot = c->meta_slot ^ 1;
@@ -1365,6 +1459,7 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
             u.n_tiles128 = n_tiles128[k];
             u.out_base = out_base;
             u.ub_index = k;
+            u.tree = nullptr;
             out_base += n_out[k];
             CK(run_ubatch(c, u));
         }
@@ -1372,6 +1467,131 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
     for (int i = 0; i < p.n; ++i) c->seq_next[p.seq[i]] = p.pos[i] + 1;
     c->out_index = p.out_index;
     c->n_outputs = p.n_outputs;
+    c->tree.n = 0;
+    c->tree_logits = false;
+    return LLM_OK;
+}
+
+extern "C" int32_t llm_decode_tree(llm_ctx *c, const llm_tree_batch *b) {
+    if (!c || !b) return fail(c, LLM_ERR_INVALID, "ctx or batch is NULL");
+    if (!c->kc) return fail(c, LLM_ERR_ALLOC, NO_CACHE);
+    const llm_model *m = c->m;
+    TreePlan p;
+    std::vector<int32_t> out_index;
+    try {
+        const int rc = plan_tree(*b, m->V, c->n_ctx, c->n_seq_max, c->n_ubatch, c->swa_window, c->seq_next, p);
+        if (rc != LLM_OK) { c->last_error = p.error; return rc; }
+        out_index.resize(p.n);
+    } catch (const std::bad_alloc &) {
+        return fail(c, LLM_ERR_ALLOC, "out of host memory");
+    }
+    if (c->kv_q4) return fail(c, LLM_ERR_INVALID, "trees need an fp16 or FP8 cache");
+    if (!c->kv_fp8 && !c->tree_maps) return fail(c, LLM_ERR_INVALID, "the cache has more rows than a tree's attention addresses");
+    const int n_tree = (int)p.seq_of.size(), T = p.n;
+    if ((long long)n_tree * m->Hkv * (((long long)p.max_nodes * (m->H / m->Hkv) + 127) / 128) > 65535)
+        return fail(c, LLM_ERR_INVALID, "the trees have more than 65535 groups of 128 rows of a kv head");
+    if (ensure_logits(c, T) != LLM_OK) return LLM_ERR_ALLOC;
+    if (!c->qkv) {
+        const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
+        if (cudaMalloc((void **)&c->qkv, (size_t)nub * m->n_qkv * sizeof(float)) != cudaSuccess) {
+            cudaGetLastError();
+            c->qkv = nullptr;
+            return fail(c, LLM_ERR_ALLOC, "tree workspace allocation failed");
+        }
+    }
+    if (!c->tree_scratch) {
+        const size_t bytes = attn_tree_scratch_bytes(1, 1, m->H, m->Hkv, m->hd, c->n_ctx);      // the same for every shape
+        if (cudaMalloc(&c->tree_scratch, bytes) != cudaSuccess) {
+            cudaGetLastError();
+            c->tree_scratch = nullptr;
+            return fail(c, LLM_ERR_ALLOC, "tree workspace allocation failed");
+        }
+        CK(cudaMemsetAsync(c->tree_scratch, 0, bytes, c->stream));
+    }
+    // tok | pos | seq | cell | row0 | seq and base of the trees | mask
+    const size_t ints = 4 * (size_t)T + 3 * (size_t)n_tree + 1 + p.mask.size();
+    if (const int32_t rc = reserve_meta(c, ints)) return rc;
+    int *hs = staging(c, ints);
+    if (!hs) return fail(c, LLM_ERR_ALLOC, "pinned staging allocation failed");
+    const int slot = c->meta_slot ^ 1;
+    size_t at = 0;
+    auto put = [&](const void *v, size_t n) {
+        memcpy(hs + at, v, n * sizeof(int));
+        const int *dev = c->meta_dev + at;
+        at += n;
+        return dev;
+    };
+    TreeDev t;
+    UbDev u;
+    memset(&u, 0, sizeof u);
+    u.tok = put(p.token.data(), T); u.pos = put(p.pos.data(), T); u.seq = put(p.seq.data(), T);
+    t.cell = put(p.cell.data(), T); t.row0 = put(p.row0.data(), n_tree + 1);
+    t.seq = put(p.seq_of.data(), n_tree); t.base = put(p.base.data(), n_tree);
+    t.mask = reinterpret_cast<const uint32_t *>(put(p.mask.data(), p.mask.size()));
+    t.n_tree = n_tree; t.max_nodes = p.max_nodes; t.words = p.words;
+    u.T = u.n_out = T;
+    u.tree = &t;
+    CK(cudaMemcpyAsync(c->meta_dev, hs, ints * sizeof(int), cudaMemcpyHostToDevice, c->stream));
+    CK(cudaEventRecord(c->meta_ev[slot], c->stream));
+    c->tree.n = 0;                 // whatever waited: its cells are written over
+    CK(run_ubatch(c, u));
+    for (int i = 0; i < T; ++i) out_index[i] = i;
+    c->out_index = std::move(out_index);
+    c->n_outputs = T;
+    c->tree = std::move(p);
+    c->tree_logits = true;
+    return LLM_OK;
+}
+
+extern "C" int32_t llm_tree_accept(llm_ctx *c, const int32_t *target, int32_t *path, int32_t *n_accept, int32_t *next) {
+    if (!c || !target) return fail(c, LLM_ERR_INVALID, "ctx or target is NULL");
+    if (!c->kc) return fail(c, LLM_ERR_ALLOC, NO_CACHE);
+    TreePlan &p = c->tree;
+    if (!p.n) return fail(c, LLM_ERR_INVALID, "no tree waits: llm_tree_accept follows llm_decode_tree");
+    const llm_model *m = c->m;
+    const int T = p.n, n_tree = (int)p.seq_of.size(), most = p.max_nodes;
+    std::vector<int32_t> stand, count;
+    try {
+        accept_path(p, target, stand, count);
+    } catch (const std::bad_alloc &) {
+        return fail(c, LLM_ERR_ALLOC, "out of host memory");
+    }
+    bool moves = false;
+    for (int i = 0; i < n_tree; ++i)
+        for (int j = 0; j < count[i]; ++j) moves |= stand[p.row0[i] + j] != j;
+    if (moves) {
+        // token | parent | target | row0 | seq | base, then what the kernel finds
+        const size_t in = 3 * (size_t)T + 3 * (size_t)n_tree + 1, out = (size_t)n_tree * (most + 2);
+        if (const int32_t rc = reserve_meta(c, in + out)) return rc;
+        int *hs = staging(c, in);
+        if (!hs) return fail(c, LLM_ERR_ALLOC, "pinned staging allocation failed");
+        const int slot = c->meta_slot ^ 1;
+        size_t at = 0;
+        auto put = [&](const void *v, size_t n) {
+            memcpy(hs + at, v, n * sizeof(int));
+            const int *dev = c->meta_dev + at;
+            at += n;
+            return dev;
+        };
+        TreeAcceptArgs a;
+        a.token = put(p.token.data(), T); a.parent = put(p.parent.data(), T); a.target = put(target, T);
+        a.row0 = put(p.row0.data(), n_tree + 1); a.seq = put(p.seq_of.data(), n_tree); a.base = put(p.base.data(), n_tree);
+        a.path = c->meta_dev + in; a.n_accept = a.path + (size_t)n_tree * most; a.next = a.n_accept + n_tree;
+        a.k = c->kc; a.v = c->vc; a.kv_type = c->kv_fp8 ? TREE_KV_E4M3 : TREE_KV_F16;
+        a.T = T; a.n_tree = n_tree; a.max_nodes = most; a.heads = m->L * m->Hkv; a.head_dim = m->hd;
+        a.n_ctx = c->n_ctx; a.n_seq = c->n_seq_max; a.err = c->err_dev;
+        CK(cudaMemcpyAsync(c->meta_dev, hs, in * sizeof(int), cudaMemcpyHostToDevice, c->stream));
+        CK(cudaEventRecord(c->meta_ev[slot], c->stream));
+        CK(timed(c, K_TREE_ACCEPT, [&] { return launch_tree_accept(a, Launch{c->stream, false, &c->launches}); }));
+    }
+    for (int i = 0; i < n_tree; ++i) {
+        const int r = p.row0[i];
+        c->seq_next[p.seq_of[i]] = p.base[i] + count[i];
+        if (n_accept) n_accept[i] = count[i];
+        if (next) next[i] = target[r + stand[r + count[i] - 1]];
+    }
+    if (path) memcpy(path, stand.data(), (size_t)T * sizeof(int32_t));
+    p.n = 0;
     return LLM_OK;
 }
 
@@ -1456,6 +1676,7 @@ extern "C" int32_t llm_generate(llm_ctx *c, int32_t seq_id, int32_t n_steps, int
     if (seq_id < 0 || seq_id >= c->n_seq_max) return fail(c, LLM_ERR_INVALID, "invalid seq_id");
     if (!c->kc) return fail(c, LLM_ERR_ALLOC, NO_CACHE);
     if (c->n_outputs < 1) return fail(c, LLM_ERR_INVALID, "no logits to start from");
+    if (c->tree_logits) return fail(c, LLM_ERR_INVALID, "the last logits are those of a tree: llm_decode comes first");
     if (c->seq_next[seq_id] + n_steps > c->n_ctx) { c->last_error = "sequence would pass n_ctx"; return LLM_NO_KV_ROOM; }
     if (c->gemv_max_rows < 1) return fail(c, LLM_ERR_INVALID, "decode kernels disabled");
     if (n_steps > c->gen_cap) {
@@ -1524,6 +1745,7 @@ extern "C" int32_t llm_generate(llm_ctx *c, int32_t seq_id, int32_t n_steps, int
         }
     }
     c->n_outputs = 1;
+    c->tree.n = 0;
     CK(cudaMemcpyAsync(tokens_out, c->gen_tokens, n_steps * sizeof(int), cudaMemcpyDeviceToDevice, c->stream));
     c->seq_next[seq_id] += n_steps;
     c->out_index.assign(1, 0);
@@ -1538,6 +1760,7 @@ extern "C" int32_t llm_seq_pos_max(llm_ctx *c, int32_t seq_id) {
 extern "C" int32_t llm_seq_clear(llm_ctx *c, int32_t seq_id) {
     if (!c || seq_id < 0 || seq_id >= c->n_seq_max) return LLM_ERR_INVALID;
     c->seq_next[seq_id] = 0;
+    c->tree.n = 0;
     return LLM_OK;
 }
 
@@ -1548,8 +1771,10 @@ extern "C" int32_t llm_seq_shift(llm_ctx *c, int32_t seq_id, int32_t p0, int32_t
         return fail(c, LLM_ERR_INVALID, "shift range outside the sequence's positions");
     const llm_model *m = c->m;
     const Launch L{c->stream, false, &c->launches};
-    CK(c->kv_q4 ? launch_kv_shift_q4(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, c->rope, L)
-                : launch_kv_shift(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, c->rope, L));
+    const float2 *rope = c->rope_unit ? c->rope_unit : c->rope;
+    CK(c->kv_q4 ? launch_kv_shift_q4(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, rope, L)
+                : launch_kv_shift(kv_view(c, 0), m->L, seq_id, p0, n_discard, end, rope, L));
+    c->tree.n = 0;
     c->seq_next[seq_id] = end - n_discard;
     return LLM_OK;
 }
@@ -1613,6 +1838,7 @@ static int32_t set_kv_q4(llm_ctx *c, bool want) {
     c->q4_scratch = p[2];
     if (p[3]) c->qkv = (float *)p[3];
     c->kv_q4 = want;
+    c->tree.n = 0;
     make_attn_maps(c);
     drop_graphs(c);
     return LLM_OK;
@@ -1676,6 +1902,7 @@ extern "C" int32_t llm_set_option(llm_ctx *c, const char *key, int32_t value) {
             return fail(c, LLM_ERR_ALLOC, "KV cache reallocation failed");
         }
         c->kv_fp8 = want;
+        c->tree.n = 0;
         make_attn_maps(c);
         drop_graphs(c);
         return LLM_OK;

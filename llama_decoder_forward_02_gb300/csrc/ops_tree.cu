@@ -71,7 +71,7 @@ extern "C" int32_t llm_op_rope_table(const llm_rope *rope, int32_t pos0, int32_t
     if (!out) return refuse(who, "a pointer is NULL");
     if (pos0 < 0 || n_pos < 1 || (long long)pos0 + n_pos > (1 << 30)) return refuse(who, "positions must lie in [0, 2^30)");
     if (!aligned(out, 16)) return refuse(who, "out must be 16-byte aligned");
-    return launched(who, launch_rope_table(rope_spec(*rope), pos0, n_pos, (float2 *)out, overlapped(stream)));
+    return launched(who, launch_rope_table(rope_spec(*rope), pos0, n_pos, rope->n_rot / 2, (float2 *)out, nullptr, overlapped(stream)));
 }
 
 extern "C" int32_t llm_op_rope_kv(const float *qkv, int32_t ld, const float *q_gain, const float *k_gain, float eps,

@@ -29,4 +29,21 @@ struct BatchPlan {
 int plan_batch(const llm_batch &b, int n_vocab, int n_ctx, int n_seq_max, int n_ubatch,
                const std::vector<int32_t> &seq_next, BatchPlan &p);
 
+// The trees of a llm_decode_tree call, rows in batch order.
+struct TreePlan {
+    int n = 0;                                    // rows
+    int max_nodes = 0, words = 0;
+    std::vector<int32_t> token, parent, pos, seq, cell;      // [n]
+    std::vector<int32_t> row0, seq_of, base;                 // [trees + 1], [trees], [trees]
+    std::vector<uint32_t> mask;                   // [n][words]: bit j of row t = it sees node j of its tree
+    std::string error;
+};
+constexpr int TREE_PLAN_MAX_NODES = 256;
+// As plan_batch; with window > 0 a node sees the window - 1 nearest of its ancestors.
+int plan_tree(const llm_tree_batch &b, int n_vocab, int n_ctx, int n_seq_max, int n_ubatch, int window,
+              const std::vector<int32_t> &seq_next, TreePlan &p);
+// The nodes of each tree that target accepts (stand, rows of the tree from row0 on,
+// the rest -1) and their number.
+void accept_path(const TreePlan &p, const int32_t *target, std::vector<int32_t> &stand, std::vector<int32_t> &count);
+
 }  // namespace llm

@@ -159,6 +159,22 @@ __global__ void convert_rows_kernel(const bf16 *src, int src_ld, f16 *dst, int d
         dst[(size_t)r * dst_ld + c] = to_f16_checked(src[(size_t)r * src_ld + c], err);
 }
 
+// Model set-up: the rows of a head, halves interleaved.  A CTA takes PAIR_COLS columns
+// of a head, read whole before any is written.
+constexpr int PAIR_COLS = 32, PAIR_THREADS = 256;
+template <typename E>
+__global__ void __launch_bounds__(PAIR_THREADS) pair_rows_kernel(E *rows, int hd, int n_rot, int cols) {
+    __shared__ E held[128 * PAIR_COLS];
+    E *head = rows + (size_t)blockIdx.x * hd * cols;
+    const int c0 = blockIdx.y * PAIR_COLS, n = min(PAIR_COLS, cols - c0);
+    for (int i = threadIdx.x; i < n_rot * n; i += PAIR_THREADS) held[i] = head[(size_t)(i / n) * cols + c0 + i % n];
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_rot * n; i += PAIR_THREADS) {
+        const int r = i / n;                         // the new row
+        head[(size_t)r * cols + c0 + i % n] = held[(r / 2 + (r & 1) * (n_rot / 2)) * n + i % n];
+    }
+}
+
 // Model set-up: pack gate and up [F][d] into [2*F_pad][d] with groups of
 // GU_GROUP gate rows followed by the GU_GROUP up rows of the same indices;
 // rows past F are zero.
@@ -236,6 +252,19 @@ cudaError_t launch_convert_rows(const bf16 *src, int src_ld, f16 *dst, int dst_l
     if (rows < 1) return cudaSuccess;
     convert_rows_kernel<<<rows, 256, 0, st>>>(src, src_ld, dst, dst_ld, rows, cols, err);
     return cudaGetLastError();
+}
+
+template <typename E>
+static cudaError_t pair_rows(E *rows, int heads, int hd, int n_rot, int cols, cudaStream_t st) {
+    if (hd > 128 || n_rot > hd) return cudaErrorInvalidValue;
+    pair_rows_kernel<<<dim3(heads, (cols + PAIR_COLS - 1) / PAIR_COLS), PAIR_THREADS, 0, st>>>(rows, hd, n_rot, cols);
+    return cudaGetLastError();
+}
+cudaError_t launch_pair_rows(f16 *rows, int heads, int hd, int n_rot, int cols, cudaStream_t st) {
+    return pair_rows(rows, heads, hd, n_rot, cols, st);
+}
+cudaError_t launch_pair_rows(float *rows, int heads, int hd, int n_rot, int cols, cudaStream_t st) {
+    return pair_rows(rows, heads, hd, n_rot, cols, st);
 }
 
 }  // namespace llm

@@ -105,3 +105,38 @@ def test_definitions():
     quarter = np.array([[[0.0, 1.0]] * 2])
     assert U.rotate(x, quarter, 4, 0)[0, 0].tolist() == [-1, 0, -3, 2, 4, 5, 6, 7]
     assert U.rotate(x, quarter, 4, 1)[0, 0].tolist() == [-2, -3, 0, 1, 4, 5, 6, 7]
+
+
+def check_tree(n_nodes, token, parent, seq_id=None, pos_max=(9, -1, 4), n_vocab=50, n_ctx=40, n_ubatch=32):
+    b, keep = lib.tree_batch(n_nodes, token, parent, seq_id)
+    n = max(len(token), 1)
+    pos, cell = (ctypes.c_int32 * n)(), (ctypes.c_int32 * n)()
+    ends = (ctypes.c_int32 * len(pos_max))(*pos_max)
+    rc = lib.llm_tree_check(n_vocab, n_ctx, len(pos_max), n_ubatch, ends, ctypes.byref(b), pos, cell)
+    return rc, list(pos), list(cell)
+
+
+def test_tree_batches():
+    rc, pos, cell = check_tree([4, 2], [1, 2, 3, 4, 5, 6], [-1, 0, 0, 2, -1, 0], [2, 1])
+    assert rc == 0 and pos == [5, 6, 6, 7, 0, 1] and cell == [5, 6, 7, 8, 0, 1]
+    rc, pos, _ = check_tree([1, 1, 1], [0, 0, 0], [-1, -1, -1])
+    assert rc == 0 and pos == [10, 0, 5]
+    assert check_tree([30], [0] * 30, [-1] + [0] * 29)[0] == 0          # cells 10 .. 39
+    assert check_tree([31], [0] * 31, [-1] + [0] * 30)[0] == lib.LLM_NO_KV_ROOM
+    for args in (([33], [0] * 33, [-1] + [0] * 32), ([257], [0] * 257, [-1] + [0] * 256), ([0], [], []),
+                 ([2], [0, 0], [-1, -1]), ([2], [0, 0], [-1, 1]), ([1], [0], [0]), ([1], [50], [-1]),
+                 ([1], [0], [-1], [3]), ([1], [0], [-1], [-1]), ([1, 1], [0, 0], [-1, -1], [2, 2]),
+                 ([1] * 4, [0] * 4, [-1] * 4, [0, 1, 2, 0])):
+        assert check_tree(*args)[0] == BAD
+    assert lib.llm_tree_check(50, 40, 3, 32, None, None, None, None) == BAD
+    with pytest.raises(ValueError):
+        lib.tree_batch([2], [1], [-1])
+
+
+def test_context_calls_refuse_null():
+    one = (ctypes.c_int32 * 1)(0)
+    b, keep = lib.tree_batch([1], [0], [-1])
+    assert lib.llm_decode_tree(None, ctypes.byref(b)) == BAD
+    assert lib.llm_tree_accept(None, one, None, None, None) == BAD
+    r = lib.rope(10000.0, 64)
+    assert lib.llm_model_set_rope(None, ctypes.byref(r), None) == BAD
