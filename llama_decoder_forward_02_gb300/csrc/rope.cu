@@ -59,11 +59,11 @@ __device__ const Directions directions = make_directions();
 
 struct Frequencies {
     unsigned long long f[MAX_PAIRS];                 // turns a position, in 2^-64
-    float scale;
+    float scale, scale_lo;                           // the factor as a pair
 };
 
 // The angle phase / 2^64 turns.
-__device__ __forceinline__ float2 turn_of(const Direction *dirs, unsigned long long phase, float scale) {
+__device__ __forceinline__ float2 turn_of(const Direction *dirs, unsigned long long phase, float scale, float scale_lo) {
     constexpr int LOW = 55;                          // bits below a direction
     const unsigned long long at = phase + (1ull << (LOW - 1));
     const Direction t = dirs[at >> LOW];
@@ -74,8 +74,9 @@ __device__ __forceinline__ float2 turn_of(const Direction *dirs, unsigned long l
     const float d = fmaf(hi, (float)(2 * PI / 4294967296.0), lo * (float)(2 * PI / 36028797018963968.0));
     const float d2 = d * d;
     const float sd = fmaf(d * d2, fmaf(d2, (float)(1.0 / 120), (float)(-1.0 / 6)), d), cd = d2 * fmaf(d2, (float)(1.0 / 24), -0.5f);
-    const float c = t.c + (t.cl + fmaf(t.c, cd, -t.s * sd)), s = t.s + (t.sl + fmaf(t.s, cd, t.c * sd));
-    return make_float2(c * scale, s * scale);
+    const float c = t.cl + fmaf(t.c, cd, -t.s * sd), s = t.sl + fmaf(t.s, cd, t.c * sd);
+    // times the factor, the large product exact in the sum
+    return make_float2(fmaf(t.c, scale, fmaf(scale, c, t.c * scale_lo)), fmaf(t.s, scale, fmaf(scale, s, t.s * scale_lo)));
 }
 
 // Rows of `width` pairs (even), of which those from `pairs` on do not turn; a thread
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(THREADS) rope_table_kernel(const __grid_consta
     int row = blockIdx.x * per + threadIdx.x / units;
     const bool turns = j < pairs;                    // pairs is even
     const unsigned long long f0 = turns ? fr.f[j] : 0ull, f1 = turns ? fr.f[j + 1] : 0ull;
-    const float scale = turns ? fr.scale : 1.f;
+    const float scale = turns ? fr.scale : 1.f, scale_lo = turns ? fr.scale_lo : 0.f;
     unsigned long long a0 = (unsigned long long)(pos0 + row) * f0, a1 = (unsigned long long)(pos0 + row) * f1;
     const unsigned long long s0 = step * f0, s1 = step * f1;
     __syncthreads();
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(THREADS) rope_table_kernel(const __grid_consta
     pdl_trigger();
     if (threadIdx.x >= per * units) return;
     for (; row < n_pos; row += step, a0 += s0, a1 += s1) {
-        const float2 x = turn_of(dirs, a0, scale), y = turn_of(dirs, a1, scale);
+        const float2 x = turn_of(dirs, a0, scale, scale_lo), y = turn_of(dirs, a1, scale, scale_lo);
         out[(size_t)row * units + u] = make_float4(x.x, x.y, y.x, y.y);
         if (T) {
             out_t[(size_t)j * n_pos + row] = x;
@@ -140,6 +141,7 @@ cudaError_t launch_rope_table(const RopeSpec &r, int pos0, int n_pos, int width,
     Frequencies fr;
     for (int i = 0; i < pairs; ++i) fr.f[i] = (unsigned long long)(f[i] / (2 * PI) * 18446744073709551616.0);
     fr.scale = (float)scale;
+    fr.scale_lo = (float)(scale - (double)fr.scale);
     // four CTAs an SM: each fetches the directions once
     const int per = THREADS / (width / 2), want = (n_pos + per - 1) / per;
     const dim3 grid(want < 4 * 152 ? want : 4 * 152), block(THREADS);
