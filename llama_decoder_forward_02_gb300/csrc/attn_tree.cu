@@ -11,26 +11,35 @@
 // reads each K and V tile of 128 keys once for all of them.  The keys are split over
 // the CTAs of a cluster, and where there are still SMs left over several clusters.
 //
-// Precision.  q, K and V are fp16 (an E4M3 value is one exactly); a weight p = 2^x,
-// x in fp32, enters O as two fp16 numbers of 22 bits together.  Rounded to one, o is
-// off by 1.4 times its own rounding.  The running maximum is raised, and O rescaled,
-// only when a tile's maximum passes it by 8 in base 2; weights are kept 2^7 times as
-// large, so that those far below the maximum stay normal fp16 numbers.
+// Precision.  q, K and V are fp16 (an E4M3 value is one exactly); a weight
+// p = 2^(s c - R), the exponent in fp32 with one rounding, enters O as two fp16 numbers
+// of 22 bits together.  Rounded to one, o is off by 1.4 times its own rounding.  R is a
+// whole number, so that changing it is exact: the row's largest s c so far, rounded up,
+// less 7 (weights far below the largest stay normal fp16 numbers), raised, with O
+// rescaled, only when a tile passes it by 8 more.
 //
-// A CTA: warps 0-7 softmax (two threads a row, 64 keys each), 8-11 bring K and
-// 12-15 V (fp16: one lane each by TMA; E4M3: all widen), 16 issues S = q K^T, 17
-// O += P V.  Tensor memory: three S buffers of 128 columns, P in the place of the
-// S it came from (of each 32 columns 16 of high pairs, 16 of low pairs), O.
+// A CTA: warps 0-7 softmax (two threads a row, 64 keys each), 8 issues S = q K^T, 9
+// O += P V, 10 brings K and 11 V by TMA (10 both of an E4M3 cache, of which 12-15 widen K
+// and 16-19 V).
+// Tensor memory: three S buffers of 128 columns, P in the place of the S it came
+// from (of each 32 columns 16 of high pairs, 16 of low pairs), O.
 //
-// Joining: a CTA sends its rows of O, their maxima and sums to the ranks that own
+// Joining: a CTA sends its rows of O, their references and sums to the ranks that own
 // them (rows / cluster size each), one cluster barrier later every rank joins its
 // rows.  With several clusters a rank leaves its rows in memory and the last one to
-// come joins them, in the clusters' order whichever it is.
+// come joins them, in the clusters' order whichever it is.  (Sent by the copy engine
+// the rows take half as long, but have to be laid down first: no gain.)
 //
 // Cells that a row does not see may hold anything: a masked score is replaced, and
 // in tiles that not every row sees whole, V is read over before its product: rows
 // outside the tree's cells become zero, and a value that is not finite makes the
 // rows that see its cell NaN and is zero for the others.
+//
+// What bounds it: not memory (64 nodes of 32000 cells, 8 kv heads of 128: 54.4 us, 2.4 TB/s)
+// nor the tensor pipe, but the chain of a tile, which one row tile an SM cannot overlap
+// with another's: S, its maximum, 2^x and the split (10.6 cycles a warp and score), P V
+// take 1.3 us for 128 keys, before them 8 us to start and after them 6 us to join.
+// Left out to see, the low products, the loads or the exponentials change it little.
 //
 // Every mbarrier wait is bounded; on a timeout the CTA raises ERRF_WAIT_TIMEOUT,
 // waits (bounded) for its own copies in flight, takes part in the cluster's barriers
@@ -54,13 +63,16 @@ using tcg::tc_fence_before;
 using tcg::tmem_ld32;
 using namespace tca;
 
-constexpr float LIFT = 7.f;                  // weights are kept 2^LIFT times as large
-constexpr float RESCALE_LOG2 = 8.f;          // raise the running maximum only past this margin
+constexpr float LIFT = 7.f;                  // a row's largest weight is at least 2^(LIFT - 1), and
+constexpr float MOST = LIFT + 8.f;           // at most 2^MOST
 constexpr int BQ = 128, BKEY = 128;
-constexpr int SM_WARPS = 8, K_WARP = 8, V_WARP = 12, W_WARPS = 4, S_WARP = 16, PV_WARP = 17;
-constexpr int THREADS = 20 * 32;             // five warpgroups; the last two warps only make up the number
-// Registers a thread: 96 at launch (640 threads), then by warpgroup: 2 x 128 + 2 x 72 + 80 = 480 of 480
+constexpr int SM_WARPS = 8, PARTS = 2, S_WARP = 8, PV_WARP = 9, K_WARP = 10, V_WARP = 11, W_WARP = 12, W_WARPS = 8;
+constexpr int threads(bool f8) { return (W_WARP + (f8 ? W_WARPS : 0)) * 32; }
+// Registers of a thread of the E4M3 kernel: at its launch, of the softmax (which at 96 spills a row's scores:
+// 16 nodes of 32000 cells 47 us, not 35), the widening and the issuers.  256 x 128 + 256 x 72 + 128 x 80 = 640 x 96.
+// With four widening warps and 128 registers for all the case takes 37.6 us.
 constexpr int L_REGS = 96, SM_REGS = 128, W_REGS = 72, I_REGS = 80;
+static_assert(SM_WARPS * SM_REGS + W_WARPS * W_REGS + (W_WARP - S_WARP) * I_REGS <= threads(true) / 32 * L_REGS, "registers");
 constexpr uint32_t BOX = 128 * 128;          // bytes of one 128-row x 64-column fp16 box
 constexpr int NS = 3;                        // S buffers
 constexpr uint32_t TMEM_COLS = 512;          // S_b / P_b [128 b, 128 b + 128), O [384, 384 + HD)
@@ -69,19 +81,22 @@ constexpr int SLOTS = 64;                    // (group, cluster) results that go
 constexpr int COUNTERS = 1024;
 
 // HD: head_dim as the tiles hold it (head_dim 32: 64, the rest zeros).
-template <int HD>
+template <int HD, bool F8>
 struct Cfg {
     static constexpr int NBX = HD / 64;                         // 64-column boxes of a row
-    static constexpr int ST = HD == 128 ? 2 : 5;                // stages of each ring
-    static constexpr uint32_t TILE = NBX * BOX;
+    static constexpr int ST = HD == 128 ? 2 : F8 ? 4 : 5;       // stages of each ring
+    static constexpr int RAWS = HD == 128 ? 3 : 6;              // E4M3 tiles on their way
+    static constexpr uint32_t TILE = NBX * BOX, RAW = BKEY * HD;
     static constexpr uint32_t K_OFF = TILE;
     static constexpr uint32_t V_OFF = K_OFF + ST * TILE;
-    static constexpr uint32_t RECV_OFF = V_OFF + ST * TILE;     // rows of O from the other ranks
+    // rows of O from the other ranks; before them, once every rank has read its own, the E4M3 tiles
+    static constexpr uint32_t RECV_OFF = V_OFF + ST * TILE;
     static constexpr uint32_t RECV = BQ * HD * 4 / MAX_CLUSTER * (MAX_CLUSTER - 1);
-    static constexpr uint32_t ML_OFF = RECV_OFF + RECV;         // their maxima and sums [rank][row][2]
-    static constexpr uint32_t X_OFF = ML_OFF + BQ * 8;          // the halves' exchange [2][half][row]
-    static constexpr uint32_t BAR_OFF = X_OFF + 2 * 2 * BQ * 4;
-    static constexpr uint32_t MISC_OFF = BAR_OFF + 256;
+    static constexpr uint32_t RECV_BYTES = F8 && RAWS * RAW > RECV ? RAWS * RAW : RECV;
+    static constexpr uint32_t ML_OFF = RECV_OFF + RECV_BYTES;        // their references and sums [rank][row][2]
+    static constexpr uint32_t X_OFF = ML_OFF + BQ * 8;          // the exchange of a row's parts [2][part][row]
+    static constexpr uint32_t BAR_OFF = X_OFF + 2 * PARTS * BQ * 4;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + 512;
     static constexpr size_t SMEM = MISC_OFF + 128;
     static constexpr uint32_t O_COL = NS * BKEY;
     // kind::f16 instruction descriptors: D fp32 (bit 4), A and B fp16, M = 128
@@ -90,10 +105,11 @@ struct Cfg {
     static constexpr uint32_t IDESC_O =
         (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((uint32_t)(BQ >> 4) << 24);
     // barriers, in units of eight bytes
-    static constexpr int B_Q = 0, B_S_FULL = 1, B_P_FULL = B_S_FULL + NS, B_PV_DONE = B_P_FULL + NS,
+    static constexpr int B_Q = 0, B_ASKED = 1, B_S_FULL = 2, B_P_FULL = B_S_FULL + NS, B_PV_DONE = B_P_FULL + NS,
                          B_K_FULL = B_PV_DONE + NS, B_K_EMPTY = B_K_FULL + ST, B_V_FULL = B_K_EMPTY + ST,
-                         B_V_EMPTY = B_V_FULL + ST, B_COUNT = B_V_EMPTY + ST;
-    static_assert(8 * B_COUNT <= 256, "barriers");
+                         B_V_EMPTY = B_V_FULL + ST, B_RAW_FULL = B_V_EMPTY + ST, B_RAW_EMPTY = B_RAW_FULL + RAWS,
+                         B_COUNT = B_RAW_EMPTY + RAWS;
+    static_assert(8 * B_COUNT <= 512, "barriers");
     // more than half of an SM's shared memory, and so much that no other kernel with tensor memory fits beside
     static_assert(SMEM <= 227 * 1024 && SMEM >= 190 * 1024, "one CTA an SM");
 };
@@ -108,6 +124,39 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 128, "shared words");
 
+// Loads and stores of 32 columns of tensor memory that are waited for together.
+__device__ __forceinline__ void tmem_ask32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// ... the wait, which the registers asked for pass through
+__device__ __forceinline__ void tmem_come32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(is));
@@ -124,15 +173,43 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
+// Through L2, where it stands among the asynchronous copies' issues.
+__device__ __forceinline__ uint4 ld_global(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
 // A 16-byte chunk of a row of a box, as TMA's 128-byte swizzle places it.
 __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int row, int chunk) {
     return tile + (uint32_t)(chunk >> 3) * BOX + (uint32_t)row * 128u + (uint32_t)(((chunk & 7) ^ (row & 7)) << 4);
 }
+// Two floats in one register pair, for the packed forms of add and fma.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
 // Two weights as hi and lo fp16 pairs: the low 13 mantissa bits are split off exactly.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const float ah = __uint_as_float(__float_as_uint(a) & 0xFFFFE000u), bh = __uint_as_float(__float_as_uint(b) & 0xFFFFE000u);
-    hi = pack_h2(ah, bh);
-    lo = pack_h2(a - ah, b - bh);
+    const uint32_t ah = __float_as_uint(a) & 0xFFFFE000u, bh = __float_as_uint(b) & 0xFFFFE000u;
+    hi = pack_h2(__uint_as_float(ah), __uint_as_float(bh));
+    const float2 l = unpack2(fma2(pack2(__uint_as_float(ah), __uint_as_float(bh)), pack2(-1.f, -1.f), pack2(a, b)));
+    lo = pack_h2(l.x, l.y);
 }
 __device__ __forceinline__ bool not_finite(uint32_t h2) {
     return (h2 & 0x7C00u) == 0x7C00u || (h2 & 0x7C000000u) == 0x7C000000u;
@@ -153,58 +230,73 @@ struct Tree {
     }
 };
 
-// Which of the keys k0 .. k0 + 63 a row sees: those from lo to base, and by the bits
+// Which of the keys k0 .. k0 + 31 a row sees: those from lo to base, and by the bits
 // of its mask those from base to end.
-__device__ __forceinline__ unsigned long long visible(int k0, int lo, int base, int end, const uint32_t *mask, int words) {
-    unsigned long long v = 0;
-    const int a0 = max(lo - k0, 0), a1 = min(base - k0, 64);
-    if (a1 > a0) v = (~0ull >> (64 - (a1 - a0))) << a0;
-    const int j0 = k0 - base, nb = min(end - k0, 64);
-    if (j0 > -64 && nb > 0) {
-        const int i0 = j0 >> 5, sh = j0 & 31;
+__device__ __forceinline__ uint32_t visible(int k0, int lo, int base, int end, const uint32_t *mask, int words) {
+    uint32_t v = 0;
+    const int a0 = max(lo - k0, 0), a1 = min(base - k0, 32);
+    if (a1 > a0) v = (~0u >> (32 - (a1 - a0))) << a0;
+    const int j0 = k0 - base, nb = min(end - k0, 32);
+    if (j0 > -32 && nb > 0) {
+        const int i0 = j0 >> 5;
         auto word = [&](int i) { return i >= 0 && i < words ? __ldcg(mask + i) : 0u; };
-        const uint32_t w0 = word(i0), w1 = word(i0 + 1), w2 = word(i0 + 2);
-        const unsigned long long t = (unsigned long long)__funnelshift_r(w1, w2, sh) << 32 | __funnelshift_r(w0, w1, sh);
-        v |= t & (~0ull >> (64 - nb));
+        v |= __funnelshift_r(word(i0), word(i0 + 1), j0 & 31) & (~0u >> (32 - nb));
     }
     return v;
 }
 
-// Brings a head's E4M3 rows as fp16 tiles, four warps for K or for V: a lane takes 16
-// elements of a row, eight lanes that write at once four pieces of two rows, which the
-// swizzle spreads over all banks.  Rows outside [lo, end) are zero.
-template <int HD>
-__device__ __forceinline__ void widen_tile(const uint8_t *head, int hd, int key0, int lo, int end, uint32_t tile, int ww, int lane) {
-    constexpr int NBX = Cfg<HD>::NBX, N = 4 * NBX;
-    const int piece = lane & 3, r8 = lane >> 2;
-    uint4 x[N];
+// An E4M3 tile of 128 rows as fp16, by half of the widening warps (ww among them): 16 elements of a row at a time, eight lanes
+// at once four pieces each of rows r and r ^ 5, whose chunks lie in different banks where they
+// are read (rows of 128 bytes swizzled by TMA, shorter ones as they are) and where they are written.
+template <int HD, bool F8>
+__device__ __forceinline__ void widen_tile(uint32_t raw, int hd, uint32_t tile, int ww, int lane) {
+    constexpr int NBX = Cfg<HD, F8>::NBX;
+    const int r8 = (lane >> 3) ^ (lane & 4 ? 5 : 0), piece = lane & 3;
+    auto row_of = [&](int i) { return ww * (BKEY / (W_WARPS / 2)) + i / NBX * 8 + r8; };
+    constexpr int N = 2 * NBX;                           // pieces in flight
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int key = key0 + ww * 32 + i / NBX * 8 + r8, at = (i % NBX) * 64 + piece * 16;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (key >= lo && key < end && at < hd) x[i] = __ldcg(reinterpret_cast<const uint4 *>(head + (size_t)key * hd + at));
-    }
+    for (int i0 = 0; i0 < BKEY / (W_WARPS / 2) / 8 * NBX; i0 += N) {
+        uint4 x[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int row = ww * 32 + i / NBX * 8 + r8, c = (i % NBX) * 8 + piece * 2;
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            h[2 * j] = e4m3x2_to_h2((uint16_t)w[j]);
-            h[2 * j + 1] = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
+        for (int i = 0; i < N; ++i) {
+            const int row = row_of(i0 + i), at = (i0 + i) % NBX * 4 + piece;      // 16-byte chunk of the raw row
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (NBX == 2) x[i] = ld_shared(raw + (uint32_t)row * 128u + (uint32_t)((at ^ (row & 7)) << 4));
+            else if (16 * at < hd) x[i] = ld_shared(raw + (uint32_t)(row * hd + 16 * at));
         }
-        st_shared(chunk_at(tile, row, c), make_uint4(h[0], h[1], h[2], h[3]));
-        st_shared(chunk_at(tile, row, c + 1), make_uint4(h[4], h[5], h[6], h[7]));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[2 * j] = e4m3x2_to_h2((uint16_t)w[j]);
+                h[2 * j + 1] = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
+            }
+            const int row = row_of(i0 + i), c = (i0 + i) % NBX * 8 + piece * 2;
+            st_shared(chunk_at(tile, row, c), make_uint4(h[0], h[1], h[2], h[3]));
+            st_shared(chunk_at(tile, row, c + 1), make_uint4(h[4], h[5], h[6], h[7]));
+        }
     }
 }
 
+// E4M3 tiles are brought and widened K0 K1 V0 K2 V1 ..: the n-th of 2 nt.
+struct Item {
+    bool k;
+    int t;
+    __device__ __forceinline__ Item(int n, int nt) {
+        const int u = n < 2 * nt - 1 ? n : 2 * nt;
+        k = u == 0 || (u & 1);
+        t = k ? (u + 1) / 2 : u / 2 - 1;
+    }
+};
+
 // grid (splits, (tree, kv head, row tile)); the splits are clusters of `cs` CTAs.
 template <int HD, bool F8>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(threads(F8), 1)
 attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnTreeArgs a,
                  const int row_tiles, const int cs) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, F8>;
     constexpr int NBX = C::NBX, ST = C::ST;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base_sm = smem_u32(smem_raw);
@@ -219,119 +311,127 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     auto k_empty = [&](int s) { return bar + 8u * (C::B_K_EMPTY + s); };
     auto v_full = [&](int s) { return bar + 8u * (C::B_V_FULL + s); };
     auto v_empty = [&](int s) { return bar + 8u * (C::B_V_EMPTY + s); };
+    auto raw_full = [&](int s) { return bar + 8u * (C::B_RAW_FULL + s); };
+    auto raw_empty = [&](int s) { return bar + 8u * (C::B_RAW_EMPTY + s); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort = &misc.abort;
 
-    cluster_arrive_relaxed();                            // started: the others may write here once they have waited
-    if (tid == 0) {
-        mbar_init(bar + 8u * C::B_Q, SM_WARPS);
-        for (int b = 0; b < NS; ++b) {
-            mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), SM_WARPS);
-            mbar_init(pv_done(b), 1);
+    if (!F8) cluster_arrive_relaxed();                   // started: the others may write here once they have waited
+    pdl_wait();
+    pdl_trigger();
+    const int hd = a.kv.head_dim, Hkv = a.kv.n_kv_head, G = a.H / Hkv;
+    const int group = blockIdx.y, mt = group % row_tiles, j = group / row_tiles % Hkv;
+    const Tree tr(a, group / row_tiles / Hkv);           // on its way while the barriers are made
+    if (warp == K_WARP) {
+        for (int i = lane; i < C::B_COUNT; i += 32) {
+            const bool of_softmax = i == C::B_Q || i == C::B_ASKED || (i >= C::B_P_FULL && i < C::B_PV_DONE);
+            const bool of_widening = F8 && ((i >= C::B_K_FULL && i < C::B_K_EMPTY) || (i >= C::B_V_FULL && i < C::B_V_EMPTY) || i >= C::B_RAW_EMPTY);
+            mbar_init(bar + 8u * i, of_softmax ? SM_WARPS : of_widening ? W_WARPS / 2 : 1);
         }
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(k_full(s), F8 ? W_WARPS : 1);
-            mbar_init(k_empty(s), 1);
-            mbar_init(v_full(s), F8 ? W_WARPS : 1);
-            mbar_init(v_empty(s), 1);
-        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (lane < 2) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(lane ? &tmV : &tmK)) : "memory");
+    } else if (warp == S_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_u32(&misc.tmem)), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else if (tid == 0) {
         misc.abort = 0;
         misc.lo_min = a.kv.n_ctx;
         misc.lo_max = 0;
         for (int i = 0; i < 12; ++i) misc.bad[i / 4][i % 4] = 0u;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == S_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     :: "r"(smem_u32(&misc.tmem)), "r"(TMEM_COLS) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem;
-    pdl_wait();
-    pdl_trigger();
 
-    const int hd = a.kv.head_dim, Hkv = a.kv.n_kv_head, G = a.H / Hkv;
-    const int group = blockIdx.y, mt = group % row_tiles, j = group / row_tiles % Hkv;
-    const Tree tr(a, group / row_tiles / Hkv);
     const int rows = min(max(tr.n * G - mt * BQ, 0), BQ);          // rows of this tile
     const int base = tr.base, end = tr.base + tr.n;
     if (!tr.ok && mt == 0 && j == 0 && blockIdx.x == 0 && tid == 0) raise_error(a.err, ERRF_BAD_INDEX);
     // thread r (and r + 128) of the softmax has row r: query head j G + g of node `node`
     const int r = tid & (BQ - 1), node = (mt * BQ + r) / G, g = (mt * BQ + r) - node * G;
     const bool row_ok = r < rows && tr.ok;
-    int lo = 0;
-    if (warp < SM_WARPS && row_ok) {
-        if (a.window > 0) lo = min(max(a.pos[tr.r0 + node] - a.window + 1, 0), base);
-        if (warp < SM_WARPS / 2) {
+    int lo = 0, lo_min = 0, lo_max = 0;
+    if (a.window > 0) {
+        if (warp < 4 && row_ok) {
+            lo = min(max(a.pos[tr.r0 + node] - a.window + 1, 0), base);
             atomicMin(&misc.lo_min, lo);
             atomicMax(&misc.lo_max, lo);
+            xch[r] = __int_as_float(lo);
         }
+        __syncthreads();
+        lo_min = misc.lo_min;
+        lo_max = misc.lo_max;
+        lo = __float_as_int(xch[r]);
+        __syncthreads();
     }
-    __syncthreads();
-    const int lo_min = misc.lo_min, lo_max = misc.lo_max;
     // this CTA's tiles of 128 keys
     const int first = lo_min / BKEY, all = tr.ok && rows > 0 ? (end + BKEY - 1) / BKEY - first : 0;
     const int S = gridDim.x, split = blockIdx.x;
     const int kt0 = first + (int)((long long)all * split / S), nt = first + (int)((long long)all * (split + 1) / S) - kt0;
 
-    if (warp < SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(SM_REGS));
-    else if (warp < S_WARP) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(W_REGS));
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(I_REGS));
-
-    float m_run = -INFINITY, l_row = 0.f;
+    const float c = 1.4426950408889634f / sqrtf((float)hd);       // scores to exponents of two
+    float R = -INFINITY, l_row = 0.f;                    // weights are 2^(s c - R)
     bool have = false;                                   // O holds this CTA's sums
+    if constexpr (F8) {
+        // no warp waits for another before its own of these three, so the softmax's does end
+        if (warp < SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(SM_REGS));
+        else if (warp < W_WARP) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(I_REGS));
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(W_REGS));
+    }
     if (nt == 0) {
         // nothing to do: on to the joining
     } else if (warp < SM_WARPS) {
-        constexpr int HK = BKEY / 2;
-        const int quarter = warp & 3, hf = warp >> 2;
+        constexpr int HK = BKEY / PARTS, QC = HD / 8 / PARTS;      // keys of a part; 16-byte chunks of a row's q or a key's V
+        const int quarter = warp & 3, part = warp >> 2;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t o_col = C::O_COL + hf * (HD / 2);     // this half's O columns
+        const uint32_t o_col = C::O_COL + part * (HD / 2);   // the part's O columns
         const bool active = quarter * 32 < rows;             // the warp's lanes hold rows
-        // q: this half's chunks of the row (rows past the last are zero)
+        // q: this part's chunks of the row (rows past the last are zero), asked for ahead of K and V, behind which it
+        // would queue for microseconds
         {
             const f16 *src = a.q + ((size_t)(tr.r0 + node) * a.H + (size_t)j * G + g) * hd;
-            uint4 x[HD / 16];
+            uint4 x[QC];
 #pragma unroll
-            for (int i = 0; i < HD / 16; ++i) {
-                const int c = hf * (HD / 16) + i;
+            for (int i = 0; i < QC; ++i) {
+                const int c = part * QC + i;
                 x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (row_ok && 8 * c < hd) x[i] = __ldcg(reinterpret_cast<const uint4 *>(src) + c);
+                if (row_ok && 8 * c < hd) x[i] = ld_global(reinterpret_cast<const uint4 *>(src) + c);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + 8u * C::B_ASKED);
 #pragma unroll
-            for (int i = 0; i < HD / 16; ++i) st_shared(chunk_at(base_sm, r, hf * (HD / 16) + i), x[i]);
+            for (int i = 0; i < QC; ++i) st_shared(chunk_at(base_sm, r, part * QC + i), x[i]);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + 8u * C::B_Q);
         }
-        const float c = 1.4426950408889634f / sqrtf((float)hd);
-        // the other half's value of the same row; two buffers in turn, so that a half one tile ahead does not overwrite
-        // what the other has not read
-        auto exchange = [&](int turn, float v) {
-            float *x = xch + (turn & 1) * 2 * BQ + r;
-            x[hf * BQ] = v;
-            named_sync(1 + quarter, 64);
-            return x[(hf ^ 1) * BQ];
+        // a row's two values, this part's among them; two buffers in turn, so that a part one tile ahead does not
+        // overwrite what the others have not read
+        auto post = [&](int turn, float v) { xch[((turn & 1) * PARTS + part) * BQ + r] = v; };
+        auto collect = [&](int turn, float (&both)[PARTS]) {
+            named_sync(1 + quarter, PARTS * 32);
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) both[i] = xch[((turn & 1) * PARTS + i) * BQ + r];
         };
-        float l_run = 0.f;
         // ok stays uniform over each warp, and every softmax thread runs all nt
         // iterations, so the named barriers (which have no time limit) are always
         // reached by all their threads; after a timeout the iterations only pass them
         bool ok = true;
-        int b = 0, round = 0, edges = 0;                     // t % NS, t / NS
+        int edges = 0;
+        float l_run = 0.f, both[PARTS];
+        int b = 0, round = 0;                                // t % NS, t / NS
         for (int t = 0; t < nt; ++t, b = b + 1 == NS ? 0 : b + 1, round += b == 0) {
-            const int tile0 = (kt0 + t) * BKEY, key0 = tile0 + hf * HK;
-            const uint32_t s_col = lane_base + b * BKEY + hf * HK;
+            const int tile0 = (kt0 + t) * BKEY;
+            const uint32_t s_col = lane_base + b * BKEY + part * HK;
             const bool edge = tile0 + BKEY > base || tile0 < lo_max;       // not every row sees the whole tile
-            unsigned long long vis = ~0ull, nan = 0ull;
+            uint32_t vis[2] = {~0u, ~0u}, nan[2] = {0u, 0u};
             if (edge) {
-                vis = row_ok ? visible(key0, lo, base, end, a.mask + (size_t)(tr.r0 + node) * a.words, a.words) : 0ull;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    vis[q] = row_ok ? visible(tile0 + part * HK + 32 * q, lo, base, end, a.mask + (size_t)(tr.r0 + node) * a.words, a.words) : 0u;
                 // two threads a key read over its V
-                const int sl = t % ST, key = tid >> 1, part = tid & 1;
+                const int sl = t % ST, key = tid >> 1, at = (tid & 1) * QC;
                 // the softmax may be ahead of V by more than its ring: the stage's tile before must have landed, or this
                 // wait would take the one before that for its own
                 if (ST <= NS && t >= ST) ok = ok && warp_wait(pv_done((t - ST) % NS), (t - ST) / NS & 1, abort, a.err);
@@ -341,135 +441,160 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     const uint32_t tile = base_sm + C::V_OFF + sl * C::TILE;
                     bool odd = false;
 #pragma unroll
-                    for (int i = 0; i < HD / 16; ++i) {
-                        const uint4 x = ld_shared(chunk_at(tile, key, part * (HD / 16) + i));
+                    for (int i = 0; i < QC; ++i) {
+                        const uint4 x = ld_shared(chunk_at(tile, key, at + i));
                         odd |= not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
                     }
                     if (!in || odd) {
 #pragma unroll
-                        for (int i = 0; i < HD / 16; ++i) st_shared(chunk_at(tile, key, part * (HD / 16) + i), make_uint4(0u, 0u, 0u, 0u));
+                        for (int i = 0; i < QC; ++i) st_shared(chunk_at(tile, key, at + i), make_uint4(0u, 0u, 0u, 0u));
                         if (in) atomicOr(&misc.bad[edges % 3][key >> 5], 1u << (key & 31));
                     }
                     fence_proxy_async();
                 }
                 named_sync(5, SM_WARPS * 32);
-                const uint32_t *bad = misc.bad[edges % 3];
-                nan = vis & ((unsigned long long)bad[2 * hf + 1] << 32 | bad[2 * hf]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) nan[q] = vis[q] & misc.bad[edges % 3][2 * part + q];
                 // the set of the tile before has been read by all, and serves the tile after the next
                 if (tid < 4) misc.bad[(edges + 2) % 3][tid] = 0u;
                 ++edges;
             }
             ok = ok && warp_wait(s_full(b), round & 1, abort, a.err);
-            if (!active) {
-                __syncwarp();
-                if (ok && lane == 0) mbar_arrive(p_full(b));
-                continue;
-            }
-            float s[HK];
-            float mx = -INFINITY;
-            if (ok) {
-                tc_fence_after();
+            if (active) {
+                uint32_t v[2][32];
+                float mx = -INFINITY;
+                if (ok) {
+                    tc_fence_after();
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};      // the part's maximum as a tree of four chains
 #pragma unroll
-                for (int q = 0; q < HK / 32; ++q) {
-                    uint32_t v[32];
-                    tmem_ld32(s_col + q * 32, v);
+                    for (int q = 0; q < 2; ++q) tmem_ask32(s_col + 32 * q, v[q]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) s[q * 32 + i] = __uint_as_float(v[i]);
+                    for (int q = 0; q < 2; ++q) {
+                        tmem_come32(v[q]);
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(vis[q] >> i & 1)) v[q][i] = 0xFF800000u;
+                            if (nan[q]) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (nan[q] >> i & 1) v[q][i] = 0x7FFFFFFFu;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[q][i]));
+                    }
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
-                if (edge) {
+                post(t, mx);
+                collect(t, both);
+                mx = fmaxf(both[0], both[1]);
+                const float top = __fmul_ru(mx, c);
+                float factor = 1.f;
+                const bool raise = ok && mx != -INFINITY && !(top - R <= MOST);
+                if (raise) {
+                    const float to = __fsub_ru(ceilf(top), LIFT);
+                    factor = R == -INFINITY ? 0.f : ex2(R - to);
+                    R = to;
+                }
+                // a raised reference rescales O, which P_{t-1} V_{t-1} must have finished
+                if (t >= 1 && __any_sync(0xffffffffu, raise)) {
+                    ok = warp_wait(pv_done(b == 0 ? NS - 1 : b - 1), (b == 0 ? round - 1 : round) & 1, abort, a.err);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; ok && q < HD / 64; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(lane_base + o_col + 32 * q, o);
 #pragma unroll
-                    for (int i = 0; i < HK; ++i)
-                        if (!(vis >> i & 1)) s[i] = -INFINITY;
-                    if (nan) {
-#pragma unroll
-                        for (int i = 0; i < HK; ++i)
-                            if (nan >> i & 1) s[i] = __uint_as_float(0x7FFFFFFFu);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                        tmem_st32(lane_base + o_col + 32 * q, o);
                     }
                 }
-                float m8[8];                                 // half-row maximum as a tree of 8 chains
+                if (ok) {
+                    // the part's weights over the columns of S they came from: 16 of hi pairs, 16 of lo pairs
+                    const float less = R == -INFINITY ? 0.f : -R;
+                    const unsigned long long c2 = pack2(c, c), less2 = pack2(less, less);
+                    unsigned long long rs[2] = {0ull, 0ull};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m8[i] = s[i];
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t p[32];
 #pragma unroll
-                for (int i = 8; i < HK; ++i) m8[i & 7] = fmaxf(m8[i & 7], s[i]);
-                mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-            }
-            mx = fmaxf(mx, exchange(t, mx));
-            if (!ok) continue;
-            float factor = 1.f;
-            const bool raise = mx != -INFINITY && (m_run == -INFINITY || (mx - m_run) * c > RESCALE_LOG2);
-            if (raise) {
-                factor = m_run == -INFINITY ? 0.f : ex2((m_run - mx) * c);
-                m_run = mx;
-            }
-            const float m0 = m_run == -INFINITY ? 0.f : m_run;
-            // a raised maximum rescales O, which P_{t-1} V_{t-1} must have finished
-            if (t >= 1 && __any_sync(0xffffffffu, raise)) {
-                ok = warp_wait(pv_done(b == 0 ? NS - 1 : b - 1), (b == 0 ? round - 1 : round) & 1, abort, a.err);
-                if (!ok) continue;
-                tc_fence_after();
-#pragma unroll 1
-                for (int q = 0; q < HD / 64; ++q) {
-                    uint32_t v[32];
-                    tmem_ld32(lane_base + o_col + q * 32, v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * factor);
-                    tmem_st32(lane_base + o_col + q * 32, v);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2, less2));
+                            const float p0 = ex2(x.x), p1 = ex2(x.y);
+                            rs[i & 1] = add2(rs[i & 1], pack2(p0, p1));
+                            split_pair(p0, p1, p[i], p[16 + i]);
+                        }
+                        tmem_put32(s_col + 32 * q, p);
+                    }
+                    tmem_put_done();
+                    const float2 sum = unpack2(add2(rs[0], rs[1]));
+                    l_run = l_run * factor + (sum.x + sum.y);
+                    tc_fence_before();
                 }
             }
-            // the weights of 32 keys over the columns of S they came from: 16 of hi pairs, 16 of lo pairs
-            float rs8[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) rs8[i] = 0.f;
-#pragma unroll
-            for (int q = 0; q < HK / 32; ++q) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p0 = ex2(fmaf(s[32 * q + 2 * i] - m0, c, LIFT)), p1 = ex2(fmaf(s[32 * q + 2 * i + 1] - m0, c, LIFT));
-                    rs8[(2 * i) & 7] += p0;
-                    rs8[(2 * i + 1) & 7] += p1;
-                    split_pair(p0, p1, p[i], p[16 + i]);
-                }
-                tmem_st32(s_col + 32 * q, p);
-            }
-            l_run = l_run * factor + (((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])));
-            tc_fence_before();
+            // (the weights of rows that do not exist are whatever S is)
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full(b));
+            if (ok && lane == 0) mbar_arrive(p_full(b));
         }
-        if (active) l_row = l_run + exchange(nt, l_run);
+        if (active) {
+            post(nt, l_run);
+            collect(nt, both);
+            l_row = both[0] + both[1];
+        }
         have = ok && warp_wait(pv_done((nt - 1) % NS), (nt - 1) / NS & 1, abort, a.err);
         tc_fence_after();
-    } else if (warp < S_WARP) {
-        // ---- K and V tiles
-        const bool k = warp < V_WARP;
-        const int ww = warp - (k ? K_WARP : V_WARP);
-        const uint32_t ring = base_sm + (k ? C::K_OFF : C::V_OFF);
-        const uint32_t full = bar + 8u * (k ? C::B_K_FULL : C::B_V_FULL), empty = bar + 8u * (k ? C::B_K_EMPTY : C::B_V_EMPTY);
-        if constexpr (F8) {
-            const uint8_t *head = (k ? a.kv.k8 : a.kv.v8) + (size_t)tr.seq * a.kv.seq_stride + (size_t)j * a.kv.n_ctx * hd;
-            for (int t = 0; t < nt; ++t) {
-                const int sl = t % ST, use = t / ST;
-                if (use > 0 && !warp_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
-                widen_tile<HD>(head, hd, (kt0 + t) * BKEY, lo_min, end, ring + sl * C::TILE, ww, lane);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + 8u * sl);
-            }
-        } else if (ww == 0 && lane == 0) {
-            const int row = (int)(a.map_row0 + (long long)tr.seq * (a.kv.seq_stride / hd) + (long long)j * a.kv.n_ctx);
-            int t = 0;
-            for (; t < nt; ++t) {
-                const int sl = t % ST, use = t / ST;
-                if (use > 0 && !mbar_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
-                mbar_expect_tx(full + 8u * sl, C::TILE);
-                for (int i = 0; i < NBX; ++i)
-                    tma_load_2d(ring + sl * C::TILE + i * BOX, k ? &tmK : &tmV, full + 8u * sl, i * 64, row + (kt0 + t) * BKEY);
+    } else if (warp == K_WARP || (!F8 && warp == V_WARP)) {
+        // ---- K and V tiles (of an E4M3 cache on their way to the widening), once q has been asked for
+        if (lane == 0) {
+            const int row = (int)(a.map_row0 + (long long)tr.seq * (a.kv.seq_stride / hd) + (long long)j * a.kv.n_ctx) + kt0 * BKEY;
+            bool ok = mbar_wait(bar + 8u * C::B_ASKED, 0, abort, a.err);
+            int sent = 0;
+            if constexpr (F8) {
+                for (; ok && sent < 2 * nt; ++sent) {
+                    const int sl = sent % C::RAWS, use = sent / C::RAWS;
+                    const Item it(sent, nt);
+                    if (use > 0 && !mbar_wait(raw_empty(sl), (use - 1) & 1, abort, a.err)) break;
+                    mbar_expect_tx(raw_full(sl), (uint32_t)(BKEY * hd));
+                    tma_load_2d(base_sm + C::RECV_OFF + sl * C::RAW, it.k ? &tmK : &tmV, raw_full(sl), 0, row + it.t * BKEY);
+                }
+            } else {
+                const bool k = warp == K_WARP;
+                const uint32_t ring = base_sm + (k ? C::K_OFF : C::V_OFF), full = k ? k_full(0) : v_full(0), empty = k ? k_empty(0) : v_empty(0);
+                for (; ok && sent < nt; ++sent) {
+                    const int sl = sent % ST, use = sent / ST;
+                    if (use > 0 && !mbar_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
+                    mbar_expect_tx(full + 8u * sl, C::TILE);
+                    for (int i = 0; i < NBX; ++i)
+                        tma_load_2d(ring + sl * C::TILE + i * BOX, k ? &tmK : &tmV, full + 8u * sl, i * 64, row + sent * BKEY);
+                }
             }
             // after a timeout: wait (bounded) for the copies in flight before the memory is released
-            for (int u = max(t - ST, 0); u < t && *abort; ++u)
-                for (uint32_t i = 0; i < WAIT_LIMIT && !mbar_try_wait(full + 8u * (u % ST), u / ST & 1); ++i) {
-                }
+            if (*abort) {
+                const int n = F8 ? C::RAWS : ST;
+                const uint32_t full = F8 ? raw_full(0) : warp == K_WARP ? k_full(0) : v_full(0);
+                for (int u = max(sent - n, 0); u < sent; ++u)
+                    for (uint32_t i = 0; i < WAIT_LIMIT && !mbar_try_wait(full + 8u * (u % n), u / n & 1); ++i) {
+                    }
+            }
+        }
+    } else if (F8 && warp >= W_WARP) {
+        // ---- widening, K by the first half of the warps and V by the second (all of them in turn: 38.0 us, not 35.2)
+        const int ww = (warp - W_WARP) % (W_WARPS / 2);
+        const bool of_k = warp < W_WARP + W_WARPS / 2;
+        for (int u = 0; u < 2 * nt; ++u) {
+            const Item it(u, nt);
+            if (it.k != of_k) continue;
+            const int sl = it.t % ST, n = it.t / ST, rs = u % C::RAWS;
+            if (!warp_wait(raw_full(rs), u / C::RAWS & 1, abort, a.err)) break;
+            if (n > 0 && !warp_wait(it.k ? k_empty(sl) : v_empty(sl), (n - 1) & 1, abort, a.err)) break;
+            widen_tile<HD, F8>(base_sm + C::RECV_OFF + rs * C::RAW, hd, base_sm + (it.k ? C::K_OFF : C::V_OFF) + sl * C::TILE, ww, lane);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(it.k ? k_full(sl) : v_full(sl));
+                mbar_arrive(raw_empty(rs));
+            }
         }
     } else if (warp == S_WARP) {
         // ---- S_t = q K_t^T into buffer t % NS, once the P that took the place of the S before has been read.  The whole
@@ -479,8 +604,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint64_t q_desc = sdesc(base_sm), k_desc = sdesc(base_sm + C::K_OFF);
         for (int t = 0; ok && t < nt; ++t) {
             const int b = t % NS, sl = t % ST;
-            if (t >= NS && !warp_wait(pv_done(b), (t / NS - 1) & 1, abort, a.err)) break;
             if (!warp_wait(k_full(sl), t / ST & 1, abort, a.err)) break;
+            if (t >= NS && !warp_wait(pv_done(b), (t / NS - 1) & 1, abort, a.err)) break;
             tc_fence_after();
             if (leader) {
 #pragma unroll
@@ -501,8 +626,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint64_t v_desc = sdesc_mn(base_sm + C::V_OFF, BOX);
         for (int t = 0; t < nt; ++t) {
             const int b = t % NS, sl = t % ST;
-            if (!warp_wait(p_full(b), t / NS & 1, abort, a.err)) break;
             if (!warp_wait(v_full(sl), t / ST & 1, abort, a.err)) break;
+            if (!warp_wait(p_full(b), t / NS & 1, abort, a.err)) break;
             tc_fence_after();
             if (leader) {
                 const uint64_t vd = v_desc + (uint32_t)sl * (C::TILE >> 4);
@@ -520,41 +645,40 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
     }
 
-    // Back to the registers of the launch, for what follows is every warp's.  The others take theirs only after the
-    // softmax has taken and returned its own: before, theirs could be the ones that it waits for.
     __syncwarp();
-    if (warp < SM_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L_REGS));
-    __syncthreads();
-    if (warp >= SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L_REGS));
-
     // ---- joining.  Row r belongs to rank r / share; what it is sent lies in its shared memory, its own part over
     // its K tiles, which all products have read.
     const int rank = cs > 1 ? (int)cluster_rank() : 0, share = max((rows + cs - 1) / cs, 1);
-    cluster_wait();                                      // the others have started
+    if constexpr (F8) {
+        // Back to the registers of the launch, for what follows is every warp's.  The others take theirs only after the
+        // softmax has taken and returned its own: before, theirs could be the ones that it waits for.
+        if (warp < SM_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L_REGS));
+        __syncthreads();                                 // the E4M3 tiles have been read (and, after a timeout, have come)
+        if (warp >= SM_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L_REGS));
+        cluster_arrive();
+    }
+    cluster_wait();                                      // the others' memory may be written
     auto part_at = [&](int of, int to) {                 // where rank `to` has the rows of rank `of`
         return of == to ? C::K_OFF : C::RECV_OFF + (uint32_t)((of < to ? of : of - 1) * share) * (HD * 4);
     };
-    if (warp < SM_WARPS && r < rows) {
-        const int hf = warp >> 2, to = r / share, at = r - to * share;
-        if (hf == 0) {
-            const uint32_t dst = dsmem(ml + rank * share + at, to);
-            dsmem_st_u64(dst, (unsigned long long)__float_as_uint(l_row) << 32 | __float_as_uint(m_run));
-        }
+    if (warp < 4 && r < rows) {
+        const int to = r / share, at = r - to * share;
+        dsmem_st_u64(dsmem(ml + rank * share + at, to), (unsigned long long)__float_as_uint(l_row) << 32 | __float_as_uint(R));
     }
-    if (warp < SM_WARPS && (warp & 3) * 32 < rows && have) {       // whole warps: the loads from tensor memory are the warp's
-        const int hf = warp >> 2, to = min(r / share, cs - 1), at = r - to * share;
+    if (warp < SM_WARPS && (warp & 3) * 32 < rows && have) {       // whole warps, as tensor memory is read
+        const int part = warp >> 2, to = min(r / share, cs - 1), at = r - to * share;
         const uint32_t dst = dsmem(smem_raw + part_at(rank, to), to) + (uint32_t)at * (HD * 4);
 #pragma unroll 1
         for (int q = 0; q < HD / 64; ++q) {
             uint32_t v[32];
-            tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::O_COL + hf * (HD / 2) + q * 32, v);
-            if (r < rows && hf * (HD / 2) < hd) {
+            tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::O_COL + part * (HD / 2) + q * 32, v);
+            if (r < rows && part * (HD / 2) < hd) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int chunk = hf * (HD / 8) + q * 8 + i;
+                    const int chunk = part * (HD / 8) + q * 8 + i;
                     dsmem_st_f32x4(dst + (uint32_t)((chunk ^ (at & 7)) << 4),
-                                   make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                               __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+                                   make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                               __uint_as_float(v[4 * i + 3])));
                 }
             }
         }
@@ -569,7 +693,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
 
     const int my_rows = min(share, rows - rank * share), per = hd / 4, clusters = S / cs, mine = split / cs;
-    const float c = 1.4426950408889634f / sqrtf((float)hd);
     unsigned *const counters = reinterpret_cast<unsigned *>(a.scratch);
     float *const slots = reinterpret_cast<float *>(counters + COUNTERS);
     auto slot_o = [&](int ci, int row) { return slots + ((size_t)(group * clusters + ci) * BQ + row) * (HD + 4); };
@@ -579,7 +702,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             *reinterpret_cast<uint2 *>(a.o + ((size_t)t * a.H + (size_t)j * G + (at - nd * G)) * hd + 4 * chunk) =
                 make_uint2(pack_h2(v.x, v.y), pack_h2(v.z, v.w));
     };
-    for (int i = tid; i < my_rows * per; i += THREADS) {
+    for (int i = tid; i < my_rows * per; i += threads(F8)) {
         const int at = i / per, chunk = i - at * per;
         float M = -INFINITY, L = 0.f;
         for (int s = 0; s < cs; ++s) M = fmaxf(M, ml[s * share + at].x);
@@ -587,7 +710,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         for (int s = 0; s < cs; ++s) {
             const float2 v = ml[s * share + at];
             if (v.y == 0.f) continue;                    // that rank saw nothing of the row
-            const float f = ex2((v.x - M) * c);
+            const float f = ex2(v.x - M);
             const float4 x = *reinterpret_cast<const float4 *>(smem_raw + part_at(s, rank) + (uint32_t)at * (HD * 4) + ((chunk ^ (at & 7)) << 4));
             L = fmaf(f, v.y, L);
             o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
@@ -614,7 +737,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
     __syncthreads();
     if (!misc.last) return;
-    for (int i = tid; i < my_rows * per; i += THREADS) {
+    for (int i = tid; i < my_rows * per; i += threads(F8)) {
         const int at = i / per, chunk = i - at * per, row = rank * share + at;
         float M = -INFINITY, L = 0.f;
         for (int s = 0; s < clusters; ++s) M = fmaxf(M, __ldcg(slot_o(s, row) + HD));
@@ -623,7 +746,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             const float *src = slot_o(s, row);
             const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + HD));
             if (v.y == 0.f) continue;
-            const float f = ex2((v.x - M) * c);
+            const float f = ex2(v.x - M);
             const float4 x = __ldcg(reinterpret_cast<const float4 *>(src) + chunk);
             L = fmaf(f, v.y, L);
             o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
@@ -639,7 +762,9 @@ int max_clusters[MAX_DEV][MAX_CLUSTER + 1];
 
 // CTAs of a cluster and clusters of a group: the split that keeps most SMs busy, of
 // equals the one with the larger clusters (a join in shared memory costs less than
-// one through memory); every split has a tile where the cache is full.
+// one through memory).  Several clusters only where a CTA keeps four tiles: their join
+// through memory costs as much as two (8 nodes of 700 cells: 7.0 us, with up to a tile
+// for each CTA 9.5; 16 of 2100: 12.4 and 15.8).
 struct Plan { int cs, clusters; };
 Plan plan(int groups, int n_ctx) {
     int dev = 0;
@@ -649,7 +774,7 @@ Plan plan(int groups, int n_ctx) {
     for (int cs = MAX_CLUSTER; cs >= 2; cs /= 2) {
         if (groups > max_clusters[dev][cs] || cs > tiles) continue;
         int k = max_clusters[dev][cs] / groups;
-        if (k > tiles / cs) k = tiles / cs;
+        if (k > tiles / (4 * cs)) k = tiles / (4 * cs);
         if (k > SLOTS / groups) k = SLOTS / groups;
         if (k < 1) k = 1;
         if (cs * k > best.cs * best.clusters) best = Plan{cs, k};
@@ -663,38 +788,37 @@ size_t attn_tree_scratch_bytes(int, int, int, int, int hd, int) {
     return COUNTERS * sizeof(unsigned) + (size_t)SLOTS * BQ * ((hd == 128 ? 128 : 64) + 4) * sizeof(float);
 }
 
-cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap *mK, const TmaMap *mV, const Launch &l) {
+cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap &mK, const TmaMap &mV, const Launch &l) {
     const int hd = a.kv.head_dim, Hkv = a.kv.n_kv_head;
-    if (Hkv < 1 || a.H % Hkv || (!a.kv.k8 && (!mK || !mV))) return cudaErrorInvalidValue;
+    if (Hkv < 1 || a.H % Hkv) return cudaErrorInvalidValue;
     const int row_tiles = (a.max_nodes * (a.H / Hkv) + BQ - 1) / BQ, groups = a.n_tree * Hkv * row_tiles;
     if (groups > 65535) return cudaErrorInvalidValue;
     const Plan p = plan(groups, a.kv.n_ctx);
-    static const CUtensorMap none = {};
-    const CUtensorMap &k = mK ? *reinterpret_cast<const CUtensorMap *>(mK) : none, &v = mV ? *reinterpret_cast<const CUtensorMap *>(mV) : none;
-    const dim3 grid(p.cs * p.clusters, groups), block(THREADS);
+    const CUtensorMap &k = reinterpret_cast<const CUtensorMap &>(mK), &v = reinterpret_cast<const CUtensorMap &>(mV);
+    const dim3 grid(p.cs * p.clusters, groups), block(threads(a.kv.k8 != nullptr));
     const bool f8 = a.kv.k8;
     if (hd == 128)
         return launch_cluster_kernel(f8 ? attn_tree_kernel<128, true> : attn_tree_kernel<128, false>, grid, block, p.cs,
-                                     Cfg<128>::SMEM, l, k, v, a, row_tiles, p.cs);
+                                     f8 ? Cfg<128, true>::SMEM : Cfg<128, false>::SMEM, l, k, v, a, row_tiles, p.cs);
     if (hd == 64 || hd == 32)
         return launch_cluster_kernel(f8 ? attn_tree_kernel<64, true> : attn_tree_kernel<64, false>, grid, block, p.cs,
-                                     Cfg<64>::SMEM, l, k, v, a, row_tiles, p.cs);
+                                     f8 ? Cfg<64, true>::SMEM : Cfg<64, false>::SMEM, l, k, v, a, row_tiles, p.cs);
     return cudaErrorInvalidValue;
 }
 
 cudaError_t init_attn_tree_attributes() {
-    cudaError_t e = allow_smem(attn_tree_kernel<128, false>, Cfg<128>::SMEM);
-    if (!e) e = allow_smem(attn_tree_kernel<128, true>, Cfg<128>::SMEM);
-    if (!e) e = allow_smem(attn_tree_kernel<64, false>, Cfg<64>::SMEM);
-    if (!e) e = allow_smem(attn_tree_kernel<64, true>, Cfg<64>::SMEM);
+    cudaError_t e = allow_smem(attn_tree_kernel<128, false>, Cfg<128, false>::SMEM);
+    if (!e) e = allow_smem(attn_tree_kernel<128, true>, Cfg<128, true>::SMEM);
+    if (!e) e = allow_smem(attn_tree_kernel<64, false>, Cfg<64, false>::SMEM);
+    if (!e) e = allow_smem(attn_tree_kernel<64, true>, Cfg<64, true>::SMEM);
     int dev = 0;
     if (!e) e = cudaGetDevice(&dev);
     if (e || dev < 0 || dev >= MAX_DEV) return e;
     for (int cs = 2; cs <= MAX_CLUSTER; cs *= 2) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(cs);
-        cfg.blockDim = dim3(THREADS);
-        cfg.dynamicSmemBytes = Cfg<128>::SMEM;
+        cfg.blockDim = dim3(threads(false));
+        cfg.dynamicSmemBytes = Cfg<128, false>::SMEM;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = cs;

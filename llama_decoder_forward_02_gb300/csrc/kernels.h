@@ -212,6 +212,8 @@ bool make_operand_map(TmaMap *m, const f16 *ptr, int rows, int cols, int box_row
 // An fp16 cache [rows][head_dim] in boxes of 128 rows x 64; of head_dim 32 the
 // other half of a box reads zeros.
 bool make_cache_map(TmaMap *m, const f16 *ptr, long long rows, int head_dim);
+// An E4M3 cache in boxes of 128 whole rows, those of 128 bytes with 128-byte swizzle.
+bool make_cache8_map(TmaMap *m, const uint8_t *ptr, long long rows, int head_dim);
 // The tcgen05/TMEM GEMM on CTA pairs (cta_group::2): 256 x bn tiles, bn in
 // {128, 192, 256}; mA boxes 128 x 64 over A [>=M][K], mB boxes of bn / 2 x 64
 // over W [N][K].
@@ -420,8 +422,8 @@ struct AttnTreeArgs {
     long long map_row0 = 0;    // the layer's first row in the caches' maps
 };
 size_t attn_tree_scratch_bytes(int n_tree, int max_nodes, int H, int Hkv, int hd, int n_ctx);
-// mK, mV: maps of the fp16 caches (boxes of 128 rows x 64), unused with E4M3
-cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap *mK, const TmaMap *mV, const Launch &l);
+// mK, mV: maps of the caches (make_cache_map, make_cache8_map)
+cudaError_t launch_attn_tree(const AttnTreeArgs &a, const TmaMap &mK, const TmaMap &mV, const Launch &l);
 
 // Path of a tree that its targets accept, and the move of its cells (tree_accept.cu).
 enum { TREE_KV_F16 = 0, TREE_KV_E4M3 = 1, TREE_KV_Q4_0 = 2 };       // as LLM_KV_*

@@ -556,8 +556,9 @@ static void make_attn_maps(llm_ctx *c) {
     const llm_model *m = c->m;
     const long long rows = (long long)c->n_seq_max * m->L * m->Hkv * c->n_ctx;
     const int nub = c->n_ubatch < 8 ? 8 : c->n_ubatch;
-    c->tree_maps = !c->kv_q4 && !c->kv_fp8 && make_cache_map(&c->tree_k, c->kc, rows, m->hd) &&
-                   make_cache_map(&c->tree_v, c->vc, rows, m->hd);
+    const uint8_t *k8 = reinterpret_cast<uint8_t *>(c->kc), *v8 = reinterpret_cast<uint8_t *>(c->vc);
+    c->tree_maps = !c->kv_q4 && (c->kv_fp8 ? make_cache8_map(&c->tree_k, k8, rows, m->hd) && make_cache8_map(&c->tree_v, v8, rows, m->hd)
+                                           : make_cache_map(&c->tree_k, c->kc, rows, m->hd) && make_cache_map(&c->tree_v, c->vc, rows, m->hd));
     if (c->kv_q4) {
         c->attn_pair_ok = false;
         c->attn_tc_ok = attn_prefill_q4_tc_ok(m->hd) && make_operand_map(&c->aq, c->qb, nub, m->n_q, 128);
@@ -920,8 +921,7 @@ cudaError_t attn_tree(llm_ctx *c, const UbDev &u, int layer, const Launch &L) {
     a.n_tree = u.tree->n_tree; a.max_nodes = u.tree->max_nodes; a.words = u.tree->words; a.window = c->swa_window;
     a.scratch = c->tree_scratch; a.err = c->err_dev;
     a.map_row0 = (long long)layer * m->Hkv * c->n_ctx;
-    const bool maps = !c->kv_fp8;
-    return timed(c, K_ATTN_TREE, [&] { return launch_attn_tree(a, maps ? &c->tree_k : nullptr, maps ? &c->tree_v : nullptr, L); });
+    return timed(c, K_ATTN_TREE, [&] { return launch_attn_tree(a, c->tree_k, c->tree_v, L); });
 }
 
 cudaError_t attn_decode(llm_ctx *c, const UbDev &u, int layer) {
@@ -1486,7 +1486,7 @@ extern "C" int32_t llm_decode_tree(llm_ctx *c, const llm_tree_batch *b) {
         return fail(c, LLM_ERR_ALLOC, "out of host memory");
     }
     if (c->kv_q4) return fail(c, LLM_ERR_INVALID, "trees need an fp16 or FP8 cache");
-    if (!c->kv_fp8 && !c->tree_maps) return fail(c, LLM_ERR_INVALID, "the cache has more rows than a tree's attention addresses");
+    if (!c->tree_maps) return fail(c, LLM_ERR_INVALID, "the cache has more rows than a tree's attention addresses");
     const int n_tree = (int)p.seq_of.size(), T = p.n;
     if ((long long)n_tree * m->Hkv * (((long long)p.max_nodes * (m->H / m->Hkv) + 127) / 128) > 65535)
         return fail(c, LLM_ERR_INVALID, "the trees have more than 65535 groups of 128 rows of a kv head");

@@ -134,13 +134,14 @@ extern "C" int32_t llm_op_attn_tree(const void *q, const void *k_cache, const vo
     a.T = T; a.n_tree = n_tree; a.max_nodes = max_nodes; a.words = (max_nodes + 31) / 32; a.H = H; a.window = window;
     a.scratch = scratch; a.err = err;
     TmaMap mk, mv;
-    const bool f16_cache = kv_type == LLM_KV_F16;
     const long long rows = (long long)n_seq * Hkv * n_ctx;
-    if (f16_cache && (!make_cache_map(&mk, a.kv.k, rows, hd) || !make_cache_map(&mv, a.kv.v, rows, hd))) {
+    const bool made = kv_type == LLM_KV_F16 ? make_cache_map(&mk, a.kv.k, rows, hd) && make_cache_map(&mv, a.kv.v, rows, hd)
+                                            : make_cache8_map(&mk, a.kv.k8, rows, hd) && make_cache8_map(&mv, a.kv.v8, rows, hd);
+    if (!made) {
         set_global_error("llm_op_attn_tree: TMA descriptor creation failed");
         return LLM_ERR_COMPUTE;
     }
-    return launched(who, launch_attn_tree(a, f16_cache ? &mk : nullptr, f16_cache ? &mv : nullptr, overlapped(stream)));
+    return launched(who, launch_attn_tree(a, mk, mv, overlapped(stream)));
 }
 
 extern "C" int32_t llm_op_tree_accept(const int32_t *token, const int32_t *parent, const int32_t *target,

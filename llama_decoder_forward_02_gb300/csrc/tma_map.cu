@@ -59,6 +59,19 @@ bool make_cache_map(TmaMap *m, const f16 *ptr, long long rows, int head_dim) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_cache8_map(TmaMap *m, const uint8_t *ptr, long long rows, int head_dim) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || !ptr || head_dim > 128 || head_dim % 32 || rows < 1 || rows >= (1ll << 31) || (reinterpret_cast<uintptr_t>(ptr) & 15))
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)head_dim};
+    const cuuint32_t box[2] = {(cuuint32_t)head_dim, 128};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(reinterpret_cast<CUtensorMap *>(m), CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)ptr, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_f32_tile_map(TmaMap *m, const float *ptr, int rows, int cols) {
     EncodeTiledFn fn = encode_fn();
     if (!fn || !ptr || cols % 32 || rows < 1 || (reinterpret_cast<uintptr_t>(ptr) & 15)) return false;
