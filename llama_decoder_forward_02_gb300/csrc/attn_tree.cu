@@ -19,8 +19,8 @@
 // rescaled, only when a tile passes it by 8 more.
 //
 // A CTA: warps 0-7 softmax (two threads a row, 64 keys each), 8 issues S = q K^T, 9
-// O += P V, 10 brings K and 11 V by TMA (10 both of an E4M3 cache, of which 12-15 widen K
-// and 16-19 V).
+// O += P V, 10 brings K and 11 V by TMA, of an E4M3 cache to warps 12-15 and 16-19, which
+// widen them.
 // Tensor memory: three S buffers of 128 columns, P in the place of the S it came
 // from (of each 32 columns 16 of high pairs, 16 of low pairs), O.
 //
@@ -85,16 +85,16 @@ template <int HD, bool F8>
 struct Cfg {
     static constexpr int NBX = HD / 64;                         // 64-column boxes of a row
     static constexpr int ST = HD == 128 ? 2 : F8 ? 4 : 5;       // stages of each ring
-    static constexpr int RAWS = HD == 128 ? 3 : 6;              // E4M3 tiles on their way
+    static constexpr int RAWS = HD == 128 ? 2 : 4;              // E4M3 tiles of K, and of V, on their way
     static constexpr uint32_t TILE = NBX * BOX, RAW = BKEY * HD;
     static constexpr uint32_t K_OFF = TILE;
     static constexpr uint32_t V_OFF = K_OFF + ST * TILE;
     // rows of O from the other ranks; before them, once every rank has read its own, the E4M3 tiles
     static constexpr uint32_t RECV_OFF = V_OFF + ST * TILE;
     static constexpr uint32_t RECV = BQ * HD * 4 / MAX_CLUSTER * (MAX_CLUSTER - 1);
-    static constexpr uint32_t RECV_BYTES = F8 && RAWS * RAW > RECV ? RAWS * RAW : RECV;
-    static constexpr uint32_t ML_OFF = RECV_OFF + RECV_BYTES;        // their references and sums [rank][row][2]
-    static constexpr uint32_t X_OFF = ML_OFF + BQ * 8;          // the exchange of a row's parts [2][part][row]
+    static constexpr uint32_t ML_OFF = RECV_OFF + RECV;         // their references and sums [rank][row][2]
+    static constexpr uint32_t RECV_END = ML_OFF + BQ * 8, RAW_END = RECV_OFF + (F8 ? 2 * RAWS * RAW : 0);
+    static constexpr uint32_t X_OFF = RECV_END > RAW_END ? RECV_END : RAW_END;      // the exchange of a row's parts [2][part][row]
     static constexpr uint32_t BAR_OFF = X_OFF + 2 * PARTS * BQ * 4;
     static constexpr uint32_t MISC_OFF = BAR_OFF + 512;
     static constexpr size_t SMEM = MISC_OFF + 128;
@@ -107,8 +107,8 @@ struct Cfg {
     // barriers, in units of eight bytes
     static constexpr int B_Q = 0, B_ASKED = 1, B_S_FULL = 2, B_P_FULL = B_S_FULL + NS, B_PV_DONE = B_P_FULL + NS,
                          B_K_FULL = B_PV_DONE + NS, B_K_EMPTY = B_K_FULL + ST, B_V_FULL = B_K_EMPTY + ST,
-                         B_V_EMPTY = B_V_FULL + ST, B_RAW_FULL = B_V_EMPTY + ST, B_RAW_EMPTY = B_RAW_FULL + RAWS,
-                         B_COUNT = B_RAW_EMPTY + RAWS;
+                         B_V_EMPTY = B_V_FULL + ST, B_RAW_FULL = B_V_EMPTY + ST, B_RAW_EMPTY = B_RAW_FULL + 2 * RAWS,
+                         B_COUNT = B_RAW_EMPTY + 2 * RAWS;
     static_assert(8 * B_COUNT <= 512, "barriers");
     // more than half of an SM's shared memory, and so much that no other kernel with tensor memory fits beside
     static_assert(SMEM <= 227 * 1024 && SMEM >= 190 * 1024, "one CTA an SM");
@@ -279,17 +279,6 @@ __device__ __forceinline__ void widen_tile(uint32_t raw, int hd, uint32_t tile, 
         }
     }
 }
-
-// E4M3 tiles are brought and widened K0 K1 V0 K2 V1 ..: the n-th of 2 nt.
-struct Item {
-    bool k;
-    int t;
-    __device__ __forceinline__ Item(int n, int nt) {
-        const int u = n < 2 * nt - 1 ? n : 2 * nt;
-        k = u == 0 || (u & 1);
-        t = k ? (u + 1) / 2 : u / 2 - 1;
-    }
-};
 
 // grid (splits, (tree, kv head, row tile)); the splits are clusters of `cs` CTAs.
 template <int HD, bool F8>
@@ -544,56 +533,46 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         have = ok && warp_wait(pv_done((nt - 1) % NS), (nt - 1) / NS & 1, abort, a.err);
         tc_fence_after();
-    } else if (warp == K_WARP || (!F8 && warp == V_WARP)) {
-        // ---- K and V tiles (of an E4M3 cache on their way to the widening), once q has been asked for
+    } else if (warp == K_WARP || warp == V_WARP) {
+        // ---- K or V tiles (of an E4M3 cache on their way to the widening), once q has been asked for
         if (lane == 0) {
+            const bool k = warp == K_WARP;
             const int row = (int)(a.map_row0 + (long long)tr.seq * (a.kv.seq_stride / hd) + (long long)j * a.kv.n_ctx) + kt0 * BKEY;
-            bool ok = mbar_wait(bar + 8u * C::B_ASKED, 0, abort, a.err);
+            constexpr int N = F8 ? C::RAWS : ST;
+            constexpr uint32_t BYTES = F8 ? C::RAW : C::TILE;
+            const uint32_t ring = base_sm + (F8 ? C::RECV_OFF + (k ? 0 : N * BYTES) : k ? C::K_OFF : C::V_OFF);
+            const uint32_t full = F8 ? raw_full(k ? 0 : N) : k ? k_full(0) : v_full(0), empty = F8 ? raw_empty(k ? 0 : N) : k ? k_empty(0) : v_empty(0);
+            const bool ok = mbar_wait(bar + 8u * C::B_ASKED, 0, abort, a.err);
             int sent = 0;
-            if constexpr (F8) {
-                for (; ok && sent < 2 * nt; ++sent) {
-                    const int sl = sent % C::RAWS, use = sent / C::RAWS;
-                    const Item it(sent, nt);
-                    if (use > 0 && !mbar_wait(raw_empty(sl), (use - 1) & 1, abort, a.err)) break;
-                    mbar_expect_tx(raw_full(sl), (uint32_t)(BKEY * hd));
-                    tma_load_2d(base_sm + C::RECV_OFF + sl * C::RAW, it.k ? &tmK : &tmV, raw_full(sl), 0, row + it.t * BKEY);
-                }
-            } else {
-                const bool k = warp == K_WARP;
-                const uint32_t ring = base_sm + (k ? C::K_OFF : C::V_OFF), full = k ? k_full(0) : v_full(0), empty = k ? k_empty(0) : v_empty(0);
-                for (; ok && sent < nt; ++sent) {
-                    const int sl = sent % ST, use = sent / ST;
-                    if (use > 0 && !mbar_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
-                    mbar_expect_tx(full + 8u * sl, C::TILE);
-                    for (int i = 0; i < NBX; ++i)
-                        tma_load_2d(ring + sl * C::TILE + i * BOX, k ? &tmK : &tmV, full + 8u * sl, i * 64, row + sent * BKEY);
-                }
+            for (; ok && sent < nt; ++sent) {
+                const int sl = sent % N, use = sent / N;
+                if (use > 0 && !mbar_wait(empty + 8u * sl, (use - 1) & 1, abort, a.err)) break;
+                mbar_expect_tx(full + 8u * sl, F8 ? (uint32_t)(BKEY * hd) : BYTES);
+                for (int i = 0; i < (F8 ? 1 : NBX); ++i)
+                    tma_load_2d(ring + sl * BYTES + i * BOX, k ? &tmK : &tmV, full + 8u * sl, i * 64, row + sent * BKEY);
             }
             // after a timeout: wait (bounded) for the copies in flight before the memory is released
-            if (*abort) {
-                const int n = F8 ? C::RAWS : ST;
-                const uint32_t full = F8 ? raw_full(0) : warp == K_WARP ? k_full(0) : v_full(0);
-                for (int u = max(sent - n, 0); u < sent; ++u)
-                    for (uint32_t i = 0; i < WAIT_LIMIT && !mbar_try_wait(full + 8u * (u % n), u / n & 1); ++i) {
+            if (*abort)
+                for (int u = max(sent - N, 0); u < sent; ++u)
+                    for (uint32_t i = 0; i < WAIT_LIMIT && !mbar_try_wait(full + 8u * (u % N), u / N & 1); ++i) {
                     }
-            }
         }
     } else if (F8 && warp >= W_WARP) {
-        // ---- widening, K by the first half of the warps and V by the second (all of them in turn: 38.0 us, not 35.2)
+        // ---- widening, K by the first half of the warps and V by the second (all of them in turn: 38.0 us, not 35.2),
+        // each with a ring of its own, so that none waits for a phase it may be two behind
         const int ww = (warp - W_WARP) % (W_WARPS / 2);
-        const bool of_k = warp < W_WARP + W_WARPS / 2;
-        for (int u = 0; u < 2 * nt; ++u) {
-            const Item it(u, nt);
-            if (it.k != of_k) continue;
-            const int sl = it.t % ST, n = it.t / ST, rs = u % C::RAWS;
-            if (!warp_wait(raw_full(rs), u / C::RAWS & 1, abort, a.err)) break;
-            if (n > 0 && !warp_wait(it.k ? k_empty(sl) : v_empty(sl), (n - 1) & 1, abort, a.err)) break;
-            widen_tile<HD, F8>(base_sm + C::RECV_OFF + rs * C::RAW, hd, base_sm + (it.k ? C::K_OFF : C::V_OFF) + sl * C::TILE, ww, lane);
+        const bool k = warp < W_WARP + W_WARPS / 2;
+        const uint32_t raws = base_sm + C::RECV_OFF + (k ? 0 : C::RAWS * C::RAW), tiles = base_sm + (k ? C::K_OFF : C::V_OFF);
+        for (int t = 0; t < nt; ++t) {
+            const int sl = t % ST, rs = t % C::RAWS, ring = (k ? 0 : C::RAWS) + rs;
+            if (!warp_wait(raw_full(ring), t / C::RAWS & 1, abort, a.err)) break;
+            if (t >= ST && !warp_wait(k ? k_empty(sl) : v_empty(sl), (t / ST - 1) & 1, abort, a.err)) break;
+            widen_tile<HD, F8>(raws + rs * C::RAW, hd, tiles + sl * C::TILE, ww, lane);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(it.k ? k_full(sl) : v_full(sl));
-                mbar_arrive(raw_empty(rs));
+                mbar_arrive(k ? k_full(sl) : v_full(sl));
+                mbar_arrive(raw_empty(ring));
             }
         }
     } else if (warp == S_WARP) {

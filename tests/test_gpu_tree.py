@@ -312,6 +312,21 @@ def test_many_tiles_a_split(lib, hd, H, kt, n):
     t.check()
 
 
+@pytest.mark.parametrize("hd,kt", [(128, 0), (128, 1), (64, 0), (64, 1)])
+def test_repeats_over_many_tiles(lib, hd, kt):
+    """Splits of some twenty tiles: the rings of K and V go round often, whatever the order in which their tiles land."""
+    t = Trees(lib, hd, 32, 8, [(9900, 16), (9000, 5), (10000, 1), (7777, 12)], 10016, kt)
+    t.run()
+    t.check()
+    first, flush = t.O.clone(), torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(12):
+        t.O.fill_(9.0)
+        if i & 1:
+            flush.zero_()                         # K and V from memory, else from L2
+        t.run()
+        assert torch.equal(first, t.O)
+
+
 def test_many_trees(lib):
     """More groups than the GPU holds at once, some trees without nodes."""
     trees = [(37 * i % 400, i % 7) for i in range(90)]
