@@ -20,6 +20,10 @@
 // 32.8).  With four elements a lane the shuffles, addresses and branches of
 // twice as many lanes took 42.7 us, bound by issue.
 //
+// Rotated by halves ((e, e + n_rot / 2) instead of adjacent pairs) the 4096 rows take
+// 31.9 us, and 512 rows of heads of 64, half of each rotated, 3.1; the normed queries
+// and keys of 16 rows 1.8.
+//
 // Into a Q4_0 cache 512 rows take 7.2 us (4.8 into an fp16 one), 8 rows 3.7.
 //
 // Q4_0 codes are those of the exact values.  A float32 value carries a few
@@ -45,8 +49,8 @@ __device__ __forceinline__ float group_sum(float v) {
 
 constexpr int E = 8;                      // elements of a lane
 
-// The head's values after norm and rotation.
-template <int HD>
+// The head's values after norm and rotation: of the pairs of elements 2 k and 2 k + 1, or of k and k + 4 (SPLIT).
+template <int HD, bool SPLIT>
 __device__ __forceinline__ void transform(const float (&x)[E], const float (&gain)[E], const float2 (&cs)[E / 2], bool norm,
                                           bool turn, float eps, float (&u)[E]) {
     // the shuffles run for every lane: heads without a norm share the warp
@@ -56,11 +60,12 @@ __device__ __forceinline__ void transform(const float (&x)[E], const float (&gai
     ss = group_sum<HD / E>(ss);
     const float r = rsqrtf(ss / (float)HD + eps);                    // 2 ulp
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        const float a = norm ? x[e] * r * gain[e] : x[e], b = norm ? x[e + 1] * r * gain[e + 1] : x[e + 1];
-        const float2 c = cs[e / 2];
-        u[e] = turn ? a * c.x - b * c.y : a;
-        u[e + 1] = turn ? a * c.y + b * c.x : b;
+    for (int k = 0; k < E / 2; ++k) {
+        const int i = SPLIT ? k : 2 * k, j = SPLIT ? k + E / 2 : 2 * k + 1;
+        const float a = norm ? x[i] * r * gain[i] : x[i], b = norm ? x[j] * r * gain[j] : x[j];
+        const float2 c = cs[k];
+        u[i] = turn ? a * c.x - b * c.y : a;
+        u[j] = turn ? a * c.y + b * c.x : b;
     }
 }
 
@@ -97,7 +102,8 @@ __device__ __forceinline__ void transform(const float (&x)[E], const float (&gai
     }
 }
 
-// Rotation by halves: element e < half of a head turns with element e + half,
+// Rotation by halves into a Q4_0 cache, whose words are of eight neighbouring
+// elements: element e < half of a head turns with element e + half,
 // half = n_rot / 2 a multiple of 4.  A lane's partners are whole groups of four
 // elements in other lanes of the head, fetched after the norm (shuffles; reading
 // them again from memory would also need their gains).
@@ -242,26 +248,48 @@ __device__ __forceinline__ void encode_exact(const float (&u)[E], bool used, int
     }
 }
 
-__device__ __forceinline__ void load8(float (&v)[E], const float *p) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+// four elements at p and four `apart` behind
+__device__ __forceinline__ void load8(float (&v)[E], const float *p, int apart = 4) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + apart);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// eight values, four at p and four `apart` behind
+__device__ __forceinline__ void store8(f16 *p, int apart, const uint4 &v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2 *>(p + apart) = make_uint2(v.z, v.w);
+}
+__device__ __forceinline__ void store8(uint8_t *p, int apart, const uint2 &v) {
+    *reinterpret_cast<uint32_t *>(p) = v.x;
+    *reinterpret_cast<uint32_t *>(p + apart) = v.y;
+}
+
+// What of a head is rotated: all of it in adjacent pairs, its first n_rot elements in
+// pairs (one more register, with which the first form would spill), or those by halves.
+enum { WHOLE, PART, HALVES };
+
 // grid (row, part): part p of gridDim.y takes the warps' heads p, p + parts, ..
 // Q4: the cache is Q4_0 (its exact path would take registers from the others).
-// HALF: rotation by halves instead of adjacent pairs.
-// Four or five CTAs an SM keep the loads in flight (three by halves, whose
-// partners and signed sines take registers).
-template <int HD, bool Q4, bool HALF>
-__global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_kernel(const QkNormArgs a) {
+// By halves a lane that turns takes
+// four elements and their four partners, half a rotation behind (SPLIT), so that the
+// pairs are its own; only words of Q4_0 codes need neighbours and their partners from
+// other lanes.  (With neighbours and shuffles for every cache 4096 rows took 41.4 us.)
+// Four or five CTAs an SM keep the loads in flight (three where partners and signed
+// sines take registers; by halves five spill: 512 rows 4.1 us instead of 3.1).
+template <int HD, bool Q4, int ROT>
+__global__ void __launch_bounds__(THREADS, Q4 ? ROT == HALVES ? 3 : 4 : ROT == HALVES ? 4 : 5) qk_norm_rope_kernel(const QkNormArgs a) {
     constexpr int L = HD / E, PER = 32 / L;           // lanes of a head, heads of a warp at once
+    constexpr bool FETCH = ROT == HALVES && Q4, SPLIT = ROT == HALVES && !Q4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, e0 = E * sub;
     const int Hkv = a.kv.n_kv_head, heads = a.H + 2 * Hkv;
     const int t = blockIdx.x;
     int h0 = ((int)blockIdx.y * (THREADS / 32) + warp) * PER;        // the warp's first head
     const int step = (int)gridDim.y * (THREADS / 32) * PER;
-    const float *row = a.qkv + (size_t)t * a.ld + e0;
+    // the lane's elements: four at lo, four at lo + apart; they turn whole or (but with partners to fetch) not at all
+    const bool mine = ROT == WHOLE || FETCH || e0 < a.n_rot;
+    const int lo = SPLIT && mine ? e0 / 2 : e0, apart = SPLIT && mine ? a.n_rot / 2 : 4;
+    const float *row = a.qkv + (size_t)t * a.ld + lo;
     // every lane stays for the shuffles; heads past the last repeat it and store nothing
     const float *first = row + (size_t)min(h0 + lane / L, heads - 1) * HD;
     float next[E];
@@ -269,15 +297,14 @@ __global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_k
         pdl_wait();
         pdl_trigger();
         if (h0 >= heads) return;                      // whole warps
-        load8(next, first);
+        load8(next, first, apart);
     }
     const int pos = a.pos[t], cell = a.cell[t], seq = a.seq[t];
     const bool ok = pos >= 0 && pos < a.n_pos && cell >= 0 && cell < a.kv.n_ctx && seq >= 0 && seq < a.kv.n_seq;
     const Halves hv(a.n_rot, sub, lane);
-    const bool mine = HALF || e0 < a.n_rot;           // by pairs a lane turns whole or not at all
-    const float2 *angles = a.rope + (size_t)(ok ? pos : 0) * (a.n_rot / 2);
-    float2 turn[HALF ? E : E / 2];
-    if constexpr (HALF) hv.turn(angles, ok, sub, a.n_rot, turn);
+    const float2 *angles = a.rope + (size_t)(ok ? pos : 0) * ((ROT == WHOLE ? HD : a.n_rot) / 2);
+    float2 turn[FETCH ? E : E / 2];
+    if constexpr (FETCH) hv.turn(angles, ok, sub, a.n_rot, turn);
     else {
 #pragma unroll
         for (int e = 0; e < E / 2; e += 2) {
@@ -291,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_k
         pdl_wait();
         pdl_trigger();
         if (h0 >= heads) return;
-        load8(next, first);
+        load8(next, first, apart);
     }
     if (!ok && h0 == 0 && lane == 0) raise_error(a.err, ERRF_BAD_INDEX);
     bool out_of_range = false;
@@ -300,31 +327,31 @@ __global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_k
         float x[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = next[e];
-        if (h0 + step < heads) load8(next, row + (size_t)min(h + step, heads - 1) * HD);
+        if (h0 + step < heads) load8(next, row + (size_t)min(h + step, heads - 1) * HD, apart);
         const bool in = h < heads, is_q = h < a.H, is_k = !is_q && h < a.H + Hkv;
         const float *gp = is_q ? a.q_gain : is_k ? a.k_gain : nullptr;
         float gain[E];
-        if (gp) load8(gain, gp + e0);                 // a few cache lines, the same for every row
+        if (gp) load8(gain, gp + lo, apart);                 // a few cache lines, the same for every row
         else {
 #pragma unroll
             for (int e = 0; e < E; ++e) gain[e] = 1.f;
         }
         float u[E];
-        if constexpr (HALF) transform<HD>(x, gain, turn, hv, gp != nullptr, is_q || is_k, a.eps, u);
-        else transform<HD>(x, gain, turn, gp != nullptr, (is_q || is_k) && mine, a.eps, u);
+        if constexpr (FETCH) transform<HD>(x, gain, turn, hv, gp != nullptr, is_q || is_k, a.eps, u);
+        else transform<HD, SPLIT>(x, gain, turn, gp != nullptr, (is_q || is_k) && mine, a.eps, u);
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) bad |= f16_bad(u[e]);
         const uint4 packed = make_uint4(pack_h2(u[0], u[1]), pack_h2(u[2], u[3]), pack_h2(u[4], u[5]), pack_h2(u[6], u[7]));
         if (is_q && in) {
-            const size_t off = (size_t)t * a.H * HD + (size_t)h * HD + e0;
+            const size_t off = (size_t)t * a.H * HD + (size_t)h * HD + lo;
             if (a.q32) {                              // a row outside the cache has zero queries
-                float4 *q = reinterpret_cast<float4 *>(a.q32 + off);
-                q[0] = ok ? make_float4(u[0], u[1], u[2], u[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                q[1] = ok ? make_float4(u[4], u[5], u[6], u[7]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(a.q32 + off) = ok ? make_float4(u[0], u[1], u[2], u[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4 *>(a.q32 + off + apart) = ok ? make_float4(u[4], u[5], u[6], u[7]) : make_float4(0.f, 0.f, 0.f, 0.f);
             } else {
                 out_of_range |= bad && ok;
-                *reinterpret_cast<uint4 *>(a.q16 + off) = ok ? packed : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (SPLIT) store8(a.q16 + off, apart, ok ? packed : make_uint4(0u, 0u, 0u, 0u));
+                else *reinterpret_cast<uint4 *>(a.q16 + off) = ok ? packed : make_uint4(0u, 0u, 0u, 0u);
             }
         }
         const bool put = in && ok && !is_q;
@@ -335,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_k
             float d;
             uint32_t word;
             encode_exact(u, put, lane, d, word, [&](float up, q4::Pair (&u2)[E]) {
-                if constexpr (HALF) transform<HD>(x, gain, turn, hv, gp != nullptr, is_k, a.eps, up, u2);
+                if constexpr (FETCH) transform<HD>(x, gain, turn, hv, gp != nullptr, is_k, a.eps, up, u2);
                 else transform<HD>(x, gain, turn, gp != nullptr, is_k && mine, a.eps, up, u2);
             });
             if (put) {
@@ -346,12 +373,16 @@ __global__ void __launch_bounds__(THREADS, HALF ? 3 : Q4 ? 4 : 5) qk_norm_rope_k
             }
         } else if (put) {
             if (a.kv.k8) {
-                *reinterpret_cast<uint2 *>((is_k ? a.kv.k8 : a.kv.v8) + base + e0) =
-                    make_uint2((uint32_t)pack_e4m3x2(u[0], u[1]) | (uint32_t)pack_e4m3x2(u[2], u[3]) << 16,
-                               (uint32_t)pack_e4m3x2(u[4], u[5]) | (uint32_t)pack_e4m3x2(u[6], u[7]) << 16);
+                uint8_t *to = (is_k ? a.kv.k8 : a.kv.v8) + base + lo;
+                const uint2 codes = make_uint2((uint32_t)pack_e4m3x2(u[0], u[1]) | (uint32_t)pack_e4m3x2(u[2], u[3]) << 16,
+                                               (uint32_t)pack_e4m3x2(u[4], u[5]) | (uint32_t)pack_e4m3x2(u[6], u[7]) << 16);
+                if constexpr (SPLIT) store8(to, apart, codes);
+                else *reinterpret_cast<uint2 *>(to) = codes;
             } else {
                 out_of_range |= bad;
-                *reinterpret_cast<uint4 *>((is_k ? a.kv.k : a.kv.v) + base + e0) = packed;
+                f16 *to = (is_k ? a.kv.k : a.kv.v) + base + lo;
+                if constexpr (SPLIT) store8(to, apart, packed);
+                else *reinterpret_cast<uint4 *>(to) = packed;
             }
         }
     }
@@ -390,7 +421,7 @@ __global__ void __launch_bounds__(SHIFT_THREADS) kv_shift_q4_kernel(KvView kv, i
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = (float)((int)((w >> q4::shift_of(e)) & 15u) - 8) * d;     // exact
         uint32_t out;
-        transform<HD>(x, gain, back, false, true, 0.f, u);
+        transform<HD, false>(x, gain, back, false, true, 0.f, u);
         encode_exact(u, true, lane, nd, out,
                      [&](float up, q4::Pair (&u2)[E]) { transform<HD>(x, gain, back, false, true, 0.f, up, u2); });
         __syncthreads();
@@ -427,9 +458,10 @@ cudaError_t launch_kv_shift_q4(const KvView &kv0, int n_layer, int seq, int p0, 
 template <int HD>
 static cudaError_t launch_qk(const QkNormArgs &a, dim3 grid, const Launch &l) {
     const dim3 block(THREADS);
-    if (a.halves)
-        return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<HD, true, true> : qk_norm_rope_kernel<HD, false, true>, grid, block, 0, l, a);
-    return launch_kernel(a.kv.k4 ? qk_norm_rope_kernel<HD, true, false> : qk_norm_rope_kernel<HD, false, false>, grid, block, 0, l, a);
+    const bool q4 = a.kv.k4;
+    if (a.halves) return launch_kernel(q4 ? qk_norm_rope_kernel<HD, true, HALVES> : qk_norm_rope_kernel<HD, false, HALVES>, grid, block, 0, l, a);
+    if (a.n_rot < HD) return launch_kernel(q4 ? qk_norm_rope_kernel<HD, true, PART> : qk_norm_rope_kernel<HD, false, PART>, grid, block, 0, l, a);
+    return launch_kernel(q4 ? qk_norm_rope_kernel<HD, true, WHOLE> : qk_norm_rope_kernel<HD, false, WHOLE>, grid, block, 0, l, a);
 }
 
 cudaError_t launch_qk_norm_rope(const QkNormArgs &a0, const Launch &l) {
