@@ -13,6 +13,11 @@ fp16's smallest normal).  What the fp32 arithmetic before it adds:
       exponent's error, and with it the weights' relative one; 2^-19 more for the
       weights' 22 bits, the exponential and the sums.  Both are relative to the
       weighted sum of |V|."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -449,6 +454,207 @@ def test_streams_graphs_and_scratch(lib):
         t.O.fill_(9.0)
         t.run(scratch=big)
         t.check()
+
+
+FIRST_IN_CAPTURE = """
+import sys
+sys.path.insert(0, {root!r}); sys.path.insert(0, {tests!r})
+import torch
+import test_gpu_tree as t
+import llama_decoder_forward_02_gb300 as lib
+a = t.Trees(lib, {hd}, 8, 2, [(900, 12), (30, 4)], 1000, {kt})
+r = lib.rope(10000.0, 64)
+tab = torch.zeros((100, 32, 2), device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a.run()
+    lib.check(lib.llm_op_rope_table(r, 0, 100, tab.data_ptr(), t.stream()))
+g.replay()
+a.check()
+assert torch.all(tab[0, :, 0] == 1) and torch.all(tab[1:, 0, 1] != 0)
+"""
+
+
+@pytest.mark.parametrize("hd,kt", [(128, 0), (64, 1)])
+def test_first_calls_of_a_process_captured(lib, hd, kt):
+    """The calls' set-up of the device does not disturb a capture that runs before any other call."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_IN_CAPTURE.format(root=os.path.dirname(tests), tests=tests, hd=hd, kt=kt)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_calls_of_two_threads(lib):
+    """Two threads that call at once, on a stream and with a scratch each."""
+    parts = [Trees(lib, 128, 8, 2, [(1500, 16), (77, 3)], 1600, seed=1), Trees(lib, 64, 12, 4, [(600, 40)], 700, 1, seed=2)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(t):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    t.run()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(t,)) for t in parts]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed
+    for t in parts:
+        t.check()
+
+
+def test_windows_of_any_size(lib):
+    """Positions and windows at the ends of their type: what pos - window would be passes 32 bits."""
+    t = Trees(lib, 64, 4, 2, [(300, 6), (200, 3)], 400, window=2 ** 31 - 1)
+    t.run()
+    t.check()
+    whole = t.O.clone()
+    t.POS[:] = -2 ** 31
+    t.run()
+    assert torch.equal(whole, t.O)                 # every earlier cell is inside
+    t.POS[:] = 2 ** 31 - 1
+    t.window = 1
+    t.run()
+    t.pos[:] = 2 ** 31 - 1                         # none is
+    t.check()
+
+
+@pytest.mark.parametrize("hd,kt", [(128, 0), (64, 1)])
+def test_values_that_are_not_finite(lib, hd, kt):
+    """In a query: its row and head alone; in a key or value that some rows see: theirs, of the heads of its kv head."""
+    t = Trees(lib, hd, 8, 2, [(400, 10)], 500, kt)
+    clean = t.run().view(t.T, 8, hd).clone()
+    q = t.Q.clone()
+    t.Q[3, 5, 7] = float("inf")
+    t.Q[4, 0, 0] = float("nan")
+    t.run()
+    got = t.O.view(t.T, 8, hd)
+    hit = torch.zeros((t.T, 8), dtype=torch.bool, device="cuda")
+    hit[3, 5] = hit[4, 0] = True
+    assert torch.equal(got[~hit], clean[~hit])
+    assert not torch.isfinite(got[hit]).any()
+    t.Q.copy_(q)
+    node = 4
+    sees = torch.from_numpy(t.seen[0][:, node]).cuda()
+    assert sees.any() and not sees.all()
+    for c in t.KV:
+        keep = c.clone()
+        (c.view(torch.uint8) if kt else c)[t.seq[0], 1, 400 + node, 3] = 0x7f if kt else float("nan")
+        t.run()
+        got = t.O.view(t.T, 8, hd)
+        assert torch.equal(got[:, :4], clean[:, :4]) and torch.equal(got[~sees], clean[~sees])
+        bad = ~torch.isfinite(got[sees][:, 4:])
+        assert bad.any(-1).all()
+        c.copy_(keep)
+
+
+def test_captured_step_replayed(lib):
+    """Rotation, attention and acceptance as one graph, replayed on other inputs in the same memory: each replay as eager calls."""
+    H, Hkv, hd, n_ctx, n, base = 8, 2, 64, 200, 9, 100
+    rng = np.random.default_rng(5)
+    par = U.parents(rng, n)
+    tab = torch.empty((n_ctx, hd // 2, 2), device="cuda")
+    lib.check(lib.llm_op_rope_table(lib.rope(10000.0, hd), 0, n_ctx, tab.data_ptr(), stream()))
+    R, S, B, C = ints([0, n]), ints([0]), ints([base]), ints(base + np.arange(n))
+    P, M, pr = ints(base + U.depths(par)), dev(U.pack_mask(U.ancestors(par), n).view(np.int32)), ints(par)
+    x, tok, tgt = torch.empty((n, (H + 2 * Hkv) * hd), device="cuda"), ints([0] * n), ints([0] * n)
+    kv = [torch.empty((1, Hkv, n_ctx, hd), dtype=torch.float16, device="cuda") for _ in range(2)]
+    q, o = (torch.empty((n, H * hd), dtype=torch.float16, device="cuda") for _ in range(2))
+    path, count, nxt = torch.empty((1, n), dtype=torch.int32, device="cuda"), ints([0]), ints([0])
+    sc = torch.zeros(lib.llm_op_attn_tree_scratch_bytes(1, n, H, Hkv, hd, n_ctx), dtype=torch.uint8, device="cuda")
+
+    def step():
+        lib.check(lib.llm_op_rope_kv(x.data_ptr(), x.shape[1], None, None, 0.0, tab.data_ptr(), n_ctx, hd, 1, P.data_ptr(),
+                                     C.data_ptr(), zeros.data_ptr(), q.data_ptr(), 1, kv[0].data_ptr(), kv[1].data_ptr(), 0, n,
+                                     H, Hkv, hd, n_ctx, 1, None, stream()))
+        lib.check(lib.llm_op_attn_tree(q.data_ptr(), kv[0].data_ptr(), kv[1].data_ptr(), R.data_ptr(), S.data_ptr(), B.data_ptr(),
+                                       M.data_ptr(), None, o.data_ptr(), n, 1, n, H, Hkv, hd, n_ctx, 1, 0, 0, sc.data_ptr(),
+                                       sc.numel(), None, stream()))
+        lib.check(lib.llm_op_tree_accept(tok.data_ptr(), pr.data_ptr(), tgt.data_ptr(), R.data_ptr(), S.data_ptr(), B.data_ptr(),
+                                         kv[0].data_ptr(), kv[1].data_ptr(), 0, path.data_ptr(), count.data_ptr(), nxt.data_ptr(),
+                                         n, 1, n, 1, Hkv, hd, n_ctx, 1, None, stream()))
+    zeros = ints([0] * n)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(4):
+        x.copy_(dev(rng.standard_normal(x.shape).astype(np.float32)))
+        tok.copy_(ints(rng.integers(0, 3, n)))
+        tgt.copy_(ints(rng.integers(0, 3, n)))
+        past = [torch.randn_like(c) for c in kv]
+        outs = []
+        for call in (step, g.replay):
+            for c, p in zip(kv, past):
+                c.copy_(p)
+            o.fill_(9.0)
+            call()
+            outs.append([t.clone() for t in (*kv, o, path, count, nxt)])
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+        want, nx = U.accept(tok.cpu().numpy(), par, tgt.cpu().numpy())
+        assert path[0, :len(want)].tolist() == want and int(nxt) == nx
+
+
+def test_cells_past_32_bits(lib):
+    """A cache whose elements pass 2^31: rotation and append, attention and acceptance in its last sequence, and none elsewhere."""
+    H, Hkv, hd, n_ctx, n_seq, n, base = 4, 1, 128, 1048576 + 77, 17, 6, 1048576 + 60
+    at = n_seq - 1
+    assert at * n_ctx * hd > 2 ** 31
+    kv = [torch.zeros((n_seq, Hkv, n_ctx, hd), dtype=torch.float16, device="cuda") for _ in range(2)]
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    for c in kv:
+        c[at, 0, :base] = torch.randn((base, hd), generator=gen, device="cuda")
+    rng = np.random.default_rng(2)
+    par = np.array([-1, 0, 0, 2, 3, 1])
+    pos = base + U.depths(par)
+    tab = torch.empty((100, hd // 2, 2), device="cuda")
+    lib.check(lib.llm_op_rope_table(lib.rope(500000.0, hd), base, 100, tab.data_ptr(), stream()))
+    x = dev(rng.standard_normal((n, (H + 2 * Hkv) * hd)).astype(np.float32))
+    q, o = (torch.zeros((n, H * hd), dtype=torch.float16, device="cuda") for _ in range(2))
+    P, C, S = ints(U.depths(par)), ints(base + np.arange(n)), ints([at] * n)
+    E = err_word()
+    lib.check(lib.llm_op_rope_kv(x.data_ptr(), x.shape[1], None, None, 0.0, tab.data_ptr(), 100, hd, 0, P.data_ptr(), C.data_ptr(),
+                                 S.data_ptr(), q.data_ptr(), 1, kv[0].data_ptr(), kv[1].data_ptr(), 0, n, H, Hkv, hd, n_ctx, n_seq,
+                                 E.data_ptr(), stream()))
+    # the angles themselves are held against 64 bits above; here the rows have to stand in their cells
+    xs = x.cpu().double().numpy().reshape(n, H + 2 * Hkv, hd)
+    cs = tab.cpu().double().numpy()[U.depths(par)]
+    k_ref, v_ref = U.rotate(xs[:, H:H + 1], cs, hd, 0)[:, 0], xs[:, H + 1]
+    for c, ref in zip(kv, (k_ref, v_ref)):
+        got = c[at, 0, base:base + n].cpu().double().numpy()
+        assert np.all(np.abs(got - ref) <= U16 * np.abs(ref) + TINY16 + 12 * 2.0 ** -24 * 2 * np.abs(ref).max())
+    R, Q, B, M = ints([0, n]), ints([at]), ints([base]), dev(U.pack_mask(U.ancestors(par), n).view(np.int32))
+    sc = torch.zeros(lib.llm_op_attn_tree_scratch_bytes(1, n, H, Hkv, hd, n_ctx), dtype=torch.uint8, device="cuda")
+    lib.check(lib.llm_op_attn_tree(q.data_ptr(), kv[0].data_ptr(), kv[1].data_ptr(), R.data_ptr(), Q.data_ptr(), B.data_ptr(),
+                                   M.data_ptr(), None, o.data_ptr(), n, 1, n, H, Hkv, hd, n_ctx, n_seq, 0, 0, sc.data_ptr(),
+                                   sc.numel(), E.data_ptr(), stream()))
+    k, v = (c[at, 0, :base + n].double() for c in kv)
+    s = torch.einsum("nhd,cd->nhc", q.view(n, H, hd).double(), k) / hd ** 0.5
+    s[..., base:].masked_fill_(~torch.from_numpy(U.ancestors(par)).cuda()[:, None], float("-inf"))
+    w = torch.softmax(s, -1)
+    ref, mag = torch.einsum("nhc,cd->nhd", w, v), torch.einsum("nhc,cd->nhd", w, v.abs())
+    size = torch.sqrt(torch.einsum("nhd,cd->nhc", q.view(n, H, hd).double() ** 2, k ** 2)).amax(-1)
+    tol = U16 * ref.abs() + TINY16 + (2.0 ** -20 * size[..., None] + 2.0 ** -19) * mag
+    # more for a million cells: on 2^3 CTAs or more a sum of weights takes below 2^11 additions, off by 2^-24 each like a
+    # random walk, and a sum of products 2^4 steps a tile, 2^14 in all, off by 2^-23 each: 2^-18 and 2^-16
+    tol += (2.0 ** -18 + 2.0 ** -16) * mag
+    assert torch.all((o.view(n, H, hd).double() - ref).abs() <= tol)
+    token, target = ints([1, 2, 3, 4, 5, 6]), ints([3, 0, 4, 5, 9, 0])
+    rows = [c[at, 0, base:base + n].clone() for c in kv]
+    pr, path, count, nxt = ints(par), torch.empty((1, n), dtype=torch.int32, device="cuda"), ints([0]), ints([0])
+    lib.check(lib.llm_op_tree_accept(token.data_ptr(), pr.data_ptr(), target.data_ptr(), R.data_ptr(), Q.data_ptr(), B.data_ptr(),
+                                     kv[0].data_ptr(), kv[1].data_ptr(), 0, path.data_ptr(), count.data_ptr(), nxt.data_ptr(), n, 1,
+                                     n, 1, Hkv, hd, n_ctx, n_seq, E.data_ptr(), stream()))
+    assert path[0, :4].tolist() == [0, 2, 3, 4] and int(nxt) == 9 and int(E) == 0
+    for c, r in zip(kv, rows):
+        assert torch.equal(c[at, 0, base:base + 4], r[[0, 2, 3, 4]]) and torch.equal(c[at, 0, base + 4:base + n], r[4:])
+        assert not c[:at].any() and not c[at, 0, base + n:].any()
 
 
 # ---------------------------------------------------------------- acceptance
