@@ -343,7 +343,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     int lo = 0, lo_min = 0, lo_max = 0;
     if (a.window > 0) {
         if (warp < 4 && row_ok) {
-            lo = min(max(a.pos[tr.r0 + node] - a.window + 1, 0), base);
+            const int pos = a.pos[tr.r0 + node];          // any number
+            lo = pos >= a.window ? min(pos - a.window + 1, base) : 0;
             atomicMin(&misc.lo_min, lo);
             atomicMax(&misc.lo_max, lo);
             xch[r] = __int_as_float(lo);
