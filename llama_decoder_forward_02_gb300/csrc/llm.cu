@@ -1385,6 +1385,7 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
     const int rc = plan_batch(*b, m->V, c->n_ctx, c->n_seq_max, c->n_ubatch, c->seq_next, p);
     if (rc != LLM_OK) { c->last_error = p.error; return rc; }
     if (ensure_logits(c, p.n_outputs) != LLM_OK) return LLM_ERR_ALLOC;
+    c->tree.n = 0;                 // its cells are written over
     const bool dev_tok = (b->flags & LLM_BATCH_TOKENS_ON_DEVICE) != 0;
 
     // decode step: replay the captured graph
@@ -1467,7 +1468,6 @@ extern "C" int32_t llm_decode(llm_ctx *c, const llm_batch *b) {
     for (int i = 0; i < p.n; ++i) c->seq_next[p.seq[i]] = p.pos[i] + 1;
     c->out_index = p.out_index;
     c->n_outputs = p.n_outputs;
-    c->tree.n = 0;
     c->tree_logits = false;
     return LLM_OK;
 }
@@ -1705,6 +1705,7 @@ extern "C" int32_t llm_generate(llm_ctx *c, int32_t seq_id, int32_t n_steps, int
     hs[DEC_NSTEPS] = n_steps;
     CK(cudaMemcpyAsync(c->dec_dev, hs, DEC_INTS * sizeof(int), cudaMemcpyHostToDevice, c->stream));
     CK(cudaEventRecord(c->dec_ev[s], c->stream));
+    c->tree.n = 0;                 // its cells are written over
     const Launch L = lnch(c);
     int *step = c->dec_dev + DEC_STEP, *nst = c->dec_dev + DEC_NSTEPS;
     int *tok = c->dec_dev + DEC_TOK, *pos = c->dec_dev + DEC_POS;
@@ -1745,7 +1746,6 @@ extern "C" int32_t llm_generate(llm_ctx *c, int32_t seq_id, int32_t n_steps, int
         }
     }
     c->n_outputs = 1;
-    c->tree.n = 0;
     CK(cudaMemcpyAsync(tokens_out, c->gen_tokens, n_steps * sizeof(int), cudaMemcpyDeviceToDevice, c->stream));
     c->seq_next[seq_id] += n_steps;
     c->out_index.assign(1, 0);
