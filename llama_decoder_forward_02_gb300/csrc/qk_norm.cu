@@ -271,10 +271,10 @@ enum { WHOLE, PART, HALVES };
 
 // grid (row, part): part p of gridDim.y takes the warps' heads p, p + parts, ..
 // Q4: the cache is Q4_0 (its exact path would take registers from the others).
-// By halves a lane that turns takes
-// four elements and their four partners, half a rotation behind (SPLIT), so that the
-// pairs are its own; only words of Q4_0 codes need neighbours and their partners from
-// other lanes.  (With neighbours and shuffles for every cache 4096 rows took 41.4 us.)
+// By halves a lane that turns takes four elements and their four partners, half a
+// rotation behind (SPLIT), so that the pairs are its own; only words of Q4_0 codes need
+// neighbours, and their partners from other lanes (FETCH).  With neighbours and shuffles
+// for every cache 4096 rows took 41.4 us.
 // Four or five CTAs an SM keep the loads in flight (three where partners and signed
 // sines take registers; by halves five spill: 512 rows 4.1 us instead of 3.1).
 template <int HD, bool Q4, int ROT>
