@@ -12,11 +12,15 @@
 // the CTAs of a cluster, and where there are still SMs left over several clusters.
 //
 // Precision.  q, K and V are fp16 (an E4M3 value is one exactly); a weight
-// p = 2^(s c - R), the exponent in fp32 with one rounding, enters O as two fp16 numbers
-// of 22 bits together.  Rounded to one, o is off by 1.4 times its own rounding.  R is a
-// whole number, so that changing it is exact: the row's largest s c so far, rounded up,
-// less 7 (weights far below the largest stay normal fp16 numbers), raised, with O
-// rescaled, only when a tile passes it by 8 more.
+// p = 2^((s - z) c + x), the exponent in fp32 with one rounding, enters O as two fp16
+// numbers of 22 bits together.  Rounded to one, o is off by 1.4 times its own rounding.
+// z and x are a row's reference, raised, with O rescaled, only when a tile passes it by
+// 2^8.  Usually z is 0 and x a whole number, so that changing it is exact: 7 (weights far
+// below the largest stay normal fp16 numbers) less the row's largest s c so far, rounded
+// up.  From 2^22 on, where steps of fp32 would come to swallow the 7 and the row's
+// weights with it, z is the largest score so far and x is 7; a tile's scores are brought to
+// s - z in the branch that raises references, which other rows seldom take.  So a row's
+// largest weight lies in [2^6, 2^15] whatever its scores.
 //
 // A CTA: warps 0-7 softmax (two threads a row, 64 keys each), 8 issues S = q K^T, 9
 // O += P V, 10 brings K and 11 V by TMA, of an E4M3 cache to warps 12-15 and 16-19, which
@@ -65,6 +69,8 @@ using namespace tca;
 
 constexpr float LIFT = 7.f;                  // a row's largest weight is at least 2^(LIFT - 1), and
 constexpr float MOST = LIFT + 8.f;           // at most 2^MOST
+constexpr float FAR = 4194304.f;             // s c from which on a reference is a score (whole numbers are exact up to 2^24)
+constexpr float NONE = 1e30f;                // x of a row without a reference, which is below every other
 constexpr int BQ = 128, BKEY = 128;
 constexpr int SM_WARPS = 8, PARTS = 2, S_WARP = 8, PV_WARP = 9, K_WARP = 10, V_WARP = 11, W_WARP = 12, W_WARPS = 8;
 constexpr int threads(bool f8) { return (W_WARP + (f8 ? W_WARPS : 0)) * 32; }
@@ -92,8 +98,8 @@ struct Cfg {
     // rows of O from the other ranks; before them, once every rank has read its own, the E4M3 tiles
     static constexpr uint32_t RECV_OFF = V_OFF + ST * TILE;
     static constexpr uint32_t RECV = BQ * HD * 4 / MAX_CLUSTER * (MAX_CLUSTER - 1);
-    static constexpr uint32_t ML_OFF = RECV_OFF + RECV;         // their references and sums [rank][row][2]
-    static constexpr uint32_t RECV_END = ML_OFF + BQ * 8, RAW_END = RECV_OFF + (F8 ? 2 * RAWS * RAW : 0);
+    static constexpr uint32_t ML_OFF = RECV_OFF + RECV;         // their references and sums [rank][row][4]
+    static constexpr uint32_t RECV_END = ML_OFF + BQ * 16, RAW_END = RECV_OFF + (F8 ? 2 * RAWS * RAW : 0);
     static constexpr uint32_t X_OFF = RECV_END > RAW_END ? RECV_END : RAW_END;      // the exchange of a row's parts [2][part][row]
     static constexpr uint32_t BAR_OFF = X_OFF + 2 * PARTS * BQ * 4;
     static constexpr uint32_t MISC_OFF = BAR_OFF + 512;
@@ -119,6 +125,7 @@ struct Misc {
     int abort;
     uint32_t tmem;
     int lo_min, lo_max;                       // the rows' first visible cells
+    int base, end;                            // the tree's
     uint32_t bad[3][4];                       // keys of a tile whose V is not finite, three tiles in turn
     int last;
 };
@@ -233,6 +240,27 @@ struct Tree {
     }
 };
 
+// A row's reference: weights are 2^((s - z) c + x).
+struct Ref { float z, x; };
+// The exponent of the factor that takes sums from one reference to another: of usual ones the difference of x exactly, else with
+// one rounding.
+__device__ __forceinline__ float shift(const Ref &from, const Ref &to, float c) { return fmaf(from.z - to.z, c, to.x - from.x); }
+
+// Joined, references are pairs of floats R + R2, R2 zero but for scores; the highest has the largest R, and of those the
+// largest R2.
+template <typename Of>
+__device__ __forceinline__ float rest_of(float M, int n, Of &&of) {
+    float M2 = -INFINITY;
+#pragma unroll 1
+    for (int s = 0; s < n; ++s) {
+        const float4 v = of(s);
+        if (v.x == M) M2 = fmaxf(M2, v.z);
+    }
+    return M2;
+}
+// The factor from one to another.  R - M is exact where that matters, within a factor of two.
+__device__ __forceinline__ float moved(float R, float R2, float M, float M2) { return ex2((R - M) + (R2 - M2)); }
+
 // Which of the keys k0 .. k0 + 31 a row sees: those from lo to base, and by the bits
 // of its mask those from base to end.
 __device__ __forceinline__ uint32_t visible(int k0, int lo, int base, int end, const uint32_t *mask, int words) {
@@ -294,7 +322,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const uint32_t base_sm = smem_u32(smem_raw);
     Misc &misc = *reinterpret_cast<Misc *>(smem_raw + C::MISC_OFF);
     float *const xch = reinterpret_cast<float *>(smem_raw + C::X_OFF);
-    float2 *const ml = reinterpret_cast<float2 *>(smem_raw + C::ML_OFF);
+    float4 *const ml = reinterpret_cast<float4 *>(smem_raw + C::ML_OFF);        // R, sum, R2
     const uint32_t bar = base_sm + C::BAR_OFF;
     auto s_full = [&](int b) { return bar + 8u * (C::B_S_FULL + b); };
     auto p_full = [&](int b) { return bar + 8u * (C::B_P_FULL + b); };        // P_t written
@@ -330,6 +358,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         misc.abort = 0;
         misc.lo_min = a.kv.n_ctx;
         misc.lo_max = 0;
+        misc.base = tr.base;
+        misc.end = tr.base + tr.n;
         for (int i = 0; i < 12; ++i) misc.bad[i / 4][i % 4] = 0u;
     }
     tc_fence_before();
@@ -364,7 +394,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int kt0 = first + (int)((long long)all * split / S), nt = first + (int)((long long)all * (split + 1) / S) - kt0;
 
     const float c = 1.4426950408889634f / sqrtf((float)hd);       // scores to exponents of two
-    float R = -INFINITY, l_row = 0.f;                    // weights are 2^(s c - R)
+    Ref ref{0.f, NONE};
+    float l_row = 0.f;
     bool have = false;                                   // O holds this CTA's sums
     if constexpr (F8) {
         // no warp waits for another before its own of these three, so the softmax's does end
@@ -412,14 +443,17 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // reached by all their threads; after a timeout the iterations only pass them
         bool ok = true;
         int edges = 0;
+        const int whole_from = (lo_max + BKEY - 1) / BKEY - kt0, whole_to = base / BKEY - kt0;      // tiles that every row sees whole
         float l_run = 0.f, both[PARTS];
         int b = 0, round = 0;                                // t % NS, t / NS
         for (int t = 0; t < nt; ++t, b = b + 1 == NS ? 0 : b + 1, round += b == 0) {
             const int tile0 = (kt0 + t) * BKEY;
             const uint32_t s_col = lane_base + b * BKEY + part * HK;
-            const bool edge = tile0 + BKEY > base || tile0 < lo_max;       // not every row sees the whole tile
+            const bool edge = t >= whole_to || t < whole_from;       // not every row sees the whole tile
             uint32_t vis[2] = {~0u, ~0u}, nan[2] = {0u, 0u};
             if (edge) {
+                const volatile Misc &now = misc;             // held through the loop they spill: ragged trees 23.1 us, not 22.4
+                const int base = now.base, end = now.end;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
                     vis[q] = row_ok ? visible(tile0 + part * HK + 32 * q, lo, base, end, a.mask + (size_t)(tr.r0 + node) * a.words, a.words) : 0u;
@@ -482,38 +516,47 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 post(t, mx);
                 collect(t, both);
                 mx = fmaxf(both[0], both[1]);
-                const float top = __fmul_ru(mx, c);
-                float factor = 1.f;
-                const bool raise = ok && mx != -INFINITY && !(top - R <= MOST);
-                if (raise) {
-                    const float to = __fsub_ru(ceilf(top), LIFT);
-                    factor = R == -INFINITY ? 0.f : ex2(R - to);
-                    R = to;
-                }
-                // a raised reference rescales O, which P_{t-1} V_{t-1} must have finished
-                if (t >= 1 && __any_sync(0xffffffffu, raise)) {
-                    ok = warp_wait(pv_done(b == 0 ? NS - 1 : b - 1), (b == 0 ? round - 1 : round) & 1, abort, a.err);
-                    tc_fence_after();
+                const bool raise = ok && mx != -INFINITY && !(fmaf(mx - ref.z, c, ref.x) <= MOST);
+                if (__any_sync(0xffffffffu, raise || ref.z != 0.f)) {
+                    float factor = 1.f;
+                    if (raise) {
+                        const float top = __fmul_ru(mx, c);
+                        const bool score = fabsf(top) >= FAR && top < INFINITY;
+                        const Ref to{score ? mx : 0.f, score ? LIFT : LIFT - ceilf(top)};
+                        factor = ex2(shift(ref, to, c));
+                        ref = to;
+                    }
+                    l_run *= factor;
+                    // a raised reference rescales O, which P_{t-1} V_{t-1} must have finished
+                    if (t >= 1) {
+                        ok = warp_wait(pv_done(b == 0 ? NS - 1 : b - 1), (b == 0 ? round - 1 : round) & 1, abort, a.err);
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int q = 0; ok && q < HD / 64; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(lane_base + o_col + 32 * q, o);
+                        for (int q = 0; ok && q < HD / 64; ++q) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_base + o_col + 32 * q, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-                        tmem_st32(lane_base + o_col + 32 * q, o);
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                            tmem_st32(lane_base + o_col + 32 * q, o);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, ref.z != 0.f)) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[q][i] = __float_as_uint(__uint_as_float(v[q][i]) - ref.z);
                     }
                 }
                 if (ok) {
                     // the part's weights over the columns of S they came from: 16 of hi pairs, 16 of lo pairs
-                    const float less = R == -INFINITY ? 0.f : -R;
-                    const unsigned long long c2 = pack2(c, c), less2 = pack2(less, less);
+                    const unsigned long long c2 = pack2(c, c), x2 = pack2(ref.x, ref.x);
                     unsigned long long rs[2] = {0ull, 0ull};
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t p[32];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2, less2));
+                            const float2 x = unpack2(fma2(pack2(__uint_as_float(v[q][2 * i]), __uint_as_float(v[q][2 * i + 1])), c2, x2));
                             const float p0 = ex2(x.x), p1 = ex2(x.y);
                             rs[i & 1] = add2(rs[i & 1], pack2(p0, p1));
                             split_pair(p0, p1, p[i], p[16 + i]);
@@ -522,7 +565,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     }
                     tmem_put_done();
                     const float2 sum = unpack2(add2(rs[0], rs[1]));
-                    l_run = l_run * factor + (sum.x + sum.y);
+                    l_run += sum.x + sum.y;
                     tc_fence_before();
                 }
             }
@@ -646,7 +689,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     };
     if (warp < 4 && r < rows) {
         const int to = r / share, at = r - to * share;
-        dsmem_st_u64(dsmem(ml + rank * share + at, to), (unsigned long long)__float_as_uint(l_row) << 32 | __float_as_uint(R));
+        const float R = ref.z == 0.f ? -ref.x : __fmul_rn(ref.z, c), R2 = ref.z == 0.f ? 0.f : fmaf(ref.z, c, -R) - ref.x;
+        dsmem_st_f32x4(dsmem(ml + rank * share + at, to), make_float4(R, l_row, R2, 0.f));
     }
     if (warp < SM_WARPS && (warp & 3) * 32 < rows && have) {       // whole warps, as tensor memory is read
         const int part = warp >> 2, to = min(r / share, cs - 1), at = r - to * share;
@@ -687,13 +731,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     };
     for (int i = tid; i < my_rows * per; i += threads(F8)) {
         const int at = i / per, chunk = i - at * per;
-        float M = -INFINITY, L = 0.f;
+        float M = -INFINITY, M2 = 0.f, L = 0.f;
         for (int s = 0; s < cs; ++s) M = fmaxf(M, ml[s * share + at].x);
+        if (__builtin_expect(fabsf(M) >= FAR / 2, 0)) M2 = rest_of(M, cs, [&](int s) { return ml[s * share + at]; });
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < cs; ++s) {
-            const float2 v = ml[s * share + at];
+            const float4 v = ml[s * share + at];
             if (v.y == 0.f) continue;                    // that rank saw nothing of the row
-            const float f = ex2(v.x - M);
+            const float f = moved(v.x, v.z, M, M2);
             const float4 x = *reinterpret_cast<const float4 *>(smem_raw + part_at(s, rank) + (uint32_t)at * (HD * 4) + ((chunk ^ (at & 7)) << 4));
             L = fmaf(f, v.y, L);
             o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
@@ -705,7 +750,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         } else {
             float *dst = slot_o(mine, row);
             __stcg(reinterpret_cast<float4 *>(dst) + chunk, o);
-            if (chunk == 0) __stcg(reinterpret_cast<float2 *>(dst + HD), make_float2(M, L));
+            if (chunk == 0) __stcg(reinterpret_cast<float4 *>(dst + HD), make_float4(M, L, M2, 0.f));
         }
     }
     if (clusters == 1) return;
@@ -722,14 +767,16 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     if (!misc.last) return;
     for (int i = tid; i < my_rows * per; i += threads(F8)) {
         const int at = i / per, chunk = i - at * per, row = rank * share + at;
-        float M = -INFINITY, L = 0.f;
+        auto sums = [&](int s) { return __ldcg(reinterpret_cast<const float4 *>(slot_o(s, row) + HD)); };
+        float M = -INFINITY, M2 = 0.f, L = 0.f;
         for (int s = 0; s < clusters; ++s) M = fmaxf(M, __ldcg(slot_o(s, row) + HD));
+        if (__builtin_expect(fabsf(M) >= FAR / 2, 0)) M2 = rest_of(M, clusters, sums);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < clusters; ++s) {
             const float *src = slot_o(s, row);
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src + HD));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + HD));
             if (v.y == 0.f) continue;
-            const float f = ex2(v.x - M);
+            const float f = moved(v.x, v.z, M, M2);
             const float4 x = __ldcg(reinterpret_cast<const float4 *>(src) + chunk);
             L = fmaf(f, v.y, L);
             o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
