@@ -775,8 +775,9 @@ int32_t llm_op_rope_kv(const float *qkv, int32_t ld, const float *q_gain, const 
  *            it ready for the next, of any shape it is large enough for, and calls
  *            that may overlap need one each
  * q, K and V enter the products exactly and the softmax weights with 22 bits (below
- * 2^-21 of the row's largest with 2^-31 of it); sums are fp32.  A visible cell with an infinity or a NaN
- * gives the heads that see it values that are not finite; cells that a row does
+ * 2^-21 of the row's largest with 2^-31 of it); sums are fp32.  A score of -inf has
+ * weight 0, and a row that sees no other is NaN; a score of +inf or NaN, or a visible
+ * value that is not finite, gives its row and head values that are not finite; cells that a row does
  * not see may hold anything.  head_dim 32, 64 or 128; any H that is a multiple of
  * Hkv, up to 4096, with n_tree * Hkv * ceil(max_nodes * H / Hkv / 128) at most 65535;
  * q, the caches, o and scratch 16-byte aligned; else LLM_ERR_INVALID before

@@ -4,7 +4,8 @@
 // cells and the path to it): for row t of tree i and query head h
 //   o[t][h] = softmax_c(q[t][h] . K[c] / sqrt(hd)) V[c]
 // over the cells c < base[i] (with a window those c > pos[t] - window) and the
-// cells base[i] + j whose bit j of mask[t] is set.  A row that sees nothing is zero.
+// cells base[i] + j whose bit j of mask[t] is set.  A row that sees nothing is zero; one
+// that sees scores of -inf alone is NaN.
 //
 // The rows of a tree that share a kv head, its nodes times the query heads of the
 // group, see the same earlier cells: 128 of them are one tile of tcgen05.mma, which
@@ -125,7 +126,7 @@ struct Misc {
     int abort;
     uint32_t tmem;
     int lo_min, lo_max;                       // the rows' first visible cells
-    int base, end;                            // the tree's
+    int base, end;                            // the tree's (of one that does not fit 0)
     uint32_t bad[3][4];                       // keys of a tile whose V is not finite, three tiles in turn
     int last;
 };
@@ -358,8 +359,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         misc.abort = 0;
         misc.lo_min = a.kv.n_ctx;
         misc.lo_max = 0;
-        misc.base = tr.base;
-        misc.end = tr.base + tr.n;
+        misc.base = tr.ok ? tr.base : 0;
+        misc.end = tr.ok ? tr.base + tr.n : 0;
         for (int i = 0; i < 12; ++i) misc.bad[i / 4][i % 4] = 0u;
     }
     tc_fence_before();
@@ -395,7 +396,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 
     const float c = 1.4426950408889634f / sqrtf((float)hd);       // scores to exponents of two
     Ref ref{0.f, NONE};
-    float l_row = 0.f;
+    float l_row = -1.f;                                  // no sums
     bool have = false;                                   // O holds this CTA's sums
     if constexpr (F8) {
         // no warp waits for another before its own of these three, so the softmax's does end
@@ -729,6 +730,15 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             *reinterpret_cast<uint2 *>(a.o + ((size_t)t * a.H + (size_t)j * G + (at - nd * G)) * hd + 4 * chunk) =
                 make_uint2(pack_h2(v.x, v.y), pack_h2(v.z, v.w));
     };
+    // what a row without weights has: zeros, or NaN if it sees cells and all their scores are -inf
+    auto empty = [&](int row) {
+        const volatile Misc &now = misc;
+        const int t = tr.r0 + (mt * BQ + row) / G, base = now.base, n = now.end - base, pos = a.window > 0 && base > 0 ? a.pos[t] : 0;
+        bool sees = base > 0 && (pos < a.window || pos - a.window + 1 < base || a.window == 0);
+#pragma unroll 1
+        for (int w = 0; 32 * w < n; ++w) sees |= (__ldcg(a.mask + (size_t)t * a.words + w) & (~0u >> max(32 - (n - 32 * w), 0))) != 0u;
+        return sees ? __int_as_float(0x7FFFFFFF) : 0.f;
+    };
     for (int i = tid; i < my_rows * per; i += threads(F8)) {
         const int at = i / per, chunk = i - at * per;
         float M = -INFINITY, M2 = 0.f, L = 0.f;
@@ -737,7 +747,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < cs; ++s) {
             const float4 v = ml[s * share + at];
-            if (v.y == 0.f) continue;                    // that rank saw nothing of the row
+            if (v.y < 0.f) continue;                     // that rank has no sums
             const float f = moved(v.x, v.z, M, M2);
             const float4 x = *reinterpret_cast<const float4 *>(smem_raw + part_at(s, rank) + (uint32_t)at * (HD * 4) + ((chunk ^ (at & 7)) << 4));
             L = fmaf(f, v.y, L);
@@ -745,7 +755,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         const int row = rank * share + at;
         if (clusters == 1) {
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float inv = L == 0.f ? empty(row) : 1.f / L;
             store(row, chunk, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         } else {
             float *dst = slot_o(mine, row);
@@ -775,13 +785,12 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         for (int s = 0; s < clusters; ++s) {
             const float *src = slot_o(s, row);
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + HD));
-            if (v.y == 0.f) continue;
             const float f = moved(v.x, v.z, M, M2);
             const float4 x = __ldcg(reinterpret_cast<const float4 *>(src) + chunk);
             L = fmaf(f, v.y, L);
             o.x = fmaf(f, x.x, o.x); o.y = fmaf(f, x.y, o.y); o.z = fmaf(f, x.z, o.z); o.w = fmaf(f, x.w, o.w);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = L == 0.f ? empty(row) : 1.f / L;
         store(row, chunk, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
 }
