@@ -724,7 +724,8 @@ int32_t llm_op_attn_prefill_q4_0(const void *q, const void *k_cache, const void 
 
 /* cos and sin of positions: out fp32 [n_pos][n_rot / 2][2] holds, for position
  * pos0 + i and pair j, m cos(a) and m sin(a) of the angle a = (pos0 + i) * f_j,
- * angles in 64 bits.  With f = theta^(-2 j / n_rot), f_j is by `scaling`
+ * angles in 64 bits: f_j is float64's, rounded to 2^-64 of a turn, and an angle kept
+ * to 2^-55 of a turn.  With f = theta^(-2 j / n_rot), f_j is by `scaling`
  *   LLM_ROPE_NONE    f
  *   LLM_ROPE_LINEAR  f / factor
  *   LLM_ROPE_BANDS   f * k + f / factor * (1 - k), k = (t - slow) / (fast - slow)

@@ -4,9 +4,12 @@
 // parameters of llama_context).
 //
 // Angles are kept as fractions of a turn in 64-bit fixed point, where a position's
-// angle is one integer product that drops whole turns by itself: the frequency is
-// good to 2^-53 of it and the product exact, as good as an angle in float64 however
-// far the position.  The nearest of 512 directions e^(ia), kept as pairs of floats,
+// angle is one integer product that drops whole turns by itself.  A frequency is
+// float64's, rounded to 2^-64 of a turn, so an angle is off by 2^-53 of it and by
+// 2^-65 of a turn times the position (2^-35 of a turn at position 2^30).  Only for a pair
+// slower than 2^-41 of a turn a position (theta times factor above 10^11) does that
+// leave small sines with fewer bits than a float's.
+// The nearest of 512 directions e^(ia), kept as pairs of floats,
 // is turned by the rest |d| <= pi / 512, whose sine and cosine - 1 are two terms of
 // their series (the next is below 2^-50):
 //   cos(a + d) = cos a + (cos a (cos d - 1) - sin a sin d),  and sin alike.
@@ -140,7 +143,7 @@ cudaError_t launch_rope_table(const RopeSpec &r, int pos0, int n_pos, int width,
     double f[MAX_PAIRS], scale;
     rope_frequencies(r, f, &scale);
     Frequencies fr;
-    for (int i = 0; i < pairs; ++i) fr.f[i] = (unsigned long long)(f[i] / (2 * PI) * 18446744073709551616.0);
+    for (int i = 0; i < pairs; ++i) fr.f[i] = (unsigned long long)std::llrint(f[i] / (2 * PI) * 18446744073709551616.0);      // at most 2^62
     fr.scale = (float)scale;
     fr.scale_lo = (float)(scale - (double)fr.scale);
     // four CTAs an SM: each fetches the directions once
