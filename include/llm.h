@@ -691,7 +691,7 @@ int32_t llm_op_attn_decode_q4_0(const float *q, const void *k_cache, const void 
  * pos, seq are HOST arrays, read before the call returns: the rows of a
  * sequence are consecutive with consecutive positions, else LLM_ERR_INVALID
  * before anything is enqueued.  o fp16 [T][H*hd].  q, K and V enter the products
- * exactly and the softmax weights with 22 bits (below 2^-21 of the row's largest
+ * exactly and the softmax weights with 22 bits (below 2^-10 of the row's largest
  * with 2^-31 of it); sums are fp32.  A visible cell whose scale stands for values
  * beyond fp16's range (more than 8188, an infinity or a NaN) makes the heads that
  * see it NaN; cells that a row does not see may hold anything.  q, the caches and
@@ -776,10 +776,10 @@ int32_t llm_op_rope_kv(const float *qkv, int32_t ld, const float *q_gain, const 
  *            it ready for the next, of any shape it is large enough for, and calls
  *            that may overlap need one each
  * q, K and V enter the products exactly and the softmax weights with 22 bits (below
- * 2^-21 of the row's largest with 2^-31 of it); sums are fp32.  A score of -inf has
+ * 2^-9 of the row's largest with 2^-30 of it); sums are fp32.  A score of -inf has
  * weight 0, and a row that sees no other is NaN; a score of +inf or NaN, or a visible
- * value that is not finite, gives its row and head values that are not finite; cells that a row does
- * not see may hold anything.  head_dim 32, 64 or 128; any H that is a multiple of
+ * value that is not finite, gives its row and head values that are not finite; cells
+ * that a row does not see may hold anything.  head_dim 32, 64 or 128; any H that is a multiple of
  * Hkv, up to 4096, with n_tree * Hkv * ceil(max_nodes * H / Hkv / 128) at most 65535;
  * q, the caches, o and scratch 16-byte aligned; else LLM_ERR_INVALID before
  * anything is enqueued.  *err is ORed with 4 when a bounded wait of the kernel

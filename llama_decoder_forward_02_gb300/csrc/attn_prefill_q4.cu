@@ -31,8 +31,8 @@
 //     them.  S_{t+3} is issued once O += P_t V_t is done.
 // The running maximum is raised, and O rescaled, only when a tile's maximum
 // passes it by 8 in base 2; weights are kept 2^7 times as large, so that those
-// far below the maximum stay normal fp16 numbers (below 2^-21 of it their parts
-// step by 2^-31 of it).
+// far below the maximum stay normal fp16 numbers (their low parts down to 2^-10 of it;
+// below that a weight is off by up to 2^-31 of it).
 //
 // Bound by the tensor cores and the shared memory that feeds them: 40 MMAs a key
 // tile where the fp16 cache's kernel has 16, 224 KB read by them and 128 KB

@@ -14,14 +14,16 @@
 //
 // Precision.  q, K and V are fp16 (an E4M3 value is one exactly); a weight
 // p = 2^((s - z) c + x), the exponent in fp32 with one rounding, enters O as two fp16
-// numbers of 22 bits together.  Rounded to one, o is off by 1.4 times its own rounding.
+// numbers of 22 bits together (below 2^-3, where the low one has no full 11, to 2^-24).
+// Rounded to one, o is off by 1.4 times its own rounding.
 // z and x are a row's reference, raised, with O rescaled, only when a tile passes it by
 // 2^8.  Usually z is 0 and x a whole number, so that changing it is exact: 7 (weights far
 // below the largest stay normal fp16 numbers) less the row's largest s c so far, rounded
 // up.  From 2^22 on, where steps of fp32 would come to swallow the 7 and the row's
 // weights with it, z is the largest score so far and x is 7; a tile's scores are brought to
 // s - z in the branch that raises references, which other rows seldom take.  So a row's
-// largest weight lies in [2^6, 2^15] whatever its scores.
+// largest weight lies in [2^6, 2^15] whatever its scores, and its weights have 22 bits down
+// to 2^-9 of that, and 2^-30 of it below.
 //
 // A CTA: warps 0-7 softmax (two threads a row, 64 keys each), 8 issues S = q K^T, 9
 // O += P V, 10 brings K and 11 V by TMA, of an E4M3 cache to warps 12-15 and 16-19, which
