@@ -232,11 +232,13 @@ int32_t llm_decode(llm_ctx *c, const llm_batch *b);
  * (llm_get_argmax's or llm_sample's output): node 0 stands, after a node that
  * stands its child whose token is the node's target, the lowest of several.  The
  * keys and values of the nodes that stand are moved behind the cached positions
- * and the sequence continues after them: it holds the same as if their tokens
- * had been decoded one by one.  HOST outputs, each may be NULL: path[] one entry a
- * node in batch order, for tree i the nodes that stand from its first entry on,
- * then -1; n_accept[i] their number; next[i] the target of the last, node 0 of the
- * sequence's next tree.  Any call in between that changes a cache (llm_decode,
+ * and the sequence continues after them: it holds what it would had their tokens
+ * been decoded one by one, up to rounding (a tree's queries are rounded to fp16, as
+ * a prompt's are, and more than 8 nodes in all go through the prefill's products; a
+ * step of one row keeps its queries in fp32).  HOST outputs, each may be NULL:
+ * path[] one entry a node in batch order, for tree i the nodes that stand from its
+ * first entry on, then -1; n_accept[i] their number; next[i] the target of the
+ * last, node 0 of the sequence's next tree.  Any call in between that changes a cache (llm_decode,
  * llm_generate, llm_seq_clear, llm_seq_shift) drops the tree; the logits stay
  * until the next call that makes some, but llm_generate does not start from
  * those of a tree.  Asynchronous like llm_decode.  Return codes as llm_decode:
