@@ -42,7 +42,7 @@
 // outside the tree's cells become zero, and a value that is not finite makes the
 // rows that see its cell NaN and is zero for the others.
 //
-// What bounds it: not memory (64 nodes of 32000 cells, 8 kv heads of 128: 52.5 us, 2.5 TB/s)
+// What bounds it: not memory (64 nodes of 32000 cells, 8 kv heads of 128: 51 us, 2.6 TB/s)
 // nor the tensor pipe, but the chain of a tile, which one row tile an SM cannot overlap
 // with another's: S, its maximum, 2^x and the split (10.6 cycles a warp and score), P V
 // take 1.2 us for 128 keys, before them 8 us to start and after them 6 us to join.
@@ -78,8 +78,8 @@ constexpr int BQ = 128, BKEY = 128;
 constexpr int SM_WARPS = 8, PARTS = 2, S_WARP = 8, PV_WARP = 9, K_WARP = 10, V_WARP = 11, W_WARP = 12, W_WARPS = 8;
 constexpr int threads(bool f8) { return (W_WARP + (f8 ? W_WARPS : 0)) * 32; }
 // Registers of a thread of the E4M3 kernel: at its launch, of the softmax (which at 96 spills a row's scores:
-// 16 nodes of 32000 cells 47 us, not 35), the widening and the issuers.  256 x 128 + 256 x 72 + 128 x 80 = 640 x 96.
-// With four widening warps and 128 registers for all the case takes 37.6 us.
+// 16 nodes of 32000 cells 48.5 us, not 33.6), the widening and the issuers.  256 x 128 + 256 x 72 + 128 x 80 = 640 x 96.
+// With four widening warps and 128 registers for all the case takes 34.1 us.
 constexpr int L_REGS = 96, SM_REGS = 128, W_REGS = 72, I_REGS = 80;
 static_assert(SM_WARPS * SM_REGS + W_WARPS * W_REGS + (W_WARP - S_WARP) * I_REGS <= threads(true) / 32 * L_REGS, "registers");
 constexpr uint32_t BOX = 128 * 128;          // bytes of one 128-row x 64-column fp16 box
@@ -608,7 +608,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     }
         }
     } else if (F8 && warp >= W_WARP) {
-        // ---- widening, K by the first half of the warps and V by the second (all of them in turn: 38.0 us, not 35.2),
+        // ---- widening, K by the first half of the warps and V by the second (all of them in turn were 8% slower),
         // each with a ring of its own, so that none waits for a phase it may be two behind
         const int ww = (warp - W_WARP) % (W_WARPS / 2);
         const bool k = warp < W_WARP + W_WARPS / 2;
@@ -804,8 +804,10 @@ int max_clusters[MAX_DEV][MAX_CLUSTER + 1];
 // CTAs of a cluster and clusters of a group: the split that keeps most SMs busy, of
 // equals the one with the larger clusters (a join in shared memory costs less than
 // one through memory).  Several clusters only where a CTA keeps four tiles: their join
-// through memory costs as much as two (8 nodes of 700 cells: 7.0 us, with up to a tile
-// for each CTA 9.5; 16 of 2100: 12.4 and 15.8).
+// through memory costs as much as two (8 nodes of 700 cells: 7.1 us, with up to a tile
+// for each CTA 9.4; 16 of 2100: 12.3 and 15.4).  How many cells are in use is known on the
+// device alone, so this goes by the cache's capacity: short trees in caches of 6144
+// cells and more pay for the join all the same (9.4 and 15.5 us).
 struct Plan { int cs, clusters; };
 Plan plan(int groups, int n_ctx) {
     int dev = 0;

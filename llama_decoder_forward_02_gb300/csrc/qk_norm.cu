@@ -15,14 +15,14 @@
 // magnitude are a few shuffles for several heads at once and every access is a
 // vector; a CTA takes a row, whose position, cosines and gains each lane reads
 // once.  Bound by memory: 4 bytes read and about 2 written an element.  4096
-// rows of 32 + 8 + 8 heads of 128 into an fp16 cache take 29.6 us, 76% of the
+// rows of 32 + 8 + 8 heads of 128 into an fp16 cache take 29.9 us, 76% of the
 // copy bandwidth for their 153 MB (five CTAs of 48 registers an SM; four took
 // 32.8).  With four elements a lane the shuffles, addresses and branches of
 // twice as many lanes took 42.7 us, bound by issue.
 //
 // Rotated by halves ((e, e + n_rot / 2) instead of adjacent pairs) the 4096 rows take
-// 31.9 us, and 512 rows of heads of 64, half of each rotated, 3.1; the normed queries
-// and keys of 16 rows 1.8.
+// 31.9 us, and 512 rows of heads of 64, half of each rotated, 3.1; 16 rows of
+// tree nodes in pairs 1.7.
 //
 // Into a Q4_0 cache 512 rows take 7.2 us (4.8 into an fp16 one), 8 rows 3.7.
 //

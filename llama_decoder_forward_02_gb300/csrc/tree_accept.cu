@@ -16,8 +16,8 @@
 // Bound by latency: row numbers, then parents, then their targets, the walk, then the
 // rows, each a load that waits for the one before.  One tree of 16 nodes, 5 accepted, of
 // 32 layers of 8 kv heads of 128: 2.7 us back to back, eight trees of 64 6.2 us, where
-// the bytes would take 1.5.  Fewer CTAs with several planes each (6.0 us) or eight
-// units of a thread in flight (8.3) change little.
+// the bytes would take 1.5.  Fewer CTAs with several planes each take about the same
+// (6.0 us), eight units of a thread in flight more (8.3).
 #include "common.cuh"
 #include "launch.cuh"
 
