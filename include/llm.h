@@ -238,14 +238,16 @@ int32_t llm_decode(llm_ctx *c, const llm_batch *b);
  * step of one row keeps its queries in fp32).  HOST outputs, each may be NULL:
  * path[] one entry a node in batch order, for tree i the nodes that stand from its
  * first entry on, then -1; n_accept[i] their number; next[i] the target of the
- * last, node 0 of the sequence's next tree.  Any call in between that changes a cache (llm_decode,
- * llm_generate, llm_seq_clear, llm_seq_shift) drops the tree; the logits stay
- * until the next call that makes some, but llm_generate does not start from
+ * last, node 0 of the sequence's next tree.  Any call in between that changes a
+ * cache (llm_decode, llm_generate, llm_seq_clear, llm_seq_shift) drops the tree; the
+ * logits stay until the next call that makes some, but llm_generate does not start from
  * those of a tree.  Asynchronous like llm_decode.  Return codes as llm_decode:
  * LLM_NO_KV_ROOM (nothing written) if a tree's nodes would pass n_ctx;
- * LLM_ERR_INVALID for an invalid batch, more nodes than n_ubatch, a Q4_0 cache, or
- * llm_tree_accept without a tree that waits.  The first llm_decode_tree of a
- * context allocates its workspace (LLM_ERR_ALLOC if that fails). */
+ * LLM_ERR_INVALID for an invalid batch, more nodes than n_ubatch, a Q4_0 cache, a
+ * cache of 2^31 rows (n_seq_max * n_layer * n_head_kv * n_ctx) or more, trees of more
+ * groups than llm_op_attn_tree takes, or llm_tree_accept without a tree that waits.
+ * The first llm_decode_tree of a context allocates its workspace (LLM_ERR_ALLOC if
+ * that fails). */
 typedef struct {
     int32_t n_trees;
     const int32_t *n_nodes;
@@ -781,10 +783,10 @@ int32_t llm_op_rope_kv(const float *qkv, int32_t ld, const float *q_gain, const 
  * 2^-9 of the row's largest with 2^-30 of it); sums are fp32.  A score of -inf has
  * weight 0, and a row that sees no other is NaN; a score of +inf or NaN, or a visible
  * value that is not finite, gives its row and head values that are not finite; cells
- * that a row does not see may hold anything.  head_dim 32, 64 or 128; any H that is a multiple of
- * Hkv, up to 4096, with n_tree * Hkv * ceil(max_nodes * H / Hkv / 128) at most 65535;
- * q, the caches, o and scratch 16-byte aligned; else LLM_ERR_INVALID before
- * anything is enqueued.  *err is ORed with 4 when a bounded wait of the kernel
+ * that a row does not see may hold anything.  head_dim 32, 64 or 128; any H that is
+ * a multiple of Hkv, up to 4096, with n_tree * Hkv * ceil(max_nodes * H / Hkv / 128)
+ * at most 65535; q, the caches, o and scratch 16-byte aligned; else LLM_ERR_INVALID
+ * before anything is enqueued.  *err is ORed with 4 when a bounded wait of the kernel
  * timed out. */
 int64_t llm_op_attn_tree_scratch_bytes(int32_t n_tree, int32_t max_nodes, int32_t H, int32_t Hkv, int32_t hd,
                                        int32_t n_ctx);
